@@ -22,6 +22,11 @@ __all__ = ["CoatError", "coat_fp8_adamw_step", "coat_fp8_adamw_step_host",
            "coat_fp8_adamw_step_host_workspace_bytes", "coat_fp8_adamw_step_host_static",
            "coat_dre_quantize", "coat_fp8_quantize_absmax", "coat_act_quantize_fp8",
            "coat_fp8_linear_group_quantize",
+           "coat_rmsnorm_ckpt", "coat_rmsnorm_ckpt_backward",
+           "coat_rmsnorm_ckpt_backward_workspace_bytes", "coat_swiglu_ckpt",
+           "coat_swiglu_ckpt_backward", "coat_qk_norm_rope_ckpt",
+           "coat_qk_norm_rope_ckpt_backward", "coat_qk_norm_rope_ckpt_backward_workspace_bytes",
+           "coat_ckpt_weight_grad", "coat_ckpt_weight_grad_workspace_bytes",
            "coat_dre_dequantize", "coat_exact_recompute_counts", "coat_kernel_wait_timeouts",
            "coat_status_string",
            "coat_r_e4m3", "coat_version", "lib",
@@ -43,6 +48,11 @@ EXPORTS = ("coat_fp8_adamw_step", "coat_fp8_adamw_step_host",
            "coat_fp8_adamw_step_host_workspace_bytes", "coat_fp8_adamw_step_host_static",
            "coat_dre_quantize", "coat_fp8_quantize_absmax", "coat_act_quantize_fp8",
            "coat_fp8_linear_group_quantize",
+           "coat_rmsnorm_ckpt", "coat_rmsnorm_ckpt_backward",
+           "coat_rmsnorm_ckpt_backward_workspace_bytes", "coat_swiglu_ckpt",
+           "coat_swiglu_ckpt_backward", "coat_qk_norm_rope_ckpt",
+           "coat_qk_norm_rope_ckpt_backward", "coat_qk_norm_rope_ckpt_backward_workspace_bytes",
+           "coat_ckpt_weight_grad", "coat_ckpt_weight_grad_workspace_bytes",
            "coat_dre_dequantize", "coat_exact_recompute_counts", "coat_kernel_wait_timeouts",
            "coat_status_string",
            "coat_r_e4m3", "coat_version")
@@ -101,6 +111,32 @@ def lib() -> ctypes.CDLL:
         L.coat_exact_recompute_counts.restype = ctypes.c_int
         L.coat_kernel_wait_timeouts.argtypes = [vp, i32]
         L.coat_kernel_wait_timeouts.restype = ctypes.c_int
+        L.coat_rmsnorm_ckpt.argtypes = [vp, vp, vp, f32, i64, i64, i32, vp, vp, vp, vp, vp, vp]
+        L.coat_rmsnorm_ckpt.restype = ctypes.c_int
+        L.coat_rmsnorm_ckpt_backward.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i32, vp, vp, vp,
+                                                 ctypes.c_size_t, vp]
+        L.coat_rmsnorm_ckpt_backward.restype = ctypes.c_int
+        L.coat_rmsnorm_ckpt_backward_workspace_bytes.argtypes = [i64, i64]
+        L.coat_rmsnorm_ckpt_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.coat_swiglu_ckpt.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp]
+        L.coat_swiglu_ckpt.restype = ctypes.c_int
+        L.coat_swiglu_ckpt_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, vp, vp, i64, vp, vp,
+                                                vp]
+        L.coat_swiglu_ckpt_backward.restype = ctypes.c_int
+        L.coat_qk_norm_rope_ckpt.argtypes = [vp, i64, i32, vp, i64, i32, i32, vp, vp, f32, vp, vp, i64,
+                                             i32, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.coat_qk_norm_rope_ckpt.restype = ctypes.c_int
+        L.coat_qk_norm_rope_ckpt_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp,
+                                                      vp, vp, vp, i64, i32, vp, i32, i64, i32, vp, i64,
+                                                      vp, i64, vp, vp, vp, ctypes.c_size_t, vp]
+        L.coat_qk_norm_rope_ckpt_backward.restype = ctypes.c_int
+        L.coat_qk_norm_rope_ckpt_backward_workspace_bytes.argtypes = [i64, i32]
+        L.coat_qk_norm_rope_ckpt_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.coat_ckpt_weight_grad.argtypes = [vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, vp, vp,
+                                            ctypes.c_size_t, vp]
+        L.coat_ckpt_weight_grad.restype = ctypes.c_int
+        L.coat_ckpt_weight_grad_workspace_bytes.argtypes = [i64, i64, i64]
+        L.coat_ckpt_weight_grad_workspace_bytes.restype = ctypes.c_size_t
         L.coat_status_string.argtypes = [ctypes.c_int]
         L.coat_status_string.restype = ctypes.c_char_p
         L.coat_r_e4m3.argtypes = []
@@ -363,3 +399,10 @@ def coat_dre_dequantize(q, scale, k, G: int, x, stream=None) -> None:
         st = lib().coat_dre_dequantize(pq, ps, pk, n, int(G), px, _stream_ptr(stream))
     if st != 0:
         raise CoatError(st, "coat_dre_dequantize")
+
+
+from .ckpt import (  # noqa: E402  (uses the helpers above)
+    coat_ckpt_weight_grad, coat_ckpt_weight_grad_workspace_bytes, coat_qk_norm_rope_ckpt,
+    coat_qk_norm_rope_ckpt_backward, coat_qk_norm_rope_ckpt_backward_workspace_bytes,
+    coat_rmsnorm_ckpt, coat_rmsnorm_ckpt_backward, coat_rmsnorm_ckpt_backward_workspace_bytes,
+    coat_swiglu_ckpt, coat_swiglu_ckpt_backward)

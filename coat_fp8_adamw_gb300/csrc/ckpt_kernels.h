@@ -1,0 +1,122 @@
+// ckpt_kernels.h -- internal launch interface between the C ABI (ckpt_abi.cu)
+// and the kernels of the operators with 8-bit activation checkpoints.  Not part
+// of the public header.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace coat {
+
+struct NormFwdArgs {
+    const uint16_t* x;         // M x N bf16
+    const uint16_t* residual;  // M x N bf16, or null
+    const float* weight;       // N
+    float eps;
+    int64_t M, N;
+    int32_t G;
+    uint16_t* h;               // M x N bf16: x + residual (null without a residual)
+    uint16_t* y;               // M x N bf16
+    uint8_t* q;                // M x N codes of the norm's input
+    float* scale;              // M x N/G
+    float* rstd;               // M
+};
+
+struct NormBwdArgs {
+    const uint16_t* dy;        // M x N bf16
+    const uint8_t* q;          // M x N codes
+    const float* scale;        // M x N/G
+    const float* rstd;         // M
+    const float* weight;       // N
+    const uint16_t* dresidual; // M x N bf16, or null
+    int64_t M, N;
+    int32_t G;
+    uint16_t* dx;              // M x N bf16
+    uint16_t* dweight;         // N bf16
+    float* partial;            // norm_bwd_partials(...) x N
+};
+
+struct SwigluFwdArgs {
+    const uint16_t* gate;      // M rows of N bf16, ld apart
+    const uint16_t* up;
+    int64_t ld;
+    int64_t M, N;
+    int32_t G;
+    uint16_t* h;               // M x N bf16
+    uint8_t* gate_q;           // M x N codes
+    float* gate_scale;         // M x N/G
+    uint8_t* up_q;
+    float* up_scale;
+};
+
+struct SwigluBwdArgs {
+    const uint16_t* dh;        // M x N bf16
+    const uint8_t* gate_q;
+    const float* gate_scale;
+    const uint8_t* up_q;
+    const float* up_scale;
+    int64_t M, N;
+    int32_t G;
+    uint16_t* dgate;           // M rows of N bf16, ld apart
+    uint16_t* dup;
+    int64_t ld;
+    uint8_t* h_q;              // M x N codes of silu(gate) up, or null
+    float* h_scale;            // M x N/G, or null
+};
+
+// One of the two sides (queries, keys) of the head norm; H = 0: no such side.
+struct HeadSide {
+    const uint16_t* in;        // forward: x (rows ld apart); backward: dy, contiguous
+    uint16_t* out;             // forward: y, contiguous; backward: dx (rows ld apart)
+    int64_t ld;
+    int32_t H;
+    const float* weight;       // D
+    uint8_t* codes;            // M x H x D (read in the backward pass)
+    float* scale;              // M x H x D/G
+    float* rstd;               // M x H
+    uint16_t* dweight;         // D bf16 (backward only)
+};
+struct QkArgs {
+    HeadSide q, k;
+    const float* cos;          // max_pos x rot/2
+    const float* sin;
+    const int32_t* positions;  // M
+    int64_t M, max_pos;
+    int32_t D, rot, G;
+    int32_t interleaved;
+    float eps;
+    float* partial;            // backward only
+};
+
+struct WgradArgs {
+    const uint16_t* dy;        // M rows of N bf16, dy_ld apart
+    int64_t dy_ld;
+    const uint8_t* q;          // M x K codes
+    const float* scale;        // M x K/G
+    const float* row_scale;    // M, or null
+    const float* col_scale;    // K, or null
+    int64_t M, N, K;
+    int32_t G;
+    uint16_t* dw;              // N x K bf16
+    float* partial;
+};
+
+constexpr int64_t kNormMaxN = 16384;   // columns of a normalised row
+
+int device_sms();
+int64_t norm_bwd_partials(int64_t M, int64_t N, int sms);
+int64_t qk_bwd_partials(int64_t M, int sms);
+size_t wgrad_workspace(int64_t M, int64_t N, int64_t K, int sms);
+
+cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s);
+cudaError_t launch_swiglu_fwd(const SwigluFwdArgs& a, cudaStream_t s);
+cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s);
+cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t s);
+cudaError_t launch_qk_bwd(const QkArgs& a, cudaStream_t s);
+cudaError_t launch_wgrad(const WgradArgs& a, cudaStream_t s);
+// out[c] = bf16(sum over p of partial[p * N + c]), p in order
+cudaError_t launch_column_sum(const float* partial, int64_t P, int64_t N, uint16_t* out, cudaStream_t s);
+
+}  // namespace coat

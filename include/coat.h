@@ -294,6 +294,146 @@ coat_status coat_exact_recompute_counts(uint64_t counts[2], int32_t reset);
  */
 coat_status coat_kernel_wait_timeouts(uint64_t *count, int32_t reset);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of a training step that keep their inputs as 8-bit checkpoints
+ * (COAT review page, section 3: FP8 activations kept for the backward pass,
+ * 1 x G groups for non-linear layers).
+ *
+ * A checkpoint of a bf16 or fp32 matrix [M x N] is what coat_act_quantize_fp8
+ * writes: per row and group of G consecutive columns scale = RN(max|x| / 448)
+ * and q = E4M3(x / scale), rounded to nearest even of the exact quotient; a
+ * group of zeros has scale 0 and zero codes.  It stands for scale E4M3(q).
+ *
+ * For all of them: bf16 tensors are raw 16-bit patterns; everything between
+ * input and output is float32, rounded once where an output is bf16; G is a
+ * power of two in [8, 128] (COAT_ERR_UNSUPPORTED_G otherwise); widths are
+ * multiples of 16 and of G; row counts are at least 1; row strides (`ld`, in
+ * elements) are at least the row's width and multiples of 8; every pointer is
+ * 16-byte aligned; outputs overlap neither inputs nor each other, except that
+ * two outputs with row strides may be column ranges of one tensor.  Gradients
+ * of weights come as bf16, the type that coat_fp8_adamw_step reads, and norm
+ * weights as fp32, the type of its master weights.  Results do not depend on
+ * the order in which blocks run.  `workspace` is scratch of the caller's (its
+ * content before the call does not matter, and two calls that may run at once
+ * need one each); the *_workspace_bytes functions say how much a call on the
+ * current device needs (0: bad sizes), and a smaller one is
+ * COAT_ERR_INVALID_ARG.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * RMS norm of rows with a checkpoint of its input.
+ *   h = x, or x + residual rounded to bf16;  rstd = 1 / sqrt(mean(h^2) + eps);
+ *   y = h rstd weight;  (q, scale) = the checkpoint of h.
+ *   x [M x N] bf16 in;  residual [M x N] bf16 in, or NULL;  weight [N] in;
+ *   h [M x N] bf16 out with a residual, else NULL;  y [M x N] bf16 out;
+ *   q [M x N] uint8 out;  scale [M x N/G] out;  rstd [M] out.
+ * N <= 16384; eps finite and > 0.
+ */
+coat_status coat_rmsnorm_ckpt(const uint16_t *x, const uint16_t *residual, const float *weight, float eps,
+                              int64_t M, int64_t N, int32_t G, uint16_t *h, uint16_t *y, uint8_t *q,
+                              float *scale, float *rstd, void *stream);
+
+/*
+ * Its backward pass, from the checkpoint: xh = scale E4M3(q) rstd, g = dy weight,
+ *   dx = rstd (g - xh mean(g xh)) (+ dresidual);  dweight = sum over rows of dy xh.
+ *   dy [M x N] bf16 in;  q, scale, rstd as the forward pass left them;
+ *   dresidual [M x N] bf16 in, or NULL: the gradient that reaches h past the norm;
+ *   dx [M x N] bf16 out (the gradient of x and of the residual);
+ *   dweight [N] bf16 out.
+ */
+coat_status coat_rmsnorm_ckpt_backward(const uint16_t *dy, const uint8_t *q, const float *scale,
+                                       const float *rstd, const float *weight, const uint16_t *dresidual,
+                                       int64_t M, int64_t N, int32_t G, uint16_t *dx, uint16_t *dweight,
+                                       void *workspace, size_t workspace_bytes, void *stream);
+size_t coat_rmsnorm_ckpt_backward_workspace_bytes(int64_t M, int64_t N);
+
+/*
+ * h = silu(gate) up with checkpoints of gate and up, silu(g) = g / (1 + e^-g).
+ *   gate, up  M rows of N bf16, ld apart (column ranges of one tensor, or two
+ *             tensors), in;
+ *   h [M x N] bf16 out;  gate_q, up_q [M x N] uint8 out;
+ *   gate_scale, up_scale [M x N/G] out.
+ */
+coat_status coat_swiglu_ckpt(const uint16_t *gate, const uint16_t *up, int64_t ld, int64_t M, int64_t N,
+                             int32_t G, uint16_t *h, uint8_t *gate_q, float *gate_scale, uint8_t *up_q,
+                             float *up_scale, void *stream);
+
+/*
+ * Its backward pass, with g and u as the checkpoints give them, s = 1 / (1 + e^-g):
+ *   dgate = dh u s (1 + g (1 - s));  dup = dh g s.
+ *   dh [M x N] bf16 in;  dgate, dup  M rows of N bf16, ld apart, out;
+ *   h_q [M x N] uint8, h_scale [M x N/G] out, or both NULL: the checkpoint of
+ *   g s u (of its float32 value), which is what the weight gradient of the
+ *   projection behind the product reads.
+ */
+coat_status coat_swiglu_ckpt_backward(const uint16_t *dh, const uint8_t *gate_q, const float *gate_scale,
+                                      const uint8_t *up_q, const float *up_scale, int64_t M, int64_t N,
+                                      int32_t G, uint16_t *dgate, uint16_t *dup, int64_t ld, uint8_t *h_q,
+                                      float *h_scale, void *stream);
+
+/*
+ * RMS norm of every query and key head, with the position rotation, and a
+ * checkpoint of the heads before the norm.
+ *   per token m and head x [D]: rstd = 1 / sqrt(mean(x^2) + eps), y = x rstd w;
+ *   the first rot entries of y are turned in pairs (a, b), pair i < rot/2 by
+ *   c = cos[positions[m], i], s = sin[positions[m], i]: (a c - b s, b c + a s).
+ *   Pair i is (i, i + rot/2), or (2i, 2i + 1) when `interleaved` is not 0.
+ *   q  M rows of Hq x D bf16, q_ld apart, in;  k  M rows of Hk x D, k_ld apart;
+ *   q_weight, k_weight [D] in;  cos, sin [max_pos x rot/2] in;
+ *   positions [M] int32 in (one outside [0, max_pos) turns its token's rotated
+ *   entries into NaN);
+ *   q_out [M x Hq x D] bf16, q_codes [M x Hq x D] uint8, q_scale [M x Hq x D/G],
+ *   q_rstd [M x Hq] out, and the same for k.
+ * Hq or Hk may be 0 (their pointers are ignored), not both; D a multiple of 16
+ * in [16, 256] and of G; rot a multiple of 16 in [16, D].
+ */
+coat_status coat_qk_norm_rope_ckpt(const uint16_t *q, int64_t q_ld, int32_t Hq, const uint16_t *k,
+                                   int64_t k_ld, int32_t Hk, int32_t D, const float *q_weight,
+                                   const float *k_weight, float eps, const float *cos, const float *sin,
+                                   int64_t max_pos, int32_t rot, const int32_t *positions,
+                                   int32_t interleaved, int64_t M, int32_t G, uint16_t *q_out,
+                                   uint8_t *q_codes, float *q_scale, float *q_rstd, uint16_t *k_out,
+                                   uint8_t *k_codes, float *k_scale, float *k_rstd, void *stream);
+
+/*
+ * Its backward pass, from the checkpoint: dn = the gradient of the rotated head
+ * turned back, xh = scale E4M3(codes) rstd, g = dn w:
+ *   dx = rstd (g - xh mean(g xh)) per head;  dw = sum over tokens and heads of dn xh.
+ *   dq_out [M x Hq x D], dk_out [M x Hk x D] bf16 in;
+ *   dq  M rows of Hq x D bf16, dq_ld apart, out;  dk likewise (column ranges of
+ *   one tensor, or two tensors);  dq_weight, dk_weight [D] bf16 out.
+ */
+coat_status coat_qk_norm_rope_ckpt_backward(const uint16_t *dq_out, const uint16_t *dk_out,
+                                            const uint8_t *q_codes, const float *q_scale,
+                                            const float *q_rstd, const uint8_t *k_codes,
+                                            const float *k_scale, const float *k_rstd, int32_t Hq,
+                                            int32_t Hk, int32_t D, const float *q_weight,
+                                            const float *k_weight, const float *cos, const float *sin,
+                                            int64_t max_pos, int32_t rot, const int32_t *positions,
+                                            int32_t interleaved, int64_t M, int32_t G, uint16_t *dq,
+                                            int64_t dq_ld, uint16_t *dk, int64_t dk_ld,
+                                            uint16_t *dq_weight, uint16_t *dk_weight, void *workspace,
+                                            size_t workspace_bytes, void *stream);
+size_t coat_qk_norm_rope_ckpt_backward_workspace_bytes(int64_t M, int32_t D);
+
+/*
+ * Weight gradient of a linear layer y = x W^T from the checkpoint of x:
+ *   dw[n, k] = col_scale[k] sum over m of dy[m, n] row_scale[m] scale[m, k/G] E4M3(q[m, k]).
+ *   dy  M rows of N bf16, dy_ld apart, in;  q [M x K] uint8, scale [M x K/G] in;
+ *   row_scale [M], col_scale [K] in, or NULL: factors of 1.  With a norm's rstd
+ *   and weight, the checkpoint of the norm's INPUT stands for its output, so
+ *   one checkpoint serves the norm and the linear layers behind it;
+ *   dw [N x K] bf16 out (the weight's layout, out_features x in_features).
+ * N a multiple of 8, K of 16 and of G.
+ */
+coat_status coat_ckpt_weight_grad(const uint16_t *dy, int64_t dy_ld, const uint8_t *q, const float *scale,
+                                  const float *row_scale, const float *col_scale, int64_t M, int64_t N,
+                                  int64_t K, int32_t G, uint16_t *dw, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+size_t coat_ckpt_weight_grad_workspace_bytes(int64_t M, int64_t N, int64_t K);
+
 /* Static description of a status code (never NULL). */
 const char *coat_status_string(coat_status status);
 
