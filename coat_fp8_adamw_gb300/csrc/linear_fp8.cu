@@ -29,14 +29,13 @@
 // finish, frees its tensor memory and returns.
 #include <atomic>
 #include <cstdint>
-#include <cuda.h>   // CUtensorMap and its enums; the encoder is fetched at run time
 
+#include "ckpt_kernels.h"
 #include "coat_device.cuh"
 #include "coat_kernels.h"
+#include "tc_pipeline.cuh"
 
 namespace coat {
-
-__device__ unsigned long long g_wait_timeouts;
 
 namespace {
 
@@ -56,84 +55,11 @@ constexpr uint32_t kTmemCols = 2 * kBN;        // two accumulators of 256 f32 co
 constexpr int kBarOff = kStages * kStageBytes;
 constexpr int kNumBars = 2 * kStages + 5;      // full, empty, acc full x2, acc empty x2, done
 constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 1024-B alignment
-constexpr uint32_t kSpinLimit = 1u << 26;
 
 // Instruction descriptor of the pair's MMA: D in f32 (bits 4-5 = 1), A and B
 // E4M3 (bits 7-9 and 10-12 = 0), both K-major (bits 15, 16 = 0), N / 8 in
 // bits 17-22, M / 16 in bits 24-28 (M = 256 over the two CTAs).
 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)((2 * kBM) >> 4) << 24);
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-// ---- mbarriers ----
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0u;
-}
-// Wait for the phase of parity `parity` to complete, at most kSpinLimit
-// polls; give up early once another role has aborted (when `abort` is given).
-__device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
-        if (mbar_try(bar, parity)) return true;
-        if (abort && (i & 255u) == 255u && *abort) return false;
-    }
-    atomicAdd(&g_wait_timeouts, 1ull);
-    if (abort) *abort = 1u;
-    return false;
-}
-// the common case (the phase has already completed) without the call
-__device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
-    return mbar_try(bar, parity) || mbar_wait(bar, parity, abort);
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-// arrive on an mbarrier of either CTA of the cluster (a shared::cluster address)
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
-}
-
-// ---- clusters ----
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// the shared::cluster address of this CTA's shared address `a` in CTA `rank`
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t a, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    return r;
-}
-// every thread of both CTAs (the non-.aligned form: lanes of a warp may arrive apart)
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// ---- TMA ----
-// A 2-D tile into this CTA's shared memory, its bytes counted on `cbar`, an
-// mbarrier of either CTA of the pair (shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                                 uint32_t cbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(cbar)
-        : "memory");
-}
 
 // ---- tcgen05 ----
 // Shared-memory matrix descriptor of a K-major operand in the 128-byte
@@ -154,36 +80,6 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, 
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(kIdesc), "r"(accumulate)
-        : "memory");
-}
-// arrive on the mbarrier at shared address `bar` in every CTA of `mask` once
-// every MMA this thread issued before has completed
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"(mask)
-        : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 lanes x N consecutive 32-bit columns: thread i receives lane (taddr's lane + i)
-// (the wait for the registers is part of the same statement)
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]);
-template <>
-__device__ __forceinline__ void tmem_ld<32>(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-        "%30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
         : "memory");
 }
 
@@ -492,24 +388,6 @@ linear_fp8_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant
                      : "memory");
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                 CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-    static const EncodeTiled fn = []() -> EncodeTiled {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
 // rows x K bytes, row-major; boxes of 128 bytes x box_rows rows, 128-byte swizzle,
 // zeros outside the tensor
 bool encode_operand(CUtensorMap* map, const uint8_t* base, int64_t rows, int64_t K, uint32_t box_rows) {
@@ -583,10 +461,13 @@ cudaError_t launch_linear_fp8(const LinArgs& a, int G, cudaStream_t s) {
 }
 
 cudaError_t read_wait_timeouts(unsigned long long* out, bool reset) {
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_wait_timeouts, sizeof(*out));
-    if (e != cudaSuccess || !reset) return e;
     const unsigned long long zero = 0ull;
-    return cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero));
+    unsigned long long wgrad = 0ull;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_wait_timeouts, sizeof(*out));
+    if (e == cudaSuccess && reset) e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero));
+    if (e == cudaSuccess) e = read_wgrad_wait_timeouts(&wgrad, reset);
+    *out += wgrad;
+    return e;
 }
 
 }  // namespace coat
