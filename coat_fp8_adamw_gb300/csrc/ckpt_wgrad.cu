@@ -20,6 +20,7 @@
 // and X for its 128 columns:
 //   TMA warp       dY (two 64-column boxes, 128-byte swizzle; both CTAs' bytes
 //                  counted on the even CTA's barrier) and the raw codes;
+//   scale warp     the stage's group scales and token factors (cp.async);
 //   8 warps        codes -> bf16 operand in the swizzled layout;
 //   MMA thread     (even CTA) four tcgen05.mma.cta_group::2 kind::f16, M = N = 256,
 //                  K = 16, into one of two 256-column accumulators;
@@ -55,7 +56,11 @@ constexpr int kEpiWarps = 4;
 constexpr int kDeqWarps = 8;
 constexpr int kWgThreads = 32 * (4 + kEpiWarps + kDeqWarps);
 constexpr uint32_t kTmemCols = 2 * kTile;      // two accumulators of 256 f32 columns
-constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kMaxGroups = kHalf / 8;           // scale groups of a CTA's 128 columns
+constexpr int kSPitch = kTok + 4;              // floats between two groups' scales: banks 4 apart
+constexpr int kScaleBytes = (kMaxGroups * kSPitch + kTok) * 4;   // a stage's scales, and its tokens' r
+constexpr int kScaleOff = kStages * kStageBytes;
+constexpr int kBarOff = kScaleOff + kStages * kScaleBytes;
 constexpr int kNumBars = 4 * kStages + 5;      // dY full, codes full, X full, empty; acc full x2, acc empty x2, done
 constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 1024-B alignment
 constexpr int kMinSteps = 8;                   // fewest steps of a split's part
@@ -83,6 +88,14 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(kIdesc), "r"(accumulate)
         : "memory");
+}
+// 4 bytes global -> shared, asynchronously; zero where `ok` is not set
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+// one arrival on `bar` once every cp.async that this thread issued before has landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // a 2-D tile into this CTA's shared memory, counted on this CTA's own barrier
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -161,6 +174,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
     return v;
 }
+__device__ __forceinline__ float lds32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -190,7 +208,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(y_full(s), 1);
-            mbar_init(q_full(s), 1);
+            mbar_init(q_full(s), 1 + 32);   // the codes' copy, and every lane's scales
             mbar_init(x_full(s), 2 * kDeqWarps);
             mbar_init(empty(s), 1);
         }
@@ -272,6 +290,37 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
             mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
         }
         mbar_wait(done, 0u, nullptr);
+    } else if (warp == 3) {
+        // ---- scale loader (both CTAs): two tokens per lane, every group of this CTA's columns ----
+        const int64_t ngr = a.K / a.G;
+        const int groups = kHalf / a.G;
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int64_t i = cid; ok && i < items; i += nclusters) {
+            const Item it = item_at(i, plan);
+            const int64_t g0 = (it.k * kTile + rank * kHalf) / a.G;
+            for (int32_t st = it.from; st < it.to; ++st) {
+                if (!mbar_wait_fast(empty(s), ph ^ 1u, abort)) { ok = false; break; }
+                const uint32_t dst = sb + kScaleOff + (uint32_t)(s * kScaleBytes);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t m = (int64_t)st * kTok + lane + 32 * h;
+                    const bool row_ok = m < a.M;
+                    const float* src = a.scale + (row_ok ? m * ngr : 0);
+                    const uint32_t d = dst + 4u * (uint32_t)(lane + 32 * h);
+                    for (int j = 0; j < groups; ++j) {
+                        const bool in = row_ok && g0 + j < ngr;
+                        cp_async4(d + 4u * (uint32_t)(j * kSPitch), in ? src + g0 + j : a.scale, in);
+                    }
+                    if (a.row_scale)
+                        cp_async4(d + 4u * (uint32_t)(kMaxGroups * kSPitch), a.row_scale + (row_ok ? m : 0), row_ok);
+                }
+                cp_async_arrive(q_full(s));
+                if (++s == kStages) { s = 0; ph ^= 1u; }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp >= 4 && warp < 4 + kEpiWarps) {
         // ---- epilogue: lane = one row n of the tile ----
         const int q4 = warp & 3;
@@ -324,52 +373,37 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         // ---- codes -> bf16 operand: a thread takes 16 columns of two tokens per stage ----
         const int t = threadIdx.x - 32 * (4 + kEpiWarps);
         const int r0 = t >> 3, c = t & 7;              // token of the stage (and r0 + 32), 16-column chunk
-        const int64_t ngr = a.K / a.G;
         const uint32_t xb0 = map_to_rank(x_full(0), 0);
+        // the scales of the chunk's first and last eight columns, and the tokens' factors
+        const uint32_t s0 = 4u * (uint32_t)(((16 * c) / a.G) * kSPitch + r0);
+        const uint32_t s1 = 4u * (uint32_t)(((16 * c + 8) / a.G) * kSPitch + r0);
+        const uint32_t sr = 4u * (uint32_t)(kMaxGroups * kSPitch + r0);
+        const int u = 2 * (c & 3);         // 16-byte unit of the row; the swizzle XORs it with row % 8
+        const bool swap = c >= 4;          // the order of a chunk's halves that keeps a quarter-warp's eight stores on different banks
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
         for (int64_t i = cid; ok && i < items; i += nclusters) {
             const Item it = item_at(i, plan);
-            const int64_t k = it.k * kTile + rank * kHalf + 16 * c;
-            const bool col_ok = k < a.K;               // K % 16 == 0: all 16 columns or none
-            const int64_t g0 = k / a.G, g1 = (k + 8) / a.G;
-            float sc[2][2];                            // scales of the two tokens' first and last eight columns
-            auto load_scales = [&](int32_t st) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t m = (int64_t)st * kTok + r0 + 32 * h;
-                    sc[h][0] = sc[h][1] = 0.0f;
-                    if (col_ok && m < a.M) {
-                        const float r = a.row_scale ? __ldg(a.row_scale + m) : 1.0f;
-                        sc[h][0] = __ldg(a.scale + m * ngr + g0) * r;
-                        sc[h][1] = g1 == g0 ? sc[h][0] : __ldg(a.scale + m * ngr + g1) * r;
-                    }
-                }
-            };
-            load_scales(it.from);
             for (int32_t st = it.from; st < it.to; ++st) {
                 if (!mbar_wait_fast(q_full(s), ph, abort)) { ok = false; break; }
-                const uint32_t sa = sb + (uint32_t)(s * kStageBytes);
-                uint4 out[2][2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 v = lds128(sa + kYBytes + kXBytes + (uint32_t)((r0 + 32 * h) * kHalf + 16 * c));
-                    out[h][0] = make_uint4(deq2(v.x & 0xFFFFu, sc[h][0]), deq2(v.x >> 16, sc[h][0]),
-                                           deq2(v.y & 0xFFFFu, sc[h][0]), deq2(v.y >> 16, sc[h][0]));
-                    out[h][1] = make_uint4(deq2(v.z & 0xFFFFu, sc[h][1]), deq2(v.z >> 16, sc[h][1]),
-                                           deq2(v.w & 0xFFFFu, sc[h][1]), deq2(v.w >> 16, sc[h][1]));
-                }
-                if (st + 1 < it.to) load_scales(st + 1);
+                const uint32_t sa = sb + (uint32_t)(s * kStageBytes), ss = sb + kScaleOff + (uint32_t)(s * kScaleBytes);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int row = r0 + 32 * h;
+                    const uint4 v = lds128(sa + kYBytes + kXBytes + (uint32_t)(row * kHalf + 16 * c));
+                    float f0 = lds32(ss + s0 + 128u * h), f1 = lds32(ss + s1 + 128u * h);
+                    if (a.row_scale) {
+                        const float r = lds32(ss + sr + 128u * h);
+                        f0 *= r;
+                        f1 *= r;
+                    }
+                    const uint4 lo = make_uint4(deq2(v.x & 0xFFFFu, f0), deq2(v.x >> 16, f0), deq2(v.y & 0xFFFFu, f0), deq2(v.y >> 16, f0));
+                    const uint4 hi = make_uint4(deq2(v.z & 0xFFFFu, f1), deq2(v.z >> 16, f1), deq2(v.w & 0xFFFFu, f1), deq2(v.w >> 16, f1));
                     const uint32_t base = sa + kYBytes + (uint32_t)((c >> 2) * kBoxBytes + row * 128);
-                    const int u = 2 * (c & 3);         // 16-byte unit of the row; the swizzle XORs it with row % 8
-                    // the two halves in the order that keeps a quarter-warp's eight stores on different banks
-                    const int first = c >> 2;
-                    sts128(base + (uint32_t)(((u + first) ^ (row & 7)) * 16), out[h][first]);
-                    sts128(base + (uint32_t)(((u + 1 - first) ^ (row & 7)) * 16), out[h][1 - first]);
+                    const uint32_t a0 = base + (uint32_t)((u ^ (row & 7)) * 16), a1 = base + (uint32_t)(((u + 1) ^ (row & 7)) * 16);
+                    sts128(swap ? a1 : a0, swap ? hi : lo);
+                    sts128(swap ? a0 : a1, swap ? lo : hi);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
