@@ -388,18 +388,29 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
             for (int32_t st = it.from; st < it.to; ++st) {
                 if (!mbar_wait_fast(q_full(s), ph, abort)) { ok = false; break; }
                 const uint32_t sa = sb + (uint32_t)(s * kStageBytes), ss = sb + kScaleOff + (uint32_t)(s * kScaleBytes);
+                uint4 v[2];
+                float f0[2], f1[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v[h] = lds128(sa + kYBytes + kXBytes + (uint32_t)((r0 + 32 * h) * kHalf + 16 * c));
+                    f0[h] = lds32(ss + s0 + 128u * h);
+                    f1[h] = lds32(ss + s1 + 128u * h);
+                }
+                if (a.row_scale) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float r = lds32(ss + sr + 128u * h);
+                        f0[h] *= r;
+                        f1[h] *= r;
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int row = r0 + 32 * h;
-                    const uint4 v = lds128(sa + kYBytes + kXBytes + (uint32_t)(row * kHalf + 16 * c));
-                    float f0 = lds32(ss + s0 + 128u * h), f1 = lds32(ss + s1 + 128u * h);
-                    if (a.row_scale) {
-                        const float r = lds32(ss + sr + 128u * h);
-                        f0 *= r;
-                        f1 *= r;
-                    }
-                    const uint4 lo = make_uint4(deq2(v.x & 0xFFFFu, f0), deq2(v.x >> 16, f0), deq2(v.y & 0xFFFFu, f0), deq2(v.y >> 16, f0));
-                    const uint4 hi = make_uint4(deq2(v.z & 0xFFFFu, f1), deq2(v.z >> 16, f1), deq2(v.w & 0xFFFFu, f1), deq2(v.w >> 16, f1));
+                    const uint4 lo = make_uint4(deq2(v[h].x & 0xFFFFu, f0[h]), deq2(v[h].x >> 16, f0[h]),
+                                                deq2(v[h].y & 0xFFFFu, f0[h]), deq2(v[h].y >> 16, f0[h]));
+                    const uint4 hi = make_uint4(deq2(v[h].z & 0xFFFFu, f1[h]), deq2(v[h].z >> 16, f1[h]),
+                                                deq2(v[h].w & 0xFFFFu, f1[h]), deq2(v[h].w >> 16, f1[h]));
                     const uint32_t base = sa + kYBytes + (uint32_t)((c >> 2) * kBoxBytes + row * 128);
                     const uint32_t a0 = base + (uint32_t)((u ^ (row & 7)) * 16), a1 = base + (uint32_t)(((u + 1) ^ (row & 7)) * 16);
                     sts128(swap ? a1 : a0, swap ? hi : lo);
@@ -407,7 +418,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(xb0 + 8u * (uint32_t)s);
+                if (lane == 0) mbar_arrive_at(xb0 + 8u * (uint32_t)s);
                 if (++s == kStages) { s = 0; ph ^= 1u; }
             }
         }

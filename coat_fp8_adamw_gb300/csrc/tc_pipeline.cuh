@@ -60,6 +60,14 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
+// The same in the instruction's default form (release at CTA scope).  For a
+// signal whose data stays in the arriving CTA's shared memory and is read there
+// by the pair's MMA: the writes are ordered before that asynchronous read by
+// each writer's fence.proxy.async, not by the arrival, which only has to come
+// after it.  (A release to the cluster holds the arriving warp for about 0.6 us.)
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cbar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+}
 
 // ---- clusters ----
 __device__ __forceinline__ uint32_t cluster_rank() {
