@@ -9,22 +9,31 @@
 // linear layer behind the norm too.
 //
 // The sum runs over tokens, and a scale belongs to one token and G columns, so
-// it cannot be taken out of the sum: X is formed in shared memory as a bf16
-// operand, RN((S r) E4M3(q)), one rounding of a relative 2^-9 at most (dY is
-// bf16 already), and the products are summed in float32 by the tensor cores.
-// Both operands lie in memory with the output index along the row, which
-// the tensor cores read as "MN-major" operands: nothing is transposed.
+// it cannot be taken out of the sum: X is formed on the way as a bf16 operand,
+// RN((S r) E4M3(q)), one rounding of a relative 2^-8 at most (dY is bf16
+// already), and the products are summed in float32 by the tensor cores.
 //
 // Persistent CTA pairs (clusters of two, one CTA per SM) walk 256 x 256 tiles of
-// dW, 64 tokens per step.  Per step a CTA holds dY for its 128 rows of the tile
-// and X for its 128 columns:
-//   TMA warp       dY (two 64-column boxes, 128-byte swizzle; both CTAs' bytes
-//                  counted on the even CTA's barrier) and the raw codes;
-//   scale warp     the stage's group scales and token factors (cp.async);
-//   8 warps        codes -> bf16 operand in the swizzled layout;
-//   MMA thread     (even CTA) four tcgen05.mma.cta_group::2 kind::f16, M = N = 256,
-//                  K = 16, into one of two 256-column accumulators;
-//   4 warps        the finished accumulator: times c, to bf16, stored.
+// dW, 64 tokens per step, and compute dW^T: M = 256 columns k (128 per CTA),
+// N = 256 rows n.  X is the MMA's first operand and lies in TENSOR memory, dY the
+// second one in shared memory as it comes ("MN-major": the output index along the
+// row; nothing is transposed).  Per step:
+//   TMA warp        dY (64 tokens x this CTA's 128 rows n, two 128-byte-swizzled
+//                   boxes; both CTAs' bytes counted on the even CTA's barrier)
+//                   and the codes (64 tokens x this CTA's 128 columns k);
+//   2 scale warps   S r of the 64 tokens and the columns' groups, into shared memory;
+//   8 warps         codes -> X: a 16 x 16 block of codes is read transposed
+//                   (ldmatrix .b8), so that a thread has four tokens of one
+//                   column, and goes to tensor memory as 16 lanes x 16 bf16;
+//   MMA thread      (even CTA) four tcgen05.mma.cta_group::2 kind::f16, K = 16;
+//   4 warps         the finished accumulator: times c, to bf16, stored.
+// X in tensor memory is what makes the tensor cores the bound: with X written to
+// and read from shared memory its traffic (copies in, codes out, X in, both
+// operands out: 5 KB for each of the 128 B per clock that 512 clocks of MMA
+// leave) held the 8192 x 11008 x 4096 product at 0.54 ms.  The price is half of
+// tensor memory, so there is one accumulator, and the MMAs of a tile wait until
+// the last one's is read.
+//
 // Tiles left over after the last full round of the pairs are split along the
 // tokens, so that they too keep every pair busy: each part leaves a float32
 // tile in the workspace, and a second kernel adds the parts in order.
@@ -43,33 +52,31 @@ namespace {
 using namespace ckpt;
 
 constexpr int kTile = 256;                     // rows (n) and columns (k) of a pair's tile of dW
-constexpr int kHalf = kTile / 2;               // a CTA's rows of it, and its columns of X
+constexpr int kHalf = kTile / 2;               // a CTA's columns k of it, and its rows n of dY
 constexpr int kTok = 64;                       // tokens per stage
 constexpr int kMmaTok = 16;                    // tokens of one kind::f16 MMA
-constexpr int kStages = 5;
+constexpr int kStages = 8;
 constexpr int kBoxBytes = kTok * 128;          // 64 tokens x 64 bf16 columns
 constexpr int kYBytes = 2 * kBoxBytes;         // dY: 64 tokens x 128 columns
-constexpr int kXBytes = 2 * kBoxBytes;         // X in bf16
 constexpr int kQBytes = kTok * kHalf;          // the codes
-constexpr int kStageBytes = kYBytes + kXBytes + kQBytes;
+constexpr int kStageBytes = kYBytes + kQBytes;
 constexpr int kEpiWarps = 4;
 constexpr int kDeqWarps = 8;
 constexpr int kWgThreads = 32 * (4 + kEpiWarps + kDeqWarps);
-constexpr uint32_t kTmemCols = 2 * kTile;      // two accumulators of 256 f32 columns
-constexpr int kMaxGroups = kHalf / 8;           // scale groups of a CTA's 128 columns
-constexpr int kSPitch = kTok + 4;              // floats between two groups' scales: banks 4 apart
-constexpr int kScaleBytes = (kMaxGroups * kSPitch + kTok) * 4;   // a stage's scales, and its tokens' r
-constexpr int kScaleOff = kStages * kStageBytes;
-constexpr int kBarOff = kScaleOff + kStages * kScaleBytes;
-constexpr int kNumBars = 4 * kStages + 5;      // dY full, codes full, X full, empty; acc full x2, acc empty x2, done
-constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 1024-B alignment
+constexpr uint32_t kXCols = kTok / 2;          // tensor-memory columns of a stage of X
+constexpr uint32_t kTmemCols = 512;            // the accumulator (256) and the stages of X
+static_assert(kTile + kStages * kXCols <= kTmemCols, "tensor memory");
+constexpr int kNumBars = 4 * kStages + 3;      // dY full, codes full, X full, empty; acc full, acc empty, done
 constexpr int kMinSteps = 8;                   // fewest steps of a split's part
+constexpr int scale_bytes(int G) { return kTok * (kHalf / G) * 4; }   // of a stage
+constexpr int bar_off(int G) { return kStages * (kStageBytes + scale_bytes(G)); }
+constexpr int smem_bytes(int G) { return bar_off(G) + 8 * kNumBars + 16 + 1024; }   // + slack for 1024-B alignment
 
 // Instruction descriptor: D in f32 (bits 4-5 = 1), A and B bf16 (bits 7-9 and
-// 10-12 = 1), both MN-major (bits 15, 16), N / 8 in bits 17-22, M / 16 in bits
-// 24-28 (M = 256 over the two CTAs).
-constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                            ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+// 10-12 = 1), A as tensor memory holds it, B MN-major (bit 16), N / 8 in bits
+// 17-22, M / 16 in bits 24-28 (M = 256 over the two CTAs).
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kTile >> 3) << 17) |
+                            ((uint32_t)(kTile >> 4) << 24);
 
 // Shared-memory matrix descriptor of an MN-major operand in the 128-byte
 // swizzled layout: rows (tokens) of 128 bytes = 64 columns, 8-row (1024-byte)
@@ -81,21 +88,14 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBoxBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t accumulate) {
+// a_tmem: lane = row of A, K consecutive bf16 values, two per column
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(kIdesc), "r"(accumulate)
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(kIdesc), "r"(accumulate)
         : "memory");
-}
-// 4 bytes global -> shared, asynchronously; zero where `ok` is not set
-__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
-}
-// one arrival on `bar` once every cp.async that this thread issued before has landed
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 // a 2-D tile into this CTA's shared memory, counted on this CTA's own barrier
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
@@ -159,47 +159,65 @@ __device__ __forceinline__ Item item_at(int64_t i, const Plan& p) {
     return it;
 }
 
-// Two codes as bf16(value * s), packed
-__device__ __forceinline__ uint32_t deq2(uint32_t codes, float s) {
-    uint32_t h;
-    float lo, hi;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)codes));
+// Two 16 x 16 blocks of bytes, transposed: lane's address = row `lane` of the two
+// blocks (16 bytes each); r[2 b + h] = bytes 4 (lane % 4) .. + 3 of the
+// transposed block b's row lane / 4 + 8 h.
+__device__ __forceinline__ void ldmatrix_bytes(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+// 16 lanes x 16 columns: registers 4 b + 2 h + i of a thread are columns
+// 8 b + 2 (lane % 4) + i of tensor-memory lane taddr's + lane / 4 + 8 h.
+__device__ __forceinline__ void tmem_st_16x256x2(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Four codes as bf16(value * s), two to a register
+__device__ __forceinline__ void deq4(uint32_t codes, float4 s, uint32_t& r0, uint32_t& r1) {
+    uint32_t h0, h1;
+    float x0, x1, x2, x3;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((unsigned short)(codes & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((unsigned short)(codes >> 16)));
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(h));
-    return bf16x2(lo * s, hi * s);
+        : "=f"(x0), "=f"(x1)
+        : "r"(h0));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(x2), "=f"(x3)
+        : "r"(h1));
+    r0 = bf16x2(x0 * s.x, x1 * s.y);
+    r1 = bf16x2(x2 * s.z, x3 * s.w);
 }
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
     return v;
 }
-__device__ __forceinline__ float lds32(uint32_t a) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+__device__ __forceinline__ void sts32(uint32_t a, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
+template <int G>
 __global__ void __launch_bounds__(kWgThreads, 1)
 wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CUtensorMap tmq, const WgradArgs a,
              const Plan plan) {
+    constexpr int kGroups = kHalf / G;             // scale groups of this CTA's columns
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);   // the same offset in both CTAs
     const uint32_t sb = smem_u32(smem);
-    const uint32_t bar0 = sb + kBarOff;
+    const uint32_t scales0 = sb + kStages * kStageBytes;   // per stage [group][token]
+    const uint32_t bar0 = sb + bar_off(G);
     auto bar = [&](int kind, int s) { return bar0 + 8u * (uint32_t)(kind * kStages + s); };
     auto y_full = [&](int s) { return bar(0, s); };
     auto q_full = [&](int s) { return bar(1, s); };
     auto x_full = [&](int s) { return bar(2, s); };
     auto empty = [&](int s) { return bar(3, s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (uint32_t)(4 * kStages + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (uint32_t)(4 * kStages + 2 + b); };
-    const uint32_t done = bar0 + 8u * (uint32_t)(4 * kStages + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * kNumBars);
+    const uint32_t acc_full = bar0 + 8u * (uint32_t)(4 * kStages);
+    const uint32_t acc_empty = acc_full + 8u, done = acc_full + 16u;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + bar_off(G) + 8 * kNumBars);
     volatile uint32_t* abort = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -208,11 +226,12 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(y_full(s), 1);
-            mbar_init(q_full(s), 1 + 32);   // the codes' copy, and every lane's scales
+            mbar_init(q_full(s), 2);               // the codes' copy, and the scale warp
             mbar_init(x_full(s), 2 * kDeqWarps);
             mbar_init(empty(s), 1);
         }
-        for (int b = 0; b < 2; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 2 * kEpiWarps); }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 2 * kEpiWarps);
         mbar_init(done, 1);
         *abort = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -228,7 +247,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     tc_fence_before();
     cluster_sync();   // barriers initialised and tensor memory allocated in both CTAs
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = *tmem_slot, xmem = tmem + (uint32_t)kTile;
 
     const int64_t items = plan.whole + plan.tail * plan.parts;
     const int64_t cid = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
@@ -247,7 +266,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 if (leader) mbar_expect_tx(y_full(s), (uint32_t)(2 * kYBytes));
                 mbar_expect_tx(q_full(s), (uint32_t)kQBytes);
                 const uint32_t sa = sb + (uint32_t)(s * kStageBytes), yb = yb0 + 8u * (uint32_t)s;
-                tma_load_2d(sa + kYBytes + kXBytes, &tmq, k0, st * kTok, q_full(s));
+                tma_load_2d(sa + kYBytes, &tmq, k0, st * kTok, q_full(s));
                 tma_load_2d_pair(sa, &tmy, n0, st * kTok, yb);
                 tma_load_2d_pair(sa + kBoxBytes, &tmy, n0 + 64, st * kTok, yb);
                 issued |= 1u << s;
@@ -261,162 +280,181 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     } else if (warp == 1 && lane == 0) {
         if (leader) {
             // ---- MMA issuer ----
-            int s = 0, acc = 0;
+            int s = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
-            const uint64_t ydesc0 = mn_desc(sb), xdesc0 = mn_desc(sb + kYBytes);
-            for (int64_t i = cid; ok && i < items; i += nclusters) {
+            const uint64_t ydesc0 = mn_desc(sb);
+            for (int64_t i = cid; ok && i < items; i += nclusters, aph ^= 1u) {
                 const Item it = item_at(i, plan);
-                if (!mbar_wait_fast(acc_empty(acc), aph ^ 1u, abort)) break;
+                if (!mbar_wait_fast(acc_empty, aph ^ 1u, abort)) break;
                 tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * kTile);
                 for (int32_t st = it.from; st < it.to; ++st) {
                     if (!mbar_wait_fast(y_full(s), ph, abort) || !mbar_wait_fast(x_full(s), ph, abort)) { ok = false; break; }
                     tc_fence_after();
-                    const uint64_t so = (uint64_t)(s * (kStageBytes >> 4));
+                    const uint64_t yd = ydesc0 + (uint64_t)(s * (kStageBytes >> 4));
+                    const uint32_t xd = xmem + (uint32_t)s * kXCols;
 #pragma unroll
-                    for (int kk = 0; kk < kTok / kMmaTok; ++kk) {
-                        const uint64_t off = so + (uint64_t)(kk * ((kMmaTok * 128) >> 4));
-                        mma_bf16_pair(d, ydesc0 + off, xdesc0 + off, st != it.from || kk != 0);
-                    }
+                    for (int kk = 0; kk < kTok / kMmaTok; ++kk)
+                        mma_bf16_pair(tmem, xd + (uint32_t)(kk * (kMmaTok / 2)), yd + (uint64_t)(kk * ((kMmaTok * 128) >> 4)),
+                                      st != it.from || kk != 0);
                     mma_commit_pair(empty(s), 0x3);   // both CTAs' stage s is free once read
                     if (++s == kStages) { s = 0; ph ^= 1u; }
                 }
                 if (!ok) break;
-                mma_commit_pair(acc_full(acc), 0x3);
-                acc ^= 1;
-                if (acc == 0) aph ^= 1u;
+                mma_commit_pair(acc_full, 0x3);
             }
             mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
         }
         mbar_wait(done, 0u, nullptr);
-    } else if (warp == 3) {
-        // ---- scale loader (both CTAs): two tokens per lane, every group of this CTA's columns ----
-        const int64_t ngr = a.K / a.G;
-        const int groups = kHalf / a.G;
-        int s = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        for (int64_t i = cid; ok && i < items; i += nclusters) {
-            const Item it = item_at(i, plan);
-            const int64_t g0 = (it.k * kTile + rank * kHalf) / a.G;
-            for (int32_t st = it.from; st < it.to; ++st) {
-                if (!mbar_wait_fast(empty(s), ph ^ 1u, abort)) { ok = false; break; }
-                const uint32_t dst = sb + kScaleOff + (uint32_t)(s * kScaleBytes);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t m = (int64_t)st * kTok + lane + 32 * h;
-                    const bool row_ok = m < a.M;
-                    const float* src = a.scale + (row_ok ? m * ngr : 0);
-                    const uint32_t d = dst + 4u * (uint32_t)(lane + 32 * h);
-                    for (int j = 0; j < groups; ++j) {
-                        const bool in = row_ok && g0 + j < ngr;
-                        cp_async4(d + 4u * (uint32_t)(j * kSPitch), in ? src + g0 + j : a.scale, in);
-                    }
-                    if (a.row_scale)
-                        cp_async4(d + 4u * (uint32_t)(kMaxGroups * kSPitch), a.row_scale + (row_ok ? m : 0), row_ok);
+    } else if (warp == 2 || warp == 3) {
+        // ---- scale loaders: every other step each; a lane has two tokens and all groups, its loads two of its
+        // steps ahead of their use ----
+        const int64_t ngr = a.K / G;
+        int64_t ai = cid;
+        Item ait = item_at(ai < items ? ai : 0, plan);
+        int32_t ast = ait.from;
+        auto next = [&]() {                        // one step on, over the items' ends
+            if (++ast >= ait.to) {
+                ai += nclusters;
+                if (ai < items) {
+                    ait = item_at(ai, plan);
+                    ast = ait.from;
                 }
-                cp_async_arrive(q_full(s));
-                if (++s == kStages) { s = 0; ph ^= 1u; }
             }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp >= 4 && warp < 4 + kEpiWarps) {
-        // ---- epilogue: lane = one row n of the tile ----
-        const int q4 = warp & 3;
-        int acc = 0;
-        uint32_t aph = 0;
+        };
+        auto fetch = [&](float (&f)[2][kGroups], float (&r)[2]) {
+            const int64_t g0 = (ait.k * kTile + rank * kHalf) / G;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t m = (int64_t)ast * kTok + lane + 32 * h;
+                r[h] = 1.0f;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) f[h][j] = 0.0f;
+                if (ai < items && m < a.M) {
+                    if (a.row_scale) r[h] = __ldg(a.row_scale + m);
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j)
+                        if (g0 + j < ngr) f[h][j] = __ldg(a.scale + m * ngr + g0 + j);
+                }
+            }
+            next();
+            next();
+        };
+        if (warp == 3) next();
+        float f[2][2][kGroups], r[2][2];
+        const bool any = ai < items;
+        fetch(f[0], r[0]);
+        fetch(f[1], r[1]);
+        // steps of this pair in all
+        int64_t steps = 0;
         for (int64_t i = cid; i < items; i += nclusters) {
             const Item it = item_at(i, plan);
-            if (!mbar_wait_fast(acc_full(acc), aph, abort)) break;
+            steps += it.to - it.from;
+        }
+        int s = warp - 2;
+        uint32_t ph = 0;
+        bool ok = any;
+        int64_t j0 = warp - 2;
+        while (ok && j0 < steps) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (ok && j0 < steps) {
+                    if (__all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort))) {
+                        const uint32_t d = scales0 + (uint32_t)(s * scale_bytes(G)) + 4u * (uint32_t)lane;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) sts32(d + (uint32_t)(4 * (kTok * j + 32 * h)), f[b][h][j] * r[b][h]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_at(q_full(s));
+                        fetch(f[b], r[b]);
+                        j0 += 2;
+                        s += 2;
+                        if (s >= kStages) { s -= kStages; ph ^= 1u; }
+                    } else {
+                        ok = false;
+                    }
+                }
+            }
+        }
+    } else if (warp >= 4 && warp < 4 + kEpiWarps) {
+        // ---- epilogue: lane = one column k of the tile; tensor-memory columns = rows n ----
+        const int q4 = warp & 3;
+        uint32_t aph = 0;
+        for (int64_t i = cid; i < items; i += nclusters, aph ^= 1u) {
+            const Item it = item_at(i, plan);
+            if (!__all_sync(kFull, mbar_wait_fast(acc_full, aph, abort))) break;
             tc_fence_after();
-            const int row = (int)rank * kHalf + 32 * q4 + lane;
-            const int64_t n = it.n * kTile + row, k0 = it.k * kTile;
-            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kTile);
+            const int kl = (int)rank * kHalf + 32 * q4 + lane;
+            const int64_t k = it.k * kTile + kl, n0 = it.n * kTile;
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16);
+            const float cs = a.col_scale && k < a.K ? __ldg(a.col_scale + k) : 1.0f;
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 32) {
-                if (k0 + c >= a.K) break;   // the same for the whole warp
+                if (n0 + c >= a.N) break;   // the same for the whole warp
                 uint32_t v[32];
                 __syncwarp();
                 tmem_ld<32>(taddr + (uint32_t)c, v);
                 if (it.part >= 0) {
-                    float4* p = reinterpret_cast<float4*>(a.partial + (it.part * kTile + row) * kTile + c);
+                    // the parts' tiles are [n][k]
+                    float* p = a.partial + (it.part * kTile + c) * kTile + kl;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        p[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]),
-                                           __uint_as_float(v[4 * e + 2]), __uint_as_float(v[4 * e + 3]));
-                } else if (n < a.N) {
+                    for (int e = 0; e < 32; ++e) p[e * kTile] = __uint_as_float(v[e]);
+                } else {
+                    // two lanes exchange a value, so that each has two neighbours k of one row: the even lane of
+                    // row n + e, the odd one of row n + e + 1
+                    const int odd = lane & 1;
+                    uint16_t* p = a.dw + (n0 + c + odd) * a.K + (k - odd);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        const int64_t k = k0 + c + j;
-                        if (k >= a.K) break;
-                        float x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[j + e]);
-                        if (a.col_scale) {
-                            const float4 f0 = __ldg(reinterpret_cast<const float4*>(a.col_scale + k));
-                            const float4 f1 = __ldg(reinterpret_cast<const float4*>(a.col_scale + k) + 1);
-                            x[0] *= f0.x; x[1] *= f0.y; x[2] *= f0.z; x[3] *= f0.w;
-                            x[4] *= f1.x; x[5] *= f1.y; x[6] *= f1.z; x[7] *= f1.w;
-                        }
-                        *reinterpret_cast<uint4*>(a.dw + n * a.K + k) = pack8(x);
+                    for (int e = 0; e < 32; e += 2) {
+                        const float x0 = __uint_as_float(v[e]) * cs, x1 = __uint_as_float(v[e + 1]) * cs;
+                        const float got = __shfl_xor_sync(kFull, odd ? x0 : x1, 1);
+                        const uint32_t w = odd ? bf16x2(got, x1) : bf16x2(x0, got);
+                        if (k < a.K && n0 + c + odd + e < a.N) *reinterpret_cast<uint32_t*>(p + (int64_t)e * a.K) = w;
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(acc_empty(acc), 0));
-            acc ^= 1;
-            if (acc == 0) aph ^= 1u;
+            if (lane == 0) mbar_arrive_at(map_to_rank(acc_empty, 0));
         }
     } else if (warp >= 4 + kEpiWarps) {
-        // ---- codes -> bf16 operand: a thread takes 16 columns of two tokens per stage ----
-        const int t = threadIdx.x - 32 * (4 + kEpiWarps);
-        const int r0 = t >> 3, c = t & 7;              // token of the stage (and r0 + 32), 16-column chunk
+        // ---- codes -> X: a warp takes the 32 columns k of its tensor-memory lanes, and 32 of the 64 tokens ----
+        const int q4 = warp & 3, th = (warp - 4 - kEpiWarps) >> 2;
         const uint32_t xb0 = map_to_rank(x_full(0), 0);
-        // the scales of the chunk's first and last eight columns, and the tokens' factors
-        const uint32_t s0 = 4u * (uint32_t)(((16 * c) / a.G) * kSPitch + r0);
-        const uint32_t s1 = 4u * (uint32_t)(((16 * c + 8) / a.G) * kSPitch + r0);
-        const uint32_t sr = 4u * (uint32_t)(kMaxGroups * kSPitch + r0);
-        const int u = 2 * (c & 3);         // 16-byte unit of the row; the swizzle XORs it with row % 8
-        const bool swap = c >= 4;          // the order of a chunk's halves that keeps a quarter-warp's eight stores on different banks
+        const int row = 32 * th + lane;                            // token of this lane's ldmatrix address
+        uint32_t q_at[2];                                          // 16-byte unit of the row, as the 128-byte swizzle puts it
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh)
+            q_at[kh] = (uint32_t)(kYBytes + row * 128 + (((2 * q4 + kh) ^ (row & 7)) * 16));
+        const uint32_t s_at = (uint32_t)(4 * (32 * th + 4 * (lane & 3)));
+        const uint32_t x_at = xmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(16 * th);
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
         for (int64_t i = cid; ok && i < items; i += nclusters) {
             const Item it = item_at(i, plan);
             for (int32_t st = it.from; st < it.to; ++st) {
-                if (!mbar_wait_fast(q_full(s), ph, abort)) { ok = false; break; }
-                const uint32_t sa = sb + (uint32_t)(s * kStageBytes), ss = sb + kScaleOff + (uint32_t)(s * kScaleBytes);
-                uint4 v[2];
-                float f0[2], f1[2];
+                if (!__all_sync(kFull, mbar_wait_fast(q_full(s), ph, abort))) { ok = false; break; }
+                const uint32_t sa = sb + (uint32_t)(s * kStageBytes), ss = scales0 + (uint32_t)(s * scale_bytes(G)) + s_at;
+                uint32_t q[2][4];
+                ldmatrix_bytes(sa + q_at[0], q[0]);
+                ldmatrix_bytes(sa + q_at[1], q[1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    v[h] = lds128(sa + kYBytes + kXBytes + (uint32_t)((r0 + 32 * h) * kHalf + 16 * c));
-                    f0[h] = lds32(ss + s0 + 128u * h);
-                    f1[h] = lds32(ss + s1 + 128u * h);
-                }
-                if (a.row_scale) {
+                for (int kh = 0; kh < 2; ++kh) {
+                    uint32_t x[8];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float r = lds32(ss + sr + 128u * h);
-                        f0[h] *= r;
-                        f1[h] *= r;
-                    }
-                }
+                    for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = r0 + 32 * h;
-                    const uint4 lo = make_uint4(deq2(v[h].x & 0xFFFFu, f0[h]), deq2(v[h].x >> 16, f0[h]),
-                                                deq2(v[h].y & 0xFFFFu, f0[h]), deq2(v[h].y >> 16, f0[h]));
-                    const uint4 hi = make_uint4(deq2(v[h].z & 0xFFFFu, f1[h]), deq2(v[h].z >> 16, f1[h]),
-                                                deq2(v[h].w & 0xFFFFu, f1[h]), deq2(v[h].w >> 16, f1[h]));
-                    const uint32_t base = sa + kYBytes + (uint32_t)((c >> 2) * kBoxBytes + row * 128);
-                    const uint32_t a0 = base + (uint32_t)((u ^ (row & 7)) * 16), a1 = base + (uint32_t)(((u + 1) ^ (row & 7)) * 16);
-                    sts128(swap ? a1 : a0, swap ? hi : lo);
-                    sts128(swap ? a0 : a1, swap ? lo : hi);
+                        for (int h = 0; h < 2; ++h) {
+                            const int g = (32 * q4 + 16 * kh + 8 * h) / G;
+                            const float4 f = lds128f(ss + (uint32_t)(4 * (kTok * g + 16 * b)));
+                            deq4(q[kh][2 * b + h], f, x[4 * b + 2 * h], x[4 * b + 2 * h + 1]);
+                        }
+                    tmem_st_16x256x2(x_at + (uint32_t)s * kXCols + ((uint32_t)(16 * kh) << 16), x);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_at(xb0 + 8u * (uint32_t)s);
                 if (++s == kStages) { s = 0; ph ^= 1u; }
@@ -426,6 +464,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     tc_fence_before();
     cluster_sync();   // no arrival or copy is still on its way to either CTA
     tc_fence_after();
+    __syncwarp();
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                      : "memory");
@@ -465,12 +504,34 @@ bool encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int6
     const cuuint32_t elem[2] = {1, 1};
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
               strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // CTA pairs: the plan (and with it the workspace and the order of the sums) goes by the SM count alone
 int64_t pairs_of(int sms) { return sms / 2; }
+
+template <int G>
+cudaError_t launch_pairs(const WgradArgs& a, const Plan& p, int64_t pairs, cudaStream_t s) {
+    alignas(64) CUtensorMap tmy, tmq;
+    if (!encode(&tmy, a.dy, a.M, a.N, a.dy_ld, true) || !encode(&tmq, a.q, a.M, a.K, a.K, false)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(G));
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kWgThreads);
+    cfg.dynamicSmemBytes = smem_bytes(G);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const int64_t items = p.whole + p.tail * p.parts;
+    cfg.gridDim = dim3(2u * (unsigned)(items < pairs ? items : pairs));
+    return cudaLaunchKernelEx(&cfg, wgrad_kernel<G>, tmy, tmq, a, p);
+}
 
 }  // namespace
 
@@ -483,24 +544,15 @@ cudaError_t launch_wgrad(const WgradArgs& a, cudaStream_t s) {
     const int64_t pairs = pairs_of(device_sms());
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     const Plan p = make_plan(a.M, a.N, a.K, pairs);
-    alignas(64) CUtensorMap tmy, tmq;
-    if (!encode(&tmy, a.dy, a.M, a.N, a.dy_ld, true) || !encode(&tmq, a.q, a.M, a.K, a.K, false)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (a.G) {
+        case 8: e = launch_pairs<8>(a, p, pairs, s); break;
+        case 16: e = launch_pairs<16>(a, p, pairs, s); break;
+        case 32: e = launch_pairs<32>(a, p, pairs, s); break;
+        case 64: e = launch_pairs<64>(a, p, pairs, s); break;
+        case 128: e = launch_pairs<128>(a, p, pairs, s); break;
+    }
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kWgThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const int64_t items = p.whole + p.tail * p.parts;
-    cfg.gridDim = dim3(2u * (unsigned)(items < pairs ? items : pairs));
-    if ((e = cudaLaunchKernelEx(&cfg, wgrad_kernel, tmy, tmq, a, p)) != cudaSuccess) return e;
     if (p.tail > 0) wgrad_join_kernel<<<(unsigned)(p.tail * 32), 256, 0, s>>>(a, p);
     return cudaGetLastError();
 }
