@@ -16,10 +16,34 @@ import torch
 
 from . import CoatError, _check, _stream_ptr, lib
 
+_BF16, _F32, _U8, _I32 = torch.bfloat16, torch.float32, torch.uint8, torch.int32
+_functions = {}
+
+
+def _ptr(t, dtype, numel: int, name: str, device):
+    """The pointer of a contiguous tensor of that dtype and size on ``device``.
+    These checks are most of a short call's time on the host, so they are made
+    in one expression; _check says what is wrong where they fail."""
+    try:
+        if (t.dtype is dtype and t.get_device() == device.index and t.is_contiguous()
+                and t.numel() == numel):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _check(t, dtype, numel, name, device)
+
 
 def _rows(t, M: int, width: int, name: str, device):
     """A bf16 tensor of M rows of ``width`` elements that lie together, the rows
     at any distance: its pointer and the distance in elements."""
+    try:   # the common layouts in one expression, as in _ptr
+        if t.dtype is _BF16 and t.get_device() == device.index and t.numel() == M * width:
+            st = t.stride()
+            if (st[-1] == 1 and t.shape[0] == M > 1
+                    and (len(st) == 2 or (len(st) == 3 and st[1] == t.shape[2]))):
+                return t.data_ptr(), st[0]
+    except (AttributeError, IndexError):
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
@@ -51,8 +75,20 @@ def _groups(n: int, G: int) -> int:
 
 
 def _call(name: str, device, stream, *args) -> None:
-    with torch.cuda.device(device):
-        st = getattr(lib(), name)(*args, _stream_ptr(stream))
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
+    if device.type != "cuda":
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = _stream_ptr(stream)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
     if st != 0:
         raise CoatError(st, name)
 
@@ -73,14 +109,14 @@ def coat_rmsnorm_ckpt(x, weight, eps: float, G: int, y, q, scale, rstd, residual
         raise ValueError("x must be a 2-D [M, N] tensor")
     if (residual is None) != (h is None):
         raise ValueError("residual and h come together")
-    (M, N), dev, bf16, f32 = x.shape, x.device, torch.bfloat16, torch.float32
+    (M, N), dev = x.shape, x.device
     n = M * N
-    _call("coat_rmsnorm_ckpt", dev, stream, _check(x, bf16, n, "x"),
-          None if residual is None else _check(residual, bf16, n, "residual", dev),
-          _check(weight, f32, N, "weight", dev), float(eps), M, N, int(G),
-          None if h is None else _check(h, bf16, n, "h", dev), _check(y, bf16, n, "y", dev),
-          _check(q, torch.uint8, n, "q", dev), _check(scale, f32, _groups(n, G), "scale", dev),
-          _check(rstd, f32, M, "rstd", dev))
+    _call("coat_rmsnorm_ckpt", dev, stream, _ptr(x, _BF16, n, "x", dev),
+          None if residual is None else _ptr(residual, _BF16, n, "residual", dev),
+          _ptr(weight, _F32, N, "weight", dev), float(eps), M, N, int(G),
+          None if h is None else _ptr(h, _BF16, n, "h", dev), _ptr(y, _BF16, n, "y", dev),
+          _ptr(q, _U8, n, "q", dev), _ptr(scale, _F32, _groups(n, G), "scale", dev),
+          _ptr(rstd, _F32, M, "rstd", dev))
 
 
 def coat_rmsnorm_ckpt_backward_workspace_bytes(M: int, N: int, device=None) -> int:
@@ -95,13 +131,13 @@ def coat_rmsnorm_ckpt_backward(dy, q, scale, rstd, weight, G: int, dx, dweight, 
     dresidual (bf16 [M, N]) is the gradient that reaches h past the norm."""
     if dy.dim() != 2:
         raise ValueError("dy must be a 2-D [M, N] tensor")
-    (M, N), dev, bf16, f32 = dy.shape, dy.device, torch.bfloat16, torch.float32
+    (M, N), dev = dy.shape, dy.device
     n = M * N
-    _call("coat_rmsnorm_ckpt_backward", dev, stream, _check(dy, bf16, n, "dy"),
-          _check(q, torch.uint8, n, "q", dev), _check(scale, f32, _groups(n, G), "scale", dev),
-          _check(rstd, f32, M, "rstd", dev), _check(weight, f32, N, "weight", dev),
-          None if dresidual is None else _check(dresidual, bf16, n, "dresidual", dev), M, N, int(G),
-          _check(dx, bf16, n, "dx", dev), _check(dweight, bf16, N, "dweight", dev),
+    _call("coat_rmsnorm_ckpt_backward", dev, stream, _ptr(dy, _BF16, n, "dy", dev),
+          _ptr(q, _U8, n, "q", dev), _ptr(scale, _F32, _groups(n, G), "scale", dev),
+          _ptr(rstd, _F32, M, "rstd", dev), _ptr(weight, _F32, N, "weight", dev),
+          None if dresidual is None else _ptr(dresidual, _BF16, n, "dresidual", dev), M, N, int(G),
+          _ptr(dx, _BF16, n, "dx", dev), _ptr(dweight, _BF16, N, "dweight", dev),
           *_workspace(workspace, dev))
 
 
@@ -110,17 +146,17 @@ def coat_swiglu_ckpt(gate, up, G: int, h, gate_q, gate_scale, up_q, up_scale, st
     up are bf16 [M, N] whose rows may be apart (halves of one tensor)."""
     if gate.dim() != 2:
         raise ValueError("gate must be a 2-D [M, N] tensor")
-    (M, N), dev, f32 = gate.shape, gate.device, torch.float32
+    (M, N), dev = gate.shape, gate.device
     n = M * N
     pg, ld = _rows(gate, M, N, "gate", dev)
     pu, ldu = _rows(up, M, N, "up", dev)
     if ld != ldu:
         raise ValueError(f"gate and up must have the same row stride, got {ld} and {ldu}")
     _call("coat_swiglu_ckpt", dev, stream, pg, pu, ld, M, N, int(G),
-          _check(h, torch.bfloat16, n, "h", dev), _check(gate_q, torch.uint8, n, "gate_q", dev),
-          _check(gate_scale, f32, _groups(n, G), "gate_scale", dev),
-          _check(up_q, torch.uint8, n, "up_q", dev),
-          _check(up_scale, f32, _groups(n, G), "up_scale", dev))
+          _ptr(h, _BF16, n, "h", dev), _ptr(gate_q, _U8, n, "gate_q", dev),
+          _ptr(gate_scale, _F32, _groups(n, G), "gate_scale", dev),
+          _ptr(up_q, _U8, n, "up_q", dev),
+          _ptr(up_scale, _F32, _groups(n, G), "up_scale", dev))
 
 
 def coat_swiglu_ckpt_backward(dh, gate_q, gate_scale, up_q, up_scale, G: int, dgate, dup, h_q=None,
@@ -132,28 +168,28 @@ def coat_swiglu_ckpt_backward(dh, gate_q, gate_scale, up_q, up_scale, G: int, dg
         raise ValueError("dh must be a 2-D [M, N] tensor")
     if (h_q is None) != (h_scale is None):
         raise ValueError("h_q and h_scale come together")
-    (M, N), dev, f32 = dh.shape, dh.device, torch.float32
+    (M, N), dev = dh.shape, dh.device
     n = M * N
     pg, ld = _rows(dgate, M, N, "dgate", dev)
     pu, ldu = _rows(dup, M, N, "dup", dev)
     if ld != ldu:
         raise ValueError(f"dgate and dup must have the same row stride, got {ld} and {ldu}")
-    _call("coat_swiglu_ckpt_backward", dev, stream, _check(dh, torch.bfloat16, n, "dh"),
-          _check(gate_q, torch.uint8, n, "gate_q", dev),
-          _check(gate_scale, f32, _groups(n, G), "gate_scale", dev),
-          _check(up_q, torch.uint8, n, "up_q", dev),
-          _check(up_scale, f32, _groups(n, G), "up_scale", dev), M, N, int(G), pg, pu, ld,
-          None if h_q is None else _check(h_q, torch.uint8, n, "h_q", dev),
-          None if h_scale is None else _check(h_scale, f32, _groups(n, G), "h_scale", dev))
+    _call("coat_swiglu_ckpt_backward", dev, stream, _ptr(dh, _BF16, n, "dh", dev),
+          _ptr(gate_q, _U8, n, "gate_q", dev),
+          _ptr(gate_scale, _F32, _groups(n, G), "gate_scale", dev),
+          _ptr(up_q, _U8, n, "up_q", dev),
+          _ptr(up_scale, _F32, _groups(n, G), "up_scale", dev), M, N, int(G), pg, pu, ld,
+          None if h_q is None else _ptr(h_q, _U8, n, "h_q", dev),
+          None if h_scale is None else _ptr(h_scale, _F32, _groups(n, G), "h_scale", dev))
 
 
 def _tables(cos, sin, positions, M: int, D: int, dev):
     if cos.dim() != 2:
         raise ValueError("cos must be a 2-D [max_pos, rot/2] tensor")
     max_pos, half = cos.shape
-    return (_check(cos, torch.float32, max_pos * half, "cos", dev),
-            _check(sin, torch.float32, max_pos * half, "sin", dev), max_pos, 2 * half,
-            _check(positions, torch.int32, M, "positions", dev))
+    return (_ptr(cos, _F32, max_pos * half, "cos", dev),
+            _ptr(sin, _F32, max_pos * half, "sin", dev), max_pos, 2 * half,
+            _ptr(positions, _I32, M, "positions", dev))
 
 
 def _heads(t, name: str):
@@ -164,15 +200,15 @@ def _heads(t, name: str):
 
 def _side(side: str, M: int, H: int, D: int, G: int, dev, codes, scale, rstd):
     n = M * H * D
-    return (_check(codes, torch.uint8, n, f"{side}_codes", dev),
-            _check(scale, torch.float32, _groups(n, G), f"{side}_scale", dev),
-            _check(rstd, torch.float32, M * H, f"{side}_rstd", dev))
+    return (_ptr(codes, _U8, n, f"{side}_codes", dev),
+            _ptr(scale, _F32, _groups(n, G), f"{side}_scale", dev),
+            _ptr(rstd, _F32, M * H, f"{side}_rstd", dev))
 
 
 def coat_qk_norm_rope_ckpt(q, k, q_weight, k_weight, eps: float, cos, sin, positions, G: int, q_out,
                            q_codes, q_scale, q_rstd, k_out=None, k_codes=None, k_scale=None,
                            k_rstd=None, interleaved: bool = False, stream=None) -> None:
-    """RMS norm of every head of q [M, Hq, D] and k [M, Hk, D] (bf16, the tokens'
+    """RMS norm of every head of q [M, Hq, D] and k [M, Hk, D] (_BF16, the tokens'
     rows at any distance: ranges of one projection's output), the position
     rotation of the normed heads, and a checkpoint of the heads as they came.
 
@@ -182,7 +218,7 @@ def coat_qk_norm_rope_ckpt(q, k, q_weight, k_weight, eps: float, cos, sin, posit
     entries of a head are turned in pairs (i, i + rot/2), or (2i, 2i + 1) when
     ``interleaved``.  k may be None (with k_weight and k's outputs)."""
     M, Hq, D = _heads(q, "q")
-    dev, f32, bf16 = q.device, torch.float32, torch.bfloat16
+    dev = q.device
     pq, q_ld = _rows(q, M, Hq * D, "q", dev)
     pk, k_ld, Hk, pkw, kout = None, 0, 0, None, (None, None, None, None)
     if k is not None:
@@ -190,13 +226,13 @@ def coat_qk_norm_rope_ckpt(q, k, q_weight, k_weight, eps: float, cos, sin, posit
         if (Mk, Dk) != (M, D):
             raise ValueError(f"k must be [{M}, heads, {D}], got {tuple(k.shape)}")
         pk, k_ld = _rows(k, M, Hk * D, "k", dev)
-        pkw = _check(k_weight, f32, D, "k_weight", dev)
-        kout = (_check(k_out, bf16, M * Hk * D, "k_out", dev),
+        pkw = _ptr(k_weight, _F32, D, "k_weight", dev)
+        kout = (_ptr(k_out, _BF16, M * Hk * D, "k_out", dev),
                 *_side("k", M, Hk, D, G, dev, k_codes, k_scale, k_rstd))
     pcos, psin, max_pos, rot, ppos = _tables(cos, sin, positions, M, D, dev)
     _call("coat_qk_norm_rope_ckpt", dev, stream, pq, q_ld, Hq, pk, k_ld, Hk, D,
-          _check(q_weight, f32, D, "q_weight", dev), pkw, float(eps), pcos, psin, max_pos, rot, ppos,
-          int(bool(interleaved)), M, int(G), _check(q_out, bf16, M * Hq * D, "q_out", dev),
+          _ptr(q_weight, _F32, D, "q_weight", dev), pkw, float(eps), pcos, psin, max_pos, rot, ppos,
+          int(bool(interleaved)), M, int(G), _ptr(q_out, _BF16, M * Hq * D, "q_out", dev),
           *_side("q", M, Hq, D, G, dev, q_codes, q_scale, q_rstd), *kout)
 
 
@@ -214,25 +250,25 @@ def coat_qk_norm_rope_ckpt_backward(dq_out, dk_out, q_codes, q_scale, q_rstd, k_
     ranges of one gradient buffer), dq_weight and dk_weight bf16 [D].  dk_out may
     be None (with everything of k)."""
     M, Hq, D = _heads(dq_out, "dq_out")
-    dev, f32, bf16 = dq_out.device, torch.float32, torch.bfloat16
+    dev = dq_out.device
     pdq, dq_ld = _rows(dq, M, Hq * D, "dq", dev)
     pdko, Hk, kin, pkw, pdk, dk_ld, pdkw = None, 0, (None, None, None), None, None, 0, None
     if dk_out is not None:
         Mk, Hk, Dk = _heads(dk_out, "dk_out")
         if (Mk, Dk) != (M, D):
             raise ValueError(f"dk_out must be [{M}, heads, {D}], got {tuple(dk_out.shape)}")
-        pdko = _check(dk_out, bf16, M * Hk * D, "dk_out", dev)
+        pdko = _ptr(dk_out, _BF16, M * Hk * D, "dk_out", dev)
         kin = _side("k", M, Hk, D, G, dev, k_codes, k_scale, k_rstd)
-        pkw = _check(k_weight, f32, D, "k_weight", dev)
+        pkw = _ptr(k_weight, _F32, D, "k_weight", dev)
         pdk, dk_ld = _rows(dk, M, Hk * D, "dk", dev)
-        pdkw = _check(dk_weight, bf16, D, "dk_weight", dev)
+        pdkw = _ptr(dk_weight, _BF16, D, "dk_weight", dev)
     pcos, psin, max_pos, rot, ppos = _tables(cos, sin, positions, M, D, dev)
     _call("coat_qk_norm_rope_ckpt_backward", dev, stream,
-          _check(dq_out, bf16, M * Hq * D, "dq_out"), pdko,
+          _ptr(dq_out, _BF16, M * Hq * D, "dq_out", dev), pdko,
           *_side("q", M, Hq, D, G, dev, q_codes, q_scale, q_rstd), *kin, Hq, Hk, D,
-          _check(q_weight, f32, D, "q_weight", dev), pkw, pcos, psin, max_pos, rot, ppos,
+          _ptr(q_weight, _F32, D, "q_weight", dev), pkw, pcos, psin, max_pos, rot, ppos,
           int(bool(interleaved)), M, int(G), pdq, dq_ld, pdk, dk_ld,
-          _check(dq_weight, bf16, D, "dq_weight", dev), pdkw, *_workspace(workspace, dev))
+          _ptr(dq_weight, _BF16, D, "dq_weight", dev), pdkw, *_workspace(workspace, dev))
 
 
 def coat_ckpt_weight_grad_workspace_bytes(M: int, N: int, K: int, device=None) -> int:
@@ -250,10 +286,10 @@ def coat_ckpt_weight_grad(dy, q, scale, G: int, dw, workspace, row_scale=None, c
     output."""
     if dy.dim() != 2 or q.dim() != 2:
         raise ValueError("dy [M, N] and q [M, K] must be 2-D")
-    (M, N), K, dev, f32 = dy.shape, q.shape[1], dy.device, torch.float32
+    (M, N), K, dev = dy.shape, q.shape[1], dy.device
     pdy, ld = _rows(dy, M, N, "dy", dev)
-    _call("coat_ckpt_weight_grad", dev, stream, pdy, ld, _check(q, torch.uint8, M * K, "q", dev),
-          _check(scale, f32, _groups(M * K, G), "scale", dev),
-          None if row_scale is None else _check(row_scale, f32, M, "row_scale", dev),
-          None if col_scale is None else _check(col_scale, f32, K, "col_scale", dev), M, N, K, int(G),
-          _check(dw, torch.bfloat16, N * K, "dw", dev), *_workspace(workspace, dev))
+    _call("coat_ckpt_weight_grad", dev, stream, pdy, ld, _ptr(q, _U8, M * K, "q", dev),
+          _ptr(scale, _F32, _groups(M * K, G), "scale", dev),
+          None if row_scale is None else _ptr(row_scale, _F32, M, "row_scale", dev),
+          None if col_scale is None else _ptr(col_scale, _F32, K, "col_scale", dev), M, N, K, int(G),
+          _ptr(dw, _BF16, N * K, "dw", dev), *_workspace(workspace, dev))

@@ -26,7 +26,7 @@
 //                   (ldmatrix .b8), so that a thread has four tokens of one
 //                   column, and goes to tensor memory as 16 lanes x 16 bf16;
 //   MMA thread      (even CTA) four tcgen05.mma.cta_group::2 kind::f16, K = 16;
-//   4 warps         the finished accumulator: times c, to bf16, stored.
+//   8 warps         the finished accumulator into registers, times c, to bf16, stored.
 // X in tensor memory is what makes the tensor cores the bound: with X written to
 // and read from shared memory its traffic (copies in, codes out, X in, both
 // operands out: 5 KB for each of the 128 B per clock that 512 clocks of MMA
@@ -60,7 +60,8 @@ constexpr int kBoxBytes = kTok * 128;          // 64 tokens x 64 bf16 columns
 constexpr int kYBytes = 2 * kBoxBytes;         // dY: 64 tokens x 128 columns
 constexpr int kQBytes = kTok * kHalf;          // the codes
 constexpr int kStageBytes = kYBytes + kQBytes;
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;                   // two per SM sub-partition, each half the rows n
+constexpr int kEpiRows = kTile / (kEpiWarps / 4);
 constexpr int kDeqWarps = 8;
 constexpr int kWgThreads = 32 * (4 + kEpiWarps + kDeqWarps);
 constexpr uint32_t kXCols = kTok / 2;          // tensor-memory columns of a stage of X
@@ -307,8 +308,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         }
         mbar_wait(done, 0u, nullptr);
     } else if (warp == 2 || warp == 3) {
-        // ---- scale loaders: every other step each; a lane has two tokens and all groups, its loads two of its
-        // steps ahead of their use ----
+        // ---- scale loaders: every other step each; a lane has two tokens and all groups, loaded two of its
+        // steps ahead of their use (one where the groups are many) ----
+        constexpr int kDeep = kGroups > 8 ? 1 : 2;
         const int64_t ngr = a.K / G;
         int64_t ai = cid;
         Item ait = item_at(ai < items ? ai : 0, plan);
@@ -341,10 +343,10 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
             next();
         };
         if (warp == 3) next();
-        float f[2][2][kGroups], r[2][2];
+        float f[kDeep][2][kGroups], r[kDeep][2];
         const bool any = ai < items;
-        fetch(f[0], r[0]);
-        fetch(f[1], r[1]);
+#pragma unroll
+        for (int b = 0; b < kDeep; ++b) fetch(f[b], r[b]);
         // steps of this pair in all
         int64_t steps = 0;
         for (int64_t i = cid; i < items; i += nclusters) {
@@ -357,7 +359,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         int64_t j0 = warp - 2;
         while (ok && j0 < steps) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kDeep; ++b) {
                 if (ok && j0 < steps) {
                     if (__all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort))) {
                         const uint32_t d = scales0 + (uint32_t)(s * scale_bytes(G)) + 4u * (uint32_t)lane;
@@ -379,44 +381,58 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         }
     } else if (warp >= 4 && warp < 4 + kEpiWarps) {
         // ---- epilogue: lane = one column k of the tile; tensor-memory columns = rows n ----
-        const int q4 = warp & 3;
+        const int q4 = warp & 3, nh = ((warp - 4) >> 2) * kEpiRows;
+        const uint32_t ae = map_to_rank(acc_empty, 0);
+        auto release = [&]() {                     // the accumulator has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(ae);
+        };
         uint32_t aph = 0;
         for (int64_t i = cid; i < items; i += nclusters, aph ^= 1u) {
             const Item it = item_at(i, plan);
             if (!__all_sync(kFull, mbar_wait_fast(acc_full, aph, abort))) break;
             tc_fence_after();
             const int kl = (int)rank * kHalf + 32 * q4 + lane;
-            const int64_t k = it.k * kTile + kl, n0 = it.n * kTile;
-            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16);
-            const float cs = a.col_scale && k < a.K ? __ldg(a.col_scale + k) : 1.0f;
+            const int64_t k = it.k * kTile + kl, n0 = it.n * kTile + nh;
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)nh;
+            if (it.part >= 0) {
+                // the parts' tiles are [n][k]
+                float* p = a.partial + (it.part * kTile + nh) * kTile + kl;
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-                if (n0 + c >= a.N) break;   // the same for the whole warp
-                uint32_t v[32];
-                __syncwarp();
-                tmem_ld<32>(taddr + (uint32_t)c, v);
-                if (it.part >= 0) {
-                    // the parts' tiles are [n][k]
-                    float* p = a.partial + (it.part * kTile + c) * kTile + kl;
+                for (int c = 0; c < kEpiRows; c += 32) {
+                    if (n0 + c >= a.N) break;   // the same for the whole warp
+                    uint32_t v[32];
+                    tmem_ld<32>(taddr + (uint32_t)c, v);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) p[e * kTile] = __uint_as_float(v[e]);
-                } else {
-                    // two lanes exchange a value, so that each has two neighbours k of one row: the even lane of
-                    // row n + e, the odd one of row n + e + 1
-                    const int odd = lane & 1;
-                    uint16_t* p = a.dw + (n0 + c + odd) * a.K + (k - odd);
+                    for (int e = 0; e < 32; ++e) p[(c + e) * kTile] = __uint_as_float(v[e]);
+                }
+                release();
+            } else {
+                // all of it into registers, as pairs of rows, so that the next tile's MMAs may start
+                const float cs = a.col_scale && k < a.K ? __ldg(a.col_scale + k) : 1.0f;
+                uint32_t w[kEpiRows / 2];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float x0 = __uint_as_float(v[e]) * cs, x1 = __uint_as_float(v[e + 1]) * cs;
-                        const float got = __shfl_xor_sync(kFull, odd ? x0 : x1, 1);
-                        const uint32_t w = odd ? bf16x2(got, x1) : bf16x2(x0, got);
-                        if (k < a.K && n0 + c + odd + e < a.N) *reinterpret_cast<uint32_t*>(p + (int64_t)e * a.K) = w;
-                    }
+                for (int c = 0; c < kEpiRows; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld<16>(taddr + (uint32_t)c, v);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2)
+                        w[(c + e) / 2] = bf16x2(__uint_as_float(v[e]) * cs, __uint_as_float(v[e + 1]) * cs);
+                }
+                release();
+                // two lanes exchange, so that each has two neighbours k of one row: the even lane of row n + e, the
+                // odd one of row n + e + 1
+                const int odd = lane & 1;
+                uint16_t* p = a.dw + (n0 + odd) * a.K + (k - odd);
+                const int rows = k < a.K ? (int)(a.N - n0 - odd < kEpiRows ? a.N - n0 - odd : kEpiRows) : 0;
+#pragma unroll
+                for (int e = 0; e < kEpiRows; e += 2) {
+                    const uint32_t got = __shfl_xor_sync(kFull, w[e / 2], 1);
+                    const uint32_t out = odd ? __byte_perm(got, w[e / 2], 0x7632) : __byte_perm(w[e / 2], got, 0x5410);
+                    if (e < rows) *reinterpret_cast<uint32_t*>(p + (int64_t)e * a.K) = out;
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_at(map_to_rank(acc_empty, 0));
         }
     } else if (warp >= 4 + kEpiWarps) {
         // ---- codes -> X: a warp takes the 32 columns k of its tensor-memory lanes, and 32 of the 64 tokens ----
