@@ -5,8 +5,7 @@
 // A checkpoint of a row is the one coat_act_quantize_fp8 writes: per group of G
 // consecutive elements S = RN(max|x| / 448) and q = E4M3(x / S), rounded to
 // nearest even of the exact quotient (COAT review page, section 3: FP8
-// quantization, 1 x G groups for non-linear layers).  A thread holds eight
-// consecutive elements; a group of G lies in G / 8 adjacent lanes.
+// quantization, 1 x G groups for non-linear layers).
 #pragma once
 
 #include <cstdint>
@@ -18,10 +17,43 @@ namespace ckpt {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// ---- memory: N consecutive 32-bit words, streamed past L1 ----
+template <int N>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[N]);
+template <>
+__device__ __forceinline__ void load_words<4>(const void* p, uint32_t (&w)[4]) {
+    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+        : "l"(p));
+}
+// 32 bytes: one 256-bit access where `wide` (the address is a multiple of 32), else two
+__device__ __forceinline__ void load_words8(const void* p, bool wide, uint32_t (&w)[8]) {
+    if (wide) {
+        asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+            : "l"(p));
+    } else {
+        asm("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+        asm("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4 + 16];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+    }
+}
+__device__ __forceinline__ void store_words8(void* p, bool wide, const uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// ---- bf16 and E4M3 ----
+// 2 W bf16 values as float32
+template <int W>
+__device__ __forceinline__ void unpack(const uint32_t (&w)[W], float (&x)[2 * W]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
@@ -31,82 +63,143 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
+template <int W>
+__device__ __forceinline__ void pack(const float (&x)[2 * W], uint32_t (&w)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = bf16x2(x[2 * i], x[2 * i + 1]);
 }
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return (uint16_t)(bf16x2(x, 0.0f) & 0xFFFFu); }
 
-// Eight E4M3 codes as their values (exact: an E4M3 value is a half value).
-__device__ __forceinline__ void decode8(uint2 c, float (&x)[8]) {
-    const uint32_t w[2] = {c.x, c.y};
+// 4 W E4M3 codes as their values (exact: an E4M3 value is a half value)
+template <int W>
+__device__ __forceinline__ void decode(const uint32_t (&c)[W], float (&x)[4 * W]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * W; ++i) {
         uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)(w[i >> 1] >> (16 * (i & 1)))));
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)(c[i >> 1] >> (16 * (i & 1)))));
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
             : "=f"(x[2 * i]), "=f"(x[2 * i + 1])
             : "r"(h));
     }
 }
 
-// max|x| over the group: the thread's eight, then the G / 8 lanes that hold the
-// group (G a power of two in [8, 128], the same in every lane of the warp).
-__device__ __forceinline__ float group_max(const float (&x)[8], int G) {
-    float mx = max3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2]));
-    mx = max3(mx, fabsf(x[3]), fabsf(x[4]));
-    mx = max3(mx, fabsf(x[5]), fabsf(x[6]));
-    mx = fmaxf(mx, fabsf(x[7]));
-    for (int off = G >> 4; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+// max|x| of n (even) values from x[from]
+template <int from, int n, int L>
+__device__ __forceinline__ float max_of(const float (&x)[L]) {
+    float mx = fmaxf(fabsf(x[from]), fabsf(x[from + 1]));
+#pragma unroll
+    for (int e = from + 2; e < from + n; e += 2) mx = max3(mx, fabsf(x[e]), fabsf(x[e + 1]));
     return mx;
 }
+// the maximum over `lanes` adjacent lanes (a power of two, the same for the whole warp)
+__device__ __forceinline__ float lanes_max(float v, int lanes) {
+    for (int off = lanes >> 1; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, off));
+    return v;
+}
 
-// RN(m / 448) of a non-negative bf16 value: the product with RN(1/448) and one
-// FMA correction from the exact remainder (Markstein's division by a known
-// divisor; right for every non-negative finite bf16 value).
-__device__ __forceinline__ float scale_of_bf16_max(float m) {
+// A group's scale, and what turns its elements into quotients: x / S is taken
+// as fma(x, inv, x e), inv + e = 1 / S to about 2^-46 (and a bias, below).
+struct Scale {
+    float S, inv, e;
+};
+// Scales whose reciprocal or correction would leave the normal range: by division.
+__device__ __forceinline__ bool by_division(const Scale& q) { return !(q.S < 0x1p96f) || (q.S < 0x1p-96f && q.S > 0.0f); }
+
+// The scale of a group of bf16 values with maximum m: S = RN(m / 448), as the
+// product with RN(1/448) and one FMA correction from the exact remainder
+// (Markstein's division by a known divisor; right for every bf16 m >= 0).
+//
+// The codes have to round the EXACT quotient x / S.  With x = X 2^a and
+// m = Y 2^b, X, Y < 256, and an E4M3 midpoint Z 2^c, Z < 32, the ratio of
+// 448 x / m and the midpoint is 7 X 2^d / (Y Z): it is 1, or at least 1 / 7905
+// away from it.  Where it is 1, x / S lies on the side of the midpoint that S's
+// own rounding decides, the same for the whole group: above it when S < m / 448,
+// below when S > m / 448, on it when S is exact.  So a bias of 2^-18 to that
+// side (far below 1 / 7905, far above float32's errors) decides every such
+// element, and no element on its own needs a second look; when S is exact
+// there is no bias, and the quotient, within 2^-45 of the midpoint, rounds to it
+// and then to even.
+__device__ __forceinline__ Scale scale_of_bf16_max(float m) {
     constexpr float y = 1.0f / 448.0f;
     const float q = __fmul_rn(m, y);
-    return fmaf(fmaf(-q, 448.0f, m), y, q);
+    Scale s;
+    s.S = fmaf(fmaf(-q, 448.0f, m), y, q);
+    s.inv = s.S > 0.0f ? rcp_approx(s.S) : 0.0f;   // a group of zeros: zero codes
+    const float rem = fmaf(-448.0f, s.S, m);        // 448 (m / 448 - S), exact
+    const float bias = rem > 0.0f ? 0x1p-18f : rem < 0.0f ? -0x1p-18f : 0.0f;
+    s.e = s.inv * (fmaf(-s.S, s.inv, 1.0f) + bias);
+    return s;
 }
-// RN(m / 448) of any non-negative float32
-__device__ __forceinline__ float scale_of_max(float m) { return __fdiv_rn(m, 448.0f); }
+// The scale of a group of float32 values with maximum m: their quotients are rounded to float32 before they are to E4M3.
+__device__ __forceinline__ Scale scale_of_max(float m) {
+    Scale s;
+    s.S = __fdiv_rn(m, 448.0f);
+    s.inv = s.S > 0.0f ? rcp_approx(s.S) : 0.0f;
+    s.e = s.inv * fmaf(-s.S, s.inv, 1.0f);
+    return s;
+}
 
-// The codes of eight elements of one group with scale S: the codes of
-// y (1 - 2^-20) and y (1 + 2^-20), y = x RN(1/S), agree unless an E4M3 midpoint
-// lies beside x / S; those few are decided from the exact quotient.  S = 0 (a
-// group of zeros) gives zero codes.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float S) {
-    const float inv = S > 0.0f ? rcp_approx(S) : 0.0f;
-    uint32_t codes[2] = {0u, 0u}, diff[2] = {0u, 0u};
+// The codes of n (a multiple of 4) elements of one group from x[from], as words from w[from / 4].
+template <int from, int n, int L>
+__device__ __forceinline__ void encode(const float (&x)[L], const Scale& q, uint32_t (&w)[L / 4]) {
+    if (by_division(q)) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const uint64_t yy = fma2(pk(x[e], x[e + 1]), pk(inv, inv), pk(0.0f, 0.0f));   // +0 for a zero of either sign
-        float l0, l1, h0, h1;
-        upk(mul2(yy, pk(kDn, kDn)), l0, l1);
-        upk(mul2(yy, pk(kUp, kUp)), h0, h1);
-        const uint32_t clo = e4m3x2(l0, l1), chi = e4m3x2(h0, h1);
-        codes[e / 4] |= clo << (16 * ((e >> 1) & 1));
-        diff[e / 4] |= (clo ^ chi) << (16 * ((e >> 1) & 1));
-    }
-    if (!(inv <= 3.40282347e38f)) {   // a subnormal scale: every element by division
+        for (int e = from; e < from + n; e += 4) {
+            uint32_t c = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int sh = 8 * (e & 3);
-            codes[e / 4] = (codes[e / 4] & ~(0xFFu << sh)) | (e4m3_code_of_quotient_exact(x[e], S) << sh);
+            for (int i = 0; i < 4; ++i) c |= e4m3_code_of_quotient_exact(x[e + i], q.S) << (8 * i);
+            w[e / 4] = e4m3_canonical_zero(c);
         }
-    } else if ((diff[0] | diff[1]) != 0u) {   // quotients beside a midpoint: the midpoint decides
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int wd = i >> 1, sh = 16 * (i & 1);
-            const uint32_t d = (diff[wd] >> sh) & 0xFFFFu;
-            if (d != 0u) {
-                const uint32_t lo = (codes[wd] >> sh) & 0xFFFFu;
-                const uint32_t c = e4m3x2_resolve(lo, lo ^ d, x[2 * i], x[2 * i + 1], S, S);
-                codes[wd] = (codes[wd] & ~(0xFFFFu << sh)) | (c << sh);
-            }
-        }
+        return;
     }
-    return make_uint2(e4m3_canonical_zero(codes[0]), e4m3_canonical_zero(codes[1]));
+    const uint64_t inv2 = pk(q.inv, q.inv), e2 = pk(q.e, q.e);
+#pragma unroll
+    for (int e = from; e < from + n; e += 4) {
+        uint32_t c[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint64_t xx = pk(x[e + 2 * i], x[e + 2 * i + 1]);
+            float y0, y1;
+            upk(fma2(xx, inv2, mul2(xx, e2)), y0, y1);
+            c[i] = e4m3x2(y0, y1);
+        }
+        w[e / 4] = e4m3_canonical_zero(c[0] | (c[1] << 16));
+    }
+}
+
+// Sixteen consecutive elements of a thread: scales and codes.  A group of 8 is
+// half of them (two scales), one of 16 all of them, a wider one G / 16 lanes.
+struct Scales16 {
+    Scale lo, hi;   // equal unless G = 8
+};
+template <bool kBf16>
+__device__ __forceinline__ void quantize16(const float (&x)[16], int G, Scales16& q, uint32_t (&w)[4]) {
+    const float m0 = max_of<0, 8>(x), m1 = max_of<8, 8>(x);
+    if (G == 8) {
+        q.lo = kBf16 ? scale_of_bf16_max(m0) : scale_of_max(m0);
+        q.hi = kBf16 ? scale_of_bf16_max(m1) : scale_of_max(m1);
+    } else {
+        const float m = lanes_max(fmaxf(m0, m1), G >> 4);
+        q.lo = q.hi = kBf16 ? scale_of_bf16_max(m) : scale_of_max(m);
+    }
+    encode<0, 8>(x, q.lo, w);
+    encode<8, 8>(x, q.hi, w);
+}
+// Stores the scales of the sixteen elements from flat index `at`.
+__device__ __forceinline__ void store_scales16(float* scale, int64_t at, int G, int gshift, const Scales16& q) {
+    if (G == 8)
+        *reinterpret_cast<float2*>(scale + (at >> 3)) = make_float2(q.lo.S, q.hi.S);
+    else if ((at & (G - 1)) == 0)
+        scale[at >> gshift] = q.lo.S;
+}
+__device__ __forceinline__ void load_scales16(const float* scale, int64_t at, int G, int gshift, float& lo, float& hi) {
+    if (G == 8) {
+        const float2 f = __ldg(reinterpret_cast<const float2*>(scale + (at >> 3)));
+        lo = f.x;
+        hi = f.y;
+    } else {
+        lo = hi = __ldg(scale + (at >> gshift));
+    }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

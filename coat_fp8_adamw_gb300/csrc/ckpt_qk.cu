@@ -28,6 +28,12 @@ namespace {
 
 using namespace ckpt;
 
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) { const uint32_t w[4] = {u.x, u.y, u.z, u.w}; unpack(w, x); }
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) { uint32_t w[4]; pack(x, w); return make_uint4(w[0], w[1], w[2], w[3]); }
+__device__ __forceinline__ void decode8(uint2 c, float (&x)[8]) { const uint32_t w[2] = {c.x, c.y}; decode(w, x); }
+__device__ __forceinline__ float group_max(const float (&x)[8], int G) { return lanes_max(max_of<0, 8>(x), G >> 3); }
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], const Scale& S) { uint32_t w[2]; encode<0, 8>(x, S, w); return make_uint2(w[0], w[1]); }
+
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
 
@@ -139,13 +145,13 @@ __global__ void __launch_bounds__(kBlock) qk_fwd_kernel(const QkArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = x[e] * r * w[e];
             turn8(t, a.interleaved != 0, y);
-            const float S = scale_of_bf16_max(group_max(x, a.G));
+            const Scale S = scale_of_bf16_max(group_max(x, a.G));
             const uint2 c = encode8(x, S);
             if (ok) {
                 const int64_t at = (m * sd.H + h) * a.D + l * 8;
                 st_cs(reinterpret_cast<uint4*>(sd.out + at), pack8(y));
                 __stcs(reinterpret_cast<uint2*>(sd.codes + at), c);
-                if (((l * 8) & (a.G - 1)) == 0) sd.scale[at / a.G] = S;
+                if (((l * 8) & (a.G - 1)) == 0) sd.scale[at / a.G] = S.S;
                 if (l == 0) sd.rstd[m * sd.H + h] = r;
             }
         }

@@ -11,9 +11,11 @@
 //
 // Everything between input and output is float32; h, dg and du are rounded
 // once to bf16, and the product's checkpoint is taken from its float32 value.
-// A thread holds eight consecutive elements.  Codes and scales are contiguous,
-// so the threads walk the flat element range in 16-byte chunks; gate and up
-// (and their gradients) may be column ranges of a wider tensor.
+// A thread holds sixteen consecutive elements (one 256-bit access of a bf16
+// tensor, one 128-bit access of codes), so that a group's maximum takes one
+// shuffle less than with eight.  Codes and scales are contiguous, so the threads
+// walk the flat element range; gate and up (and their gradients) may be column
+// ranges of a wider tensor.
 #include <cstdint>
 
 #include "ckpt_device.cuh"
@@ -27,109 +29,162 @@ using namespace ckpt;
 
 constexpr int kBlock = 256;
 
-// Chunk i of the flat range [M x nc chunks]: its first element in a tensor whose rows are ld apart.
-__device__ __forceinline__ int64_t strided_at(int64_t i, int64_t nc, int64_t ld) {
-    const int64_t r = i / nc;
-    return r * ld + (i - r * nc) * 8;
+// n / d for n < 2^31, d >= 1: (n mul) >> (32 + shift) with mul = ceil(2^(32 + shift) / d), shift = ceil(log2 d) - 1
+// (the error of mul is below 2^-shift of its unit times n < 2^31: it never reaches the next quotient).
+struct Divider {
+    uint32_t d, mul;
+    int shift;
+};
+Divider divider(uint32_t d) {
+    Divider v{d, 0u, 0};
+    if (d == 1) return v;
+    while ((1ull << (v.shift + 1)) < d) ++v.shift;
+    v.mul = (uint32_t)(((1ull << (32 + v.shift)) + d - 1) / d);
+    return v;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divider& v) {
+    return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift;
 }
 
-__global__ void __launch_bounds__(kBlock) swiglu_fwd_kernel(const SwigluFwdArgs a) {
-    const int64_t nc = a.N >> 3, total = a.M * nc;
-    // a warp's lanes run past the end together: the group maximum needs them all
-    for (int64_t i0 = (int64_t)blockIdx.x * kBlock; i0 < total; i0 += (int64_t)gridDim.x * kBlock) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool ok = i < total;
-        uint4 gv = make_uint4(0u, 0u, 0u, 0u), uv = gv;
-        if (ok) {
-            const int64_t at = strided_at(i, nc, a.ld);
-            gv = ld_cs(reinterpret_cast<const uint4*>(a.gate + at));
-            uv = ld_cs(reinterpret_cast<const uint4*>(a.up + at));
-        }
-        float g[8], u[8], h[8];
-        unpack8(gv, g);
-        unpack8(uv, u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
-        const float Sg = scale_of_bf16_max(group_max(g, a.G)), Su = scale_of_bf16_max(group_max(u, a.G));
-        const uint2 cg = encode8(g, Sg), cu = encode8(u, Su);
-        if (ok) {
-            const int64_t at = i * 8;
-            st_cs(reinterpret_cast<uint4*>(a.h + at), pack8(h));
-            __stcs(reinterpret_cast<uint2*>(a.gate_q + at), cg);
-            __stcs(reinterpret_cast<uint2*>(a.up_q + at), cu);
-            if ((at & (a.G - 1)) == 0) {
-                a.gate_scale[at / a.G] = Sg;
-                a.up_scale[at / a.G] = Su;
-            }
-        }
+// Chunk i of the rows of nc chunks: its first element in a tensor whose rows are ld apart.
+__device__ __forceinline__ int64_t strided_at(uint32_t i, const Divider& nc, int64_t ld) {
+    const uint32_t r = divide(i, nc);
+    return (int64_t)r * ld + (int64_t)(i - r * nc.d) * 16;
+}
+
+__global__ void __launch_bounds__(kBlock) swiglu_fwd_kernel(const SwigluFwdArgs a, const Divider nc, bool wide) {
+    const uint32_t total = (uint32_t)a.M * nc.d, i = blockIdx.x * kBlock + threadIdx.x;
+    const int gshift = 31 - __clz(a.G);
+    const bool ok = i < total;       // the lanes past the end take part in the shuffles
+    uint32_t gv[8] = {}, uv[8] = {};
+    if (ok) {
+        const int64_t at = strided_at(i, nc, a.ld);
+        load_words8(a.gate + at, wide, gv);
+        load_words8(a.up + at, wide, uv);
     }
+    float g[16], u[16], h[16];
+    unpack(gv, g);
+    unpack(uv, u);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
+    Scales16 sg, su;
+    uint32_t cg[4], cu[4], hv[8];
+    quantize16<true>(g, a.G, sg, cg);
+    quantize16<true>(u, a.G, su, cu);
+    if (!ok) return;
+    const int64_t at = (int64_t)i * 16;
+    pack(h, hv);
+    store_words8(a.h + at, wide, hv);
+    *reinterpret_cast<uint4*>(a.gate_q + at) = make_uint4(cg[0], cg[1], cg[2], cg[3]);
+    *reinterpret_cast<uint4*>(a.up_q + at) = make_uint4(cu[0], cu[1], cu[2], cu[3]);
+    store_scales16(a.gate_scale, at, a.G, gshift, sg);
+    store_scales16(a.up_scale, at, a.G, gshift, su);
 }
 
 template <bool kH>
-__global__ void __launch_bounds__(kBlock) swiglu_bwd_kernel(const SwigluBwdArgs a) {
-    const int64_t nc = a.N >> 3, total = a.M * nc;
-    for (int64_t i0 = (int64_t)blockIdx.x * kBlock; i0 < total; i0 += (int64_t)gridDim.x * kBlock) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool ok = i < total;
-        uint4 dv = make_uint4(0u, 0u, 0u, 0u);
-        uint2 gq = make_uint2(0u, 0u), uq = gq;
-        float Sg = 0.0f, Su = 0.0f;
-        if (ok) {
-            const int64_t at = i * 8;
-            dv = ld_cs(reinterpret_cast<const uint4*>(a.dh + at));
-            gq = __ldcs(reinterpret_cast<const uint2*>(a.gate_q + at));
-            uq = __ldcs(reinterpret_cast<const uint2*>(a.up_q + at));
-            Sg = __ldg(a.gate_scale + at / a.G);
-            Su = __ldg(a.up_scale + at / a.G);
-        }
-        float d[8], g[8], u[8], h[8], dg[8], du[8];
-        unpack8(dv, d);
-        decode8(gq, g);
-        decode8(uq, u);
+__global__ void __launch_bounds__(kBlock) swiglu_bwd_kernel(const SwigluBwdArgs a, const Divider nc, bool wide) {
+    const uint32_t total = (uint32_t)a.M * nc.d, i = blockIdx.x * kBlock + threadIdx.x;
+    const int gshift = 31 - __clz(a.G);
+    const bool ok = i < total;
+    const int64_t at = (int64_t)i * 16;
+    uint32_t dv[8] = {}, gq[4] = {}, uq[4] = {};
+    float Sg[2] = {0.0f, 0.0f}, Su[2] = {0.0f, 0.0f};
+    if (ok) {
+        load_words8(a.dh + at, wide, dv);
+        load_words<4>(a.gate_q + at, gq);
+        load_words<4>(a.up_q + at, uq);
+        load_scales16(a.gate_scale, at, a.G, gshift, Sg[0], Sg[1]);
+        load_scales16(a.up_scale, at, a.G, gshift, Su[0], Su[1]);
+    }
+    float d[16], g[16], u[16], h[16];
+    unpack(dv, d);
+    decode(gq, g);
+    decode(uq, u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            g[e] *= Sg;
-            u[e] *= Su;
-            const float s = sigmoid(g[e]), gs = g[e] * s;
-            h[e] = gs * u[e];
-            du[e] = d[e] * gs;
-            dg[e] = d[e] * u[e] * fmaf(gs, 1.0f - s, s);
-        }
+    for (int e = 0; e < 16; ++e) {
+        g[e] *= Sg[e >> 3];
+        u[e] *= Su[e >> 3];
+        const float s = sigmoid(g[e]), gs = g[e] * s;
+        h[e] = gs * u[e];
+        u[e] = d[e] * u[e] * fmaf(gs, 1.0f - s, s);   // d gate
+        g[e] = d[e] * gs;                             // d up
+    }
+    if (ok) {
+        const int64_t to = strided_at(i, nc, a.ld);
+        uint32_t w[8];
+        pack(u, w);
+        store_words8(a.dgate + to, wide, w);
+        pack(g, w);
+        store_words8(a.dup + to, wide, w);
+    }
+    if constexpr (kH) {
+        Scales16 sh;
+        uint32_t ch[4];
+        quantize16<false>(h, a.G, sh, ch);
         if (ok) {
-            const int64_t at = strided_at(i, nc, a.ld);
-            st_cs(reinterpret_cast<uint4*>(a.dgate + at), pack8(dg));
-            st_cs(reinterpret_cast<uint4*>(a.dup + at), pack8(du));
-        }
-        if constexpr (kH) {
-            const float Sh = scale_of_max(group_max(h, a.G));
-            const uint2 ch = encode8(h, Sh);
-            if (ok) {
-                const int64_t at = i * 8;
-                __stcs(reinterpret_cast<uint2*>(a.h_q + at), ch);
-                if ((at & (a.G - 1)) == 0) a.h_scale[at / a.G] = Sh;
-            }
+            *reinterpret_cast<uint4*>(a.h_q + at) = make_uint4(ch[0], ch[1], ch[2], ch[3]);
+            store_scales16(a.h_scale, at, a.G, gshift, sh);
         }
     }
 }
 
-unsigned swiglu_blocks(int64_t M, int64_t N) {
-    const int64_t need = (M * (N >> 3) + kBlock - 1) / kBlock, most = (int64_t)1 << 30;
-    return (unsigned)(need < most ? need : most);
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+// rows per launch: its chunks are counted in 31 bits
+int64_t slab_rows(int64_t N) {
+    const int64_t rows = (((int64_t)1 << 31) - kBlock) / (N / 16);
+    return rows;
 }
+unsigned blocks_of(int64_t M, int64_t N) { return (unsigned)((M * (N / 16) + kBlock - 1) / kBlock); }
 
 }  // namespace
 
-cudaError_t launch_swiglu_fwd(const SwigluFwdArgs& a, cudaStream_t s) {
-    swiglu_fwd_kernel<<<swiglu_blocks(a.M, a.N), kBlock, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_swiglu_fwd(const SwigluFwdArgs& all, cudaStream_t s) {
+    const int64_t N = all.N, slab = slab_rows(N);
+    const Divider nc = divider((uint32_t)(N / 16));
+    const bool wide = aligned32(all.gate) && aligned32(all.up) && aligned32(all.h) && all.ld % 16 == 0;
+    for (int64_t r = 0; r < all.M; r += slab) {
+        SwigluFwdArgs a = all;
+        a.M = all.M - r < slab ? all.M - r : slab;
+        a.gate += r * a.ld;
+        a.up += r * a.ld;
+        a.h += r * N;
+        a.gate_q += r * N;
+        a.up_q += r * N;
+        a.gate_scale += r * (N / a.G);
+        a.up_scale += r * (N / a.G);
+        swiglu_fwd_kernel<<<blocks_of(a.M, N), kBlock, 0, s>>>(a, nc, wide);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
-cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s) {
-    if (a.h_q)
-        swiglu_bwd_kernel<true><<<swiglu_blocks(a.M, a.N), kBlock, 0, s>>>(a);
-    else
-        swiglu_bwd_kernel<false><<<swiglu_blocks(a.M, a.N), kBlock, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& all, cudaStream_t s) {
+    const int64_t N = all.N, slab = slab_rows(N);
+    const Divider nc = divider((uint32_t)(N / 16));
+    const bool wide = aligned32(all.dgate) && aligned32(all.dup) && aligned32(all.dh) && all.ld % 16 == 0;
+    for (int64_t r = 0; r < all.M; r += slab) {
+        SwigluBwdArgs a = all;
+        a.M = all.M - r < slab ? all.M - r : slab;
+        a.dh += r * N;
+        a.gate_q += r * N;
+        a.up_q += r * N;
+        a.gate_scale += r * (N / a.G);
+        a.up_scale += r * (N / a.G);
+        a.dgate += r * a.ld;
+        a.dup += r * a.ld;
+        if (a.h_q) {
+            a.h_q += r * N;
+            a.h_scale += r * (N / a.G);
+            swiglu_bwd_kernel<true><<<blocks_of(a.M, N), kBlock, 0, s>>>(a, nc, wide);
+        } else {
+            swiglu_bwd_kernel<false><<<blocks_of(a.M, N), kBlock, 0, s>>>(a, nc, wide);
+        }
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace coat

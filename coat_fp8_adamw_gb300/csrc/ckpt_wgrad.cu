@@ -507,7 +507,9 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradArgs a, cons
         x[0] *= f0.x; x[1] *= f0.y; x[2] *= f0.z; x[3] *= f0.w;
         x[4] *= f1.x; x[5] *= f1.y; x[6] *= f1.z; x[7] *= f1.w;
     }
-    *reinterpret_cast<uint4*>(a.dw + n * a.K + k) = pack8(x);
+    uint32_t w[4];
+    pack(x, w);
+    *reinterpret_cast<uint4*>(a.dw + n * a.K + k) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // rows x cols elements, row-major, ld elements apart; boxes of box_cols x 64 rows, zeros outside the tensor
