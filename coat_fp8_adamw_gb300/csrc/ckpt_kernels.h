@@ -116,8 +116,9 @@ cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& a, cudaStream_t s);
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t s);
 cudaError_t launch_qk_bwd(const QkArgs& a, cudaStream_t s);
 cudaError_t launch_wgrad(const WgradArgs& a, cudaStream_t s);
-// bounded waits of the weight gradient's kernel that gave up, on the current device
+// bounded waits that gave up in the kernels of ckpt_wgrad.cu and ckpt_norm.cu, on the current device
 cudaError_t read_wgrad_wait_timeouts(unsigned long long* out, bool reset);
+cudaError_t read_norm_wait_timeouts(unsigned long long* out, bool reset);
 // out[c] = bf16(sum over p of partial[p * N + c]), p in order
 cudaError_t launch_column_sum(const float* partial, int64_t P, int64_t N, uint16_t* out, cudaStream_t s);
 

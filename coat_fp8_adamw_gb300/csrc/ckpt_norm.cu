@@ -22,7 +22,11 @@
 
 #include "ckpt_device.cuh"
 #include "ckpt_kernels.h"
+#include "tc_pipeline.cuh"
 
+#ifndef DEPTH
+#define DEPTH 3
+#endif
 namespace coat {
 
 namespace {
@@ -57,6 +61,29 @@ __device__ __forceinline__ float team_sum(float v, float* slots, int warps, int 
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(32 * warps) : "memory");
     const float s = lane < warps ? slots[lane] : 0.0f;
     return warp_sum(s);
+}
+
+// The same for a block whose teams keep step: a barrier of the whole block.
+__device__ __forceinline__ float block_sum(float v, float* slots, int warps, int warp, int lane) {
+    v = warp_sum(v);
+    if (lane == 0) slots[warp] = v;
+    __syncthreads();
+    if (warps == 1) return v;
+    const float s = lane < warps ? slots[lane] : 0.0f;
+    return warp_sum(s);
+}
+
+// Chunk c of a row in shared memory: eight gradients, code values and weights.
+__device__ __forceinline__ void read_chunk(const uint4* dy, const uint2* q, const float4* sw, int c, int T, float (&g)[8],
+                                           float (&x)[8], float (&w)[8]) {
+    const uint4 d = dy[c];
+    const uint2 v = q[c];
+    const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, vw[2] = {v.x, v.y};
+    unpack(dw, g);
+    decode(vw, x);
+    const float4 f0 = sw[c], f1 = sw[2 * T + c];
+    w[0] = f0.x; w[1] = f0.y; w[2] = f0.z; w[3] = f0.w;
+    w[4] = f1.x; w[5] = f1.y; w[6] = f1.z; w[7] = f1.w;
 }
 
 // The weights in shared memory: float4 j of thread t's sixteen at [j T + t], so
@@ -141,81 +168,139 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_kernel(const NormFwdArgs a, 
     }
 }
 
+// Backward: the rows come through a ring in shared memory, two to four iterations
+// of a block deep (dy, codes and dresidual of its teams' rows, each one bulk copy:
+// the rows of a block lie together), because loads kept on their way in registers
+// beside the sums for dw left too few threads.  A thread has two chunks of eight
+// columns, T chunks apart: neighbouring lanes read neighbouring 16 bytes.
+constexpr int kMaxDepth = 4;
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+struct BwdShape {
+    int T, teams;          // team of a row, rows per block and iteration
+    int N, depth;
+    uint32_t stage;        // bytes of a stage: teams rows of dy, codes, dresidual
+    uint32_t q_off, r_off; // of the codes and of dresidual in it
+};
+
 template <bool kRes>
-__global__ void __launch_bounds__(1024, 1) norm_bwd_kernel(const NormBwdArgs a, int T, int teams, bool wide) {
+__global__ void __launch_bounds__(1024, 1) norm_bwd_kernel(const NormBwdArgs a, const BwdShape sh) {
     __shared__ float slots[2][kMaxTeamWarps];
+    __shared__ uint64_t bars[kMaxDepth];
+    extern __shared__ __align__(16) unsigned char dyn[];
+    float4* sw = reinterpret_cast<float4*>(dyn);                       // float4 i of chunk c at [i 2T + c]
+    unsigned char* ring = dyn + (size_t)sh.T * kE * 4;
+    const int T = sh.T, teams = sh.teams, N = sh.N, depth = sh.depth;
     const int team = threadIdx.x / T, t = threadIdx.x - team * T;
     const int lane = threadIdx.x & 31, warps = T >> 5, warp = t >> 5;
     const int gshift = 31 - __clz(a.G);
-    const float inv_n = 1.0f / (float)a.N;
-    const int64_t col = (int64_t)t * kE, step = (int64_t)gridDim.x * teams;
-    const bool ok = col < a.N;
-    extern __shared__ float4 sw[];
-    stage_weights(a.weight, a.N, T, sw);
-    float dw[kE];
-#pragma unroll
-    for (int e = 0; e < kE; ++e) dw[e] = 0.0f;
-    uint32_t dn[8] = {}, qn[4] = {};
-    int64_t r = (int64_t)blockIdx.x * teams + team;
-    if (ok && r < a.M) {
-        load_words8(a.dy + r * a.N + col, wide, dn);
-        load_words<4>(a.q + r * a.N + col, qn);
+    const float inv_n = 1.0f / (float)N;
+    const int64_t ngr = N >> gshift;
+    const uint32_t bar0 = smem_u32(bars), ring0 = smem_u32(ring);
+    const int64_t rows_per = teams, step = (int64_t)gridDim.x * teams, first = (int64_t)blockIdx.x * teams;
+    auto issue = [&](int64_t r0, int s) {                              // rows r0 .. of this block's next iteration
+        const int64_t left = a.M - r0;
+        const uint32_t rows = (uint32_t)(left < rows_per ? left : rows_per), n = rows * (uint32_t)N;
+        const uint32_t d = ring0 + (uint32_t)s * sh.stage, bar = bar0 + 8u * (uint32_t)s;
+        mbar_expect_tx(bar, n * (kRes ? 5u : 3u));
+        bulk_load(d, a.dy + r0 * N, 2 * n, bar);
+        bulk_load(d + sh.q_off, a.q + r0 * N, n, bar);
+        if constexpr (kRes) bulk_load(d + sh.r_off, a.dresidual + r0 * N, 2 * n, bar);
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < depth; ++s) mbar_init(bar0 + 8u * (uint32_t)s, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int s = 0; s < depth; ++s)
+            if (first + s * step < a.M) issue(first + s * step, s);
     }
-    for (int par = 0; r < a.M; r += step, par ^= 1) {
-        const int64_t at = r * a.N + col;
-        const float rstd = __ldg(a.rstd + r);
-        float S[2] = {0.0f, 0.0f};
-        if (ok) load_scales16(a.scale, at, a.G, gshift, S[0], S[1]);
-        S[0] *= rstd;
-        S[1] *= rstd;
-        uint32_t dv[8], qv[4], rv[8] = {};
+    for (int i = threadIdx.x; i < 2 * T * 2; i += blockDim.x) {        // 2 T chunks of two float4s
+        const int c = i >> 1, j = i & 1;
+        sw[j * 2 * T + c] = 8 * c < N ? __ldg(reinterpret_cast<const float4*>(a.weight) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __syncthreads();
+    bool ok[2];
+    int col[2];
+    float dw[2][8], Sn[2] = {0.0f, 0.0f}, rn = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dv[i] = dn[i];
+    for (int j = 0; j < 2; ++j) {
+        col[j] = (j * T + t) * 8;
+        ok[j] = col[j] < N;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) qv[i] = qn[i];
-        if (ok) {
-            if constexpr (kRes) load_words8(a.dresidual + at, wide, rv);
-            if (r + step < a.M) {
-                load_words8(a.dy + at + step * a.N, wide, dn);
-                load_words<4>(a.q + at + step * a.N, qn);
-            }
+        for (int e = 0; e < 8; ++e) dw[j][e] = 0.0f;
+    }
+    auto fetch_scales = [&](int64_t r) {                               // one iteration ahead
+        if (r < a.M) {
+            rn = __ldg(a.rstd + r);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (ok[j]) Sn[j] = __ldg(a.scale + r * ngr + (col[j] >> gshift));
         }
+    };
+    fetch_scales(first + team);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int64_t r0 = first, it = 0; r0 < a.M; r0 += step, ++it) {
+        const int64_t r = r0 + team;
+        const bool live = r < a.M;                                     // a team past the last row only keeps step
+        const float rstd = rn, S[2] = {Sn[0] * rn, Sn[1] * rn};
+        fetch_scales(r + step);
+        if (!mbar_wait_fast(bar0 + 8u * (uint32_t)s, ph, nullptr)) break;
+        const unsigned char* st = ring + (size_t)s * sh.stage;
+        const uint4* dyp = reinterpret_cast<const uint4*>(st + (size_t)team * N * 2);
+        const uint2* qp = reinterpret_cast<const uint2*>(st + sh.q_off + (size_t)team * N);
+        const uint4* rp = reinterpret_cast<const uint4*>(st + sh.r_off + (size_t)team * N * 2);
         float c = 0.0f;
-        {
-            float g[kE], xh[kE], w[kE];
-            unpack(dv, g);
-            decode(qv, xh);
-            weights_of(sw, T, t, w);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                const float p = g[e] * (xh[e] * S[e >> 3]);
-                dw[e] += p;
+        for (int j = 0; j < 2; ++j) {
+            if (!live || !ok[j]) continue;
+            float g[8], xh[8], w[8];
+            read_chunk(dyp, qp, sw, col[j] >> 3, T, g, xh, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float p = g[e] * (xh[e] * S[j]);
+                dw[j][e] += p;
                 c = fmaf(p, w[e], c);
             }
         }
-        c = team_sum(c, slots[par] + team * warps, warps, warp, lane, 1 + team) * inv_n;
-        forget(dv);
-        forget(qv);
-        float g[kE], xh[kE], w[kE];
-        unpack(dv, g);
-        decode(qv, xh);
-        weights_of(sw, T, t, w);
-        const float k0 = -c * S[0], k1 = -c * S[1];
-#pragma unroll
-        for (int e = 0; e < kE; ++e) g[e] = rstd * fmaf(xh[e], e < 8 ? k0 : k1, g[e] * w[e]);
-        if constexpr (kRes) {
-            unpack(rv, w);
-#pragma unroll
-            for (int e = 0; e < kE; ++e) g[e] += w[e];
+        c = block_sum(c, slots[it & 1] + team * warps, warps, warp, lane) * inv_n;
+        // behind that barrier every thread is done with the iteration before this one: its stage is free
+        if (threadIdx.x == 0 && it > 0) {
+            const int64_t rr = r0 + (depth - 1) * step;
+            if (rr < a.M) issue(rr, s == 0 ? depth - 1 : s - 1);
         }
-        pack(g, dv);
-        if (ok) store_words8(a.dx + at, wide, dv);
-    }
-    if (ok) {
-        float4* part = reinterpret_cast<float4*>(a.partial + ((int64_t)blockIdx.x * teams + team) * a.N + col);
 #pragma unroll
-        for (int i = 0; i < kE / 4; ++i) part[i] = make_float4(dw[4 * i], dw[4 * i + 1], dw[4 * i + 2], dw[4 * i + 3]);
+        for (int j = 0; j < 2; ++j) {
+            if (!live || !ok[j]) continue;
+            float g[8], xh[8], w[8];
+            read_chunk(dyp, qp, sw, col[j] >> 3, T, g, xh, w);
+            const float k = -c * S[j];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = rstd * fmaf(xh[e], k, g[e] * w[e]);
+            if constexpr (kRes) {
+                const uint4 v = rp[col[j] >> 3];
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                unpack(vw, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] += w[e];
+            }
+            uint32_t o[4];
+            pack(g, o);
+            *reinterpret_cast<uint4*>(a.dx + r * N + col[j]) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if (++s == depth) { s = 0; ph ^= 1u; }
     }
+    float* part = a.partial + (first + team) * N;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (ok[j]) {
+            reinterpret_cast<float4*>(part + col[j])[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+            reinterpret_cast<float4*>(part + col[j])[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+        }
 }
 
 // 32 columns per block; its 32 warps take every 32nd row of the partial sums, four loads on their way each
@@ -256,6 +341,24 @@ cudaError_t allow_smem(F* kernel, size_t bytes) {
                                 : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+constexpr size_t kSmem = 227u << 10;   // per SM and at most per block; 1 KB of the SM's per block is the system's
+BwdShape bwd_shape(const Team& tm, int64_t N, bool res) {
+    const uint32_t n = (uint32_t)(tm.teams * N);
+    BwdShape sh{tm.threads, tm.teams, (int)N, DEPTH, res ? 5 * n : 3 * n, 2 * n, 3 * n};
+    while (sh.depth > 2 && smem_of(tm) + sh.depth * (size_t)(5 * n) + 2048 > kSmem) --sh.depth;
+    return sh;
+}
+size_t bwd_smem(const Team& tm, const BwdShape& sh) { return smem_of(tm) + (size_t)sh.depth * sh.stage; }
+// blocks that run at once: by threads (64 registers each) and shared memory (227 KB per SM, 1 KB of it per block)
+int64_t bwd_blocks(int64_t M, const Team& tm, size_t smem, int sms) {
+    int64_t per = 1024 / (tm.threads * tm.teams);
+    const int64_t fit = (int64_t)(kSmem / (smem + 2048));
+    if (per > fit) per = fit;
+    if (per < 1) per = 1;
+    const int64_t need = (M + tm.teams - 1) / tm.teams;
+    return need < sms * per ? need : sms * per;
+}
+
 }  // namespace
 
 int device_sms() {
@@ -270,7 +373,7 @@ int device_sms() {
 
 int64_t norm_bwd_partials(int64_t M, int64_t N, int sms) {
     const Team tm = team_of(N);
-    return norm_blocks(M, tm, sms) * tm.teams;
+    return bwd_blocks(M, tm, bwd_smem(tm, bwd_shape(tm, N, true)), sms) * tm.teams;
 }
 
 cudaError_t launch_column_sum(const float* partial, int64_t P, int64_t N, uint16_t* out, cudaStream_t s) {
@@ -293,17 +396,22 @@ cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
     const Team tm = team_of(a.N);
-    const int64_t blocks = norm_blocks(a.M, tm, device_sms());
-    const bool wide = aligned32(a.dy) && aligned32(a.dresidual) && aligned32(a.dx);
-    cudaError_t e = allow_smem(a.dresidual ? norm_bwd_kernel<true> : norm_bwd_kernel<false>, smem_of(tm));
+    const bool res = a.dresidual != nullptr;
+    const BwdShape sh = bwd_shape(tm, a.N, res);
+    const size_t smem = bwd_smem(tm, sh);
+    // as many blocks as norm_bwd_partials counts, whatever the gradient past the norm
+    const int64_t blocks = bwd_blocks(a.M, tm, bwd_smem(tm, bwd_shape(tm, a.N, true)), device_sms());
+    cudaError_t e = allow_smem(res ? norm_bwd_kernel<true> : norm_bwd_kernel<false>, smem);
     if (e != cudaSuccess) return e;
-    if (a.dresidual)
-        norm_bwd_kernel<true><<<(unsigned)blocks, tm.threads * tm.teams, smem_of(tm), s>>>(a, tm.threads, tm.teams, wide);
+    if (res)
+        norm_bwd_kernel<true><<<(unsigned)blocks, tm.threads * tm.teams, smem, s>>>(a, sh);
     else
-        norm_bwd_kernel<false><<<(unsigned)blocks, tm.threads * tm.teams, smem_of(tm), s>>>(a, tm.threads, tm.teams, wide);
+        norm_bwd_kernel<false><<<(unsigned)blocks, tm.threads * tm.teams, smem, s>>>(a, sh);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_column_sum(a.partial, blocks * tm.teams, a.N, a.dweight, s);
 }
+
+cudaError_t read_norm_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }
 
 }  // namespace coat

@@ -575,10 +575,6 @@ cudaError_t launch_wgrad(const WgradArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t read_wgrad_wait_timeouts(unsigned long long* out, bool reset) {
-    const unsigned long long zero = 0ull;
-    const cudaError_t e = cudaMemcpyFromSymbol(out, g_wait_timeouts, sizeof(*out));
-    return e == cudaSuccess && reset ? cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero)) : e;
-}
+cudaError_t read_wgrad_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }
 
 }  // namespace coat

@@ -461,12 +461,11 @@ cudaError_t launch_linear_fp8(const LinArgs& a, int G, cudaStream_t s) {
 }
 
 cudaError_t read_wait_timeouts(unsigned long long* out, bool reset) {
-    const unsigned long long zero = 0ull;
-    unsigned long long wgrad = 0ull;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_wait_timeouts, sizeof(*out));
-    if (e == cudaSuccess && reset) e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero));
-    if (e == cudaSuccess) e = read_wgrad_wait_timeouts(&wgrad, reset);
-    *out += wgrad;
+    unsigned long long n[3] = {0ull, 0ull, 0ull};
+    cudaError_t e = read_own_wait_timeouts(&n[0], reset);
+    if (e == cudaSuccess) e = read_wgrad_wait_timeouts(&n[1], reset);
+    if (e == cudaSuccess) e = read_norm_wait_timeouts(&n[2], reset);
+    *out = n[0] + n[1] + n[2];
     return e;
 }
 

@@ -159,6 +159,13 @@ EncodeTiled encoder() {
     return fn;
 }
 
+// this translation unit's g_wait_timeouts, on the current device
+cudaError_t read_own_wait_timeouts(unsigned long long* out, bool reset) {
+    const unsigned long long zero = 0ull;
+    const cudaError_t e = cudaMemcpyFromSymbol(out, g_wait_timeouts, sizeof(*out));
+    return e == cudaSuccess && reset ? cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(zero)) : e;
+}
+
 }  // namespace
 
 }  // namespace coat
