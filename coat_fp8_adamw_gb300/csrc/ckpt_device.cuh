@@ -48,6 +48,20 @@ __device__ __forceinline__ void store_words8(void* p, bool wide, const uint32_t 
     }
 }
 
+// 32 bytes of shared memory
+__device__ __forceinline__ void read8(const void* p, uint32_t (&w)[8]) {
+    const uint4 lo = reinterpret_cast<const uint4*>(p)[0], hi = reinterpret_cast<const uint4*>(p)[1];
+    w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
+    w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+}
+
+// ---- programmatic dependent launch ----
+// In the kernel whose results are waited for: the next one's blocks may be
+// scheduled.  In the next one, before it reads them: wait until the first has
+// ended and its writes are visible.
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---- bf16 and E4M3 ----
 // 2 W bf16 values as float32
 template <int W>
