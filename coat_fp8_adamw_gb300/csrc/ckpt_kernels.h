@@ -119,7 +119,13 @@ cudaError_t launch_wgrad(const WgradArgs& a, cudaStream_t s);
 // bounded waits that gave up in the kernels of ckpt_wgrad.cu and ckpt_norm.cu, on the current device
 cudaError_t read_wgrad_wait_timeouts(unsigned long long* out, bool reset);
 cudaError_t read_norm_wait_timeouts(unsigned long long* out, bool reset);
-// out[c] = bf16(sum over p of partial[p * N + c]), p in order
-cudaError_t launch_column_sum(const float* partial, int64_t P, int64_t N, uint16_t* out, cudaStream_t s);
+// out[c] = bf16(sum over p of partial[p * N + c]), for one or two sums (out null or P = 0: none); launched as a
+// dependent of the kernel before it in the stream, which writes the partial sums
+struct ColumnSum {
+    const float* partial;
+    int64_t P;
+    uint16_t* out;
+};
+cudaError_t launch_column_sums(const ColumnSum& first, const ColumnSum& second, int64_t N, cudaStream_t s);
 
 }  // namespace coat

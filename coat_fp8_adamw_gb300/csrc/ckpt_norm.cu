@@ -11,8 +11,8 @@
 // are rounded once, to the bf16 tensors that the caller asks for.
 //
 // A row is held by a team of T = 32 ceil(N / 512) threads, sixteen elements each; a
-// block has as many teams as fit 256 threads, and walks the rows, so many
-// consecutive ones at a time.  They come through a ring in shared memory, two
+// block has as many teams as fit 512 threads (forward) or 256, and walks the rows,
+// so many consecutive ones at a time.  They come through a ring in shared memory, two
 // to four iterations deep, each tensor's rows one bulk copy: the copies stay
 // ahead without registers, of which the sums for dw need many.  The weights stay
 // in shared memory too.
@@ -284,33 +284,37 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
         }
 }
 
-// 32 columns per block; its 32 warps take every 32nd row of the partial sums, four loads on their way each
-__global__ void __launch_bounds__(1024) column_sum_kernel(const float* partial, int64_t P, int64_t N, uint16_t* out) {
+// 32 columns of one of two sums per block; its 32 warps take every 32nd row of the partial sums, four loads on their
+// way each
+__global__ void __launch_bounds__(1024) column_sum_kernel(const ColumnSum first, const ColumnSum second, int64_t N) {
     __shared__ float part[32][33];
+    const ColumnSum cs = blockIdx.y == 0 ? first : second;
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    if (cs.P == 0) return;
     wait_for_primary();
     float s = 0.0f;
     if (c < N) {
         int64_t p = row;
-        for (; p + 96 < P; p += 128) {
-            const float v0 = partial[p * N + c], v1 = partial[(p + 32) * N + c];
-            const float v2 = partial[(p + 64) * N + c], v3 = partial[(p + 96) * N + c];
+        for (; p + 96 < cs.P; p += 128) {
+            const float v0 = cs.partial[p * N + c], v1 = cs.partial[(p + 32) * N + c];
+            const float v2 = cs.partial[(p + 64) * N + c], v3 = cs.partial[(p + 96) * N + c];
             s += (v0 + v1) + (v2 + v3);
         }
-        for (; p < P; p += 32) s += partial[p * N + c];
+        for (; p < cs.P; p += 32) s += cs.partial[p * N + c];
     }
     part[row][lane] = s;
     __syncthreads();
     s = warp_sum(part[lane][row]);   // this warp's column `row` of the block
-    if (lane == 0 && (int64_t)blockIdx.x * 32 + row < N) out[(int64_t)blockIdx.x * 32 + row] = bf16_bits(s);
+    if (lane == 0 && (int64_t)blockIdx.x * 32 + row < N) cs.out[(int64_t)blockIdx.x * 32 + row] = bf16_bits(s);
 }
 
 constexpr size_t kSmem = 227u << 10;   // shared memory per SM, and at most per block
 
-// The widths (bytes per element) of the tensors of a stage, in the order in which they lie there.
-Shape shape_of(int64_t N, int b0, int b1, int b2) {
-    const int T = 32 * (int)((N + 32 * kE - 1) / (32 * kE)), teams = T >= 256 ? 1 : 256 / T;
+// room: threads of a block that its teams share.  b0 ..: the widths (bytes per element) of the tensors of a stage, in the
+// order in which they lie there.
+Shape shape_of(int64_t N, int room, int b0, int b1, int b2) {
+    const int T = 32 * (int)((N + 32 * kE - 1) / (32 * kE)), teams = T >= room ? 1 : room / T;
     const uint32_t n = (uint32_t)(teams * N);
     Shape sh{T, teams, (int)N, 3, (uint32_t)(b0 + b1 + b2) * n, (uint32_t)b0 * n, (uint32_t)(b0 + b1) * n};
     // three iterations deep (two or four were slower), two where a row is too wide
@@ -328,21 +332,22 @@ int64_t blocks_of(int64_t M, const Shape& sh, int regs, int sms) {
     const int64_t need = (M + sh.teams - 1) / sh.teams;
     return need < sms * per ? need : sms * per;
 }
-Shape bwd_shape(int64_t N, bool res) { return shape_of(N, 2, 1, res ? 2 : 0); }
+Shape bwd_shape(int64_t N, bool res) { return shape_of(N, 256, 2, 1, res ? 2 : 0); }
 int64_t bwd_blocks(int64_t M, int64_t N, bool res, int sms) { return blocks_of(M, bwd_shape(N, res), 96, sms); }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
-// more than the 48 KB that every kernel may have
+// more than the 48 KB that every kernel may have, its static part (under 1 KB) included
 template <typename F>
 cudaError_t allow_smem(F* kernel, size_t bytes) {
-    return bytes <= (48u << 10) ? cudaSuccess
+    return bytes <= (47u << 10) ? cudaSuccess
                                 : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 template <bool kRes>
 cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
-    const Shape sh = shape_of(a.N, 2, kRes ? 2 : 0, 0);
+    // two rows of 4096 per block: 52.8 us at 8192 rows with a residual, 55.8 with one
+    const Shape sh = shape_of(a.N, 512, 2, kRes ? 2 : 0, 0);
     const unsigned blocks = (unsigned)blocks_of(a.M, sh, 64, device_sms());
     const bool wide = aligned32(a.h) && aligned32(a.y);
     const cudaError_t e = allow_smem(norm_fwd_kernel<kRes>, smem_of(sh));
@@ -376,18 +381,18 @@ int64_t norm_bwd_partials(int64_t M, int64_t N, int sms) {
     return (with > without ? with : without) * bwd_shape(N, false).teams;
 }
 
-cudaError_t launch_column_sum(const float* partial, int64_t P, int64_t N, uint16_t* out, cudaStream_t s) {
+cudaError_t launch_column_sums(const ColumnSum& first, const ColumnSum& second, int64_t N, cudaStream_t s) {
     // may start while the kernel that writes the partial sums ends; it waits for it on the device
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((N + 31) / 32));
+    cfg.gridDim = dim3((unsigned)((N + 31) / 32), second.P > 0 ? 2 : 1);
     cfg.blockDim = dim3(1024);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, column_sum_kernel, partial, P, N, out);
+    return cudaLaunchKernelEx(&cfg, column_sum_kernel, first, second, N);
 }
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s) {
@@ -404,7 +409,7 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
     else
         e = res ? launch_bwd<true, 1024>(a, blocks, sh, s) : launch_bwd<false, 1024>(a, blocks, sh, s);
     if (e != cudaSuccess) return e;
-    return launch_column_sum(a.partial, blocks * sh.teams, a.N, a.dweight, s);
+    return launch_column_sums(ColumnSum{a.partial, blocks * sh.teams, a.dweight}, ColumnSum{nullptr, 0, nullptr}, a.N, s);
 }
 
 cudaError_t read_norm_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }

@@ -12,11 +12,15 @@
 //
 // Everything between input and output is float32, rounded once to bf16.
 //
-// A head lies in D / 8 lanes, eight elements each (the smallest power of two of
-// lanes that holds it; the others idle), so that its sums are a few shuffles,
-// and so is a half-split pair, whose partner is rot / 16 lanes away.  A block
-// takes one token at a time: the lanes keep their cosines and sines in
-// registers over the token's heads.
+// A head lies in D / 16 lanes (the next power of two of them; the others idle)
+// that hold two chunks of eight entries each, so that its sums are a few
+// shuffles.  The chunks are chosen so that both entries of a pair are in one
+// thread: lane l < rot / 16 has entries 8 l and rot / 2 + 8 l onwards when the
+// pairs are split, and every other lane 16 l onwards.  Eight cosines and
+// sines per lane then serve all heads of a token, and stay in registers.  A
+// warp takes one token and some of the heads of its queries or of its keys; a
+// block works for one of the two sides, so that a lane has one set of weights
+// and, backward, of sums for dw.
 #include <cstdint>
 
 #include "ckpt_device.cuh"
@@ -28,82 +32,63 @@ namespace {
 
 using namespace ckpt;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) { const uint32_t w[4] = {u.x, u.y, u.z, u.w}; unpack(w, x); }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) { uint32_t w[4]; pack(x, w); return make_uint4(w[0], w[1], w[2], w[3]); }
-__device__ __forceinline__ void decode8(uint2 c, float (&x)[8]) { const uint32_t w[2] = {c.x, c.y}; decode(w, x); }
-__device__ __forceinline__ float group_max(const float (&x)[8], int G) { return lanes_max(max_of<0, 8>(x), G >> 3); }
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], const Scale& S) { uint32_t w[2]; encode<0, 8>(x, S, w); return make_uint2(w[0], w[1]); }
-
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
 
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+// How a group's maximum is found.
+enum GroupMode {
+    kAdjacent,   // a lane's chunks lie together: G = 16 is a lane, G / 16 lanes beyond
+    kSplit,      // lane l has chunks l and l + D / 16: G / 8 lanes each, or all lanes together (G = D)
+    kMixed       // anything else: chunk by chunk
+};
+
+struct Task {
+    int64_t blocks_q;    // blocks below: queries; the others: keys
+    int32_t parts_q, parts_k;   // warps that share a token's heads
+    int32_t mode;
+};
+
+__device__ __forceinline__ void load8f(const float* p, float* x) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 
-// A lane's part of the rotation: out[e] = in[e] c[e] + partner(in)[e] s[e], where
-// s carries the sign of the lane's side of the pair; lanes behind rot (and a
-// position outside the tables: NaN) included.
-struct Turn {
-    float c[8], s[8];
-    int from;          // half-split: the lane that holds the partners
+// The first entries of a lane's chunks.
+struct Place {
+    int a, b;
 };
+__device__ __forceinline__ Place place_of(int l, int rot, bool interleaved) {
+    const bool split = !interleaved && 16 * l < rot;
+    return split ? Place{8 * l, rot / 2 + 8 * l} : Place{16 * l, 16 * l + 8};
+}
 
-// l: lane within the head; base: the head's first lane.
-__device__ __forceinline__ void load_turn(const QkArgs& a, int64_t m, int l, int base, bool back, Turn& t) {
-    const int half = a.rot >> 1, e0 = l * 8;
-    t.from = base + l;
+// Cosines and sines of a lane's eight pairs; 1 and 0 behind rot, NaN at a position outside the tables.
+__device__ __forceinline__ void load_turn(const QkArgs& a, int64_t m, int l, float (&c)[8], float (&s)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) { t.c[e] = 1.0f; t.s[e] = 0.0f; }
-    if (e0 >= a.rot) return;
-    const int64_t pos = a.positions[m];
-    const bool ok = pos >= 0 && pos < a.max_pos;
-    const float nan = __uint_as_float(0x7FC00000u);
-    if (a.interleaved) {
-        float4 c = make_float4(nan, nan, nan, nan), s = c;
-        if (ok) {
-            c = __ldg(reinterpret_cast<const float4*>(a.cos + pos * half + (e0 >> 1)));
-            s = __ldg(reinterpret_cast<const float4*>(a.sin + pos * half + (e0 >> 1)));
-        }
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            t.c[2 * i] = t.c[2 * i + 1] = cc[i];
-            t.s[2 * i] = back ? ss[i] : -ss[i];
-            t.s[2 * i + 1] = back ? -ss[i] : ss[i];
-        }
+    for (int e = 0; e < 8; ++e) { c[e] = 1.0f; s[e] = 0.0f; }
+    if (16 * l >= a.rot) return;
+    const int64_t pos = __ldg(a.positions + m);
+    if (pos >= 0 && pos < a.max_pos) {
+        load8f(a.cos + pos * (a.rot / 2) + 8 * l, c);
+        load8f(a.sin + pos * (a.rot / 2) + 8 * l, s);
     } else {
-        const bool low = e0 < half;
-        t.from = base + (low ? l + (half >> 3) : l - (half >> 3));
-        const int i0 = low ? e0 : e0 - half;
-        if (ok) {
-            load8(a.cos + pos * half + i0, t.c);
-            load8(a.sin + pos * half + i0, t.s);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t.c[e] = t.s[e] = nan;
-        }
-        if (low != back) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t.s[e] = -t.s[e];
-        }
+        for (int e = 0; e < 8; ++e) c[e] = s[e] = __uint_as_float(0x7FC00000u);
     }
 }
 
-// every lane of the warp takes part
-__device__ __forceinline__ void turn8(const Turn& t, bool interleaved, float (&x)[8]) {
-    float p[8];
-    if (interleaved) {
+// x[0..7], x[8..15]: the two chunks.  Turned by the angles, or back by them.  (A warp's lanes behind rot have split
+// pairs' places taken by entries that do not pair: their angle is 0.)
+template <bool kInter, bool kBack>
+__device__ __forceinline__ void turn(const float (&c)[8], const float (&s)[8], float (&x)[16]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(kFull, x[e], t.from);
+    for (int i = 0; i < 8; ++i) {
+        const int ia = kInter ? 2 * i : i, ib = kInter ? 2 * i + 1 : i + 8;
+        const float a = x[ia], b = x[ib];
+        x[ia] = fmaf(b, kBack ? s[i] : -s[i], a * c[i]);
+        x[ib] = fmaf(a, kBack ? -s[i] : s[i], b * c[i]);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(p[e], t.s[e], x[e] * t.c[e]);
 }
 
 template <int kLanes>
@@ -113,153 +98,291 @@ __device__ __forceinline__ float head_sum(float v) {
     return v;
 }
 
-template <int kLanes>
-__global__ void __launch_bounds__(kBlock) qk_fwd_kernel(const QkArgs a) {
+// Group maxima of the two chunks of every lane (bf16 values; idle lanes have zeros).
+__device__ __forceinline__ void group_maxima(float& ma, float& mb, int mode, int lanes, int l, int base, const QkArgs& a) {
+    if (a.G == 8) return;
+    if (mode == kAdjacent) {
+        ma = mb = lanes_max(fmaxf(ma, mb), a.G >> 4);
+        return;
+    }
+    if (mode == kSplit && a.G == a.D) {
+        ma = mb = lanes_max(fmaxf(ma, mb), lanes);
+        return;
+    }
+    // both maxima in one word: a bf16 value is the upper half of its float
+    uint32_t v = __byte_perm(__float_as_uint(ma), __float_as_uint(mb), 0x7632);
+    if (mode == kSplit) {
+        for (int off = a.G >> 4; off > 0; off >>= 1) {
+            const uint32_t o = __shfl_xor_sync(kFull, v, off);
+            asm("max.u16x2 %0, %0, %1;" : "+r"(v) : "r"(o));
+        }
+        ma = __uint_as_float(v << 16);
+        mb = __uint_as_float(v & 0xFFFF0000u);
+        return;
+    }
+    const int per = a.G >> 3, rl = a.rot >> 4;    // chunks of a group; lanes with split pairs
+    const Place p = place_of(l, a.rot, a.interleaved != 0);
+    const int ga = (p.a >> 3) & ~(per - 1), gb = (p.b >> 3) & ~(per - 1);
+    uint32_t wa = 0u, wb = 0u;
+    for (int j = 0; j < 2 * per; ++j) {
+        const int c = j < per ? ga + j : gb + j - per;
+        const bool second = c < 2 * rl ? c >= rl : (c & 1) != 0;
+        const int from = c < 2 * rl ? (second ? c - rl : c) : c >> 1;
+        const uint32_t o = __shfl_sync(kFull, v, base + from);
+        const uint32_t x = second ? o >> 16 : o & 0xFFFFu;
+        if (j < per) wa = wa > x ? wa : x;
+        else wb = wb > x ? wb : x;
+    }
+    ma = __uint_as_float(wa << 16);
+    mb = __uint_as_float(wb << 16);
+}
+
+__device__ __forceinline__ void load_pair(const uint16_t* p, const Place& at, uint32_t (&w)[8]) {
+    uint32_t lo[4], hi[4];
+    load_words<4>(p + at.a, lo);
+    load_words<4>(p + at.b, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { w[i] = lo[i]; w[4 + i] = hi[i]; }
+}
+__device__ __forceinline__ void store_pair(uint16_t* p, const Place& at, const uint32_t (&w)[8]) {
+    *reinterpret_cast<uint4*>(p + at.a) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p + at.b) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int kLanes, bool kInter>
+__global__ void __launch_bounds__(kBlock) qk_fwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;   // heads per warp and pass
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
-    const bool in_head = l * 8 < a.D;
+    const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
+    const bool is_q = blockIdx.x < tk.blocks_q;
+    const HeadSide sd = is_q ? a.q : a.k;
+    const int parts = is_q ? tk.parts_q : tk.parts_k;
+    const int64_t t = (int64_t)(blockIdx.x - (is_q ? 0 : tk.blocks_q)) * kWarps + (threadIdx.x >> 5);
+    const int64_t m = t / parts;
+    if (m >= a.M) return;
+    const int part = (int)(t - m * parts), passes = (sd.H + kHeads - 1) / kHeads;
+    const int from = (int)((int64_t)passes * part / parts), to = (int)((int64_t)passes * (part + 1) / parts);
+    const bool in_head = l * 16 < a.D;
+    const Place at = place_of(l, a.rot, kInter);
+    const uint16_t* in = sd.in + m * sd.ld;
+    const int64_t row = m * sd.H;         // head 0 of this token
+    const int gshift = 31 - __clz(a.G), gpr = a.D >> gshift;
     const float inv_d = 1.0f / (float)a.D;
-    const int H = a.q.H + a.k.H;
-    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-        Turn t;
-        load_turn(a, m, l, base, false, t);
-        for (int h0 = warp * kHeads; h0 < H; h0 += kWarps * kHeads) {
-            const bool ok = h0 + sub < H && in_head;
-            const bool is_q = h0 + sub < a.q.H;
-            const HeadSide& sd = is_q ? a.q : a.k;
-            const int64_t h = is_q ? h0 + sub : h0 + sub - a.q.H;
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (ok) {
-                u = ld_cs(reinterpret_cast<const uint4*>(sd.in + m * sd.ld + h * a.D + l * 8));
-                load8(sd.weight + l * 8, w);
-            }
-            float x[8], y[8];
-            unpack8(u, x);
-            float ss = 0.0f;
+    uint32_t nx[8] = {};
+    if (in_head && from * kHeads + sub < sd.H) load_pair(in + (from * kHeads + sub) * a.D, at, nx);
+    float c[8], s[8], w[16] = {};
+    load_turn(a, m, l, c, s);
+    if (in_head) {
+        load8f(sd.weight + at.a, w);
+        load8f(sd.weight + at.b, w + 8);
+    }
+    for (int p = from; p < to; ++p) {
+        const int h = p * kHeads + sub;
+        const bool ok = in_head && h < sd.H;
+        float x[16];
+        unpack(nx, x);
+        if (p + 1 < to && in_head && h + kHeads < sd.H) {
+            load_pair(in + (h + kHeads) * a.D, at, nx);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-            ss = head_sum<kLanes>(ss);
-            const float r = __frcp_rn(__fsqrt_rn(fmaf(ss, inv_d, a.eps)));
+            for (int e = 0; e < 8; ++e) nx[e] = 0u;
+        }
+        float ss = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e] * r * w[e];
-            turn8(t, a.interleaved != 0, y);
-            const Scale S = scale_of_bf16_max(group_max(x, a.G));
-            const uint2 c = encode8(x, S);
-            if (ok) {
-                const int64_t at = (m * sd.H + h) * a.D + l * 8;
-                st_cs(reinterpret_cast<uint4*>(sd.out + at), pack8(y));
-                __stcs(reinterpret_cast<uint2*>(sd.codes + at), c);
-                if (((l * 8) & (a.G - 1)) == 0) sd.scale[at / a.G] = S.S;
-                if (l == 0) sd.rstd[m * sd.H + h] = r;
-            }
+        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+        ss = head_sum<kLanes>(ss);
+        const float r = __frcp_rn(__fsqrt_rn(fmaf(ss, inv_d, a.eps)));
+        float ma = max_of<0, 8>(x), mb = max_of<8, 8>(x);
+        group_maxima(ma, mb, tk.mode, kLanes, l, base, a);
+        const Scale sa = scale_of_bf16_max(ma), sb = scale_of_bf16_max(mb);
+        uint32_t q[4], o[8];
+        encode<0, 8>(x, sa, q);
+        encode<8, 8>(x, sb, q);
+        float y[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = x[e] * r * w[e];
+        turn<kInter, false>(c, s, y);
+        pack(y, o);
+        if (ok) {
+            const int64_t hd = (row + h) * a.D;
+            store_pair(sd.out + hd, at, o);
+            *reinterpret_cast<uint2*>(sd.codes + hd + at.a) = make_uint2(q[0], q[1]);
+            *reinterpret_cast<uint2*>(sd.codes + hd + at.b) = make_uint2(q[2], q[3]);
+            float* sc = sd.scale + (row + h) * gpr;
+            if ((at.a & (a.G - 1)) == 0) sc[at.a >> gshift] = sa.S;
+            if ((at.b & (a.G - 1)) == 0) sc[at.b >> gshift] = sb.S;
+            if (l == 0) sd.rstd[row + h] = r;
         }
     }
 }
 
-template <int kLanes>
-__global__ void __launch_bounds__(kBlock) qk_bwd_kernel(const QkArgs a) {
+template <int kLanes, bool kInter>
+__global__ void __launch_bounds__(kBlock, 2) qk_bwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;
-    __shared__ float part[kBlock / kLanes][2][kLanes * 8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
-    const bool in_head = l * 8 < a.D;
+    __shared__ float part_sum[kWarps][16 * kLanes];
+    const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), sub = lane / kLanes, warp = threadIdx.x >> 5;
+    const bool is_q = blockIdx.x < tk.blocks_q;
+    const HeadSide sd = is_q ? a.q : a.k;
+    const int parts = is_q ? tk.parts_q : tk.parts_k;
+    const int64_t first = blockIdx.x - (is_q ? 0 : tk.blocks_q), blocks = is_q ? tk.blocks_q : gridDim.x - tk.blocks_q;
+    const int passes = (sd.H + kHeads - 1) / kHeads;
+    const bool in_head = l * 16 < a.D;
+    const Place at = place_of(l, a.rot, kInter);
+    const int gshift = 31 - __clz(a.G), gpr = a.D >> gshift;
     const float inv_d = 1.0f / (float)a.D;
-    const int H = a.q.H + a.k.H;
-    float dw[2][8];
+    float w[16] = {}, dw[16] = {};
+    if (in_head) {
+        load8f(sd.weight + at.a, w);
+        load8f(sd.weight + at.b, w + 8);
+    }
+    for (int64_t t = first * kWarps + warp; t < a.M * parts; t += blocks * kWarps) {
+        const int64_t m = t / parts;
+        const int part = (int)(t - m * parts);
+        const int from = (int)((int64_t)passes * part / parts), to = (int)((int64_t)passes * (part + 1) / parts);
+        const int64_t row = m * sd.H;
+        uint16_t* out = sd.out + m * sd.ld;
+        uint32_t nd[8] = {}, nq[4] = {};
+        float na = 0.0f, nb = 0.0f, nr = 0.0f;
+        auto fetch = [&](int h) {        // one pass ahead; zeros where there is no such head
+            if (in_head && h < sd.H) {
+                const int64_t hd = (row + h) * a.D;
+                load_pair(sd.in + hd, at, nd);
+                const uint2 qa = __ldg(reinterpret_cast<const uint2*>(sd.codes + hd + at.a));
+                const uint2 qb = __ldg(reinterpret_cast<const uint2*>(sd.codes + hd + at.b));
+                nq[0] = qa.x; nq[1] = qa.y; nq[2] = qb.x; nq[3] = qb.y;
+                const float* sc = sd.scale + (row + h) * gpr;
+                na = __ldg(sc + (at.a >> gshift));
+                nb = __ldg(sc + (at.b >> gshift));
+                nr = __ldg(sd.rstd + row + h);
+            } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.0f;
-    for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-        Turn t;
-        load_turn(a, m, l, base, true, t);
-        for (int h0 = warp * kHeads; h0 < H; h0 += kWarps * kHeads) {
-            const bool ok = h0 + sub < H && in_head;
-            const bool is_q = h0 + sub < a.q.H;
-            const HeadSide& sd = is_q ? a.q : a.k;
-            const int64_t h = is_q ? h0 + sub : h0 + sub - a.q.H;
-            const int64_t at = (m * sd.H + h) * a.D + l * 8;
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            uint2 q = make_uint2(0u, 0u);
-            float S = 0.0f, r = 0.0f;
-            float w[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (ok) {
-                u = ld_cs(reinterpret_cast<const uint4*>(sd.in + at));
-                q = __ldcs(reinterpret_cast<const uint2*>(sd.codes + at));
-                S = __ldg(sd.scale + at / a.G);
-                r = __ldg(sd.rstd + m * sd.H + h);
-                load8(sd.weight + l * 8, w);
+                for (int e = 0; e < 8; ++e) nd[e] = 0u;
             }
-            float g[8], xh[8];
-            unpack8(u, g);
-            decode8(q, xh);
-            turn8(t, a.interleaved != 0, g);
-            float c = 0.0f;
+        };
+        fetch(from * kHeads + sub);
+        float c[8], s[8];
+        load_turn(a, m, l, c, s);
+        for (int p = from; p < to; ++p) {
+            const int h = p * kHeads + sub;
+            const bool ok = in_head && h < sd.H;
+            float g[16], xh[16];
+            unpack(nd, g);
+            decode(nq, xh);
+            const float r = nr, sa = na * r, sb = nb * r;
+            if (p + 1 < to) fetch(h + kHeads);
+            turn<kInter, true>(c, s, g);
+            float k = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[e] = xh[e] * S * r;
-                const float d = ok ? g[e] * xh[e] : 0.0f;
-                dw[0][e] += is_q ? d : 0.0f;
-                dw[1][e] += is_q ? 0.0f : d;
-                c = fmaf(d, w[e], c);
+            for (int e = 0; e < 16; ++e) {
+                xh[e] *= e < 8 ? sa : sb;
+                const float d = g[e] * xh[e];
+                dw[e] += ok ? d : 0.0f;
                 g[e] *= w[e];
+                k = fmaf(g[e], xh[e], k);
             }
-            c = head_sum<kLanes>(c) * inv_d;
+            k = -head_sum<kLanes>(k) * inv_d;
+            uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = r * fmaf(-xh[e], c, g[e]);
-            if (ok) st_cs(reinterpret_cast<uint4*>(sd.out + m * sd.ld + h * a.D + l * 8), pack8(g));
+            for (int e = 0; e < 16; ++e) g[e] = r * fmaf(xh[e], k, g[e]);
+            pack(g, o);
+            if (ok) store_pair(out + h * a.D, at, o);
         }
     }
-    const int slot = threadIdx.x / kLanes;
+    dependents_may_start();
+    // the block's sums: the warp's heads by shuffles, then its warps in order
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        part[slot][0][l * 8 + e] = dw[0][e];
-        part[slot][1][l * 8 + e] = dw[1][e];
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+        for (int off = 16; off >= kLanes; off >>= 1) dw[e] += __shfl_xor_sync(kFull, dw[e], off);
+    }
+    if (sub == 0 && in_head) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            part_sum[warp][at.a + e] = dw[e];
+            part_sum[warp][at.b + e] = dw[8 + e];
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.D; i += kBlock) {
-        const int side = i >= a.D, c = i - side * a.D;
-        float s = 0.0f;
-        for (int p = 0; p < kBlock / kLanes; ++p) s += part[p][side][c];
-        a.partial[((int64_t)side * gridDim.x + blockIdx.x) * a.D + c] = s;
+    for (int i = threadIdx.x; i < a.D; i += kBlock) {
+        float v = 0.0f;
+#pragma unroll
+        for (int p = 0; p < kWarps; ++p) v += part_sum[p][i];
+        a.partial[(int64_t)blockIdx.x * a.D + i] = v;
     }
 }
 
-template <int kLanes>
-cudaError_t launch(const QkArgs& a, bool back, unsigned blocks, cudaStream_t s) {
+template <int kLanes, bool kInter>
+cudaError_t launch(const QkArgs& a, const Task& tk, bool back, int64_t blocks, cudaStream_t s) {
     if (back)
-        qk_bwd_kernel<kLanes><<<blocks, kBlock, 0, s>>>(a);
+        qk_bwd_kernel<kLanes, kInter><<<(unsigned)blocks, kBlock, 0, s>>>(a, tk);
     else
-        qk_fwd_kernel<kLanes><<<blocks, kBlock, 0, s>>>(a);
+        qk_fwd_kernel<kLanes, kInter><<<(unsigned)blocks, kBlock, 0, s>>>(a, tk);
     return cudaGetLastError();
 }
-
-cudaError_t launch_any(const QkArgs& a, bool back, unsigned blocks, cudaStream_t s) {
-    const int lanes = a.D / 8;
-    if (lanes <= 2) return launch<2>(a, back, blocks, s);
-    if (lanes <= 4) return launch<4>(a, back, blocks, s);
-    if (lanes <= 8) return launch<8>(a, back, blocks, s);
-    if (lanes <= 16) return launch<16>(a, back, blocks, s);
-    return launch<32>(a, back, blocks, s);
+template <int kLanes>
+cudaError_t launch(const QkArgs& a, const Task& tk, bool back, int64_t blocks, cudaStream_t s) {
+    return a.interleaved ? launch<kLanes, true>(a, tk, back, blocks, s) : launch<kLanes, false>(a, tk, back, blocks, s);
 }
+int lanes_of(int D) {
+    int n = 1;
+    while (16 * n < D) n *= 2;
+    return n;
+}
+cudaError_t launch_any(const QkArgs& a, const Task& tk, bool back, int64_t blocks, cudaStream_t s) {
+    switch (lanes_of(a.D)) {
+        case 1: return launch<1>(a, tk, back, blocks, s);
+        case 2: return launch<2>(a, tk, back, blocks, s);
+        case 4: return launch<4>(a, tk, back, blocks, s);
+        case 8: return launch<8>(a, tk, back, blocks, s);
+        default: return launch<16>(a, tk, back, blocks, s);
+    }
+}
+
+int mode_of(const QkArgs& a) {
+    if (a.interleaved) return kAdjacent;
+    if (a.rot == a.D && (a.G == a.D || a.D / 2 % a.G == 0)) return kSplit;
+    return kMixed;
+}
+
+// Warps that share a token's heads: about four passes each, so that the angles serve several heads; more of them while
+// there are too few tokens to give every SM sixteen warps.
+int parts_of(int64_t M, int H, int lanes, int sms) {
+    const int passes = (H * lanes + 31) / 32;
+    int parts = (passes + 3) / 4;
+    while (parts < passes && M * parts < (int64_t)sms * 16) parts *= 2;
+    return parts < passes ? parts : (passes > 0 ? passes : 1);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
 int64_t qk_bwd_partials(int64_t M, int sms) {
-    const int64_t room = (int64_t)sms * 4;
-    return M < room ? M : room;
+    (void)M;
+    return (int64_t)sms * 2 + 2;
 }
 
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t s) {
-    return launch_any(a, false, (unsigned)(a.M < (1 << 30) ? a.M : (1 << 30)), s);
+    const int sms = device_sms(), lanes = lanes_of(a.D);
+    Task tk{0, parts_of(a.M, a.q.H, lanes, sms), parts_of(a.M, a.k.H, lanes, sms), mode_of(a)};
+    tk.blocks_q = a.q.H > 0 ? ceil_div(a.M * tk.parts_q, kWarps) : 0;
+    const int64_t blocks_k = a.k.H > 0 ? ceil_div(a.M * tk.parts_k, kWarps) : 0;
+    if (tk.blocks_q + blocks_k >= (1LL << 31)) return cudaErrorInvalidValue;
+    return launch_any(a, tk, false, tk.blocks_q + blocks_k, s);
 }
 
 cudaError_t launch_qk_bwd(const QkArgs& a, cudaStream_t s) {
-    const int64_t blocks = qk_bwd_partials(a.M, device_sms());
-    cudaError_t e = launch_any(a, true, (unsigned)blocks, s);
-    if (e == cudaSuccess && a.q.H > 0) e = launch_column_sum(a.partial, blocks, a.D, a.q.dweight, s);
-    if (e == cudaSuccess && a.k.H > 0) e = launch_column_sum(a.partial + blocks * a.D, blocks, a.D, a.k.dweight, s);
-    return e;
+    const int sms = device_sms(), lanes = lanes_of(a.D), H = a.q.H + a.k.H;
+    Task tk{0, parts_of(a.M, a.q.H, lanes, sms), parts_of(a.M, a.k.H, lanes, sms), mode_of(a)};
+    // two blocks per SM, shared between the sides as their heads are, one at least where there are any
+    const int64_t room = (int64_t)sms * 2;
+    int64_t bq = a.q.H > 0 ? room * a.q.H / H : 0, bk = a.k.H > 0 ? room - bq : 0;
+    const int64_t need_q = ceil_div(a.M * tk.parts_q, kWarps), need_k = ceil_div(a.M * tk.parts_k, kWarps);
+    bq = a.q.H > 0 ? (bq < 1 ? 1 : bq > need_q ? need_q : bq) : 0;
+    bk = a.k.H > 0 ? (bk < 1 ? 1 : bk > need_k ? need_k : bk) : 0;
+    tk.blocks_q = bq;
+    cudaError_t e = launch_any(a, tk, true, bq + bk, s);
+    if (e != cudaSuccess) return e;
+    return launch_column_sums(ColumnSum{a.partial, bq, a.q.dweight}, ColumnSum{a.partial + bq * a.D, bk, a.k.dweight}, a.D, s);
 }
 
 }  // namespace coat
