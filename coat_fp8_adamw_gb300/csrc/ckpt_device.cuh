@@ -222,6 +222,26 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// 1 / sqrt(v), v > 0 and normal: the approximation and one Newton step, within 2^-23 relatively.
+__device__ __forceinline__ float rsqrt_newton(float v) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+}
+
+// ---- pairs of float32 (each half rounds like the scalar operation) ----
+// 2 W bf16 values as W pairs
+template <int W>
+__device__ __forceinline__ void unpack2(const uint32_t (&w)[W], uint64_t (&x)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    float a, b;
+    upk(v, a, b);
+    return a + b;
+}
+
 // sigmoid(x) = 1 / (1 + 2^(-x log2 e)); x -> -inf gives 0, +inf gives 1.
 __device__ __forceinline__ float sigmoid(float x) {
     return __fdividef(1.0f, 1.0f + ex2_ftz(-1.4426950408889634f * x));

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_kernel(const NormFwdArgs a, 
         ss = team_sum(ss, slots[it & 1] + team * warps, warps, warp, lane);
         // behind that barrier every thread has read the iteration's rows: its stage is free
         if (threadIdx.x == 0 && r0 + depth * step < a.M) issue(r0 + depth * step, s);
-        const float rstd = __frcp_rn(__fsqrt_rn(fmaf(ss, inv_n, a.eps)));
+        const float rstd = rsqrt_newton(fmaf(ss, inv_n, a.eps));
         if (ok) {
             float w[kE];
             uint32_t u[8];

@@ -78,8 +78,8 @@ __device__ __forceinline__ void load_turn(const QkArgs& a, int64_t m, int l, flo
     }
 }
 
-// x[0..7], x[8..15]: the two chunks.  Turned by the angles, or back by them.  (A warp's lanes behind rot have split
-// pairs' places taken by entries that do not pair: their angle is 0.)
+// x[0..7], x[8..15]: the two chunks.  Turned by the angles, or back by them.  (Lanes behind rot hold entries that do not
+// pair: their angle is 0.)
 template <bool kInter, bool kBack>
 __device__ __forceinline__ void turn(const float (&c)[8], const float (&s)[8], float (&x)[16]) {
 #pragma unroll
@@ -89,6 +89,10 @@ __device__ __forceinline__ void turn(const float (&c)[8], const float (&s)[8], f
         x[ia] = fmaf(b, kBack ? s[i] : -s[i], a * c[i]);
         x[ib] = fmaf(a, kBack ? -s[i] : s[i], b * c[i]);
     }
+}
+__device__ __forceinline__ void load8f2(const float* p, uint64_t* x) {
+    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
 
 template <int kLanes>
@@ -150,7 +154,7 @@ __device__ __forceinline__ void store_pair(uint16_t* p, const Place& at, const u
 }
 
 template <int kLanes, bool kInter>
-__global__ void __launch_bounds__(kBlock) qk_fwd_kernel(const QkArgs a, const Task tk) {
+__global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;   // heads per warp and pass
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
     const bool is_q = blockIdx.x < tk.blocks_q;
@@ -168,50 +172,62 @@ __global__ void __launch_bounds__(kBlock) qk_fwd_kernel(const QkArgs a, const Ta
     const int gshift = 31 - __clz(a.G), gpr = a.D >> gshift;
     const float inv_d = 1.0f / (float)a.D;
     uint32_t nx[8] = {};
-    if (in_head && from * kHeads + sub < sd.H) load_pair(in + (from * kHeads + sub) * a.D, at, nx);
-    float c[8], s[8], w[16] = {};
+    const int h0 = from * kHeads + sub;
+    const uint16_t* next = in + (int64_t)h0 * a.D;
+    if (in_head && h0 < sd.H) load_pair(next, at, nx);
+    float c[8], s[8];
+    uint64_t w[8] = {};
     load_turn(a, m, l, c, s);
     if (in_head) {
-        load8f(sd.weight + at.a, w);
-        load8f(sd.weight + at.b, w + 8);
+        load8f2(sd.weight + at.a, w);
+        load8f2(sd.weight + at.b, w + 4);
     }
-    for (int p = from; p < to; ++p) {
-        const int h = p * kHeads + sub;
+    const bool one_scale = tk.mode == kAdjacent ? a.G > 8 : tk.mode == kSplit && a.G == a.D;
+    const bool first_a = (at.a & (a.G - 1)) == 0, first_b = (at.b & (a.G - 1)) == 0;
+    int64_t hd = (row + h0) * a.D;                       // the head's place in the outputs
+    float* sc = sd.scale + (row + h0) * gpr;
+    float* rs = sd.rstd + row + h0;
+    for (int h = h0, p = from; p < to; ++p, h += kHeads) {
         const bool ok = in_head && h < sd.H;
         float x[16];
+        uint64_t x2[8], ss2 = 0ull;
         unpack(nx, x);
+        unpack2(nx, x2);
+        next += kHeads * a.D;
         if (p + 1 < to && in_head && h + kHeads < sd.H) {
-            load_pair(in + (h + kHeads) * a.D, at, nx);
+            load_pair(next, at, nx);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) nx[e] = 0u;
         }
-        float ss = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        ss = head_sum<kLanes>(ss);
-        const float r = __frcp_rn(__fsqrt_rn(fmaf(ss, inv_d, a.eps)));
+        for (int e = 0; e < 8; ++e) ss2 = fma2(x2[e], x2[e], ss2);
+        const float ss = head_sum<kLanes>(sum2(ss2));
+        const float r = rsqrt_newton(fmaf(ss, inv_d, a.eps));
         float ma = max_of<0, 8>(x), mb = max_of<8, 8>(x);
         group_maxima(ma, mb, tk.mode, kLanes, l, base, a);
-        const Scale sa = scale_of_bf16_max(ma), sb = scale_of_bf16_max(mb);
+        const Scale sa = scale_of_bf16_max(ma);
+        Scale sb = sa;
+        if (!one_scale) sb = scale_of_bf16_max(mb);
         uint32_t q[4], o[8];
         encode<0, 8>(x, sa, q);
         encode<8, 8>(x, sb, q);
-        float y[16];
+        const uint64_t r2 = pk(r, r);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = x[e] * r * w[e];
-        turn<kInter, false>(c, s, y);
-        pack(y, o);
+        for (int e = 0; e < 8; ++e) upk(mul2(mul2(x2[e], r2), w[e]), x[2 * e], x[2 * e + 1]);
+        turn<kInter, false>(c, s, x);
+        pack(x, o);
         if (ok) {
-            const int64_t hd = (row + h) * a.D;
             store_pair(sd.out + hd, at, o);
             *reinterpret_cast<uint2*>(sd.codes + hd + at.a) = make_uint2(q[0], q[1]);
             *reinterpret_cast<uint2*>(sd.codes + hd + at.b) = make_uint2(q[2], q[3]);
-            float* sc = sd.scale + (row + h) * gpr;
-            if ((at.a & (a.G - 1)) == 0) sc[at.a >> gshift] = sa.S;
-            if ((at.b & (a.G - 1)) == 0) sc[at.b >> gshift] = sb.S;
-            if (l == 0) sd.rstd[row + h] = r;
+            if (first_a) sc[at.a >> gshift] = sa.S;
+            if (first_b) sc[at.b >> gshift] = sb.S;
+            if (l == 0) *rs = r;
         }
+        hd += kHeads * a.D;
+        sc += kHeads * gpr;
+        rs += kHeads;
     }
 }
 
@@ -229,64 +245,79 @@ __global__ void __launch_bounds__(kBlock, 2) qk_bwd_kernel(const QkArgs a, const
     const Place at = place_of(l, a.rot, kInter);
     const int gshift = 31 - __clz(a.G), gpr = a.D >> gshift;
     const float inv_d = 1.0f / (float)a.D;
-    float w[16] = {}, dw[16] = {};
+    uint64_t w[8] = {}, dw2[8] = {};
     if (in_head) {
-        load8f(sd.weight + at.a, w);
-        load8f(sd.weight + at.b, w + 8);
+        load8f2(sd.weight + at.a, w);
+        load8f2(sd.weight + at.b, w + 4);
     }
     for (int64_t t = first * kWarps + warp; t < a.M * parts; t += blocks * kWarps) {
         const int64_t m = t / parts;
         const int part = (int)(t - m * parts);
         const int from = (int)((int64_t)passes * part / parts), to = (int)((int64_t)passes * (part + 1) / parts);
-        const int64_t row = m * sd.H;
-        uint16_t* out = sd.out + m * sd.ld;
+        const int h0 = from * kHeads + sub;
+        const int64_t row = m * sd.H + h0;
+        const uint16_t* din = sd.in + row * a.D;
+        const uint8_t* cp = sd.codes + row * a.D;
+        const float* sc = sd.scale + row * gpr;
+        const float* rs = sd.rstd + row;
+        uint16_t* out = sd.out + m * sd.ld + (int64_t)h0 * a.D;
         uint32_t nd[8] = {}, nq[4] = {};
         float na = 0.0f, nb = 0.0f, nr = 0.0f;
         auto fetch = [&](int h) {        // one pass ahead; zeros where there is no such head
             if (in_head && h < sd.H) {
-                const int64_t hd = (row + h) * a.D;
-                load_pair(sd.in + hd, at, nd);
-                const uint2 qa = __ldg(reinterpret_cast<const uint2*>(sd.codes + hd + at.a));
-                const uint2 qb = __ldg(reinterpret_cast<const uint2*>(sd.codes + hd + at.b));
+                load_pair(din, at, nd);
+                const uint2 qa = __ldg(reinterpret_cast<const uint2*>(cp + at.a));
+                const uint2 qb = __ldg(reinterpret_cast<const uint2*>(cp + at.b));
                 nq[0] = qa.x; nq[1] = qa.y; nq[2] = qb.x; nq[3] = qb.y;
-                const float* sc = sd.scale + (row + h) * gpr;
                 na = __ldg(sc + (at.a >> gshift));
                 nb = __ldg(sc + (at.b >> gshift));
-                nr = __ldg(sd.rstd + row + h);
+                nr = __ldg(rs);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) nd[e] = 0u;
             }
+            din += kHeads * a.D;
+            cp += kHeads * a.D;
+            sc += kHeads * gpr;
+            rs += kHeads;
         };
-        fetch(from * kHeads + sub);
+        fetch(h0);
         float c[8], s[8];
         load_turn(a, m, l, c, s);
-        for (int p = from; p < to; ++p) {
-            const int h = p * kHeads + sub;
+        for (int h = h0, p = from; p < to; ++p, h += kHeads) {
             const bool ok = in_head && h < sd.H;
-            float g[16], xh[16];
+            float g[16], xf[16];
             unpack(nd, g);
-            decode(nq, xh);
-            const float r = nr, sa = na * r, sb = nb * r;
+            decode(nq, xf);
+            const float r = nr;
+            const uint64_t sa2 = pk(na * r, na * r), sb2 = pk(nb * r, nb * r);
             if (p + 1 < to) fetch(h + kHeads);
             turn<kInter, true>(c, s, g);
-            float k = 0.0f;
+            uint64_t g2[8], xh[8], k2 = 0ull;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                xh[e] *= e < 8 ? sa : sb;
-                const float d = g[e] * xh[e];
-                dw[e] += ok ? d : 0.0f;
-                g[e] *= w[e];
-                k = fmaf(g[e], xh[e], k);
+            for (int e = 0; e < 8; ++e) {
+                xh[e] = mul2(pk(xf[2 * e], xf[2 * e + 1]), e < 4 ? sa2 : sb2);
+                g2[e] = pk(g[2 * e], g[2 * e + 1]);
+                if (ok) dw2[e] = fma2(g2[e], xh[e], dw2[e]);
+                g2[e] = mul2(g2[e], w[e]);
+                k2 = fma2(g2[e], xh[e], k2);
             }
-            k = -head_sum<kLanes>(k) * inv_d;
+            const float k = -head_sum<kLanes>(sum2(k2)) * inv_d;
+            const uint64_t kk = pk(k, k), rr = pk(r, r);
             uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) g[e] = r * fmaf(xh[e], k, g[e]);
-            pack(g, o);
-            if (ok) store_pair(out + h * a.D, at, o);
+            for (int e = 0; e < 8; ++e) {
+                float lo, hi;
+                upk(mul2(fma2(xh[e], kk, g2[e]), rr), lo, hi);
+                o[e] = bf16x2(lo, hi);
+            }
+            if (ok) store_pair(out, at, o);
+            out += kHeads * a.D;
         }
     }
+    float dw[16];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) upk(dw2[e], dw[2 * e], dw[2 * e + 1]);
     dependents_may_start();
     // the block's sums: the warp's heads by shuffles, then its warps in order
 #pragma unroll
