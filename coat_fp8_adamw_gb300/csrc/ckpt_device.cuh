@@ -97,12 +97,34 @@ __device__ __forceinline__ void decode(const uint32_t (&c)[W], float (&x)[4 * W]
     }
 }
 
-// max|x| of n (even) values from x[from]
-template <int from, int n, int L>
-__device__ __forceinline__ float max_of(const float (&x)[L]) {
-    float mx = fmaxf(fabsf(x[from]), fabsf(x[from + 1]));
+// ---- pairs of float32 (each half rounds like the scalar operation) ----
+// 2 W bf16 values as W pairs
+template <int W>
+__device__ __forceinline__ void unpack2(const uint32_t (&w)[W], uint64_t (&x)[W]) {
 #pragma unroll
-    for (int e = from + 2; e < from + n; e += 2) mx = max3(mx, fabsf(x[e]), fabsf(x[e + 1]));
+    for (int i = 0; i < W; ++i) x[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    float a, b;
+    upk(v, a, b);
+    return a + b;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// max|x| of n pairs from x[from]
+template <int from, int n, int L>
+__device__ __forceinline__ float max_of(const uint64_t (&x)[L]) {
+    float mx = 0.0f;
+#pragma unroll
+    for (int e = from; e < from + n; ++e) {
+        float a, b;
+        upk(x[e], a, b);
+        mx = max3(mx, fabsf(a), fabsf(b));
+    }
     return mx;
 }
 // the maximum over `lanes` adjacent lanes (a power of two, the same for the whole warp)
@@ -112,12 +134,14 @@ __device__ __forceinline__ float lanes_max(float v, int lanes) {
 }
 
 // A group's scale, and what turns its elements into quotients: x / S is taken
-// as fma(x, inv, x e), inv + e = 1 / S to about 2^-46 (and a bias, below).
+// as fma(x, inv, x e), inv + e = 1 / S to about 2^-46 (and a bias, below).  A
+// group of zeros has S = 0 and any inv.
 struct Scale {
     float S, inv, e;
 };
+__device__ __forceinline__ void reciprocal(Scale& s) { s.inv = rcp_ftz(s.S > 0.0f ? s.S : 1.0f); }
 // Scales whose reciprocal or correction would leave the normal range: by division.
-__device__ __forceinline__ bool by_division(const Scale& q) { return !(q.S < 0x1p96f) || (q.S < 0x1p-96f && q.S > 0.0f); }
+__device__ __forceinline__ bool by_division(const Scale& q) { return q.S > 0.0f && !(q.S > 0x1p-96f && q.S < 0x1p96f); }
 
 // The scale of a group of bf16 values with maximum m: S = RN(m / 448), as the
 // product with RN(1/448) and one FMA correction from the exact remainder
@@ -138,7 +162,7 @@ __device__ __forceinline__ Scale scale_of_bf16_max(float m) {
     const float q = __fmul_rn(m, y);
     Scale s;
     s.S = fmaf(fmaf(-q, 448.0f, m), y, q);
-    s.inv = s.S > 0.0f ? rcp_approx(s.S) : 0.0f;   // a group of zeros: zero codes
+    reciprocal(s);
     const float rem = fmaf(-448.0f, s.S, m);        // 448 (m / 448 - S), exact
     const float bias = rem > 0.0f ? 0x1p-18f : rem < 0.0f ? -0x1p-18f : 0.0f;
     s.e = s.inv * (fmaf(-s.S, s.inv, 1.0f) + bias);
@@ -148,36 +172,40 @@ __device__ __forceinline__ Scale scale_of_bf16_max(float m) {
 __device__ __forceinline__ Scale scale_of_max(float m) {
     Scale s;
     s.S = __fdiv_rn(m, 448.0f);
-    s.inv = s.S > 0.0f ? rcp_approx(s.S) : 0.0f;
+    reciprocal(s);
     s.e = s.inv * fmaf(-s.S, s.inv, 1.0f);
     return s;
 }
 
-// The codes of n (a multiple of 4) elements of one group from x[from], as words from w[from / 4].
-template <int from, int n, int L>
-__device__ __forceinline__ void encode(const float (&x)[L], const Scale& q, uint32_t (&w)[L / 4]) {
-    if (by_division(q)) {
+// The codes of sixteen elements, as pairs: the first eight with scale lo, the others with hi.
+__device__ __forceinline__ void encode16(const uint64_t (&x)[8], const Scale& lo, const Scale& hi, uint32_t (&w)[4]) {
+    if (by_division(lo) || by_division(hi)) {
 #pragma unroll
-        for (int e = from; e < from + n; e += 4) {
+        for (int i = 0; i < 4; ++i) {
+            const float S = i < 2 ? lo.S : hi.S;
             uint32_t c = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c |= e4m3_code_of_quotient_exact(x[e + i], q.S) << (8 * i);
-            w[e / 4] = e4m3_canonical_zero(c);
+            for (int j = 0; j < 2; ++j) {
+                float a, b;
+                upk(x[2 * i + j], a, b);
+                if (S > 0.0f) c |= (e4m3_code_of_quotient_exact(a, S) | e4m3_code_of_quotient_exact(b, S) << 8) << (16 * j);
+            }
+            w[i] = e4m3_canonical_zero(c);
         }
         return;
     }
-    const uint64_t inv2 = pk(q.inv, q.inv), e2 = pk(q.e, q.e);
+    const uint64_t i0 = pk(lo.inv, lo.inv), e0 = pk(lo.e, lo.e), i1 = pk(hi.inv, hi.inv), e1 = pk(hi.e, hi.e);
 #pragma unroll
-    for (int e = from; e < from + n; e += 4) {
+    for (int i = 0; i < 4; ++i) {
         uint32_t c[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint64_t xx = pk(x[e + 2 * i], x[e + 2 * i + 1]);
+        for (int j = 0; j < 2; ++j) {
+            const uint64_t xx = x[2 * i + j];
             float y0, y1;
-            upk(fma2(xx, inv2, mul2(xx, e2)), y0, y1);
-            c[i] = e4m3x2(y0, y1);
+            upk(fma2(xx, i < 2 ? i0 : i1, mul2(xx, i < 2 ? e0 : e1)), y0, y1);
+            c[j] = e4m3x2(y0, y1);
         }
-        w[e / 4] = e4m3_canonical_zero(c[0] | (c[1] << 16));
+        w[i] = e4m3_canonical_zero(c[0] | (c[1] << 16));
     }
 }
 
@@ -187,8 +215,8 @@ struct Scales16 {
     Scale lo, hi;   // equal unless G = 8
 };
 template <bool kBf16>
-__device__ __forceinline__ void quantize16(const float (&x)[16], int G, Scales16& q, uint32_t (&w)[4]) {
-    const float m0 = max_of<0, 8>(x), m1 = max_of<8, 8>(x);
+__device__ __forceinline__ void quantize16(const uint64_t (&x)[8], int G, Scales16& q, uint32_t (&w)[4]) {
+    const float m0 = max_of<0, 4>(x), m1 = max_of<4, 4>(x);
     if (G == 8) {
         q.lo = kBf16 ? scale_of_bf16_max(m0) : scale_of_max(m0);
         q.hi = kBf16 ? scale_of_bf16_max(m1) : scale_of_max(m1);
@@ -196,8 +224,7 @@ __device__ __forceinline__ void quantize16(const float (&x)[16], int G, Scales16
         const float m = lanes_max(fmaxf(m0, m1), G >> 4);
         q.lo = q.hi = kBf16 ? scale_of_bf16_max(m) : scale_of_max(m);
     }
-    encode<0, 8>(x, q.lo, w);
-    encode<8, 8>(x, q.hi, w);
+    encode16(x, q.lo, q.hi, w);
 }
 // Stores the scales of the sixteen elements from flat index `at`.
 __device__ __forceinline__ void store_scales16(float* scale, int64_t at, int G, int gshift, const Scales16& q) {
@@ -229,23 +256,8 @@ __device__ __forceinline__ float rsqrt_newton(float v) {
     return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
 }
 
-// ---- pairs of float32 (each half rounds like the scalar operation) ----
-// 2 W bf16 values as W pairs
-template <int W>
-__device__ __forceinline__ void unpack2(const uint32_t (&w)[W], uint64_t (&x)[W]) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
-}
-__device__ __forceinline__ float sum2(uint64_t v) {
-    float a, b;
-    upk(v, a, b);
-    return a + b;
-}
-
 // sigmoid(x) = 1 / (1 + 2^(-x log2 e)); x -> -inf gives 0, +inf gives 1.
-__device__ __forceinline__ float sigmoid(float x) {
-    return __fdividef(1.0f, 1.0f + ex2_ftz(-1.4426950408889634f * x));
-}
+__device__ __forceinline__ float sigmoid(float x) { return rcp_ftz(1.0f + ex2_ftz(-1.4426950408889634f * x)); }
 
 }  // namespace ckpt
 }  // namespace coat

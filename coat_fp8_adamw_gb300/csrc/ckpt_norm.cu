@@ -37,6 +37,7 @@ struct Shape {
     int N, depth;          // iterations in the ring
     uint32_t stage;        // bytes of one
     uint32_t b_off, c_off; // of its second and third tensor
+    int span;              // the power of two that a team's warps are rounded up to
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -46,14 +47,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // Each team's sum of v over its threads; a barrier of the whole block.
-// slots: one float per warp, for this use alone until the next one's barrier.
-__device__ __forceinline__ float team_sum(float v, float* slots, int warps, int warp, int lane) {
+// slots: one float per warp, for this use alone until the next one's barrier;
+// `span`: the power of two that the team's warps are rounded up to.
+__device__ __forceinline__ float team_sum(float v, float* slots, int warps, int span, int warp, int lane) {
     v = warp_sum(v);
     if (lane == 0) slots[warp] = v;
     __syncthreads();
     if (warps == 1) return v;
-    const float s = lane < warps ? slots[lane] : 0.0f;
-    return warp_sum(s);
+    const int i = lane & (span - 1);
+    float s = i < warps ? slots[i] : 0.0f;
+    for (int off = span >> 1; off > 0; off >>= 1) s += __shfl_xor_sync(kFull, s, off);
+    return s;
 }
 
 // The weights in shared memory: float4 j of the n / 4 of item i at [j items + i], so that
@@ -113,25 +117,27 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_kernel(const NormFwdArgs a, 
         const bool ok = in_row && r < a.M;
         if (!mbar_wait_fast(bar0 + 8u * (uint32_t)s, ph, nullptr)) break;
         const unsigned char* st = ring + (size_t)s * sh.stage + ((size_t)team * N + col) * 2;
-        float x[kE] = {};
-        float ss = 0.0f;
+        uint64_t x[kE / 2] = {}, ss2 = 0ull;
         if (ok) {
             uint32_t u[8];
             read8(st, u);
-            unpack(u, x);
+            unpack2(u, x);
             if constexpr (kRes) {
-                float p[kE];
+                uint64_t p[kE / 2];
                 read8(st + sh.b_off, u);
-                unpack(u, p);
+                unpack2(u, p);
 #pragma unroll
-                for (int e = 0; e < kE; ++e) x[e] += p[e];
-                pack(x, u);
-                unpack(u, x);
+                for (int e = 0; e < kE / 2; ++e) {
+                    float lo, hi;
+                    upk(add2(x[e], p[e]), lo, hi);
+                    u[e] = bf16x2(lo, hi);
+                }
+                unpack2(u, x);
                 store_words8(a.h + at, wide, u);
             }
         }
 #pragma unroll
-        for (int e = 0; e < kE; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < kE / 2; ++e) ss2 = fma2(x[e], x[e], ss2);
         Scales16 q;
         uint32_t c[4];
         quantize16<true>(x, a.G, q, c);
@@ -139,7 +145,7 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_kernel(const NormFwdArgs a, 
             *reinterpret_cast<uint4*>(a.q + at) = make_uint4(c[0], c[1], c[2], c[3]);
             store_scales16(a.scale, at, a.G, gshift, q);
         }
-        ss = team_sum(ss, slots[it & 1] + team * warps, warps, warp, lane);
+        const float ss = team_sum(sum2(ss2), slots[it & 1] + team * warps, warps, sh.span, warp, lane);
         // behind that barrier every thread has read the iteration's rows: its stage is free
         if (threadIdx.x == 0 && r0 + depth * step < a.M) issue(r0 + depth * step, s);
         const float rstd = rsqrt_newton(fmaf(ss, inv_n, a.eps));
@@ -147,9 +153,13 @@ __global__ void __launch_bounds__(1024, 1) norm_fwd_kernel(const NormFwdArgs a, 
             float w[kE];
             uint32_t u[8];
             weights_of(sw, T, t, w);
+            const uint64_t r2 = pk(rstd, rstd);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) x[e] = x[e] * rstd * w[e];
-            pack(x, u);
+            for (int e = 0; e < kE / 2; ++e) {
+                float lo, hi;
+                upk(mul2(mul2(x[e], r2), pk(w[2 * e], w[2 * e + 1])), lo, hi);
+                u[e] = bf16x2(lo, hi);
+            }
             store_words8(a.y + at, wide, u);
             if (t == 0) a.rstd[r] = rstd;
         }
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
         }
         float c0, c1;
         upk(c2, c0, c1);
-        const float c = team_sum(c0 + c1, slots[it & 1] + team * warps, warps, warp, lane) * inv_n;
+        const float c = team_sum(c0 + c1, slots[it & 1] + team * warps, warps, sh.span, warp, lane) * inv_n;
         // behind that barrier every thread is done with the iteration before this one: its stage is free
         if (threadIdx.x == 0 && it > 0) {
             const int64_t rr = r0 + (depth - 1) * step;
@@ -316,7 +326,9 @@ constexpr size_t kSmem = 227u << 10;   // shared memory per SM, and at most per 
 Shape shape_of(int64_t N, int room, int b0, int b1, int b2) {
     const int T = 32 * (int)((N + 32 * kE - 1) / (32 * kE)), teams = T >= room ? 1 : room / T;
     const uint32_t n = (uint32_t)(teams * N);
-    Shape sh{T, teams, (int)N, 3, (uint32_t)(b0 + b1 + b2) * n, (uint32_t)b0 * n, (uint32_t)(b0 + b1) * n};
+    Shape sh{T, teams, (int)N, 3, (uint32_t)(b0 + b1 + b2) * n, (uint32_t)b0 * n, (uint32_t)(b0 + b1) * n, 1};
+    sh.span = 1;
+    while (32 * sh.span < T) sh.span *= 2;
     // three iterations deep (two or four were slower), two where a row is too wide
     while (sh.depth > 2 && (size_t)T * kE * 4 + (size_t)sh.depth * sh.stage + 2048 > kSmem) --sh.depth;
     return sh;

@@ -189,9 +189,7 @@ __global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const
     float* rs = sd.rstd + row + h0;
     for (int h = h0, p = from; p < to; ++p, h += kHeads) {
         const bool ok = in_head && h < sd.H;
-        float x[16];
         uint64_t x2[8], ss2 = 0ull;
-        unpack(nx, x);
         unpack2(nx, x2);
         next += kHeads * a.D;
         if (p + 1 < to && in_head && h + kHeads < sd.H) {
@@ -204,14 +202,14 @@ __global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const
         for (int e = 0; e < 8; ++e) ss2 = fma2(x2[e], x2[e], ss2);
         const float ss = head_sum<kLanes>(sum2(ss2));
         const float r = rsqrt_newton(fmaf(ss, inv_d, a.eps));
-        float ma = max_of<0, 8>(x), mb = max_of<8, 8>(x);
+        float ma = max_of<0, 4>(x2), mb = max_of<4, 4>(x2);
         group_maxima(ma, mb, tk.mode, kLanes, l, base, a);
         const Scale sa = scale_of_bf16_max(ma);
         Scale sb = sa;
         if (!one_scale) sb = scale_of_bf16_max(mb);
         uint32_t q[4], o[8];
-        encode<0, 8>(x, sa, q);
-        encode<8, 8>(x, sb, q);
+        encode16(x2, sa, sb, q);
+        float x[16];
         const uint64_t r2 = pk(r, r);
 #pragma unroll
         for (int e = 0; e < 8; ++e) upk(mul2(mul2(x2[e], r2), w[e]), x[2 * e], x[2 * e + 1]);
@@ -374,11 +372,11 @@ int mode_of(const QkArgs& a) {
     return kMixed;
 }
 
-// Warps that share a token's heads: about four passes each, so that the angles serve several heads; more of them while
+// Warps that share a token's heads: about eight passes each, so that the angles serve several heads; more of them while
 // there are too few tokens to give every SM sixteen warps.
 int parts_of(int64_t M, int H, int lanes, int sms) {
     const int passes = (H * lanes + 31) / 32;
-    int parts = (passes + 3) / 4;
+    int parts = (passes + 7) / 8;
     while (parts < passes && M * parts < (int64_t)sms * 16) parts *= 2;
     return parts < passes ? parts : (passes > 0 ? passes : 1);
 }

@@ -62,18 +62,22 @@ __global__ void __launch_bounds__(kBlock) swiglu_fwd_kernel(const SwigluFwdArgs 
         load_words8(a.gate + at, wide, gv);
         load_words8(a.up + at, wide, uv);
     }
-    float g[16], u[16], h[16];
-    unpack(gv, g);
-    unpack(uv, u);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) h[e] = g[e] * sigmoid(g[e]) * u[e];
-    Scales16 sg, su;
+    uint64_t g2[8], u2[8];
     uint32_t cg[4], cu[4], hv[8];
-    quantize16<true>(g, a.G, sg, cg);
-    quantize16<true>(u, a.G, su, cu);
+    unpack2(gv, g2);
+    unpack2(uv, u2);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        float ga, gb, ha, hb;
+        upk(g2[e], ga, gb);
+        upk(mul2(mul2(g2[e], pk(sigmoid(ga), sigmoid(gb))), u2[e]), ha, hb);
+        hv[e] = bf16x2(ha, hb);
+    }
+    Scales16 sg, su;
+    quantize16<true>(g2, a.G, sg, cg);
+    quantize16<true>(u2, a.G, su, cu);
     if (!ok) return;
     const int64_t at = (int64_t)i * 16;
-    pack(h, hv);
     store_words8(a.h + at, wide, hv);
     *reinterpret_cast<uint4*>(a.gate_q + at) = make_uint4(cg[0], cg[1], cg[2], cg[3]);
     *reinterpret_cast<uint4*>(a.up_q + at) = make_uint4(cu[0], cu[1], cu[2], cu[3]);
@@ -96,26 +100,31 @@ __global__ void __launch_bounds__(kBlock) swiglu_bwd_kernel(const SwigluBwdArgs 
         load_scales16(a.gate_scale, at, a.G, gshift, Sg[0], Sg[1]);
         load_scales16(a.up_scale, at, a.G, gshift, Su[0], Su[1]);
     }
-    float d[16], g[16], u[16], h[16];
-    unpack(dv, d);
-    decode(gq, g);
-    decode(uq, u);
+    uint64_t d[8], h[8];
+    float gf[16], uf[16];
+    uint32_t wg[8], wu[8];
+    unpack2(dv, d);
+    decode(gq, gf);
+    decode(uq, uf);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        g[e] *= Sg[e >> 3];
-        u[e] *= Su[e >> 3];
-        const float s = sigmoid(g[e]), gs = g[e] * s;
-        h[e] = gs * u[e];
-        u[e] = d[e] * u[e] * fmaf(gs, 1.0f - s, s);   // d gate
-        g[e] = d[e] * gs;                             // d up
+    for (int e = 0; e < 8; ++e) {
+        const uint64_t g = mul2(pk(gf[2 * e], gf[2 * e + 1]), pk(Sg[e >> 2], Sg[e >> 2]));
+        const uint64_t u = mul2(pk(uf[2 * e], uf[2 * e + 1]), pk(Su[e >> 2], Su[e >> 2]));
+        float ga, gb, x, y;
+        upk(g, ga, gb);
+        const float sa = sigmoid(ga), sb = sigmoid(gb);
+        const uint64_t s = pk(sa, sb), gs = mul2(g, s);
+        h[e] = mul2(gs, u);
+        upk(mul2(d[e], gs), x, y);
+        wu[e] = bf16x2(x, y);
+        // d u (s + g s (1 - s))
+        upk(mul2(mul2(d[e], u), fma2(gs, pk(1.0f - sa, 1.0f - sb), s)), x, y);
+        wg[e] = bf16x2(x, y);
     }
     if (ok) {
         const int64_t to = strided_at(i, nc, a.ld);
-        uint32_t w[8];
-        pack(u, w);
-        store_words8(a.dgate + to, wide, w);
-        pack(g, w);
-        store_words8(a.dup + to, wide, w);
+        store_words8(a.dgate + to, wide, wg);
+        store_words8(a.dup + to, wide, wu);
     }
     if constexpr (kH) {
         Scales16 sh;
