@@ -10,12 +10,8 @@
 // Sums and every value between input and output are float32; y, h, dx and dw
 // are rounded once, to the bf16 tensors that the caller asks for.
 //
-// A row is held by a team of T = 32 ceil(N / 512) threads, sixteen elements each; a
-// block has as many teams as fit 512 threads (forward) or 256, and walks the rows,
-// so many consecutive ones at a time.  They come through a ring in shared memory, two
-// to four iterations deep, each tensor's rows one bulk copy: the copies stay
-// ahead without registers, of which the sums for dw need many.  The weights stay
-// in shared memory too.
+// A row is held by a team of T = 32 ceil(N / 512) threads, sixteen elements each;
+// a block has as many teams as fit 256 threads.
 #include <cstdint>
 
 #include "ckpt_device.cuh"
@@ -77,97 +73,75 @@ __device__ __forceinline__ void weights_of(const float4* sw, int items, int i, f
     }
 }
 
-// Forward: a thread has sixteen consecutive elements, so that a group of G >= 16 is G / 16 lanes.
-template <bool kRes>
-__global__ void __launch_bounds__(1024, 1) norm_fwd_kernel(const NormFwdArgs a, const Shape sh, bool wide) {
-    __shared__ float slots[2][kMaxWarps];
-    __shared__ uint64_t bars[kMaxDepth];
-    extern __shared__ __align__(16) unsigned char dyn[];
-    const int T = sh.T, teams = sh.teams, N = sh.N, depth = sh.depth;
-    float4* sw = reinterpret_cast<float4*>(dyn);
-    unsigned char* ring = dyn + (size_t)T * kE * 4;
+// Forward: a block has its rows once, a thread sixteen consecutive elements (so that a
+// group of G >= 16 is G / 16 lanes).  What keeps the memory busy are many small
+// blocks per SM in different phases: at 8192 x 4096 with a residual 47.4 us with
+// 40 registers (six blocks of 256 threads per SM), 51.0 with 50 (four); blocks
+// that walk the rows through a ring of bulk copies, as backward, took 53.3.
+template <bool kRes, int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const NormFwdArgs a, const Shape sh, bool wide) {
+    __shared__ float slots[kMaxWarps];
+    const int T = sh.T, teams = sh.teams, N = sh.N;
     const int team = threadIdx.x / T, t = threadIdx.x - team * T;
     const int lane = threadIdx.x & 31, warps = T >> 5, warp = t >> 5;
     const int gshift = 31 - __clz(a.G);
     const float inv_n = 1.0f / (float)N;
     const int col = t * kE;
-    const bool in_row = col < N;    // N % 16 == 0: all sixteen or none
-    const uint32_t bar0 = smem_u32(bars), ring0 = smem_u32(ring);
-    const int64_t step = (int64_t)gridDim.x * teams, first = (int64_t)blockIdx.x * teams;
-    auto issue = [&](int64_t r0, int s) {
-        const int64_t left = a.M - r0;
-        const uint32_t n = 2u * (uint32_t)(left < teams ? left : teams) * (uint32_t)N;
-        const uint32_t d = ring0 + (uint32_t)s * sh.stage, bar = bar0 + 8u * (uint32_t)s;
-        mbar_expect_tx(bar, kRes ? 2 * n : n);
-        bulk_load(d, a.x + r0 * N, n, bar);
-        if constexpr (kRes) bulk_load(d + sh.b_off, a.residual + r0 * N, n, bar);
-    };
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < depth; ++s) mbar_init(bar0 + 8u * (uint32_t)s, 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        for (int s = 0; s < depth; ++s)
-            if (first + s * step < a.M) issue(first + s * step, s);
-    }
-    stage_weights<kE>(a.weight, N, T, sw);
-    __syncthreads();
-    int s = 0;
-    uint32_t ph = 0;
-    for (int64_t r0 = first, it = 0; r0 < a.M; r0 += step, ++it) {
-        const int64_t r = r0 + team, at = r * N + col;
-        const bool ok = in_row && r < a.M;
-        if (!mbar_wait_fast(bar0 + 8u * (uint32_t)s, ph, nullptr)) break;
-        const unsigned char* st = ring + (size_t)s * sh.stage + ((size_t)team * N + col) * 2;
-        uint64_t x[kE / 2] = {}, ss2 = 0ull;
-        if (ok) {
-            uint32_t u[8];
-            read8(st, u);
+    const int64_t r = (int64_t)blockIdx.x * teams + team, at = r * N + col;
+    const bool ok = col < N && r < a.M;
+    uint64_t x[kE / 2] = {}, ss2 = 0ull;
+    if (ok) {
+        uint32_t u[8];
+        load_words8(a.x + at, wide, u);
+        if constexpr (kRes) {
+            uint32_t v[8];
+            uint64_t p[kE / 2];
+            load_words8(a.residual + at, wide, v);
             unpack2(u, x);
-            if constexpr (kRes) {
-                uint64_t p[kE / 2];
-                read8(st + sh.b_off, u);
-                unpack2(u, p);
-#pragma unroll
-                for (int e = 0; e < kE / 2; ++e) {
-                    float lo, hi;
-                    upk(add2(x[e], p[e]), lo, hi);
-                    u[e] = bf16x2(lo, hi);
-                }
-                unpack2(u, x);
-                store_words8(a.h + at, wide, u);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < kE / 2; ++e) ss2 = fma2(x[e], x[e], ss2);
-        Scales16 q;
-        uint32_t c[4];
-        quantize16<true>(x, a.G, q, c);
-        if (ok) {
-            *reinterpret_cast<uint4*>(a.q + at) = make_uint4(c[0], c[1], c[2], c[3]);
-            store_scales16(a.scale, at, a.G, gshift, q);
-        }
-        const float ss = team_sum(sum2(ss2), slots[it & 1] + team * warps, warps, sh.span, warp, lane);
-        // behind that barrier every thread has read the iteration's rows: its stage is free
-        if (threadIdx.x == 0 && r0 + depth * step < a.M) issue(r0 + depth * step, s);
-        const float rstd = rsqrt_newton(fmaf(ss, inv_n, a.eps));
-        if (ok) {
-            float w[kE];
-            uint32_t u[8];
-            weights_of(sw, T, t, w);
-            const uint64_t r2 = pk(rstd, rstd);
+            unpack2(v, p);
 #pragma unroll
             for (int e = 0; e < kE / 2; ++e) {
                 float lo, hi;
-                upk(mul2(mul2(x[e], r2), pk(w[2 * e], w[2 * e + 1])), lo, hi);
+                upk(add2(x[e], p[e]), lo, hi);
                 u[e] = bf16x2(lo, hi);
             }
-            store_words8(a.y + at, wide, u);
-            if (t == 0) a.rstd[r] = rstd;
+            store_words8(a.h + at, wide, u);
         }
-        if (++s == depth) { s = 0; ph ^= 1u; }
+        unpack2(u, x);
+    }
+#pragma unroll
+    for (int e = 0; e < kE / 2; ++e) ss2 = fma2(x[e], x[e], ss2);
+    Scales16 q;
+    uint32_t c[4];
+    quantize16<true>(x, a.G, q, c);
+    if (ok) {
+        *reinterpret_cast<uint4*>(a.q + at) = make_uint4(c[0], c[1], c[2], c[3]);
+        store_scales16(a.scale, at, a.G, gshift, q);
+    }
+    const float ss = team_sum(sum2(ss2), slots + team * warps, warps, sh.span, warp, lane);
+    const float rstd = rsqrt_newton(fmaf(ss, inv_n, a.eps));
+    if (ok) {
+        uint32_t u[8];
+        const uint64_t r2 = pk(rstd, rstd);
+        const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(a.weight + col);
+#pragma unroll
+        for (int e = 0; e < kE / 4; ++e) {
+            const ulonglong2 w = __ldg(wp + e);
+            float lo, hi;
+            upk(mul2(mul2(x[2 * e], r2), w.x), lo, hi);
+            u[2 * e] = bf16x2(lo, hi);
+            upk(mul2(mul2(x[2 * e + 1], r2), w.y), lo, hi);
+            u[2 * e + 1] = bf16x2(lo, hi);
+        }
+        store_words8(a.y + at, wide, u);
+        if (t == 0) a.rstd[r] = rstd;
     }
 }
 
-// Backward: a thread has two chunks of eight columns, T chunks apart, so that
+// Backward: the blocks walk the rows, so many consecutive ones at a time as they
+// have teams, with the sums for dw in registers.  The rows come through a ring in
+// shared memory, each tensor's one bulk copy: the copies stay ahead without
+// registers.  A thread has two chunks of eight columns, T chunks apart, so that
 // neighbouring lanes read neighbouring 16 bytes of shared memory.  kThreads: most
 // threads of a block (512 leave 128 registers, enough for a row's elements;
 // with 1024, N > 8192, some of them wait in local memory).
@@ -321,19 +295,24 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const ColumnSum first,
 
 constexpr size_t kSmem = 227u << 10;   // shared memory per SM, and at most per block
 
-// room: threads of a block that its teams share.  b0 ..: the widths (bytes per element) of the tensors of a stage, in the
-// order in which they lie there.
-Shape shape_of(int64_t N, int room, int b0, int b1, int b2) {
-    const int T = 32 * (int)((N + 32 * kE - 1) / (32 * kE)), teams = T >= room ? 1 : room / T;
-    const uint32_t n = (uint32_t)(teams * N);
-    Shape sh{T, teams, (int)N, 3, (uint32_t)(b0 + b1 + b2) * n, (uint32_t)b0 * n, (uint32_t)(b0 + b1) * n, 1};
-    sh.span = 1;
+Shape team_shape(int64_t N) {
+    const int T = 32 * (int)((N + 32 * kE - 1) / (32 * kE)), teams = T >= 256 ? 1 : 256 / T;
+    Shape sh{T, teams, (int)N, 0, 0, 0, 0, 1};
     while (32 * sh.span < T) sh.span *= 2;
-    // three iterations deep (two or four were slower), two where a row is too wide
-    while (sh.depth > 2 && (size_t)T * kE * 4 + (size_t)sh.depth * sh.stage + 2048 > kSmem) --sh.depth;
     return sh;
 }
 size_t smem_of(const Shape& sh) { return (size_t)sh.T * kE * 4 + (size_t)sh.depth * sh.stage; }
+Shape bwd_shape(int64_t N, bool res) {
+    Shape sh = team_shape(N);
+    const uint32_t n = (uint32_t)(sh.teams * N);
+    sh.stage = res ? 5 * n : 3 * n;
+    sh.b_off = 2 * n;
+    sh.c_off = 3 * n;
+    // iterations in the ring: 8192 x 4096 takes 58 us with two, 44 with three or four; fewer where a row is too wide
+    sh.depth = 3;
+    while (sh.depth > 2 && smem_of(sh) + 2048 > kSmem) --sh.depth;
+    return sh;
+}
 // Blocks that run at once: by threads (`regs` of 64 K registers each) and by shared memory (2 KB more per block: the
 // static part, and the system's).
 int64_t blocks_of(int64_t M, const Shape& sh, int regs, int sms) {
@@ -344,7 +323,6 @@ int64_t blocks_of(int64_t M, const Shape& sh, int regs, int sms) {
     const int64_t need = (M + sh.teams - 1) / sh.teams;
     return need < sms * per ? need : sms * per;
 }
-Shape bwd_shape(int64_t N, bool res) { return shape_of(N, 256, 2, 1, res ? 2 : 0); }
 int64_t bwd_blocks(int64_t M, int64_t N, bool res, int sms) { return blocks_of(M, bwd_shape(N, res), 96, sms); }
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
@@ -358,13 +336,16 @@ cudaError_t allow_smem(F* kernel, size_t bytes) {
 
 template <bool kRes>
 cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
-    // two rows of 4096 per block: 52.8 us at 8192 rows with a residual, 55.8 with one
-    const Shape sh = shape_of(a.N, 512, 2, kRes ? 2 : 0, 0);
-    const unsigned blocks = (unsigned)blocks_of(a.M, sh, 64, device_sms());
-    const bool wide = aligned32(a.h) && aligned32(a.y);
-    const cudaError_t e = allow_smem(norm_fwd_kernel<kRes>, smem_of(sh));
-    if (e != cudaSuccess) return e;
-    norm_fwd_kernel<kRes><<<blocks, sh.T * sh.teams, smem_of(sh), s>>>(a, sh, wide);
+    const Shape sh = team_shape(a.N);
+    const bool wide = aligned32(a.x) && aligned32(a.residual) && aligned32(a.h) && aligned32(a.y);
+    const unsigned blocks = (unsigned)((a.M + sh.teams - 1) / sh.teams);
+    const int threads = sh.T * sh.teams;
+    if (threads <= 256)
+        norm_fwd_kernel<kRes, 256, 6><<<blocks, threads, 0, s>>>(a, sh, wide);
+    else if (threads <= 512)
+        norm_fwd_kernel<kRes, 512, 3><<<blocks, threads, 0, s>>>(a, sh, wide);
+    else
+        norm_fwd_kernel<kRes, 1024, 1><<<blocks, threads, 0, s>>>(a, sh, wide);
     return cudaGetLastError();
 }
 
