@@ -26,6 +26,8 @@
 #include "ckpt_device.cuh"
 #include "ckpt_kernels.h"
 
+#define FP 8
+#define BP 8
 namespace coat {
 
 namespace {
@@ -42,9 +44,13 @@ enum GroupMode {
     kMixed       // anything else: chunk by chunk
 };
 
+// 2^shift warps share a token's heads of one side, `passes` passes (of the warp's lanes over heads) each.
+struct Split {
+    int32_t shift, passes;
+};
 struct Task {
     int64_t blocks_q;    // blocks below: queries; the others: keys
-    int32_t parts_q, parts_k;   // warps that share a token's heads
+    Split q, k;
     int32_t mode;
 };
 
@@ -159,12 +165,12 @@ __global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
     const bool is_q = blockIdx.x < tk.blocks_q;
     const HeadSide sd = is_q ? a.q : a.k;
-    const int parts = is_q ? tk.parts_q : tk.parts_k;
+    const Split sp = is_q ? tk.q : tk.k;
     const int64_t t = (int64_t)(blockIdx.x - (is_q ? 0 : tk.blocks_q)) * kWarps + (threadIdx.x >> 5);
-    const int64_t m = t / parts;
+    const int64_t m = t >> sp.shift;
     if (m >= a.M) return;
-    const int part = (int)(t - m * parts), passes = (sd.H + kHeads - 1) / kHeads;
-    const int from = (int)((int64_t)passes * part / parts), to = (int)((int64_t)passes * (part + 1) / parts);
+    const int from = ((int)t & ((1 << sp.shift) - 1)) * sp.passes;
+    const int to = min(from + sp.passes, (sd.H + kHeads - 1) / kHeads);
     const bool in_head = l * 16 < a.D;
     const Place at = place_of(l, a.rot, kInter);
     const uint16_t* in = sd.in + m * sd.ld;
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(kBlock, 2) qk_bwd_kernel(const QkArgs a, const
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), sub = lane / kLanes, warp = threadIdx.x >> 5;
     const bool is_q = blockIdx.x < tk.blocks_q;
     const HeadSide sd = is_q ? a.q : a.k;
-    const int parts = is_q ? tk.parts_q : tk.parts_k;
+    const Split sp = is_q ? tk.q : tk.k;
     const int64_t first = blockIdx.x - (is_q ? 0 : tk.blocks_q), blocks = is_q ? tk.blocks_q : gridDim.x - tk.blocks_q;
     const int passes = (sd.H + kHeads - 1) / kHeads;
     const bool in_head = l * 16 < a.D;
@@ -248,10 +254,9 @@ __global__ void __launch_bounds__(kBlock, 2) qk_bwd_kernel(const QkArgs a, const
         load8f2(sd.weight + at.a, w);
         load8f2(sd.weight + at.b, w + 4);
     }
-    for (int64_t t = first * kWarps + warp; t < a.M * parts; t += blocks * kWarps) {
-        const int64_t m = t / parts;
-        const int part = (int)(t - m * parts);
-        const int from = (int)((int64_t)passes * part / parts), to = (int)((int64_t)passes * (part + 1) / parts);
+    for (int64_t t = first * kWarps + warp; t < a.M << sp.shift; t += blocks * kWarps) {
+        const int64_t m = t >> sp.shift;
+        const int from = ((int)t & ((1 << sp.shift) - 1)) * sp.passes, to = min(from + sp.passes, passes);
         const int h0 = from * kHeads + sub;
         const int64_t row = m * sd.H + h0;
         const uint16_t* din = sd.in + row * a.D;
@@ -372,13 +377,16 @@ int mode_of(const QkArgs& a) {
     return kMixed;
 }
 
-// Warps that share a token's heads: about eight passes each, so that the angles serve several heads; more of them while
-// there are too few tokens to give every SM sixteen warps.
-int parts_of(int64_t M, int H, int lanes, int sms) {
+// About `most` passes each, so that the angles serve several heads; more warps per token while there are too few
+// tokens to give every SM sixteen warps.
+Split split_of(int64_t M, int H, int lanes, int most, int sms) {
     const int passes = (H * lanes + 31) / 32;
-    int parts = (passes + 7) / 8;
-    while (parts < passes && M * parts < (int64_t)sms * 16) parts *= 2;
-    return parts < passes ? parts : (passes > 0 ? passes : 1);
+    Split sp{0, passes};
+    while (sp.passes > 1 && (sp.passes > most || (M << sp.shift) < (int64_t)sms * 16)) {
+        ++sp.shift;
+        sp.passes = (passes + (1 << sp.shift) - 1) >> sp.shift;
+    }
+    return sp;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -392,20 +400,20 @@ int64_t qk_bwd_partials(int64_t M, int sms) {
 
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t s) {
     const int sms = device_sms(), lanes = lanes_of(a.D);
-    Task tk{0, parts_of(a.M, a.q.H, lanes, sms), parts_of(a.M, a.k.H, lanes, sms), mode_of(a)};
-    tk.blocks_q = a.q.H > 0 ? ceil_div(a.M * tk.parts_q, kWarps) : 0;
-    const int64_t blocks_k = a.k.H > 0 ? ceil_div(a.M * tk.parts_k, kWarps) : 0;
+    Task tk{0, split_of(a.M, a.q.H, lanes, FP, sms), split_of(a.M, a.k.H, lanes, FP, sms), mode_of(a)};
+    tk.blocks_q = a.q.H > 0 ? ceil_div(a.M << tk.q.shift, kWarps) : 0;
+    const int64_t blocks_k = a.k.H > 0 ? ceil_div(a.M << tk.k.shift, kWarps) : 0;
     if (tk.blocks_q + blocks_k >= (1LL << 31)) return cudaErrorInvalidValue;
     return launch_any(a, tk, false, tk.blocks_q + blocks_k, s);
 }
 
 cudaError_t launch_qk_bwd(const QkArgs& a, cudaStream_t s) {
     const int sms = device_sms(), lanes = lanes_of(a.D), H = a.q.H + a.k.H;
-    Task tk{0, parts_of(a.M, a.q.H, lanes, sms), parts_of(a.M, a.k.H, lanes, sms), mode_of(a)};
+    Task tk{0, split_of(a.M, a.q.H, lanes, BP, sms), split_of(a.M, a.k.H, lanes, BP, sms), mode_of(a)};
     // two blocks per SM, shared between the sides as their heads are, one at least where there are any
     const int64_t room = (int64_t)sms * 2;
     int64_t bq = a.q.H > 0 ? room * a.q.H / H : 0, bk = a.k.H > 0 ? room - bq : 0;
-    const int64_t need_q = ceil_div(a.M * tk.parts_q, kWarps), need_k = ceil_div(a.M * tk.parts_k, kWarps);
+    const int64_t need_q = ceil_div(a.M << tk.q.shift, kWarps), need_k = ceil_div(a.M << tk.k.shift, kWarps);
     bq = a.q.H > 0 ? (bq < 1 ? 1 : bq > need_q ? need_q : bq) : 0;
     bk = a.k.H > 0 ? (bk < 1 ? 1 : bk > need_k ? need_k : bk) : 0;
     tk.blocks_q = bq;
