@@ -180,18 +180,20 @@ __device__ __forceinline__ Scale scale_of_max(float m) {
 // The codes of sixteen elements, as pairs: the first eight with scale lo, the others with hi.
 __device__ __forceinline__ void encode16(const uint64_t (&x)[8], const Scale& lo, const Scale& hi, uint32_t (&w)[4]) {
     if (by_division(lo) || by_division(hi)) {
+        // one element at a time, in a loop over local memory: nothing of it is held in registers, and no function is
+        // called, which would cost every other path registers as well
+        float t[16];
+        uint32_t c[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float S = i < 2 ? lo.S : hi.S;
-            uint32_t c = 0u;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float a, b;
-                upk(x[2 * i + j], a, b);
-                if (S > 0.0f) c |= (e4m3_code_of_quotient_exact(a, S) | e4m3_code_of_quotient_exact(b, S) << 8) << (16 * j);
-            }
-            w[i] = e4m3_canonical_zero(c);
+        for (int i = 0; i < 8; ++i) upk(x[i], t[2 * i], t[2 * i + 1]);
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i) {
+            const float S = i < 8 ? lo.S : hi.S;
+            c[i] = S > 0.0f ? e4m3x2(__fadd_rn(e4m3_quotient(t[i], S), 0.0f), 0.0f) & 0xFFu : 0u;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = e4m3_canonical_zero(c[4 * i] | c[4 * i + 1] << 8 | c[4 * i + 2] << 16 | c[4 * i + 3] << 24);
         return;
     }
     const uint64_t i0 = pk(lo.inv, lo.inv), e0 = pk(lo.e, lo.e), i1 = pk(hi.inv, hi.inv), e1 = pk(hi.e, hi.e);

@@ -26,6 +26,10 @@
 #include "ckpt_device.cuh"
 #include "ckpt_kernels.h"
 
+#define FB 9
+#define FT 64
+#define BT 64
+#define BB 8
 #define FP 8
 #define BP 8
 namespace coat {
@@ -34,8 +38,10 @@ namespace {
 
 using namespace ckpt;
 
-constexpr int kBlock = 256;
+constexpr int kBlock = BT;             // threads of a block, backward
 constexpr int kWarps = kBlock / 32;
+constexpr int kFwdBlock = FT;          // forward
+constexpr int kFwdWarps = kFwdBlock / 32;
 
 // How a group's maximum is found.
 enum GroupMode {
@@ -84,16 +90,34 @@ __device__ __forceinline__ void load_turn(const QkArgs& a, int64_t m, int l, flo
     }
 }
 
-// x[0..7], x[8..15]: the two chunks.  Turned by the angles, or back by them.  (Lanes behind rot hold entries that do not
-// pair: their angle is 0.)
+// A lane's sixteen entries as pairs, chunk after chunk.  The partner of pair e's entries: the pair of the other chunk
+// (split), or the pair itself, swapped (interleaved).
+template <bool kInter>
+__device__ __forceinline__ uint64_t partner(const uint64_t (&x)[8], int e) {
+    if (!kInter) return x[e ^ 4];
+    float lo, hi;
+    upk(x[e], lo, hi);
+    return pk(hi, lo);
+}
+// The turn by the angles as out = x own + partner(x) other, the factors in the entries' order.  w: the entries' weights,
+// folded in (ones backward); kBack: the angles' signs turned.  (Lanes behind rot hold entries that do not pair: their
+// angle is 0.)
 template <bool kInter, bool kBack>
-__device__ __forceinline__ void turn(const float (&c)[8], const float (&s)[8], float (&x)[16]) {
+__device__ __forceinline__ void turn_factors(const float (&c)[8], const float (&s)[8], const float (&w)[16], uint64_t (&own)[8],
+                                             uint64_t (&other)[8]) {
+    float o[16], p[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int ia = kInter ? 2 * i : i, ib = kInter ? 2 * i + 1 : i + 8;
-        const float a = x[ia], b = x[ib];
-        x[ia] = fmaf(b, kBack ? s[i] : -s[i], a * c[i]);
-        x[ib] = fmaf(a, kBack ? -s[i] : s[i], b * c[i]);
+        o[ia] = w[ia] * c[i];
+        o[ib] = w[ib] * c[i];
+        p[ia] = kBack ? w[ib] * s[i] : -(w[ib] * s[i]);
+        p[ib] = kBack ? -(w[ia] * s[i]) : w[ia] * s[i];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        own[e] = pk(o[2 * e], o[2 * e + 1]);
+        other[e] = pk(p[2 * e], p[2 * e + 1]);
     }
 }
 __device__ __forceinline__ void load8f2(const float* p, uint64_t* x) {
@@ -159,14 +183,29 @@ __device__ __forceinline__ void store_pair(uint16_t* p, const Place& at, const u
     *reinterpret_cast<uint4*>(p + at.b) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+// What a lane will need in the next passes, copied into its own place in shared
+// memory asynchronously: three passes on their way without registers.
+constexpr int kRing = 4;
+template <int n>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (n == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but this thread's last kRing - 1 groups have landed
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory"); }
+
 template <int kLanes, bool kInter>
-__global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const Task tk) {
+__global__ void __launch_bounds__(kFwdBlock, FB) qk_fwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;   // heads per warp and pass
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
     const bool is_q = blockIdx.x < tk.blocks_q;
     const HeadSide sd = is_q ? a.q : a.k;
     const Split sp = is_q ? tk.q : tk.k;
-    const int64_t t = (int64_t)(blockIdx.x - (is_q ? 0 : tk.blocks_q)) * kWarps + (threadIdx.x >> 5);
+    const int64_t t = (int64_t)(blockIdx.x - (is_q ? 0 : tk.blocks_q)) * kFwdWarps + (threadIdx.x >> 5);
     const int64_t m = t >> sp.shift;
     if (m >= a.M) return;
     const int from = ((int)t & ((1 << sp.shift) - 1)) * sp.passes;
@@ -177,32 +216,44 @@ __global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const
     const int64_t row = m * sd.H;         // head 0 of this token
     const int gshift = 31 - __clz(a.G), gpr = a.D >> gshift;
     const float inv_d = 1.0f / (float)a.D;
-    uint32_t nx[8] = {};
+    __shared__ uint4 ring[kRing][2][kFwdBlock];
     const int h0 = from * kHeads + sub;
     const uint16_t* next = in + (int64_t)h0 * a.D;
-    if (in_head && h0 < sd.H) load_pair(next, at, nx);
-    float c[8], s[8];
-    uint64_t w[8] = {};
-    load_turn(a, m, l, c, s);
-    if (in_head) {
-        load8f2(sd.weight + at.a, w);
-        load8f2(sd.weight + at.b, w + 4);
+    auto fetch = [&](int i) {                            // pass from + i, if there is one
+        if (from + i < to && in_head && h0 + i * kHeads < sd.H) {
+            cp_async<16>(&ring[i & (kRing - 1)][0][threadIdx.x], next + at.a);
+            cp_async<16>(&ring[i & (kRing - 1)][1][threadIdx.x], next + at.b);
+        }
+        cp_async_commit();
+        next += kHeads * a.D;
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) fetch(i);
+    uint64_t own[8], other[8];
+    {
+        float c[8], s[8], w[16] = {};
+        load_turn(a, m, l, c, s);
+        if (in_head) {
+            load8f(sd.weight + at.a, w);
+            load8f(sd.weight + at.b, w + 8);
+        }
+        turn_factors<kInter, false>(c, s, w, own, other);
     }
     const bool one_scale = tk.mode == kAdjacent ? a.G > 8 : tk.mode == kSplit && a.G == a.D;
     const bool first_a = (at.a & (a.G - 1)) == 0, first_b = (at.b & (a.G - 1)) == 0;
     int64_t hd = (row + h0) * a.D;                       // the head's place in the outputs
     float* sc = sd.scale + (row + h0) * gpr;
     float* rs = sd.rstd + row + h0;
-    for (int h = h0, p = from; p < to; ++p, h += kHeads) {
+    for (int i = 0, h = h0; from + i < to; ++i, h += kHeads) {
         const bool ok = in_head && h < sd.H;
-        uint64_t x2[8], ss2 = 0ull;
-        unpack2(nx, x2);
-        next += kHeads * a.D;
-        if (p + 1 < to && in_head && h + kHeads < sd.H) {
-            load_pair(next, at, nx);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) nx[e] = 0u;
+        fetch(i + kRing - 1);
+        cp_async_wait();
+        uint64_t x2[8] = {}, ss2 = 0ull;
+        if (ok) {
+            const uint4* src = &ring[i & (kRing - 1)][0][threadIdx.x];
+            const uint4 lo = src[0], hi = src[kFwdBlock];
+            const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            unpack2(u, x2);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss2 = fma2(x2[e], x2[e], ss2);
@@ -215,12 +266,13 @@ __global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const
         if (!one_scale) sb = scale_of_bf16_max(mb);
         uint32_t q[4], o[8];
         encode16(x2, sa, sb, q);
-        float x[16];
         const uint64_t r2 = pk(r, r);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) upk(mul2(mul2(x2[e], r2), w[e]), x[2 * e], x[2 * e + 1]);
-        turn<kInter, false>(c, s, x);
-        pack(x, o);
+        for (int e = 0; e < 8; ++e) {
+            float lo, hi;
+            upk(mul2(fma2(partner<kInter>(x2, e), other[e], mul2(x2[e], own[e])), r2), lo, hi);
+            o[e] = bf16x2(lo, hi);
+        }
         if (ok) {
             store_pair(sd.out + hd, at, o);
             *reinterpret_cast<uint2*>(sd.codes + hd + at.a) = make_uint2(q[0], q[1]);
@@ -235,9 +287,16 @@ __global__ void __launch_bounds__(kBlock, 3) qk_fwd_kernel(const QkArgs a, const
     }
 }
 
+struct BwdRing {
+    uint4 dy[kRing][2][kBlock];
+    uint2 q[kRing][2][kBlock];
+    float s[kRing][3][kBlock];     // the chunks' scales, and 1 / rms
+};
+
 template <int kLanes, bool kInter>
-__global__ void __launch_bounds__(kBlock, 2) qk_bwd_kernel(const QkArgs a, const Task tk) {
+__global__ void __launch_bounds__(kBlock, BB) qk_bwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;
+    __shared__ BwdRing ring;
     __shared__ float part_sum[kWarps][16 * kLanes];
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), sub = lane / kLanes, warp = threadIdx.x >> 5;
     const bool is_q = blockIdx.x < tk.blocks_q;
@@ -264,43 +323,58 @@ __global__ void __launch_bounds__(kBlock, 2) qk_bwd_kernel(const QkArgs a, const
         const float* sc = sd.scale + row * gpr;
         const float* rs = sd.rstd + row;
         uint16_t* out = sd.out + m * sd.ld + (int64_t)h0 * a.D;
-        uint32_t nd[8] = {}, nq[4] = {};
-        float na = 0.0f, nb = 0.0f, nr = 0.0f;
-        auto fetch = [&](int h) {        // one pass ahead; zeros where there is no such head
-            if (in_head && h < sd.H) {
-                load_pair(din, at, nd);
-                const uint2 qa = __ldg(reinterpret_cast<const uint2*>(cp + at.a));
-                const uint2 qb = __ldg(reinterpret_cast<const uint2*>(cp + at.b));
-                nq[0] = qa.x; nq[1] = qa.y; nq[2] = qb.x; nq[3] = qb.y;
-                na = __ldg(sc + (at.a >> gshift));
-                nb = __ldg(sc + (at.b >> gshift));
-                nr = __ldg(rs);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) nd[e] = 0u;
+        // (every lane is done with its own ring, and nothing else reads it)
+        auto fetch = [&](int i) {                            // pass from + i, if there is one
+            if (from + i < to && in_head && h0 + i * kHeads < sd.H) {
+                const int u = i & (kRing - 1);
+                cp_async<16>(&ring.dy[u][0][threadIdx.x], din + at.a);
+                cp_async<16>(&ring.dy[u][1][threadIdx.x], din + at.b);
+                cp_async<8>(&ring.q[u][0][threadIdx.x], cp + at.a);
+                cp_async<8>(&ring.q[u][1][threadIdx.x], cp + at.b);
+                cp_async<4>(&ring.s[u][0][threadIdx.x], sc + (at.a >> gshift));
+                cp_async<4>(&ring.s[u][1][threadIdx.x], sc + (at.b >> gshift));
+                cp_async<4>(&ring.s[u][2][threadIdx.x], rs);
             }
+            cp_async_commit();
             din += kHeads * a.D;
             cp += kHeads * a.D;
             sc += kHeads * gpr;
             rs += kHeads;
         };
-        fetch(h0);
-        float c[8], s[8];
-        load_turn(a, m, l, c, s);
-        for (int h = h0, p = from; p < to; ++p, h += kHeads) {
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) fetch(i);
+        uint64_t own[8], other[8];
+        {
+            float c[8], s[8], one[16];
+            load_turn(a, m, l, c, s);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) one[e] = 1.0f;
+            turn_factors<kInter, true>(c, s, one, own, other);
+        }
+        for (int i = 0, h = h0; from + i < to; ++i, h += kHeads) {
             const bool ok = in_head && h < sd.H;
-            float g[16], xf[16];
-            unpack(nd, g);
+            fetch(i + kRing - 1);
+            cp_async_wait();
+            float xf[16], r = 0.0f, sa = 0.0f, sb = 0.0f;
+            uint64_t d2[8] = {}, g2[8], xh[8], k2 = 0ull;
+            uint32_t nq[4] = {};
+            if (ok) {
+                const int u = i & (kRing - 1);
+                const uint4 lo = ring.dy[u][0][threadIdx.x], hi = ring.dy[u][1][threadIdx.x];
+                const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                unpack2(v, d2);
+                const uint2 qa = ring.q[u][0][threadIdx.x], qb = ring.q[u][1][threadIdx.x];
+                nq[0] = qa.x; nq[1] = qa.y; nq[2] = qb.x; nq[3] = qb.y;
+                r = ring.s[u][2][threadIdx.x];
+                sa = ring.s[u][0][threadIdx.x] * r;
+                sb = ring.s[u][1][threadIdx.x] * r;
+            }
             decode(nq, xf);
-            const float r = nr;
-            const uint64_t sa2 = pk(na * r, na * r), sb2 = pk(nb * r, nb * r);
-            if (p + 1 < to) fetch(h + kHeads);
-            turn<kInter, true>(c, s, g);
-            uint64_t g2[8], xh[8], k2 = 0ull;
+            const uint64_t sa2 = pk(sa, sa), sb2 = pk(sb, sb);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 xh[e] = mul2(pk(xf[2 * e], xf[2 * e + 1]), e < 4 ? sa2 : sb2);
-                g2[e] = pk(g[2 * e], g[2 * e + 1]);
+                g2[e] = fma2(partner<kInter>(d2, e), other[e], mul2(d2[e], own[e]));
                 if (ok) dw2[e] = fma2(g2[e], xh[e], dw2[e]);
                 g2[e] = mul2(g2[e], w[e]);
                 k2 = fma2(g2[e], xh[e], k2);
@@ -349,7 +423,7 @@ cudaError_t launch(const QkArgs& a, const Task& tk, bool back, int64_t blocks, c
     if (back)
         qk_bwd_kernel<kLanes, kInter><<<(unsigned)blocks, kBlock, 0, s>>>(a, tk);
     else
-        qk_fwd_kernel<kLanes, kInter><<<(unsigned)blocks, kBlock, 0, s>>>(a, tk);
+        qk_fwd_kernel<kLanes, kInter><<<(unsigned)blocks, kFwdBlock, 0, s>>>(a, tk);
     return cudaGetLastError();
 }
 template <int kLanes>
@@ -395,14 +469,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int64_t qk_bwd_partials(int64_t M, int sms) {
     (void)M;
-    return (int64_t)sms * 2 + 2;
+    return (int64_t)sms * BB + 2;
 }
 
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t s) {
     const int sms = device_sms(), lanes = lanes_of(a.D);
     Task tk{0, split_of(a.M, a.q.H, lanes, FP, sms), split_of(a.M, a.k.H, lanes, FP, sms), mode_of(a)};
-    tk.blocks_q = a.q.H > 0 ? ceil_div(a.M << tk.q.shift, kWarps) : 0;
-    const int64_t blocks_k = a.k.H > 0 ? ceil_div(a.M << tk.k.shift, kWarps) : 0;
+    tk.blocks_q = a.q.H > 0 ? ceil_div(a.M << tk.q.shift, kFwdWarps) : 0;
+    const int64_t blocks_k = a.k.H > 0 ? ceil_div(a.M << tk.k.shift, kFwdWarps) : 0;
     if (tk.blocks_q + blocks_k >= (1LL << 31)) return cudaErrorInvalidValue;
     return launch_any(a, tk, false, tk.blocks_q + blocks_k, s);
 }
@@ -411,7 +485,7 @@ cudaError_t launch_qk_bwd(const QkArgs& a, cudaStream_t s) {
     const int sms = device_sms(), lanes = lanes_of(a.D), H = a.q.H + a.k.H;
     Task tk{0, split_of(a.M, a.q.H, lanes, BP, sms), split_of(a.M, a.k.H, lanes, BP, sms), mode_of(a)};
     // two blocks per SM, shared between the sides as their heads are, one at least where there are any
-    const int64_t room = (int64_t)sms * 2;
+    const int64_t room = (int64_t)sms * BB;
     int64_t bq = a.q.H > 0 ? room * a.q.H / H : 0, bk = a.k.H > 0 ? room - bq : 0;
     const int64_t need_q = ceil_div(a.M << tk.q.shift, kWarps), need_k = ceil_div(a.M << tk.k.shift, kWarps);
     bq = a.q.H > 0 ? (bq < 1 ? 1 : bq > need_q ? need_q : bq) : 0;
