@@ -184,7 +184,7 @@ coat_status coat_qk_norm_rope_ckpt(const uint16_t* q, int64_t q_ld, int32_t Hq, 
 size_t coat_qk_norm_rope_ckpt_backward_workspace_bytes(int64_t M, int32_t D) {
     if (M < 1 || M >= (1LL << 31) || D < 16 || D > 256 || D % 16 != 0) return 0;
     const int sms = coat::device_sms();
-    return sms > 0 ? 4 * (size_t)coat::qk_bwd_partials(M, sms) * (size_t)D : 0;
+    return sms > 0 ? 4 * (size_t)coat::qk_bwd_partials(sms) * (size_t)D : 0;
 }
 
 coat_status coat_qk_norm_rope_ckpt_backward(const uint16_t* dq_out, const uint16_t* dk_out, const uint8_t* q_codes,

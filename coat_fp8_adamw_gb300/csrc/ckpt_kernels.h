@@ -106,7 +106,7 @@ constexpr int64_t kNormMaxN = 16384;   // columns of a normalised row
 
 int device_sms();
 int64_t norm_bwd_partials(int64_t M, int64_t N, int sms);
-int64_t qk_bwd_partials(int64_t M, int sms);
+int64_t qk_bwd_partials(int sms);
 size_t wgrad_workspace(int64_t M, int64_t N, int64_t K, int sms);
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s);

@@ -268,29 +268,36 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
         }
 }
 
-// 32 columns of one of two sums per block; its 32 warps take every 32nd row of the partial sums, four loads on their
-// way each
+// kCols columns of one of two sums per block, 1024 / kCols rows of the partial sums side by side and four more on their
+// way in each thread.  32 columns read whole lines; 8 give four times the blocks, which is what few columns need.
+template <int kCols>
 __global__ void __launch_bounds__(1024) column_sum_kernel(const ColumnSum first, const ColumnSum second, int64_t N) {
-    __shared__ float part[32][33];
+    constexpr int kRows = 1024 / kCols;
+    __shared__ float part[kCols][kRows + 1];
     const ColumnSum cs = blockIdx.y == 0 ? first : second;
-    const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int col = threadIdx.x % kCols, row = threadIdx.x / kCols;
+    const int64_t c = (int64_t)blockIdx.x * kCols + col;
     if (cs.P == 0) return;
     wait_for_primary();
     float s = 0.0f;
     if (c < N) {
         int64_t p = row;
-        for (; p + 96 < cs.P; p += 128) {
-            const float v0 = cs.partial[p * N + c], v1 = cs.partial[(p + 32) * N + c];
-            const float v2 = cs.partial[(p + 64) * N + c], v3 = cs.partial[(p + 96) * N + c];
+        for (; p + 3 * kRows < cs.P; p += 4 * kRows) {
+            const float v0 = cs.partial[p * N + c], v1 = cs.partial[(p + kRows) * N + c];
+            const float v2 = cs.partial[(p + 2 * kRows) * N + c], v3 = cs.partial[(p + 3 * kRows) * N + c];
             s += (v0 + v1) + (v2 + v3);
         }
-        for (; p < cs.P; p += 32) s += cs.partial[p * N + c];
+        for (; p < cs.P; p += kRows) s += cs.partial[p * N + c];
     }
-    part[row][lane] = s;
+    part[col][row] = s;
     __syncthreads();
-    s = warp_sum(part[lane][row]);   // this warp's column `row` of the block
-    if (lane == 0 && (int64_t)blockIdx.x * 32 + row < N) cs.out[(int64_t)blockIdx.x * 32 + row] = bf16_bits(s);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= kCols) return;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; i += 32) s += part[warp][lane + i];
+    s = warp_sum(s);
+    if (lane == 0 && (int64_t)blockIdx.x * kCols + warp < N) cs.out[(int64_t)blockIdx.x * kCols + warp] = bf16_bits(s);
 }
 
 constexpr size_t kSmem = 227u << 10;   // shared memory per SM, and at most per block
@@ -380,12 +387,14 @@ cudaError_t launch_column_sums(const ColumnSum& first, const ColumnSum& second, 
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((N + 31) / 32), second.P > 0 ? 2 : 1);
+    const int cols = N <= 512 ? 8 : 32;
+    cfg.gridDim = dim3((unsigned)((N + cols - 1) / cols), second.P > 0 ? 2 : 1);
     cfg.blockDim = dim3(1024);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, column_sum_kernel, first, second, N);
+    return cols == 8 ? cudaLaunchKernelEx(&cfg, column_sum_kernel<8>, first, second, N)
+                     : cudaLaunchKernelEx(&cfg, column_sum_kernel<32>, first, second, N);
 }
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s) {

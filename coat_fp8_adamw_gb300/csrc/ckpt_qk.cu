@@ -17,31 +17,38 @@
 // shuffles.  The chunks are chosen so that both entries of a pair are in one
 // thread: lane l < rot / 16 has entries 8 l and rot / 2 + 8 l onwards when the
 // pairs are split, and every other lane 16 l onwards.  Eight cosines and
-// sines per lane then serve all heads of a token, and stay in registers.  A
-// warp takes one token and some of the heads of its queries or of its keys; a
-// block works for one of the two sides, so that a lane has one set of weights
-// and, backward, of sums for dw.
+// sines per lane then serve all heads of a token, and stay in registers as
+// factors of an entry and of its partner.  A block works for one of the two
+// sides, so that a lane has one set of weights and, backward, of sums for dw.
+// Forward a warp takes one token's heads of its side, or a share of them;
+// backward, where blocks have to stay for their sums, the passes over the
+// tokens' heads go to the warps in equal ranges.
+//
+// Both directions are bound by memory in the long run (time per further token:
+// 95 % of the copy rate forward, 86 to 93 % backward) and are sensitive to two
+// things.  Registers: three blocks of 256 threads with 80 registers, some of
+// them in local memory, took 61.6 us forward at 8192 tokens x 64 heads x 128
+// where nine of 64 threads take 55.1.  And the balance of the warps' work: equal
+// ranges of passes instead of tokens brought 4101 tokens x 50 heads x 128
+// backward from 35.9 to 31.1 us, of which about 8 are the start of two kernels.
 #include <cstdint>
 
 #include "ckpt_device.cuh"
 #include "ckpt_kernels.h"
 
-#define FB 9
-#define FT 64
-#define BT 64
-#define BB 8
-#define FP 8
-#define BP 8
 namespace coat {
 
 namespace {
 
 using namespace ckpt;
 
-constexpr int kBlock = BT;             // threads of a block, backward
-constexpr int kWarps = kBlock / 32;
-constexpr int kFwdBlock = FT;          // forward
+constexpr int kFwdBlock = 64;          // threads of a block, forward
 constexpr int kFwdWarps = kFwdBlock / 32;
+constexpr int kFwdPerSm = 9;           // blocks that the registers allow
+constexpr int kFwdPasses = 8;          // passes over heads that a warp makes for a token at most
+constexpr int kBlock = 128;            // backward
+constexpr int kWarps = kBlock / 32;
+constexpr int kPerSm = 3;
 
 // How a group's maximum is found.
 enum GroupMode {
@@ -50,7 +57,7 @@ enum GroupMode {
     kMixed       // anything else: chunk by chunk
 };
 
-// 2^shift warps share a token's heads of one side, `passes` passes (of the warp's lanes over heads) each.
+// Forward: 2^shift warps share a token's heads of one side, `passes` passes (of the warp's lanes over heads) each.
 struct Split {
     int32_t shift, passes;
 };
@@ -171,13 +178,6 @@ __device__ __forceinline__ void group_maxima(float& ma, float& mb, int mode, int
     mb = __uint_as_float(wb << 16);
 }
 
-__device__ __forceinline__ void load_pair(const uint16_t* p, const Place& at, uint32_t (&w)[8]) {
-    uint32_t lo[4], hi[4];
-    load_words<4>(p + at.a, lo);
-    load_words<4>(p + at.b, hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { w[i] = lo[i]; w[4 + i] = hi[i]; }
-}
 __device__ __forceinline__ void store_pair(uint16_t* p, const Place& at, const uint32_t (&w)[8]) {
     *reinterpret_cast<uint4*>(p + at.a) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(p + at.b) = make_uint4(w[4], w[5], w[6], w[7]);
@@ -195,11 +195,19 @@ __device__ __forceinline__ void cp_async(void* dst, const void* src) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(src), "n"(n) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// all but this thread's last kRing - 1 groups have landed
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory"); }
+// all but this thread's last n groups have landed, 1 <= n <= 3
+__device__ __forceinline__ void cp_async_wait(int n) {
+    if (n == 3)
+        asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (n == 2)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+static_assert(kRing == 4, "cp_async_wait");
 
 template <int kLanes, bool kInter>
-__global__ void __launch_bounds__(kFwdBlock, FB) qk_fwd_kernel(const QkArgs a, const Task tk) {
+__global__ void __launch_bounds__(kFwdBlock, kFwdPerSm) qk_fwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;   // heads per warp and pass
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
     const bool is_q = blockIdx.x < tk.blocks_q;
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(kFwdBlock, FB) qk_fwd_kernel(const QkArgs a, c
     for (int i = 0, h = h0; from + i < to; ++i, h += kHeads) {
         const bool ok = in_head && h < sd.H;
         fetch(i + kRing - 1);
-        cp_async_wait();
+        cp_async_wait(kRing - 1);
         uint64_t x2[8] = {}, ss2 = 0ull;
         if (ok) {
             const uint4* src = &ring[i & (kRing - 1)][0][threadIdx.x];
@@ -287,116 +295,167 @@ __global__ void __launch_bounds__(kFwdBlock, FB) qk_fwd_kernel(const QkArgs a, c
     }
 }
 
-struct BwdRing {
+// A lane's ring, and the angles of its token and of the next one.
+struct BwdShared {
     uint4 dy[kRing][2][kBlock];
     uint2 q[kRing][2][kBlock];
     float s[kRing][3][kBlock];     // the chunks' scales, and 1 / rms
+    float4 angle[2][4][kBlock];    // eight cosines, eight sines
 };
 
+// The passes of a side's tokens, in order, go to its warps in equal ranges.
 template <int kLanes, bool kInter>
-__global__ void __launch_bounds__(kBlock, BB) qk_bwd_kernel(const QkArgs a, const Task tk) {
+__global__ void __launch_bounds__(kBlock, kPerSm) qk_bwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;
-    __shared__ BwdRing ring;
+    __shared__ BwdShared sh;
     __shared__ float part_sum[kWarps][16 * kLanes];
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), sub = lane / kLanes, warp = threadIdx.x >> 5;
     const bool is_q = blockIdx.x < tk.blocks_q;
     const HeadSide sd = is_q ? a.q : a.k;
-    const Split sp = is_q ? tk.q : tk.k;
-    const int64_t first = blockIdx.x - (is_q ? 0 : tk.blocks_q), blocks = is_q ? tk.blocks_q : gridDim.x - tk.blocks_q;
+    const int64_t blocks = is_q ? tk.blocks_q : gridDim.x - tk.blocks_q;
+    const int64_t me = (int64_t)(blockIdx.x - (is_q ? 0 : tk.blocks_q)) * kWarps + warp;
     const int passes = (sd.H + kHeads - 1) / kHeads;
-    const bool in_head = l * 16 < a.D;
+    const bool in_head = l * 16 < a.D, turned = l * 16 < a.rot;
     const Place at = place_of(l, a.rot, kInter);
-    const int gshift = 31 - __clz(a.G), gpr = a.D >> gshift;
+    const int gshift = 31 - __clz(a.G), to_b = at.b - at.a;
     const float inv_d = 1.0f / (float)a.D;
     uint64_t w[8] = {}, dw2[8] = {};
     if (in_head) {
         load8f2(sd.weight + at.a, w);
         load8f2(sd.weight + at.b, w + 4);
     }
-    for (int64_t t = first * kWarps + warp; t < a.M << sp.shift; t += blocks * kWarps) {
-        const int64_t m = t >> sp.shift;
-        const int from = ((int)t & ((1 << sp.shift) - 1)) * sp.passes, to = min(from + sp.passes, passes);
-        const int h0 = from * kHeads + sub;
-        const int64_t row = m * sd.H + h0;
-        const uint16_t* din = sd.in + row * a.D;
-        const uint8_t* cp = sd.codes + row * a.D;
-        const float* sc = sd.scale + row * gpr;
-        const float* rs = sd.rstd + row;
-        uint16_t* out = sd.out + m * sd.ld + (int64_t)h0 * a.D;
-        // (every lane is done with its own ring, and nothing else reads it)
-        auto fetch = [&](int i) {                            // pass from + i, if there is one
-            if (from + i < to && in_head && h0 + i * kHeads < sd.H) {
-                const int u = i & (kRing - 1);
-                cp_async<16>(&ring.dy[u][0][threadIdx.x], din + at.a);
-                cp_async<16>(&ring.dy[u][1][threadIdx.x], din + at.b);
-                cp_async<8>(&ring.q[u][0][threadIdx.x], cp + at.a);
-                cp_async<8>(&ring.q[u][1][threadIdx.x], cp + at.b);
-                cp_async<4>(&ring.s[u][0][threadIdx.x], sc + (at.a >> gshift));
-                cp_async<4>(&ring.s[u][1][threadIdx.x], sc + (at.b >> gshift));
-                cp_async<4>(&ring.s[u][2][threadIdx.x], rs);
-            }
-            cp_async_commit();
-            din += kHeads * a.D;
-            cp += kHeads * a.D;
-            sc += kHeads * gpr;
-            rs += kHeads;
-        };
+    const int64_t all = a.M * passes, warps = blocks * kWarps;
+    const int64_t from = all / warps * me + min(me, all % warps);
+    int left = (int)(all / warps + (me < all % warps ? 1 : 0));          // passes to do, and to fetch
+    int fetches = left;
+    int64_t m = from / passes;
+    int p = (int)(from - m * passes), fp = p;
+    const int last = (passes - 1) * kHeads;
+    int64_t frow = m * sd.H + p * kHeads + sub;                          // the row (token, head) that is fetched next
+    uint16_t* out = sd.out + m * sd.ld + (int64_t)(p * kHeads + sub) * a.D + at.a;
+    // A token's angles come with its first pass; fetched are at most as many passes ahead as a token has, so that there
+    // are never more than two tokens' angles.
+    const int ahead = min(kRing - 1, passes);
+    auto position = [&](int64_t t) { return turned && t < a.M ? (int64_t)__ldg(a.positions + t) : (int64_t)-1; };
+    int64_t fm = m, pos = left > 0 ? position(m) : -1;
+    uint32_t known = 0u, place = 0u, fplace = 0u;     // known: a bit per place: the position is in the tables
+    bool fresh = true;
+    auto fetch = [&](int u) {
+        if (fetches > 0) {
+            if (fresh) {
+                const bool in = pos >= 0 && pos < a.max_pos;
+                if (in) {
+                    const int64_t t = pos * (a.rot / 2) + 8 * l;
 #pragma unroll
-        for (int i = 0; i < kRing - 1; ++i) fetch(i);
-        uint64_t own[8], other[8];
-        {
+                    for (int i = 0; i < 2; ++i) {
+                        cp_async<16>(&sh.angle[fplace][i][threadIdx.x], a.cos + t + 4 * i);
+                        cp_async<16>(&sh.angle[fplace][i + 2][threadIdx.x], a.sin + t + 4 * i);
+                    }
+                }
+                known = (known & ~(1u << fplace)) | ((in ? 1u : 0u) << fplace);
+                pos = position(++fm);
+                fplace ^= 1u;
+                fresh = false;
+            }
+            if (in_head && fp * kHeads + sub < sd.H) {
+                const int64_t off = frow * a.D + at.a;
+                cp_async<16>(&sh.dy[u][0][threadIdx.x], sd.in + off);
+                cp_async<16>(&sh.dy[u][1][threadIdx.x], sd.in + off + to_b);
+                cp_async<8>(&sh.q[u][0][threadIdx.x], sd.codes + off);
+                cp_async<8>(&sh.q[u][1][threadIdx.x], sd.codes + off + to_b);
+                cp_async<4>(&sh.s[u][0][threadIdx.x], sd.scale + (off >> gshift));
+                cp_async<4>(&sh.s[u][1][threadIdx.x], sd.scale + ((off + to_b) >> gshift));
+                cp_async<4>(&sh.s[u][2][threadIdx.x], sd.rstd + frow);
+            }
+            --fetches;
+            frow += kHeads;
+            if (++fp == passes) {
+                fp = 0;
+                frow += sd.H - last - kHeads;
+                fresh = true;
+            }
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i < ahead; ++i) fetch(i);
+    uint64_t own[8], other[8];
+    bool begins = true;
+    for (int u = 0; left > 0; --left, u = (u + 1) & (kRing - 1)) {
+        fetch((u + ahead) & (kRing - 1));
+        cp_async_wait(ahead);
+        if (begins) {
+            begins = false;
             float c[8], s[8], one[16];
-            load_turn(a, m, l, c, s);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) { c[e] = 1.0f; s[e] = 0.0f; }
+            if (turned) {
+                if ((known >> place) & 1u) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 cv = sh.angle[place][i][threadIdx.x], sv = sh.angle[place][i + 2][threadIdx.x];
+                        c[4 * i] = cv.x; c[4 * i + 1] = cv.y; c[4 * i + 2] = cv.z; c[4 * i + 3] = cv.w;
+                        s[4 * i] = sv.x; s[4 * i + 1] = sv.y; s[4 * i + 2] = sv.z; s[4 * i + 3] = sv.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) c[e] = s[e] = __uint_as_float(0x7FC00000u);
+                }
+            }
+            place ^= 1u;
 #pragma unroll
             for (int e = 0; e < 16; ++e) one[e] = 1.0f;
             turn_factors<kInter, true>(c, s, one, own, other);
         }
-        for (int i = 0, h = h0; from + i < to; ++i, h += kHeads) {
-            const bool ok = in_head && h < sd.H;
-            fetch(i + kRing - 1);
-            cp_async_wait();
-            float xf[16], r = 0.0f, sa = 0.0f, sb = 0.0f;
-            uint64_t d2[8] = {}, g2[8], xh[8], k2 = 0ull;
-            uint32_t nq[4] = {};
-            if (ok) {
-                const int u = i & (kRing - 1);
-                const uint4 lo = ring.dy[u][0][threadIdx.x], hi = ring.dy[u][1][threadIdx.x];
-                const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-                unpack2(v, d2);
-                const uint2 qa = ring.q[u][0][threadIdx.x], qb = ring.q[u][1][threadIdx.x];
-                nq[0] = qa.x; nq[1] = qa.y; nq[2] = qb.x; nq[3] = qb.y;
-                r = ring.s[u][2][threadIdx.x];
-                sa = ring.s[u][0][threadIdx.x] * r;
-                sb = ring.s[u][1][threadIdx.x] * r;
-            }
-            decode(nq, xf);
-            const uint64_t sa2 = pk(sa, sa), sb2 = pk(sb, sb);
+        const bool ok = in_head && p * kHeads + sub < sd.H;
+        float xf[16], r = 0.0f, sa = 0.0f, sb = 0.0f;
+        uint64_t d2[8] = {}, g2[8], xh[8], k2 = 0ull;
+        uint32_t nq[4] = {};
+        if (ok) {
+            const uint4 lo = sh.dy[u][0][threadIdx.x], hi = sh.dy[u][1][threadIdx.x];
+            const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            unpack2(v, d2);
+            const uint2 qa = sh.q[u][0][threadIdx.x], qb = sh.q[u][1][threadIdx.x];
+            nq[0] = qa.x; nq[1] = qa.y; nq[2] = qb.x; nq[3] = qb.y;
+            r = sh.s[u][2][threadIdx.x];
+            sa = sh.s[u][0][threadIdx.x] * r;
+            sb = sh.s[u][1][threadIdx.x] * r;
+        }
+        decode(nq, xf);
+        const uint64_t sa2 = pk(sa, sa), sb2 = pk(sb, sb);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[e] = mul2(pk(xf[2 * e], xf[2 * e + 1]), e < 4 ? sa2 : sb2);
-                g2[e] = fma2(partner<kInter>(d2, e), other[e], mul2(d2[e], own[e]));
-                if (ok) dw2[e] = fma2(g2[e], xh[e], dw2[e]);
-                g2[e] = mul2(g2[e], w[e]);
-                k2 = fma2(g2[e], xh[e], k2);
-            }
-            const float k = -head_sum<kLanes>(sum2(k2)) * inv_d;
-            const uint64_t kk = pk(k, k), rr = pk(r, r);
-            uint32_t o[8];
+        for (int e = 0; e < 8; ++e) {
+            xh[e] = mul2(pk(xf[2 * e], xf[2 * e + 1]), e < 4 ? sa2 : sb2);
+            g2[e] = fma2(partner<kInter>(d2, e), other[e], mul2(d2[e], own[e]));
+            if (ok) dw2[e] = fma2(g2[e], xh[e], dw2[e]);
+            g2[e] = mul2(g2[e], w[e]);
+            k2 = fma2(g2[e], xh[e], k2);
+        }
+        const float k = -head_sum<kLanes>(sum2(k2)) * inv_d;
+        const uint64_t kk = pk(k, k), rr = pk(r, r);
+        uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float lo, hi;
-                upk(mul2(fma2(xh[e], kk, g2[e]), rr), lo, hi);
-                o[e] = bf16x2(lo, hi);
-            }
-            if (ok) store_pair(out, at, o);
-            out += kHeads * a.D;
+        for (int e = 0; e < 8; ++e) {
+            float lo, hi;
+            upk(mul2(fma2(xh[e], kk, g2[e]), rr), lo, hi);
+            o[e] = bf16x2(lo, hi);
+        }
+        if (ok) {
+            *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(out + to_b) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        out += kHeads * a.D;
+        if (++p == passes) {
+            p = 0;
+            out += sd.ld - (int64_t)(last + kHeads) * a.D;
+            begins = true;
         }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    dependents_may_start();
+    // the block's sums: the warp's heads by shuffles, then its warps in order
     float dw[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) upk(dw2[e], dw[2 * e], dw[2 * e + 1]);
-    dependents_may_start();
-    // the block's sums: the warp's heads by shuffles, then its warps in order
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
 #pragma unroll
@@ -413,7 +472,7 @@ __global__ void __launch_bounds__(kBlock, BB) qk_bwd_kernel(const QkArgs a, cons
     for (int i = threadIdx.x; i < a.D; i += kBlock) {
         float v = 0.0f;
 #pragma unroll
-        for (int p = 0; p < kWarps; ++p) v += part_sum[p][i];
+        for (int p2 = 0; p2 < kWarps; ++p2) v += part_sum[p2][i];
         a.partial[(int64_t)blockIdx.x * a.D + i] = v;
     }
 }
@@ -451,12 +510,12 @@ int mode_of(const QkArgs& a) {
     return kMixed;
 }
 
-// About `most` passes each, so that the angles serve several heads; more warps per token while there are too few
+// At most kFwdPasses passes each, so that the angles serve several heads; more warps per token while there are too few
 // tokens to give every SM sixteen warps.
-Split split_of(int64_t M, int H, int lanes, int most, int sms) {
+Split split_of(int64_t M, int H, int lanes, int sms) {
     const int passes = (H * lanes + 31) / 32;
     Split sp{0, passes};
-    while (sp.passes > 1 && (sp.passes > most || (M << sp.shift) < (int64_t)sms * 16)) {
+    while (sp.passes > 1 && (sp.passes > kFwdPasses || (M << sp.shift) < (int64_t)sms * 16)) {
         ++sp.shift;
         sp.passes = (passes + (1 << sp.shift) - 1) >> sp.shift;
     }
@@ -467,14 +526,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-int64_t qk_bwd_partials(int64_t M, int sms) {
-    (void)M;
-    return (int64_t)sms * BB + 2;
-}
+int64_t qk_bwd_partials(int sms) { return (int64_t)sms * kPerSm + 2; }
 
 cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t s) {
     const int sms = device_sms(), lanes = lanes_of(a.D);
-    Task tk{0, split_of(a.M, a.q.H, lanes, FP, sms), split_of(a.M, a.k.H, lanes, FP, sms), mode_of(a)};
+    Task tk{0, split_of(a.M, a.q.H, lanes, sms), split_of(a.M, a.k.H, lanes, sms), mode_of(a)};
     tk.blocks_q = a.q.H > 0 ? ceil_div(a.M << tk.q.shift, kFwdWarps) : 0;
     const int64_t blocks_k = a.k.H > 0 ? ceil_div(a.M << tk.k.shift, kFwdWarps) : 0;
     if (tk.blocks_q + blocks_k >= (1LL << 31)) return cudaErrorInvalidValue;
@@ -482,12 +538,12 @@ cudaError_t launch_qk_fwd(const QkArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_qk_bwd(const QkArgs& a, cudaStream_t s) {
-    const int sms = device_sms(), lanes = lanes_of(a.D), H = a.q.H + a.k.H;
-    Task tk{0, split_of(a.M, a.q.H, lanes, BP, sms), split_of(a.M, a.k.H, lanes, BP, sms), mode_of(a)};
-    // two blocks per SM, shared between the sides as their heads are, one at least where there are any
-    const int64_t room = (int64_t)sms * BB;
-    int64_t bq = a.q.H > 0 ? room * a.q.H / H : 0, bk = a.k.H > 0 ? room - bq : 0;
-    const int64_t need_q = ceil_div(a.M << tk.q.shift, kWarps), need_k = ceil_div(a.M << tk.k.shift, kWarps);
+    const int sms = device_sms(), lanes = lanes_of(a.D);
+    Task tk{0, Split{0, 0}, Split{0, 0}, mode_of(a)};
+    // as many blocks as run at once, shared between the sides as their passes are, one at least where there are heads
+    const int64_t room = (int64_t)sms * kPerSm, pq = (a.q.H * lanes + 31) / 32, pk = (a.k.H * lanes + 31) / 32;
+    int64_t bq = room * pq / (pq + pk), bk = room - bq;
+    const int64_t need_q = ceil_div(a.M * pq, kWarps), need_k = ceil_div(a.M * pk, kWarps);
     bq = a.q.H > 0 ? (bq < 1 ? 1 : bq > need_q ? need_q : bq) : 0;
     bk = a.k.H > 0 ? (bk < 1 ? 1 : bk > need_k ? need_k : bk) : 0;
     tk.blocks_q = bq;
