@@ -55,7 +55,6 @@ constexpr int kTile = 256;                     // rows (n) and columns (k) of a 
 constexpr int kHalf = kTile / 2;               // a CTA's columns k of it, and its rows n of dY
 constexpr int kTok = 64;                       // tokens per stage
 constexpr int kMmaTok = 16;                    // tokens of one kind::f16 MMA
-constexpr int kStages = 8;
 constexpr int kBoxBytes = kTok * 128;          // 64 tokens x 64 bf16 columns
 constexpr int kYBytes = 2 * kBoxBytes;         // dY: 64 tokens x 128 columns
 constexpr int kQBytes = kTok * kHalf;          // the codes
@@ -66,12 +65,16 @@ constexpr int kDeqWarps = 8;
 constexpr int kWgThreads = 32 * (4 + kEpiWarps + kDeqWarps);
 constexpr uint32_t kXCols = kTok / 2;          // tensor-memory columns of a stage of X
 constexpr uint32_t kTmemCols = 512;            // the accumulator (256) and the stages of X
-static_assert(kTile + kStages * kXCols <= kTmemCols, "tensor memory");
-constexpr int kNumBars = 4 * kStages + 3;      // dY full, codes full, X full, empty; acc full, acc empty, done
 constexpr int kMinSteps = 8;                   // fewest steps of a split's part
-constexpr int scale_bytes(int G) { return kTok * (kHalf / G) * 4; }   // of a stage
-constexpr int bar_off(int G) { return kStages * (kStageBytes + scale_bytes(G)); }
-constexpr int smem_bytes(int G) { return bar_off(G) + 8 * kNumBars + 16 + 1024; }   // + slack for 1024-B alignment
+// By group size: stages (the scales of G = 8 leave room for seven), floats between two groups' scales (four more than
+// the tokens, so that lanes that write 32 / groups tokens of every group meet different banks), and what follows.
+constexpr int stages(int G) { return G == 8 ? 7 : 8; }
+constexpr int scale_pitch(int G) { return G == kHalf ? kTok : kTok + 4; }
+constexpr int scale_bytes(int G) { return (kHalf / G) * scale_pitch(G) * 4; }   // of a stage
+constexpr int num_bars(int G) { return 4 * stages(G) + 3; }   // dY full, codes full, X full, empty; acc full, acc empty, done
+constexpr int bar_off(int G) { return stages(G) * (kStageBytes + scale_bytes(G)); }
+constexpr int smem_bytes(int G) { return bar_off(G) + 8 * num_bars(G) + 16 + 1024; }   // + slack for 1024-B alignment
+static_assert(kTile + stages(128) * kXCols <= kTmemCols && smem_bytes(8) <= 232448 && smem_bytes(16) <= 232448, "SM");
 
 // Instruction descriptor: D in f32 (bits 4-5 = 1), A and B bf16 (bits 7-9 and
 // 10-12 = 1), A as tensor memory holds it, B MN-major (bit 16), N / 8 in bits
@@ -176,8 +179,8 @@ __device__ __forceinline__ void tmem_st_16x256x2(uint32_t taddr, const uint32_t 
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-// Four codes as bf16(value * s), two to a register
-__device__ __forceinline__ void deq4(uint32_t codes, float4 s, uint32_t& r0, uint32_t& r1) {
+// Four codes as bf16(value * s), two to a register; s: the scales as two pairs
+__device__ __forceinline__ void deq4(uint32_t codes, const ulonglong2& s, uint32_t& r0, uint32_t& r1) {
     uint32_t h0, h1;
     float x0, x1, x2, x3;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((unsigned short)(codes & 0xFFFFu)));
@@ -188,12 +191,14 @@ __device__ __forceinline__ void deq4(uint32_t codes, float4 s, uint32_t& r0, uin
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
         : "=f"(x2), "=f"(x3)
         : "r"(h1));
-    r0 = bf16x2(x0 * s.x, x1 * s.y);
-    r1 = bf16x2(x2 * s.z, x3 * s.w);
+    upk(mul2(pk(x0, x1), s.x), x0, x1);
+    upk(mul2(pk(x2, x3), s.y), x2, x3);
+    r0 = bf16x2(x0, x1);
+    r1 = bf16x2(x2, x3);
 }
-__device__ __forceinline__ float4 lds128f(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+__device__ __forceinline__ ulonglong2 lds128(uint32_t a) {
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a));
     return v;
 }
 __device__ __forceinline__ void sts32(uint32_t a, float v) {
@@ -204,7 +209,9 @@ template <int G>
 __global__ void __launch_bounds__(kWgThreads, 1)
 wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CUtensorMap tmq, const WgradArgs a,
              const Plan plan) {
+    constexpr int kStages = stages(G);
     constexpr int kGroups = kHalf / G;             // scale groups of this CTA's columns
+    constexpr int kPitch = scale_pitch(G);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);   // the same offset in both CTAs
@@ -218,7 +225,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     auto empty = [&](int s) { return bar(3, s); };
     const uint32_t acc_full = bar0 + 8u * (uint32_t)(4 * kStages);
     const uint32_t acc_empty = acc_full + 8u, done = acc_full + 16u;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + bar_off(G) + 8 * kNumBars);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + bar_off(G) + 8 * num_bars(G));
     volatile uint32_t* abort = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -308,10 +315,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         }
         mbar_wait(done, 0u, nullptr);
     } else if (warp == 2 || warp == 3) {
-        // ---- scale loaders: every other step each; a lane has two tokens and all groups, loaded two of its
-        // steps ahead of their use (one where the groups are many) ----
+        // ---- scale loaders: every other step each.  A lane has one group of every 32 / groups-th token, so that a
+        // load reads the groups of a token together; loaded two of its steps ahead of their use (one where the
+        // groups are many).  The tokens' factors come from the lanes that hold two tokens each. ----
         constexpr int kDeep = kGroups > 8 ? 1 : 2;
+        constexpr int kVals = 2 * kGroups, kRows = 32 / kGroups;   // scales per lane; tokens between two of them
         const int64_t ngr = a.K / G;
+        const int grp = lane % kGroups, tok = lane / kGroups;
         int64_t ai = cid;
         Item ait = item_at(ai < items ? ai : 0, plan);
         int32_t ast = ait.from;
@@ -324,49 +334,57 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 }
             }
         };
-        auto fetch = [&](float (&f)[2][kGroups], float (&r)[2]) {
-            const int64_t g0 = (ait.k * kTile + rank * kHalf) / G;
+        auto fetch = [&](float (&f)[kVals], float (&r)[2]) {
+            const int64_t g = (ait.k * kTile + rank * kHalf) / G + grp, m0 = (int64_t)ast * kTok;
+            const bool in = ai < items && g < ngr;
+            const float* p = a.scale + (m0 + tok) * ngr + g;
+            const int64_t step = kRows * ngr;
+            if (m0 + kTok <= a.M) {                // all but the last step of all
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t m = (int64_t)ast * kTok + lane + 32 * h;
-                r[h] = 1.0f;
+                for (int i = 0; i < kVals; ++i, p += step) f[i] = in ? __ldg(p) : 0.0f;
+            } else {
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) f[h][j] = 0.0f;
-                if (ai < items && m < a.M) {
-                    if (a.row_scale) r[h] = __ldg(a.row_scale + m);
+                for (int i = 0; i < kVals; ++i, p += step) f[i] = in && m0 + tok + i * kRows < a.M ? __ldg(p) : 0.0f;
+            }
+            if (a.row_scale) {
 #pragma unroll
-                    for (int j = 0; j < kGroups; ++j)
-                        if (g0 + j < ngr) f[h][j] = __ldg(a.scale + m * ngr + g0 + j);
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t m = m0 + lane + 32 * h;
+                    r[h] = ai < items && m < a.M ? __ldg(a.row_scale + m) : 0.0f;
                 }
             }
             next();
             next();
         };
         if (warp == 3) next();
-        float f[kDeep][2][kGroups], r[kDeep][2];
-        const bool any = ai < items;
-#pragma unroll
-        for (int b = 0; b < kDeep; ++b) fetch(f[b], r[b]);
+        float f[kDeep][kVals], r[kDeep][2];
         // steps of this pair in all
         int64_t steps = 0;
         for (int64_t i = cid; i < items; i += nclusters) {
             const Item it = item_at(i, plan);
             steps += it.to - it.from;
         }
+#pragma unroll
+        for (int b = 0; b < kDeep; ++b) fetch(f[b], r[b]);
         int s = warp - 2;
         uint32_t ph = 0;
-        bool ok = any;
+        bool ok = true;
         int64_t j0 = warp - 2;
         while (ok && j0 < steps) {
 #pragma unroll
             for (int b = 0; b < kDeep; ++b) {
                 if (ok && j0 < steps) {
                     if (__all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort))) {
-                        const uint32_t d = scales0 + (uint32_t)(s * scale_bytes(G)) + 4u * (uint32_t)lane;
+                        const uint32_t d = scales0 + (uint32_t)(s * scale_bytes(G) + 4 * (grp * kPitch + tok));
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int j = 0; j < kGroups; ++j) sts32(d + (uint32_t)(4 * (kTok * j + 32 * h)), f[b][h][j] * r[b][h]);
+                        for (int i = 0; i < kVals; ++i) {
+                            float v = f[b][i];
+                            if (a.row_scale) {
+                                constexpr int kPerHalf = 32 / kRows;   // values of the first 32 tokens
+                                v *= kGroups == 1 ? r[b][i] : __shfl_sync(kFull, r[b][i / kPerHalf], tok + (i % kPerHalf) * kRows);
+                            }
+                            sts32(d + (uint32_t)(4 * i * kRows), v);
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_at(q_full(s));
                         fetch(f[b], r[b]);
@@ -456,17 +474,21 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 uint32_t q[2][4];
                 ldmatrix_bytes(sa + q_at[0], q[0]);
                 ldmatrix_bytes(sa + q_at[1], q[1]);
+                // the scales of its tokens (four of each block) for the groups of its 32 columns: one, two or four
+                constexpr int kSets = G >= 32 ? 1 : 32 / G;
+                ulonglong2 f[kSets][2];
+#pragma unroll
+                for (int j = 0; j < kSets; ++j)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) f[j][b] = lds128(ss + (uint32_t)(4 * ((32 * q4 / G + j) * kPitch + 16 * b)));
 #pragma unroll
                 for (int kh = 0; kh < 2; ++kh) {
                     uint32_t x[8];
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int g = (32 * q4 + 16 * kh + 8 * h) / G;
-                            const float4 f = lds128f(ss + (uint32_t)(4 * (kTok * g + 16 * b)));
-                            deq4(q[kh][2 * b + h], f, x[4 * b + 2 * h], x[4 * b + 2 * h + 1]);
-                        }
+                        for (int h = 0; h < 2; ++h)
+                            deq4(q[kh][2 * b + h], f[(16 * kh + 8 * h) * kSets / 32][b], x[4 * b + 2 * h], x[4 * b + 2 * h + 1]);
                     tmem_st_16x256x2(x_at + (uint32_t)s * kXCols + ((uint32_t)(16 * kh) << 16), x);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -477,6 +499,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
             }
         }
     }
+    dependents_may_start();
     tc_fence_before();
     cluster_sync();   // no arrival or copy is still on its way to either CTA
     tc_fence_after();
@@ -494,6 +517,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradArgs a, cons
     tile_at(plan.whole + j, plan, tn, tk);
     const int64_t n = tn * kTile + row, k = tk * kTile + c;
     if (n >= a.N || k >= a.K) return;
+    wait_for_primary();
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int p = 0; p < plan.parts; ++p) {
         const float4* src = reinterpret_cast<const float4*>(a.partial + ((j * plan.parts + p) * kTile + row) * kTile + c);
@@ -571,8 +595,18 @@ cudaError_t launch_wgrad(const WgradArgs& a, cudaStream_t s) {
         case 128: e = launch_pairs<128>(a, p, pairs, s); break;
     }
     if (e != cudaSuccess) return e;
-    if (p.tail > 0) wgrad_join_kernel<<<(unsigned)(p.tail * 32), 256, 0, s>>>(a, p);
-    return cudaGetLastError();
+    if (p.tail == 0) return cudaSuccess;
+    // may start while the last pairs end; it waits for them on the device
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.tail * 32));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, wgrad_join_kernel, a, p);
 }
 
 cudaError_t read_wgrad_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }
