@@ -21,11 +21,11 @@
 //   TMA warp        dY (64 tokens x this CTA's 128 rows n, two 128-byte-swizzled
 //                   boxes; both CTAs' bytes counted on the even CTA's barrier)
 //                   and the codes (64 tokens x this CTA's 128 columns k);
-//   2 scale warps   S r of the 64 tokens and the columns' groups, into shared memory;
+//   scale warp      S of the 64 tokens and the columns' groups, and r (cp.async);
 //   8 warps         codes -> X: a 16 x 16 block of codes is read transposed
 //                   (ldmatrix .b8), so that a thread has four tokens of one
 //                   column, and goes to tensor memory as 16 lanes x 16 bf16;
-//   MMA thread      (even CTA) four tcgen05.mma.cta_group::2 kind::f16, K = 16;
+//   MMA warp        (even CTA) four tcgen05.mma.cta_group::2 kind::f16, K = 16;
 //   8 warps         the finished accumulator into registers, times c, to bf16, stored.
 // X in tensor memory is what makes the tensor cores the bound: with X written to
 // and read from shared memory its traffic (copies in, codes out, X in, both
@@ -33,6 +33,11 @@
 // leave) held the 8192 x 11008 x 4096 product at 0.54 ms.  The price is half of
 // tensor memory, so there is one accumulator, and the MMAs of a tile wait until
 // the last one's is read.
+//
+// Measured (8192 tokens, G = 128): N x K = 11008 x 4096 0.44 ms alone (1.69 PFLOP/s)
+// and 0.50 ms when repeated for seconds, where the GPU stands at its power limit;
+// 4096 x 4096 0.165 ms, 2048 x 2048 0.048 ms; the smallest calls about 9 us
+// (launch, tensor memory, first tiles, join).
 //
 // Tiles left over after the last full round of the pairs are split along the
 // tokens, so that they too keep every pair busy: each part leaves a float32
@@ -62,7 +67,9 @@ constexpr int kStageBytes = kYBytes + kQBytes;
 constexpr int kEpiWarps = 8;                   // two per SM sub-partition, each half the rows n
 constexpr int kEpiRows = kTile / (kEpiWarps / 4);
 constexpr int kDeqWarps = 8;
-constexpr int kWgThreads = 32 * (4 + kEpiWarps + kDeqWarps);
+constexpr int kFirstEpi = 3;                    // TMA, MMA and tensor-memory warp; then the epilogue, then the conversion
+constexpr int kFirstDeq = kFirstEpi + kEpiWarps;
+constexpr int kWgThreads = 32 * (kFirstDeq + kDeqWarps);
 constexpr uint32_t kXCols = kTok / 2;          // tensor-memory columns of a stage of X
 constexpr uint32_t kTmemCols = 512;            // the accumulator (256) and the stages of X
 constexpr int kMinSteps = 8;                   // fewest steps of a split's part
@@ -70,7 +77,7 @@ constexpr int kMinSteps = 8;                   // fewest steps of a split's part
 // the tokens, so that lanes that write 32 / groups tokens of every group meet different banks), and what follows.
 constexpr int stages(int G) { return G == 8 ? 7 : 8; }
 constexpr int scale_pitch(int G) { return G == kHalf ? kTok : kTok + 4; }
-constexpr int scale_bytes(int G) { return (kHalf / G) * scale_pitch(G) * 4; }   // of a stage
+constexpr int scale_bytes(int G) { return ((kHalf / G) * scale_pitch(G) + kTok) * 4; }   // of a stage, with the tokens' factors
 constexpr int num_bars(int G) { return 4 * stages(G) + 3; }   // dY full, codes full, X full, empty; acc full, acc empty, done
 constexpr int bar_off(int G) { return stages(G) * (kStageBytes + scale_bytes(G)); }
 constexpr int smem_bytes(int G) { return bar_off(G) + 8 * num_bars(G) + 16 + 1024; }   // + slack for 1024-B alignment
@@ -163,6 +170,29 @@ __device__ __forceinline__ Item item_at(int64_t i, const Plan& p) {
     return it;
 }
 
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p;
+}
+
+// whether the phase is over, without a wait (a try may hold the warp until its phase ends)
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
+
 // Two 16 x 16 blocks of bytes, transposed: lane's address = row `lane` of the two
 // blocks (16 bytes each); r[2 b + h] = bytes 4 (lane % 4) .. + 3 of the
 // transposed block b's row lane / 4 + 8 h.
@@ -201,8 +231,13 @@ __device__ __forceinline__ ulonglong2 lds128(uint32_t a) {
     asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a));
     return v;
 }
-__device__ __forceinline__ void sts32(uint32_t a, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+// 4 bytes global -> shared, asynchronously; zero where `in` is not set
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// one arrival on `bar` once every cp.async that this thread issued before has landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 template <int G>
@@ -212,6 +247,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     constexpr int kStages = stages(G);
     constexpr int kGroups = kHalf / G;             // scale groups of this CTA's columns
     constexpr int kPitch = scale_pitch(G);
+    constexpr uint32_t kFactors = 4u * kGroups * kPitch;   // the tokens' factors, behind the scales
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);   // the same offset in both CTAs
@@ -228,13 +264,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + bar_off(G) + 8 * num_bars(G));
     volatile uint32_t* abort = tmem_slot + 1;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();   // 0: the CTA that issues the pair's MMAs
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(y_full(s), 1);
-            mbar_init(q_full(s), 2);               // the codes' copy, and the scale warp
+            mbar_init(q_full(s), 1 + 32);          // the codes' copy, and every lane's scales
             mbar_init(x_full(s), 2 * kDeqWarps);
             mbar_init(empty(s), 1);
         }
@@ -285,121 +321,90 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         // every stage issued has been read by the MMAs before the CTA may exit
         for (int i = 0; i < kStages; ++i)
             if (issued & (1u << i)) mbar_wait(empty(i), (last_ph >> i) & 1u, nullptr);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         if (leader) {
-            // ---- MMA issuer ----
+            // ---- MMA issuer: the whole warp walks, so that addresses and descriptors stay in uniform registers, and one
+            // elected lane issues.  The tensor cores queue only a few MMAs, so what lies between two steps' MMAs has to
+            // be short: the next stage's barriers are asked before this one's MMAs are issued, and the answers come
+            // while they run.  (4096 x 4096, 8192 tokens: 181 us with one thread that waits, issues and turns, and two
+            // scale warps that read into registers; 165 us so.) ----
             int s = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
+            const uint32_t elected = elect_one();
             const uint64_t ydesc0 = mn_desc(sb);
+            bool ready = false;
             for (int64_t i = cid; ok && i < items; i += nclusters, aph ^= 1u) {
                 const Item it = item_at(i, plan);
-                if (!mbar_wait_fast(acc_empty, aph ^ 1u, abort)) break;
+                ok = __all_sync(kFull, mbar_wait_fast(acc_empty, aph ^ 1u, abort));
+                if (!ok) break;
                 tc_fence_after();
                 for (int32_t st = it.from; st < it.to; ++st) {
-                    if (!mbar_wait_fast(y_full(s), ph, abort) || !mbar_wait_fast(x_full(s), ph, abort)) { ok = false; break; }
+                    if (!ready) {
+                        ok = __all_sync(kFull, mbar_wait_fast(y_full(s), ph, abort) && mbar_wait_fast(x_full(s), ph, abort));
+                        if (!ok) break;
+                    }
                     tc_fence_after();
                     const uint64_t yd = ydesc0 + (uint64_t)(s * (kStageBytes >> 4));
-                    const uint32_t xd = xmem + (uint32_t)s * kXCols;
-#pragma unroll
-                    for (int kk = 0; kk < kTok / kMmaTok; ++kk)
-                        mma_bf16_pair(tmem, xd + (uint32_t)(kk * (kMmaTok / 2)), yd + (uint64_t)(kk * ((kMmaTok * 128) >> 4)),
-                                      st != it.from || kk != 0);
-                    mma_commit_pair(empty(s), 0x3);   // both CTAs' stage s is free once read
+                    const uint32_t xd = xmem + (uint32_t)s * kXCols, freed = empty(s);
                     if (++s == kStages) { s = 0; ph ^= 1u; }
+                    const bool y_in = mbar_test(y_full(s), ph), x_in = mbar_test(x_full(s), ph);
+                    if (elected) {
+#pragma unroll
+                        for (int kk = 0; kk < kTok / kMmaTok; ++kk)
+                            mma_bf16_pair(tmem, xd + (uint32_t)(kk * (kMmaTok / 2)), yd + (uint64_t)(kk * ((kMmaTok * 128) >> 4)),
+                                          st != it.from || kk != 0);
+                        mma_commit_pair(freed, 0x3);   // both CTAs' stage is free once read
+                        if (st + 1 == it.to) mma_commit_pair(acc_full, 0x3);
+                    }
+                    ready = __all_sync(kFull, y_in && x_in);
                 }
-                if (!ok) break;
-                mma_commit_pair(acc_full, 0x3);
             }
-            mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
+            if (elected) mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
         }
-        mbar_wait(done, 0u, nullptr);
-    } else if (warp == 2 || warp == 3) {
-        // ---- scale loaders: every other step each.  A lane has one group of every 32 / groups-th token, so that a
-        // load reads the groups of a token together; loaded two of its steps ahead of their use (one where the
-        // groups are many).  The tokens' factors come from the lanes that hold two tokens each. ----
-        constexpr int kDeep = kGroups > 8 ? 1 : 2;
+        if (lane == 0) mbar_wait(done, 0u, nullptr);
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---- scales: a lane has one group of every 32 / groups-th token, so that an access reads the groups of a token
+        // together; and two tokens' factors ----
         constexpr int kVals = 2 * kGroups, kRows = 32 / kGroups;   // scales per lane; tokens between two of them
-        const int64_t ngr = a.K / G;
+        const int64_t ngr = a.K / G, step = kRows * ngr;
         const int grp = lane % kGroups, tok = lane / kGroups;
-        int64_t ai = cid;
-        Item ait = item_at(ai < items ? ai : 0, plan);
-        int32_t ast = ait.from;
-        auto next = [&]() {                        // one step on, over the items' ends
-            if (++ast >= ait.to) {
-                ai += nclusters;
-                if (ai < items) {
-                    ait = item_at(ai, plan);
-                    ast = ait.from;
-                }
-            }
-        };
-        auto fetch = [&](float (&f)[kVals], float (&r)[2]) {
-            const int64_t g = (ait.k * kTile + rank * kHalf) / G + grp, m0 = (int64_t)ast * kTok;
-            const bool in = ai < items && g < ngr;
-            const float* p = a.scale + (m0 + tok) * ngr + g;
-            const int64_t step = kRows * ngr;
-            if (m0 + kTok <= a.M) {                // all but the last step of all
-#pragma unroll
-                for (int i = 0; i < kVals; ++i, p += step) f[i] = in ? __ldg(p) : 0.0f;
-            } else {
-#pragma unroll
-                for (int i = 0; i < kVals; ++i, p += step) f[i] = in && m0 + tok + i * kRows < a.M ? __ldg(p) : 0.0f;
-            }
-            if (a.row_scale) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t m = m0 + lane + 32 * h;
-                    r[h] = ai < items && m < a.M ? __ldg(a.row_scale + m) : 0.0f;
-                }
-            }
-            next();
-            next();
-        };
-        if (warp == 3) next();
-        float f[kDeep][kVals], r[kDeep][2];
-        // steps of this pair in all
-        int64_t steps = 0;
-        for (int64_t i = cid; i < items; i += nclusters) {
-            const Item it = item_at(i, plan);
-            steps += it.to - it.from;
-        }
-#pragma unroll
-        for (int b = 0; b < kDeep; ++b) fetch(f[b], r[b]);
-        int s = warp - 2;
+        int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        int64_t j0 = warp - 2;
-        while (ok && j0 < steps) {
+        for (int64_t i = cid; ok && i < items; i += nclusters) {
+            const Item it = item_at(i, plan);
+            const int64_t g = (it.k * kTile + rank * kHalf) / G + grp;
+            const bool in = g < ngr;
+            const float* p0 = a.scale + ((int64_t)it.from * kTok + tok) * ngr + (in ? g : 0);
+            for (int32_t st = it.from; st < it.to; ++st, p0 += kTok * ngr) {
+                ok = __all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort));
+                if (!ok) break;
+                const uint32_t d = scales0 + (uint32_t)(s * scale_bytes(G));
+                const int64_t m0 = (int64_t)st * kTok;
+                const int rest = a.M - m0 < kTok ? (int)(a.M - m0) : kTok;   // tokens of this step
+                const float* p = p0;
 #pragma unroll
-            for (int b = 0; b < kDeep; ++b) {
-                if (ok && j0 < steps) {
-                    if (__all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort))) {
-                        const uint32_t d = scales0 + (uint32_t)(s * scale_bytes(G) + 4 * (grp * kPitch + tok));
+                for (int v = 0; v < kVals; ++v, p += step) {
+                    const bool here = in && tok + v * kRows < rest;
+                    cp_async4(d + (uint32_t)(4 * (grp * kPitch + tok + v * kRows)), here ? p : a.scale, here);
+                }
+                if (a.row_scale) {
 #pragma unroll
-                        for (int i = 0; i < kVals; ++i) {
-                            float v = f[b][i];
-                            if (a.row_scale) {
-                                constexpr int kPerHalf = 32 / kRows;   // values of the first 32 tokens
-                                v *= kGroups == 1 ? r[b][i] : __shfl_sync(kFull, r[b][i / kPerHalf], tok + (i % kPerHalf) * kRows);
-                            }
-                            sts32(d + (uint32_t)(4 * i * kRows), v);
-                        }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_at(q_full(s));
-                        fetch(f[b], r[b]);
-                        j0 += 2;
-                        s += 2;
-                        if (s >= kStages) { s -= kStages; ph ^= 1u; }
-                    } else {
-                        ok = false;
+                    for (int h = 0; h < 2; ++h) {
+                        const bool here = lane + 32 * h < rest;
+                        cp_async4(d + kFactors + 4u * (uint32_t)(lane + 32 * h), a.row_scale + (here ? m0 + lane + 32 * h : 0), here);
                     }
                 }
+                cp_async_arrive(q_full(s));
+                if (++s == kStages) { s = 0; ph ^= 1u; }
             }
         }
-    } else if (warp >= 4 && warp < 4 + kEpiWarps) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp >= kFirstEpi && warp < kFirstDeq) {
         // ---- epilogue: lane = one column k of the tile; tensor-memory columns = rows n ----
-        const int q4 = warp & 3, nh = ((warp - 4) >> 2) * kEpiRows;
+        const int q4 = warp & 3, nh = ((warp - kFirstEpi) >> 2) * kEpiRows;
         const uint32_t ae = map_to_rank(acc_empty, 0);
         auto release = [&]() {                     // the accumulator has been read
             tc_fence_before();
@@ -452,9 +457,9 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 }
             }
         }
-    } else if (warp >= 4 + kEpiWarps) {
+    } else if (warp >= kFirstDeq) {
         // ---- codes -> X: a warp takes the 32 columns k of its tensor-memory lanes, and 32 of the 64 tokens ----
-        const int q4 = warp & 3, th = (warp - 4 - kEpiWarps) >> 2;
+        const int q4 = warp & 3, th = (warp - kFirstDeq) >> 2;
         const uint32_t xb0 = map_to_rank(x_full(0), 0);
         const int row = 32 * th + lane;                            // token of this lane's ldmatrix address
         uint32_t q_at[2];                                          // 16-byte unit of the row, as the 128-byte swizzle puts it
@@ -481,6 +486,14 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 for (int j = 0; j < kSets; ++j)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) f[j][b] = lds128(ss + (uint32_t)(4 * ((32 * q4 / G + j) * kPitch + 16 * b)));
+                if (a.row_scale) {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const ulonglong2 r = lds128(ss + kFactors + (uint32_t)(64 * b));
+#pragma unroll
+                        for (int j = 0; j < kSets; ++j) f[j][b] = make_ulonglong2(mul2(f[j][b].x, r.x), mul2(f[j][b].y, r.y));
+                    }
+                }
 #pragma unroll
                 for (int kh = 0; kh < 2; ++kh) {
                     uint32_t x[8];
