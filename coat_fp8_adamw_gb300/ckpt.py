@@ -208,7 +208,7 @@ def _side(side: str, M: int, H: int, D: int, G: int, dev, codes, scale, rstd):
 def coat_qk_norm_rope_ckpt(q, k, q_weight, k_weight, eps: float, cos, sin, positions, G: int, q_out,
                            q_codes, q_scale, q_rstd, k_out=None, k_codes=None, k_scale=None,
                            k_rstd=None, interleaved: bool = False, stream=None) -> None:
-    """RMS norm of every head of q [M, Hq, D] and k [M, Hk, D] (_BF16, the tokens'
+    """RMS norm of every head of q [M, Hq, D] and k [M, Hk, D] (bf16, the tokens'
     rows at any distance: ranges of one projection's output), the position
     rotation of the normed heads, and a checkpoint of the heads as they came.
 
