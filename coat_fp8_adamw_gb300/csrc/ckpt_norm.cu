@@ -11,7 +11,17 @@
 // are rounded once, to the bf16 tensors that the caller asks for.
 //
 // A row is held by a team of T = 32 ceil(N / 512) threads, sixteen elements each;
-// a block has as many teams as fit 256 threads.
+// a block has as many teams as fit 256 threads.  Sixteen elements are one 256-bit
+// access of a bf16 tensor and one 128-bit access of codes; every tensor is read
+// and written once.
+//
+// Bound by memory.  8192 x 4096, G = 128, with a residual: forward 47.1 us, 96 %
+// of the copy rate; backward 43.9 us, of which 8 to 9 do not depend on the rows
+// (two launches, the ring's first rows, the sum over the blocks' dw: 4099 x 5120
+// takes 27.3 us, 59 % of the copy rate).  Forward one row per block and no loop,
+// so that blocks in different phases keep loads on their way; backward persistent
+// blocks, since each keeps its sums for dw in registers, fed by a ring of rows in
+// shared memory.
 #include <cstdint>
 
 #include "ckpt_device.cuh"

@@ -287,7 +287,8 @@ coat_status coat_exact_recompute_counts(uint64_t counts[2], int32_t reset);
 /*
  * How many bounded waits inside the library's kernels gave up on the current
  * device since the library was loaded there (or since the last reset).  The
- * pipelined kernels (coat_fp8_linear_group_quantize) wait on their own
+ * pipelined kernels (coat_fp8_linear_group_quantize, coat_ckpt_weight_grad,
+ * coat_rmsnorm_ckpt_backward) wait on their own
  * producers with an iteration limit instead of forever; a non-zero count
  * means a launch returned without finishing its work.  reset != 0 clears the
  * counter after reading it.  Synchronizes with the current device.
@@ -365,8 +366,9 @@ coat_status coat_swiglu_ckpt(const uint16_t *gate, const uint16_t *up, int64_t l
  *   dgate = dh u s (1 + g (1 - s));  dup = dh g s.
  *   dh [M x N] bf16 in;  dgate, dup  M rows of N bf16, ld apart, out;
  *   h_q [M x N] uint8, h_scale [M x N/G] out, or both NULL: the checkpoint of
- *   g s u (of its float32 value), which is what the weight gradient of the
- *   projection behind the product reads.
+ *   g s u, which is what the weight gradient of the projection behind the
+ *   product reads (of its float32 value, and its quotients by the scale are
+ *   rounded to float32 before they are rounded to E4M3).
  */
 coat_status coat_swiglu_ckpt_backward(const uint16_t *dh, const uint8_t *gate_q, const float *gate_scale,
                                       const uint8_t *up_q, const float *up_scale, int64_t M, int64_t N,
