@@ -18,23 +18,25 @@ namespace ckpt {
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
 // ---- memory: N consecutive 32-bit words, streamed past L1 ----
+// Ordinary loads, and volatile: the kernels start before the one ahead of them has ended, so that no load of theirs may
+// count as one of constant data (ld.global.nc) or be moved ahead of the wait for it.
 template <int N>
 __device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[N]);
 template <>
 __device__ __forceinline__ void load_words<4>(const void* p, uint32_t (&w)[4]) {
-    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
         : "l"(p));
 }
 // 32 bytes: one 256-bit access where `wide` (the address is a multiple of 32), else two
 __device__ __forceinline__ void load_words8(const void* p, bool wide, uint32_t (&w)[8]) {
     if (wide) {
-        asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
             : "l"(p));
     } else {
-        asm("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-        asm("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4 + 16];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4 + 16];" : "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
     }
 }
 __device__ __forceinline__ void store_words8(void* p, bool wide, const uint32_t (&w)[8]) {
@@ -56,9 +58,11 @@ __device__ __forceinline__ void read8(const void* p, uint32_t (&w)[8]) {
 }
 
 // ---- programmatic dependent launch ----
-// In the kernel whose results are waited for: the next one's blocks may be
-// scheduled.  In the next one, before it reads them: wait until the first has
-// ended and its writes are visible.
+// Every kernel here may start while the one before it in the stream ends (launch_next): its launch and what it prepares
+// on the SM then cost nothing (2.3 to 2.6 us less per call when calls follow one another, 0.4 in a graph).  Before a thread's
+// first access to global memory, reads and writes alike: wait until that kernel has ended and its writes are visible.
+// A block of every kernel does so, so that a kernel's end implies the end of all before it.
+// In a kernel whose blocks end together: the next one's blocks may be scheduled.
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -237,11 +241,11 @@ __device__ __forceinline__ void store_scales16(float* scale, int64_t at, int G, 
 }
 __device__ __forceinline__ void load_scales16(const float* scale, int64_t at, int G, int gshift, float& lo, float& hi) {
     if (G == 8) {
-        const float2 f = __ldg(reinterpret_cast<const float2*>(scale + (at >> 3)));
+        const float2 f = *reinterpret_cast<const float2*>(scale + (at >> 3));
         lo = f.x;
         hi = f.y;
     } else {
-        lo = hi = __ldg(scale + (at >> gshift));
+        lo = hi = scale[at >> gshift];
     }
 }
 

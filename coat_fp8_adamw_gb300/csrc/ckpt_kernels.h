@@ -9,6 +9,23 @@
 
 namespace coat {
 
+// Launch a kernel that may start when the one before it in the stream has no block left to run, or allows it earlier;
+// every thread waits for that kernel's end (wait_for_primary) before its first access to global memory.
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 blocks, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = blocks;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct NormFwdArgs {
     const uint16_t* x;         // M x N bf16
     const uint16_t* residual;  // M x N bf16, or null

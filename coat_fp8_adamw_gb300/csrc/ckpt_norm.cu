@@ -72,7 +72,7 @@ template <int n>
 __device__ __forceinline__ void stage_weights(const float* w, int N, int items, float4* sw) {
     for (int i = threadIdx.x; i < items * (n / 4); i += blockDim.x)
         sw[(i % (n / 4)) * items + i / (n / 4)] =
-            4 * i < N ? __ldg(reinterpret_cast<const float4*>(w) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            4 * i < N ? reinterpret_cast<const float4*>(w)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 template <int n>
 __device__ __forceinline__ void weights_of(const float4* sw, int items, int i, float (&w)[n]) {
@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const NormF
     const int64_t r = (int64_t)blockIdx.x * teams + team, at = r * N + col;
     const bool ok = col < N && r < a.M;
     uint64_t x[kE / 2] = {}, ss2 = 0ull;
+    wait_for_primary();
     if (ok) {
         uint32_t u[8];
         load_words8(a.x + at, wide, u);
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const NormF
         const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(a.weight + col);
 #pragma unroll
         for (int e = 0; e < kE / 4; ++e) {
-            const ulonglong2 w = __ldg(wp + e);
+            const ulonglong2 w = wp[e];
             float lo, hi;
             upk(mul2(mul2(x[2 * e], r2), w.x), lo, hi);
             u[2 * e] = bf16x2(lo, hi);
@@ -182,6 +183,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
     if (threadIdx.x == 0) {
         for (int s = 0; s < depth; ++s) mbar_init(bar0 + 8u * (uint32_t)s, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    wait_for_primary();
+    if (threadIdx.x == 0) {
         for (int s = 0; s < depth; ++s)
             if (first + s * step < a.M) issue(first + s * step, s);
     }
@@ -200,10 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
     }
     auto fetch_scales = [&](int64_t r) {   // one iteration ahead
         if (r < a.M) {
-            rn = __ldg(a.rstd + r);
+            rn = a.rstd[r];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (in_row[j]) Sn[j] = __ldg(a.scale + r * ngr + (col[j] >> gshift));
+                if (in_row[j]) Sn[j] = a.scale[r * ngr + (col[j] >> gshift)];
         }
     };
     fetch_scales(first + team);
@@ -358,20 +362,17 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
     const unsigned blocks = (unsigned)((a.M + sh.teams - 1) / sh.teams);
     const int threads = sh.T * sh.teams;
     if (threads <= 256)
-        norm_fwd_kernel<kRes, 256, 6><<<blocks, threads, 0, s>>>(a, sh, wide);
-    else if (threads <= 512)
-        norm_fwd_kernel<kRes, 512, 3><<<blocks, threads, 0, s>>>(a, sh, wide);
-    else
-        norm_fwd_kernel<kRes, 1024, 1><<<blocks, threads, 0, s>>>(a, sh, wide);
-    return cudaGetLastError();
+        return launch_next(norm_fwd_kernel<kRes, 256, 6>, blocks, threads, 0, s, a, sh, wide);
+    if (threads <= 512)
+        return launch_next(norm_fwd_kernel<kRes, 512, 3>, blocks, threads, 0, s, a, sh, wide);
+    return launch_next(norm_fwd_kernel<kRes, 1024, 1>, blocks, threads, 0, s, a, sh, wide);
 }
 
 template <bool kRes, int kThreads>
 cudaError_t launch_bwd(const NormBwdArgs& a, int64_t blocks, const Shape& sh, cudaStream_t s) {
     const cudaError_t e = allow_smem(norm_bwd_kernel<kRes, kThreads>, smem_of(sh));
     if (e != cudaSuccess) return e;
-    norm_bwd_kernel<kRes, kThreads><<<(unsigned)blocks, sh.T * sh.teams, smem_of(sh), s>>>(a, sh);
-    return cudaGetLastError();
+    return launch_next(norm_bwd_kernel<kRes, kThreads>, (unsigned)blocks, sh.T * sh.teams, smem_of(sh), s, a, sh);
 }
 
 }  // namespace
@@ -392,19 +393,9 @@ int64_t norm_bwd_partials(int64_t M, int64_t N, int sms) {
 }
 
 cudaError_t launch_column_sums(const ColumnSum& first, const ColumnSum& second, int64_t N, cudaStream_t s) {
-    // may start while the kernel that writes the partial sums ends; it waits for it on the device
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     const int cols = N <= 512 ? 8 : 32;
-    cfg.gridDim = dim3((unsigned)((N + cols - 1) / cols), second.P > 0 ? 2 : 1);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cols == 8 ? cudaLaunchKernelEx(&cfg, column_sum_kernel<8>, first, second, N)
-                     : cudaLaunchKernelEx(&cfg, column_sum_kernel<32>, first, second, N);
+    const dim3 grid((unsigned)((N + cols - 1) / cols), second.P > 0 ? 2 : 1);
+    return launch_next(cols == 8 ? column_sum_kernel<8> : column_sum_kernel<32>, grid, 1024, 0, s, first, second, N);
 }
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, cudaStream_t s) {

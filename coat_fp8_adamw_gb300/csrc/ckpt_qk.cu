@@ -68,7 +68,7 @@ struct Task {
 };
 
 __device__ __forceinline__ void load8f(const float* p, float* x) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = *reinterpret_cast<const float4*>(p), b = reinterpret_cast<const float4*>(p)[1];
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
@@ -87,7 +87,7 @@ __device__ __forceinline__ void load_turn(const QkArgs& a, int64_t m, int l, flo
 #pragma unroll
     for (int e = 0; e < 8; ++e) { c[e] = 1.0f; s[e] = 0.0f; }
     if (16 * l >= a.rot) return;
-    const int64_t pos = __ldg(a.positions + m);
+    const int64_t pos = a.positions[m];
     if (pos >= 0 && pos < a.max_pos) {
         load8f(a.cos + pos * (a.rot / 2) + 8 * l, c);
         load8f(a.sin + pos * (a.rot / 2) + 8 * l, s);
@@ -128,7 +128,7 @@ __device__ __forceinline__ void turn_factors(const float (&c)[8], const float (&
     }
 }
 __device__ __forceinline__ void load8f2(const float* p, uint64_t* x) {
-    const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(p)), b = __ldg(reinterpret_cast<const ulonglong2*>(p) + 1);
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(p), b = reinterpret_cast<const ulonglong2*>(p)[1];
     x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
 
@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kFwdBlock, kFwdPerSm) qk_fwd_kernel(const QkAr
     const int gshift = 31 - __clz(a.G), gpr = a.D >> gshift;
     const float inv_d = 1.0f / (float)a.D;
     __shared__ uint4 ring[kRing][2][kFwdBlock];
+    wait_for_primary();
     const int h0 = from * kHeads + sub;
     const uint16_t* next = in + (int64_t)h0 * a.D;
     auto fetch = [&](int i) {                            // pass from + i, if there is one
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(kBlock, kPerSm) qk_bwd_kernel(const QkArgs a, 
     const int gshift = 31 - __clz(a.G), to_b = at.b - at.a;
     const float inv_d = 1.0f / (float)a.D;
     uint64_t w[8] = {}, dw2[8] = {};
+    wait_for_primary();
     if (in_head) {
         load8f2(sd.weight + at.a, w);
         load8f2(sd.weight + at.b, w + 4);
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kBlock, kPerSm) qk_bwd_kernel(const QkArgs a, 
     // A token's angles come with its first pass; fetched are at most as many passes ahead as a token has, so that there
     // are never more than two tokens' angles.
     const int ahead = min(kRing - 1, passes);
-    auto position = [&](int64_t t) { return turned && t < a.M ? (int64_t)__ldg(a.positions + t) : (int64_t)-1; };
+    auto position = [&](int64_t t) { return turned && t < a.M ? (int64_t)a.positions[t] : (int64_t)-1; };
     int64_t fm = m, pos = left > 0 ? position(m) : -1;
     uint32_t known = 0u, place = 0u, fplace = 0u;     // known: a bit per place: the position is in the tables
     bool fresh = true;
@@ -480,10 +482,8 @@ __global__ void __launch_bounds__(kBlock, kPerSm) qk_bwd_kernel(const QkArgs a, 
 template <int kLanes, bool kInter>
 cudaError_t launch(const QkArgs& a, const Task& tk, bool back, int64_t blocks, cudaStream_t s) {
     if (back)
-        qk_bwd_kernel<kLanes, kInter><<<(unsigned)blocks, kBlock, 0, s>>>(a, tk);
-    else
-        qk_fwd_kernel<kLanes, kInter><<<(unsigned)blocks, kFwdBlock, 0, s>>>(a, tk);
-    return cudaGetLastError();
+        return launch_next(qk_bwd_kernel<kLanes, kInter>, (unsigned)blocks, kBlock, 0, s, a, tk);
+    return launch_next(qk_fwd_kernel<kLanes, kInter>, (unsigned)blocks, kFwdBlock, 0, s, a, tk);
 }
 template <int kLanes>
 cudaError_t launch(const QkArgs& a, const Task& tk, bool back, int64_t blocks, cudaStream_t s) {

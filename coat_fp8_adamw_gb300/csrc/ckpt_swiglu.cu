@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kBlock) swiglu_fwd_kernel(const SwigluFwdArgs 
     const int gshift = 31 - __clz(a.G);
     const bool ok = i < total;       // the lanes past the end take part in the shuffles
     uint32_t gv[8] = {}, uv[8] = {};
+    wait_for_primary();
     if (ok) {
         const int64_t at = strided_at(i, nc, a.ld);
         load_words8(a.gate + at, wide, gv);
@@ -98,6 +99,7 @@ __global__ void __launch_bounds__(kBlock) swiglu_bwd_kernel(const SwigluBwdArgs 
     const int64_t at = (int64_t)i * 16;
     uint32_t dv[8] = {}, gq[4] = {}, uq[4] = {};
     float Sg[2] = {0.0f, 0.0f}, Su[2] = {0.0f, 0.0f};
+    wait_for_primary();
     if (ok) {
         load_words8(a.dh + at, wide, dv);
         load_words<4>(a.gate_q + at, gq);
@@ -167,8 +169,7 @@ cudaError_t launch_swiglu_fwd(const SwigluFwdArgs& all, cudaStream_t s) {
         a.up_q += r * N;
         a.gate_scale += r * (N / a.G);
         a.up_scale += r * (N / a.G);
-        swiglu_fwd_kernel<<<blocks_of(a.M, N), kBlock, 0, s>>>(a, nc, wide);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_next(swiglu_fwd_kernel, blocks_of(a.M, N), kBlock, 0, s, a, nc, wide);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -191,11 +192,9 @@ cudaError_t launch_swiglu_bwd(const SwigluBwdArgs& all, cudaStream_t s) {
         if (a.h_q) {
             a.h_q += r * N;
             a.h_scale += r * (N / a.G);
-            swiglu_bwd_kernel<true><<<blocks_of(a.M, N), kBlock, 0, s>>>(a, nc, wide);
-        } else {
-            swiglu_bwd_kernel<false><<<blocks_of(a.M, N), kBlock, 0, s>>>(a, nc, wide);
         }
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_next(a.h_q ? swiglu_bwd_kernel<true> : swiglu_bwd_kernel<false>, blocks_of(a.M, N), kBlock,
+                                          0, s, a, nc, wide);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

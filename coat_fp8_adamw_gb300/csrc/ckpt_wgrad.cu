@@ -291,6 +291,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
     tc_fence_before();
     cluster_sync();   // barriers initialised and tensor memory allocated in both CTAs
     tc_fence_after();
+    wait_for_primary();
     const uint32_t tmem = *tmem_slot, xmem = tmem + (uint32_t)kTile;
 
     const int64_t items = plan.whole + plan.tail * plan.parts;
@@ -433,7 +434,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 release();
             } else {
                 // all of it into registers, as pairs of rows, so that the next tile's MMAs may start
-                const float cs = a.col_scale && k < a.K ? __ldg(a.col_scale + k) : 1.0f;
+                const float cs = a.col_scale && k < a.K ? a.col_scale[k] : 1.0f;
                 uint32_t w[kEpiRows / 2];
 #pragma unroll
                 for (int c = 0; c < kEpiRows; c += 16) {
@@ -539,8 +540,8 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradArgs a, cons
         x[4] += f1.x; x[5] += f1.y; x[6] += f1.z; x[7] += f1.w;
     }
     if (a.col_scale) {
-        const float4 f0 = __ldg(reinterpret_cast<const float4*>(a.col_scale + k));
-        const float4 f1 = __ldg(reinterpret_cast<const float4*>(a.col_scale + k) + 1);
+        const float4 f0 = *reinterpret_cast<const float4*>(a.col_scale + k);
+        const float4 f1 = reinterpret_cast<const float4*>(a.col_scale + k)[1];
         x[0] *= f0.x; x[1] *= f0.y; x[2] *= f0.z; x[3] *= f0.w;
         x[4] *= f1.x; x[5] *= f1.y; x[6] *= f1.z; x[7] *= f1.w;
     }
@@ -572,17 +573,19 @@ cudaError_t launch_pairs(const WgradArgs& a, const Plan& p, int64_t pairs, cudaS
     if (!encode(&tmy, a.dy, a.M, a.N, a.dy_ld, true) || !encode(&tmq, a.q, a.M, a.K, a.K, false)) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(wgrad_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(G));
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kWgThreads);
     cfg.dynamicSmemBytes = smem_bytes(G);
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     const int64_t items = p.whole + p.tail * p.parts;
     cfg.gridDim = dim3(2u * (unsigned)(items < pairs ? items : pairs));
     return cudaLaunchKernelEx(&cfg, wgrad_kernel<G>, tmy, tmq, a, p);
@@ -609,17 +612,7 @@ cudaError_t launch_wgrad(const WgradArgs& a, cudaStream_t s) {
     }
     if (e != cudaSuccess) return e;
     if (p.tail == 0) return cudaSuccess;
-    // may start while the last pairs end; it waits for them on the device
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.tail * 32));
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, wgrad_join_kernel, a, p);
+    return launch_next(wgrad_join_kernel, (unsigned)(p.tail * 32), 256, 0, s, a, p);
 }
 
 cudaError_t read_wgrad_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }

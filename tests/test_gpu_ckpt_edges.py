@@ -273,3 +273,81 @@ def test_swiglu_of_many_row_counts(N, G):
         near(h, ref, bf16_bound(ref) + silu_bound(ref, g.double()) + 2.0 ** -120 * (g.double() * u.double()).abs(), "h")
         check_checkpoint(gq, gs, g.contiguous(), G, "gate")
         check_checkpoint(uq, us, u.contiguous(), G, "up")
+
+
+def test_calls_that_follow_one_another_at_once():
+    """Kernels start before the one ahead of them has ended: each has to see its results, and must not write what it still
+    reads.  A chain over two buffers, also behind copies, in a graph, and behind another stream's work."""
+    M, N, G, D = 1031, 2048, 32, 64
+    x0, w, w2 = acts(M, N, 51), norm_w(N, 52), norm_w(D, 53)
+    cos, sin = rope_tables(M, D)
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")
+    a, b, c, dw, dw2 = empty(M, N), empty(M, N), empty(M, N), empty(N), empty(N // 8, N)
+    q, S, rstd, rh = empty(M, N, dtype=U8), empty(M, N // G, dtype=F32), empty(M, dtype=F32), empty(M, N // D, dtype=F32)
+    q2, S2, q3, S3 = empty(M, N, dtype=U8), empty(M, N // G, dtype=F32), empty(M, N, dtype=U8), empty(M, N // G, dtype=F32)
+    ws = workspace(max(coat.coat_rmsnorm_ckpt_backward_workspace_bytes(M, N),
+                       coat.coat_ckpt_weight_grad_workspace_bytes(M, N // 8, N)))
+    dy = grads(M, N // 8, 54)
+    heads = lambda t, n=D: t.view(M, N // D, n)  # noqa: E731
+    sums = torch.zeros(1, dtype=torch.float64, device="cuda")
+
+    def chain(rounds, sync):
+        for i in range(rounds):
+            coat.coat_rmsnorm_ckpt(a, w, EPS, G, b, q, S, rstd)
+            sync()
+            coat.coat_qk_norm_rope_ckpt(heads(b), None, w2, None, EPS, cos, sin, pos, G, heads(a), heads(q), heads(S, D // G), rh)
+            sync()
+            coat.coat_swiglu_ckpt(a, b, G, c, q, S, q2, S2)
+            sync()
+            coat.coat_ckpt_weight_grad(dy, q, S, G, dw2, ws)
+            sync()
+            coat.coat_rmsnorm_ckpt_backward(c, q2, S2, rstd, w, G, a, dw, ws)
+            sync()
+            coat.coat_swiglu_ckpt_backward(a, q, S, q2, S2, G, b, c, h_q=q3, h_scale=S3)
+            sync()
+            coat.coat_rmsnorm_ckpt(b, w, EPS, G, a, q, S, rstd, residual=x0, h=c)
+            sync()
+        return [t.clone() for t in (a, b, c, dw, dw2, q, S, q2, S2, q3, S3, rstd)]
+
+    a.copy_(x0)
+    want = chain(4, torch.cuda.synchronize)
+    assert all(torch.isfinite(t.double()).all() for t in want)
+    for _ in range(5):
+        a.zero_()
+        torch.cuda.synchronize()
+        a.copy_(x0)
+        got = chain(4, lambda: None)
+        assert all(torch.equal(u, v) for u, v in zip(want, got))
+
+    host = x0.cpu().pin_memory()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        a.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2_000_000)
+            a.copy_(host, non_blocking=True)
+        main.wait_stream(side)
+        got = chain(4, lambda: None)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            sums[0] = got[0].double().sum()
+        main.wait_stream(side)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(want, got))
+    assert sums[0] == want[0].double().sum()
+
+    other = torch.cuda.Stream()
+    a.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(2_000_000)
+        a.copy_(x0)
+    torch.cuda.current_stream().wait_stream(other)
+    got = chain(4, lambda: None)
+    assert all(torch.equal(u, v) for u, v in zip(want, got))
