@@ -255,10 +255,11 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// 1 / sqrt(v), v > 0 and normal: the approximation and one Newton step, within 2^-23 relatively.
+// 1 / sqrt(v), v > 0 (also subnormal: a zero row and an eps below 2^-126): the approximation and one Newton step, within
+// 2^-23 relatively for normal v.
 __device__ __forceinline__ float rsqrt_newton(float v) {
     float r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
     return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
 }
 

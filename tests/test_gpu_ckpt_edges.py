@@ -351,3 +351,26 @@ def test_calls_that_follow_one_another_at_once():
     torch.cuda.current_stream().wait_stream(other)
     got = chain(4, lambda: None)
     assert all(torch.equal(u, v) for u, v in zip(want, got))
+
+
+@pytest.mark.parametrize("eps", [1e-40, 2.0 ** -126, 1e-12, 1.0, 3e38])
+def test_every_positive_eps(eps):
+    """A zero row's 1/rms is 1/sqrt(eps), also of a subnormal one; its outputs are zeros.  (The sum's last bit is 2^-149.)"""
+    eps = float(torch.tensor(eps, dtype=F32))
+    M, N, G, D = 5, 256, 16, 64
+    x, w = acts(M, N, 61, spread=0.5), norm_w(N, 62)
+    y, q, S, rstd = empty(M, N), empty(M, N, dtype=U8), empty(M, N // G, dtype=F32), empty(M, dtype=F32)
+    coat.coat_rmsnorm_ckpt(x, w, eps, G, y, q, S, rstd)
+    ref, rr = R.rmsnorm(x.double(), w.double(), eps)
+    near(rstd, rr, 2.0 ** -19 * rr, "rstd")
+    near(y, ref, bf16_bound(ref) + 2.0 ** -19 * ref.abs(), "y")
+    assert not y[1].float().any()
+    cos, sin = rope_tables(M, D)
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")
+    y = empty(M, N // D, D)
+    rh = torch.empty(M, N // D, device="cuda")
+    coat.coat_qk_norm_rope_ckpt(x.view(M, N // D, D), None, w[:D].clone(), None, eps, cos, sin, pos, G, y, q.view(M, N // D, D),
+                                S.view(M, N // D, D // G), rh)
+    rr = R.rmsnorm(x.double().view(M, N // D, D), w[:D].double(), eps)[1]
+    near(rh, rr, 2.0 ** -19 * rr, "head rstd")
+    assert not y[1].float().any()
