@@ -15,10 +15,10 @@
 // access of a bf16 tensor and one 128-bit access of codes; every tensor is read
 // and written once.
 //
-// Bound by memory.  8192 x 4096, G = 128, with a residual: forward 47.1 us, 96 %
-// of the copy rate; backward 43.9 us, of which 8 to 9 do not depend on the rows
-// (two launches, the ring's first rows, the sum over the blocks' dw: 4099 x 5120
-// takes 27.3 us, 59 % of the copy rate).  Forward one row per block and no loop,
+// Bound by memory.  8192 x 4096, G = 128, with a residual: forward 46.8 us, 97 %
+// of the copy rate; backward 43.6 us, of which 8 to 9 do not depend on the rows
+// (two kernels, the ring's first rows, the sum over the blocks' dw: 4099 x 5120
+// takes 27.0 us, 60 % of the copy rate).  Forward one row per block and no loop,
 // so that blocks in different phases keep loads on their way; backward persistent
 // blocks, since each keeps its sums for dw in registers, fed by a ring of rows in
 // shared memory.
@@ -85,7 +85,7 @@ __device__ __forceinline__ void weights_of(const float4* sw, int items, int i, f
 
 // Forward: a block has its rows once, a thread sixteen consecutive elements (so that a
 // group of G >= 16 is G / 16 lanes).  What keeps the memory busy are many small
-// blocks per SM in different phases: at 8192 x 4096 with a residual 47.4 us with
+// blocks per SM in different phases: at 8192 x 4096 with a residual 46.8 us with
 // 40 registers (six blocks of 256 threads per SM), 51.0 with 50 (four); blocks
 // that walk the rows through a ring of bulk copies, as backward, took 53.3.
 template <bool kRes, int kThreads, int kBlocks>

@@ -34,10 +34,10 @@
 // tensor memory, so there is one accumulator, and the MMAs of a tile wait until
 // the last one's is read.
 //
-// Measured (8192 tokens, G = 128): N x K = 11008 x 4096 0.44 ms alone (1.69 PFLOP/s)
-// and 0.50 ms when repeated for seconds, where the GPU stands at its power limit;
-// 4096 x 4096 0.167 ms, 2048 x 2048 0.048 ms; the smallest calls about 9 us
-// (launch, tensor memory, first tiles, join).
+// Measured (8192 tokens, G = 128): N x K = 11008 x 4096 0.42 to 0.44 ms alone (1.7
+// PFLOP/s) and 0.50 ms when repeated for seconds, where the GPU stands at its power
+// limit; 4096 x 4096 0.160 to 0.168 ms, 2048 x 2048 0.046 to 0.048 ms; the smallest
+// calls about 8 us (launch, tensor memory, first tiles, stores).
 //
 // Tiles left over after the last full round of the pairs are split along the
 // tokens, so that they too keep every pair busy: each part leaves a float32
@@ -328,7 +328,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
             // elected lane issues.  The tensor cores queue only a few MMAs, so what lies between two steps' MMAs has to
             // be short: the next stage's barriers are asked before this one's MMAs are issued, and the answers come
             // while they run.  (4096 x 4096, 8192 tokens: 181 us with one thread that waits, issues and turns, and two
-            // scale warps that read into registers; 167 us so.) ----
+            // scale warps that read into registers; 160 to 168 us so.) ----
             int s = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
