@@ -34,10 +34,10 @@
 // tensor memory, so there is one accumulator, and the MMAs of a tile wait until
 // the last one's is read.
 //
-// Measured (8192 tokens, G = 128): N x K = 11008 x 4096 0.42 to 0.44 ms alone (1.7
-// PFLOP/s) and 0.50 ms when repeated for seconds, where the GPU stands at its power
-// limit; 4096 x 4096 0.160 to 0.168 ms, 2048 x 2048 0.046 to 0.048 ms; the smallest
-// calls about 8 us (launch, tensor memory, first tiles, stores).
+// Measured (8192 tokens, G = 128): N x K = 11008 x 4096 0.44 ms alone (1.69 PFLOP/s)
+// and 0.50 ms when repeated for seconds, where the GPU stands at its power limit;
+// 4096 x 4096 0.167 ms, 2048 x 2048 0.048 ms; the smallest calls about 9 us
+// (launch, tensor memory, first tiles, join).
 //
 // Tiles left over after the last full round of the pairs are split along the
 // tokens, so that they too keep every pair busy: each part leaves a float32
@@ -328,7 +328,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
             // elected lane issues.  The tensor cores queue only a few MMAs, so what lies between two steps' MMAs has to
             // be short: the next stage's barriers are asked before this one's MMAs are issued, and the answers come
             // while they run.  (4096 x 4096, 8192 tokens: 181 us with one thread that waits, issues and turns, and two
-            // scale warps that read into registers; 160 to 168 us so.) ----
+            // scale warps that read into registers; 167 us so.) ----
             int s = 0;
             uint32_t ph = 0, aph = 0;
             bool ok = true;
@@ -415,6 +415,13 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         uint32_t aph = 0;
         for (int64_t i = cid; i < items; i += nclusters, aph ^= 1u) {
             const Item it = item_at(i, plan);
+            // the column's factor on its way: it is read when the MMAs have ended, between them and the next tile's (in a
+            // register it would be one too many: 112 bytes of this kernel's registers then lie in local memory, and
+            // every call takes 3 us longer)
+            if (a.col_scale) {
+                const int64_t kp = it.k * kTile + (int64_t)rank * kHalf + 32 * q4 + lane;
+                if (kp < a.K) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.col_scale + kp));
+            }
             if (!__all_sync(kFull, mbar_wait_fast(acc_full, aph, abort))) break;
             tc_fence_after();
             const int kl = (int)rank * kHalf + 32 * q4 + lane;
@@ -433,15 +440,16 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 }
                 release();
             } else {
-                // all of it into registers, as pairs of rows, so that the next tile's MMAs may start
+                // all of it into registers, as pairs of rows, so that the next tile's MMAs may start; 8 columns at a
+                // time, which leaves nothing in local memory (16: 0.3 us more per call)
                 const float cs = a.col_scale && k < a.K ? a.col_scale[k] : 1.0f;
                 uint32_t w[kEpiRows / 2];
 #pragma unroll
-                for (int c = 0; c < kEpiRows; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld<16>(taddr + (uint32_t)c, v);
+                for (int c = 0; c < kEpiRows; c += 8) {
+                    uint32_t v[8];
+                    tmem_ld<8>(taddr + (uint32_t)c, v);
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2)
+                    for (int e = 0; e < 8; e += 2)
                         w[(c + e) / 2] = bf16x2(__uint_as_float(v[e]) * cs, __uint_as_float(v[e + 1]) * cs);
                 }
                 release();
