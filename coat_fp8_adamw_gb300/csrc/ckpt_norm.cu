@@ -154,10 +154,15 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const NormF
 // shared memory, each tensor's one bulk copy: the copies stay ahead without
 // registers.  A thread has two chunks of eight columns, T chunks apart, so that
 // neighbouring lanes read neighbouring 16 bytes of shared memory.  kThreads: most
-// threads of a block (512 leave 128 registers, enough for a row's elements;
-// with 1024, N > 8192, some of them wait in local memory).
+// threads of a block.  512: the compiler takes 96 registers, or 98 with a residual,
+// which is one too many for the 20 warps of two blocks of 320 threads (8192 x 5120
+// 67 us, a second wave); 320, bound to 96, is for them (52 us; where both fit, 2 %
+// slower).  1024 (N > 8192): 64 registers, so a row's elements are formed again
+// from shared memory after its sum instead of being held over it (8192 x 12288
+// and 16384 103 and 128 us; held, in local memory, 164 and 222; at N <= 5120 forming
+// them again for three or more blocks per SM costs 4 to 8 us).
 template <bool kRes, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs a, const Shape sh) {
+__global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_kernel(const NormBwdArgs a, const Shape sh) {
     __shared__ float slots[2][kMaxWarps];
     __shared__ uint64_t bars[kMaxDepth];
     extern __shared__ __align__(16) unsigned char dyn[];
@@ -221,9 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
         if (!mbar_wait_fast(bar0 + 8u * (uint32_t)s, ph, nullptr)) break;
         const unsigned char* st = ring + (size_t)s * sh.stage;
         uint64_t g[2][4], xh[2][4], c2 = 0ull;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (!live || !in_row[j]) continue;
+        auto values = [&](int j, uint64_t (&dy)[4]) {   // of eight elements: dy, g and xh
             const uint4 d = *reinterpret_cast<const uint4*>(st + ((size_t)team * N + col[j]) * 2);
             const uint2 q = *reinterpret_cast<const uint2*>(st + sh.b_off + (size_t)team * N + col[j]);
             const uint32_t dw4[4] = {d.x, d.y, d.z, d.w}, qw[2] = {q.x, q.y};
@@ -234,10 +237,19 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
             const uint64_t SS = pk(S[j], S[j]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint64_t gg = pk(gf[2 * e], gf[2 * e + 1]), ww = pk(w[2 * e], w[2 * e + 1]);
+                dy[e] = pk(gf[2 * e], gf[2 * e + 1]);
                 xh[j][e] = mul2(pk(xf[2 * e], xf[2 * e + 1]), SS);
-                dw[j][e] = fma2(gg, xh[j][e], dw[j][e]);
-                g[j][e] = mul2(gg, ww);
+                g[j][e] = mul2(dy[e], pk(w[2 * e], w[2 * e + 1]));
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (!live || !in_row[j]) continue;
+            uint64_t dy[4];
+            values(j, dy);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dw[j][e] = fma2(dy[e], xh[j][e], dw[j][e]);
                 c2 = fma2(g[j][e], xh[j][e], c2);
             }
         }
@@ -253,6 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_bwd_kernel(const NormBwdArgs
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if (!live || !in_row[j]) continue;
+            if constexpr (kThreads > 512) {   // formed again: 64 registers do not hold them over the barrier
+                uint64_t dy[4];
+                values(j, dy);
+            }
             uint32_t o[4];
             uint32_t p[4] = {};
             if constexpr (kRes) {
@@ -329,22 +345,27 @@ Shape bwd_shape(int64_t N, bool res) {
     sh.stage = res ? 5 * n : 3 * n;
     sh.b_off = 2 * n;
     sh.c_off = 3 * n;
-    // iterations in the ring: 8192 x 4096 takes 58 us with two, 44 with three or four; fewer where a row is too wide
-    sh.depth = 3;
+    // iterations in the ring: 8192 x 4096 takes 58 us with two, 44 with three or four; one block per SM (T > 320) wants
+    // four: 8192 x 8192 69 us with three, 66 with four; fewer where a row is too wide
+    sh.depth = sh.T > 320 ? 4 : 3;
     while (sh.depth > 2 && smem_of(sh) + 2048 > kSmem) --sh.depth;
     return sh;
 }
-// Blocks that run at once: by threads (`regs` of 64 K registers each) and by shared memory (2 KB more per block: the
-// static part, and the system's).
+// Blocks that run at once, so that the grid is one wave: by registers (`regs` per thread, a multiple of eight; each of the
+// SM's four parts has 16384 of them for whole warps) and by shared memory (2 KB more per block: the static part, and the
+// system's).
 int64_t blocks_of(int64_t M, const Shape& sh, int regs, int sms) {
-    int64_t per = 65536 / regs / (sh.T * sh.teams);
+    int64_t per = 4 * (16384 / (32 * regs)) / (sh.T * sh.teams / 32);
     const int64_t fit = (int64_t)(kSmem / (smem_of(sh) + 2048));
     if (per > fit) per = fit;
     if (per < 1) per = 1;
     const int64_t need = (M + sh.teams - 1) / sh.teams;
     return need < sms * per ? need : sms * per;
 }
-int64_t bwd_blocks(int64_t M, int64_t N, bool res, int sms) { return blocks_of(M, bwd_shape(N, res), 96, sms); }
+int64_t bwd_blocks(int64_t M, int64_t N, bool res, int sms) {
+    const Shape sh = bwd_shape(N, res);
+    return blocks_of(M, sh, sh.T <= 320 ? 96 : sh.T <= 512 ? 128 : 64, sms);
+}
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
@@ -407,7 +428,9 @@ cudaError_t launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s) {
     const Shape sh = bwd_shape(a.N, res);
     const int64_t blocks = bwd_blocks(a.M, a.N, res, device_sms());
     cudaError_t e;
-    if (sh.T <= 512)
+    if (res && sh.T <= 320 && sh.T * sh.teams != 256)   // 256 threads: two blocks with 104 registers as with 96
+        e = launch_bwd<true, 320>(a, blocks, sh, s);
+    else if (sh.T <= 512)
         e = res ? launch_bwd<true, 512>(a, blocks, sh, s) : launch_bwd<false, 512>(a, blocks, sh, s);
     else
         e = res ? launch_bwd<true, 1024>(a, blocks, sh, s) : launch_bwd<false, 1024>(a, blocks, sh, s);

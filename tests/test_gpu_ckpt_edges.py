@@ -374,3 +374,10 @@ def test_every_positive_eps(eps):
     rr = R.rmsnorm(x.double().view(M, N // D, D), w[:D].double(), eps)[1]
     near(rh, rr, 2.0 ** -19 * rr, "head rstd")
     assert not y[1].float().any()
+
+
+@pytest.mark.parametrize("N", [3584, 4608, 5120, 5136, 6656, 8192, 8208, 9728, 16384])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_around_the_widths_where_blocks_change(N, res):
+    """Rows for several rounds of one, two or three blocks per SM."""
+    _norm_both_ways(1201, N, 16, N + 1, res)
