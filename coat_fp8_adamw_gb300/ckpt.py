@@ -39,9 +39,9 @@ def _rows(t, M: int, width: int, name: str, device):
     try:   # the common layouts in one expression, as in _ptr
         if t.dtype is _BF16 and t.get_device() == device.index and t.numel() == M * width:
             st = t.stride()
-            if (st[-1] == 1 and t.shape[0] == M > 1
+            if (st[-1] == 1 and t.shape[0] == M
                     and (len(st) == 2 or (len(st) == 3 and st[1] == t.shape[2]))):
-                return t.data_ptr(), st[0]
+                return t.data_ptr(), (st[0] if M > 1 else width)
     except (AttributeError, IndexError):
         pass
     if not isinstance(t, torch.Tensor):
@@ -84,7 +84,7 @@ def _call(name: str, device, stream, *args) -> None:
         raw = torch._C._cuda_getCurrentRawStream(device.index)
     else:
         raw = _stream_ptr(stream)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
