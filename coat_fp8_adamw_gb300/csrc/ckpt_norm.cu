@@ -15,8 +15,8 @@
 // access of a bf16 tensor and one 128-bit access of codes; every tensor is read
 // and written once.
 //
-// Bound by memory.  8192 x 4096, G = 128, with a residual: forward 46.8 us, 97 %
-// of the copy rate; backward 43.6 us, of which 8 to 9 do not depend on the rows
+// Bound by memory.  8192 x 4096, G = 128, with a residual: forward 46.3 us, 98 %
+// of the copy rate (without a residual 31.5 us, 80 %); backward 43.6 us, of which 8 to 9 do not depend on the rows
 // (two kernels, the ring's first rows, the sum over the blocks' dw: 4099 x 5120
 // takes 27.0 us, 60 % of the copy rate).  Forward one row per block and no loop,
 // so that blocks in different phases keep loads on their way; backward persistent
@@ -83,13 +83,24 @@ __device__ __forceinline__ void weights_of(const float4* sw, int items, int i, f
     }
 }
 
+// Eight weights, in pairs: one 256-bit access where `wide`, which L1 serves in half the passes of two (a lane's sixteen
+// lie 64 bytes from the next lane's; 8192 x 4096 without a residual 35.4 us with 128-bit accesses, 31.5 so)
+__device__ __forceinline__ void load_weights8(const float* p, bool wide, uint64_t (&w)[4]) {
+    if (wide) {
+        asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(w[0]), "=l"(w[1]), "=l"(w[2]), "=l"(w[3]) : "l"(p));
+    } else {
+        const ulonglong2 lo = reinterpret_cast<const ulonglong2*>(p)[0], hi = reinterpret_cast<const ulonglong2*>(p)[1];
+        w[0] = lo.x; w[1] = lo.y; w[2] = hi.x; w[3] = hi.y;
+    }
+}
+
 // Forward: a block has its rows once, a thread sixteen consecutive elements (so that a
 // group of G >= 16 is G / 16 lanes).  What keeps the memory busy are many small
-// blocks per SM in different phases: at 8192 x 4096 with a residual 46.8 us with
+// blocks per SM in different phases: at 8192 x 4096 with a residual 46.3 us with
 // 40 registers (six blocks of 256 threads per SM), 51.0 with 50 (four); blocks
 // that walk the rows through a ring of bulk copies, as backward, took 53.3.
 template <bool kRes, int kThreads, int kBlocks>
-__global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const NormFwdArgs a, const Shape sh, bool wide) {
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const NormFwdArgs a, const Shape sh, bool wide, bool wide_w) {
     __shared__ float slots[kMaxWarps];
     const int T = sh.T, teams = sh.teams, N = sh.N;
     const int team = threadIdx.x / T, t = threadIdx.x - team * T;
@@ -134,15 +145,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const NormF
     if (ok) {
         uint32_t u[8];
         const uint64_t r2 = pk(rstd, rstd);
-        const ulonglong2* wp = reinterpret_cast<const ulonglong2*>(a.weight + col);
 #pragma unroll
-        for (int e = 0; e < kE / 4; ++e) {
-            const ulonglong2 w = wp[e];
-            float lo, hi;
-            upk(mul2(mul2(x[2 * e], r2), w.x), lo, hi);
-            u[2 * e] = bf16x2(lo, hi);
-            upk(mul2(mul2(x[2 * e + 1], r2), w.y), lo, hi);
-            u[2 * e + 1] = bf16x2(lo, hi);
+        for (int h = 0; h < 2; ++h) {
+            uint64_t w[4];
+            load_weights8(a.weight + col + 8 * h, wide_w, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float lo, hi;
+                upk(mul2(mul2(x[4 * h + e], r2), w[e]), lo, hi);
+                u[4 * h + e] = bf16x2(lo, hi);
+            }
         }
         store_words8(a.y + at, wide, u);
         if (t == 0) a.rstd[r] = rstd;
@@ -380,15 +392,16 @@ template <bool kRes>
 cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
     const Shape sh = team_shape(a.N);
     const bool wide = aligned32(a.x) && aligned32(a.residual) && aligned32(a.h) && aligned32(a.y);
+    const bool wide_w = aligned32(a.weight);
     const unsigned blocks = (unsigned)((a.M + sh.teams - 1) / sh.teams);
     const int threads = sh.T * sh.teams;
     if (threads <= 256)
-        return launch_next(norm_fwd_kernel<kRes, 256, 6>, blocks, threads, 0, s, a, sh, wide);
+        return launch_next(norm_fwd_kernel<kRes, 256, 6>, blocks, threads, 0, s, a, sh, wide, wide_w);
     if (threads <= 512)
-        return launch_next(norm_fwd_kernel<kRes, 512, 3>, blocks, threads, 0, s, a, sh, wide);
+        return launch_next(norm_fwd_kernel<kRes, 512, 3>, blocks, threads, 0, s, a, sh, wide, wide_w);
     // two blocks per SM up to N = 12288 (8192 x 12288: 169 us with one, 117 with two)
-    if (threads <= 768) return launch_next(norm_fwd_kernel<kRes, 768, 2>, blocks, threads, 0, s, a, sh, wide);
-    return launch_next(norm_fwd_kernel<kRes, 1024, 1>, blocks, threads, 0, s, a, sh, wide);
+    if (threads <= 768) return launch_next(norm_fwd_kernel<kRes, 768, 2>, blocks, threads, 0, s, a, sh, wide, wide_w);
+    return launch_next(norm_fwd_kernel<kRes, 1024, 1>, blocks, threads, 0, s, a, sh, wide, wide_w);
 }
 
 template <bool kRes, int kThreads>
