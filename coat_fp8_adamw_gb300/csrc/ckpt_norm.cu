@@ -399,7 +399,7 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
         return launch_next(norm_fwd_kernel<kRes, 256, 6>, blocks, threads, 0, s, a, sh, wide, wide_w);
     if (threads <= 512)
         return launch_next(norm_fwd_kernel<kRes, 512, 3>, blocks, threads, 0, s, a, sh, wide, wide_w);
-    // two blocks per SM up to N = 12288 (8192 x 12288: 169 us with one, 117 with two)
+    // two blocks per SM up to N = 12288 (8192 x 12288 without a residual: 169 us with one, 117 with two; 103 now)
     if (threads <= 768) return launch_next(norm_fwd_kernel<kRes, 768, 2>, blocks, threads, 0, s, a, sh, wide, wide_w);
     return launch_next(norm_fwd_kernel<kRes, 1024, 1>, blocks, threads, 0, s, a, sh, wide, wide_w);
 }
