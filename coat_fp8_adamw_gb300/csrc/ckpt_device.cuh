@@ -8,6 +8,7 @@
 // quantization, 1 x G groups for non-linear layers).
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 #include "coat_device.cuh"
@@ -262,6 +263,13 @@ __device__ __forceinline__ float rsqrt_newton(float v) {
     asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
     return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
 }
+
+// Where a mean square is past float32 (elements from about 2^57 on, finite ones), it is formed of kFar times the elements:
+// the largest sum, 16384 squares of 2^56, and the smallest that comes here, 2^128 kFar^2, are normal numbers.  far_rsqrt:
+// what such elements are multiplied with, 1 / sqrt of their mean square; 0 if one is infinite, as 1 / sqrt(inf).  kFar
+// times that is 1 / rms itself.
+constexpr float kFar = 0x1p-72f;
+__device__ __forceinline__ float far_rsqrt(float v) { return v == INFINITY ? 0.0f : rsqrt_newton(v); }
 
 // sigmoid(x) = 1 / (1 + 2^(-x log2 e)); x -> -inf gives 0, +inf gives 1.
 __device__ __forceinline__ float sigmoid(float x) { return rcp_ftz(1.0f + ex2_ftz(-1.4426950408889634f * x)); }

@@ -206,8 +206,42 @@ __device__ __forceinline__ void cp_async_wait(int n) {
 }
 static_assert(kRing == 4, "cp_async_wait");
 
+// The output and 1 / rms of those of a warp's heads, `from` to `to` of token m, whose mean square left float32's range (the
+// usual path has written NaN): the sum is formed of kFar times the entries.  The whole warp comes here, behind its last
+// pass, and takes everything from memory, so that the passes only note that there is such a head.
+__device__ __noinline__ void far_heads(const QkArgs& a, const HeadSide& sd, int64_t m, int from, int to, int lane) {
+    __syncwarp();                              // the lanes see each other's 1 / rms
+    const int64_t pos = a.positions[m];
+    const int half = a.rot / 2;
+    for (int h = from; h < to; ++h) {
+        const int64_t row = m * sd.H + h;
+        if (sd.rstd[row] > 0.0f) continue;
+        const uint16_t* x = sd.in + m * sd.ld + (int64_t)h * a.D;
+        auto entry = [&](int c) { return __uint_as_float((uint32_t)x[c] << 16) * kFar; };
+        float ss = 0.0f;
+        for (int c = lane; c < a.D; c += 32) ss = fmaf(entry(c), entry(c), ss);
+        const float r = far_rsqrt(fmaf(warp_sum(ss), 1.0f / (float)a.D, a.eps * kFar * kFar));
+        for (int c = lane; c < a.D; c += 32) {
+            float y = entry(c) * sd.weight[c];
+            if (c < a.rot) {
+                const bool second = a.interleaved ? (c & 1) != 0 : c >= half;
+                const int i = a.interleaved ? c >> 1 : second ? c - half : c;      // the pair, and its other entry
+                const int p = a.interleaved ? c ^ 1 : second ? c - half : c + half;
+                const bool in = pos >= 0 && pos < a.max_pos;
+                const float co = in ? a.cos[pos * half + i] : __uint_as_float(0x7FC00000u);
+                const float si = in ? a.sin[pos * half + i] : co;
+                const float z = entry(p) * sd.weight[p] * si;
+                y = fmaf(y, co, second ? z : -z);
+            }
+            sd.out[row * a.D + c] = bf16_bits(y * r);
+        }
+        __syncwarp();
+        if (lane == 0) sd.rstd[row] = r * kFar;
+    }
+}
+
 template <int kLanes, bool kInter>
-__global__ void __launch_bounds__(kFwdBlock, kFwdPerSm) qk_fwd_kernel(const QkArgs a, const Task tk) {
+__global__ void __launch_bounds__(kFwdBlock, kFwdPerSm) qk_fwd_kernel(const __grid_constant__ QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;   // heads per warp and pass
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), base = lane - l, sub = lane / kLanes;
     const bool is_q = blockIdx.x < tk.blocks_q;
@@ -253,6 +287,7 @@ __global__ void __launch_bounds__(kFwdBlock, kFwdPerSm) qk_fwd_kernel(const QkAr
     int64_t hd = (row + h0) * a.D;                       // the head's place in the outputs
     float* sc = sd.scale + (row + h0) * gpr;
     float* rs = sd.rstd + row + h0;
+    bool far = false;
     for (int i = 0, h = h0; from + i < to; ++i, h += kHeads) {
         const bool ok = in_head && h < sd.H;
         fetch(i + kRing - 1);
@@ -267,7 +302,8 @@ __global__ void __launch_bounds__(kFwdBlock, kFwdPerSm) qk_fwd_kernel(const QkAr
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss2 = fma2(x2[e], x2[e], ss2);
         const float ss = head_sum<kLanes>(sum2(ss2));
-        const float r = rsqrt_newton(fmaf(ss, inv_d, a.eps));
+        const float v = fmaf(ss, inv_d, a.eps), r = rsqrt_newton(v);
+        far |= !(v < INFINITY);
         float ma = max_of<0, 4>(x2), mb = max_of<4, 4>(x2);
         group_maxima(ma, mb, tk.mode, kLanes, l, base, a);
         const Scale sa = scale_of_bf16_max(ma);
@@ -294,6 +330,7 @@ __global__ void __launch_bounds__(kFwdBlock, kFwdPerSm) qk_fwd_kernel(const QkAr
         sc += kHeads * gpr;
         rs += kHeads;
     }
+    if (__any_sync(kFull, far)) far_heads(a, is_q ? a.q : a.k, m, from * kHeads, min(to * kHeads, sd.H), lane);
 }
 
 // A lane's ring, and the angles of its token and of the next one.
