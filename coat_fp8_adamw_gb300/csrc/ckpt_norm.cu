@@ -26,6 +26,7 @@
 
 #include "ckpt_device.cuh"
 #include "ckpt_kernels.h"
+#include "ring.h"
 #include "tc_pipeline.cuh"
 
 namespace coat {
@@ -55,10 +56,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // Each team's sum of v over its threads; a barrier of the whole block.
 // slots: one float per warp, for this use alone until the next one's barrier;
 // `span`: the power of two that the team's warps are rounded up to.
-__device__ __forceinline__ float team_sum(float v, float* slots, int warps, int span, int warp, int lane) {
+// `stop`, where it is given: set to what `flag` holds behind the barrier.
+__device__ __forceinline__ float team_sum(float v, float* slots, int warps, int span, int warp, int lane,
+                                          const volatile uint32_t* flag = nullptr, uint32_t* stop = nullptr) {
     v = warp_sum(v);
     if (lane == 0) slots[warp] = v;
     __syncthreads();
+    if (flag) *stop = *flag;
     if (warps == 1) return v;
     const int i = lane & (span - 1);
     float s = i < warps ? slots[i] : 0.0f;
@@ -196,8 +200,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const __gri
 // shared memory, each tensor's one bulk copy: the copies stay ahead without
 // registers.  A thread has two chunks of eight columns, T chunks apart, so that
 // neighbouring lanes read neighbouring 16 bytes of shared memory.  kThreads: most
-// threads of a block.  512: the compiler takes 96 registers, or 98 with a residual,
-// which is one too many for the 20 warps of two blocks of 320 threads (8192 x 5120
+// threads of a block.  512: the compiler takes 96 registers, or 99 with a residual,
+// which is too many for the 20 warps of two blocks of 320 threads (8192 x 5120
 // 67 us, a second wave); 320, bound to 96, is for them (52 us; where both fit, 2 %
 // slower).  1024 (N > 8192): 64 registers, so a row's elements are formed again
 // from shared memory after its sum instead of being held over it (8192 x 12288
@@ -207,6 +211,7 @@ template <bool kRes, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_kernel(const NormBwdArgs a, const Shape sh) {
     __shared__ float slots[2][kMaxWarps];
     __shared__ uint64_t bars[kMaxDepth];
+    __shared__ uint32_t lost[2];       // a wait gave up in an even, in an odd iteration
     extern __shared__ __align__(16) unsigned char dyn[];
     const int T = sh.T, teams = sh.teams, N = sh.N, depth = sh.depth;
     float4* sw = reinterpret_cast<float4*>(dyn);
@@ -217,24 +222,26 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
     const float inv_n = 1.0f / (float)N;
     const int64_t ngr = N >> gshift;
     const uint32_t bar0 = smem_u32(bars), ring0 = smem_u32(ring);
-    const int64_t step = (int64_t)gridDim.x * teams, first = (int64_t)blockIdx.x * teams;
-    auto issue = [&](int64_t r0, int s) {
-        const int64_t left = a.M - r0;
-        const uint32_t n = (uint32_t)(left < teams ? left : teams) * (uint32_t)N;
+    // rows as 32-bit numbers: M < 2^31, and a ring's rows beyond the last one stay far below 2^32
+    const uint32_t M = (uint32_t)a.M, step = gridDim.x * (uint32_t)teams, first = blockIdx.x * (uint32_t)teams;
+    auto issue = [&](uint32_t r0, int s) {
+        const uint32_t n = min(M - r0, (uint32_t)teams) * (uint32_t)N;
         const uint32_t d = ring0 + (uint32_t)s * sh.stage, bar = bar0 + 8u * (uint32_t)s;
         mbar_expect_tx(bar, n * (kRes ? 5u : 3u));
-        bulk_load(d, a.dy + r0 * N, 2 * n, bar);
-        bulk_load(d + sh.b_off, a.q + r0 * N, n, bar);
-        if constexpr (kRes) bulk_load(d + sh.c_off, a.dresidual + r0 * N, 2 * n, bar);
+        const int64_t at = (int64_t)r0 * N;
+        bulk_load(d, a.dy + at, 2 * n, bar);
+        bulk_load(d + sh.b_off, a.q + at, n, bar);
+        if constexpr (kRes) bulk_load(d + sh.c_off, a.dresidual + at, 2 * n, bar);
     };
     if (threadIdx.x == 0) {
         for (int s = 0; s < depth; ++s) mbar_init(bar0 + 8u * (uint32_t)s, 1);
+        lost[0] = lost[1] = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     wait_for_primary();
     if (threadIdx.x == 0) {
         for (int s = 0; s < depth; ++s)
-            if (first + s * step < a.M) issue(first + s * step, s);
+            if (first + s * step < M) issue(first + s * step, s);
     }
     stage_weights<8>(a.weight, N, 2 * T, sw);
     __syncthreads();
@@ -249,23 +256,24 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw[j][e] = 0ull;
     }
-    auto fetch_scales = [&](int64_t r) {   // one iteration ahead
-        if (r < a.M) {
+    auto fetch_scales = [&](uint32_t r) {   // one iteration ahead
+        if (r < M) {
             rn = a.rstd[r];
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (in_row[j]) Sn[j] = a.scale[r * ngr + (col[j] >> gshift)];
+                if (in_row[j]) Sn[j] = a.scale[(int64_t)r * ngr + (col[j] >> gshift)];
         }
     };
     fetch_scales(first + team);
     int s = 0;
     uint32_t ph = 0;
-    for (int64_t r0 = first, it = 0; r0 < a.M; r0 += step, ++it) {
-        const int64_t r = r0 + team;
-        const bool live = r < a.M;         // a team past the last row only keeps step
+    uint32_t r0 = first, it = 0;
+    for (; r0 < M; r0 += step, ++it) {
+        const uint32_t r = r0 + team;
+        bool live = r < M;                 // a team past the last row only keeps step
         const float rstd = rn, S[2] = {Sn[0] * rn, Sn[1] * rn};
         fetch_scales(r + step);
-        if (!mbar_wait_fast(bar0 + 8u * (uint32_t)s, ph, nullptr)) break;
+        mbar_wait_fast(bar0 + 8u * (uint32_t)s, ph, &lost[it & 1]);   // what it says is asked behind the barrier
         const unsigned char* st = ring + (size_t)s * sh.stage;
         uint64_t g[2][4], xh[2][4], c2 = 0ull;
         auto values = [&](int j, uint64_t (&dy)[4]) {   // of eight elements: dy, g and xh
@@ -297,11 +305,15 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
         }
         float c0, c1;
         upk(c2, c0, c1);
-        const float c = team_sum(c0 + c1, slots[it & 1] + team * warps, warps, sh.span, warp, lane) * inv_n;
+        uint32_t stop;
+        const float c = team_sum(c0 + c1, slots[it & 1] + team * warps, warps, sh.span, warp, lane, &lost[it & 1], &stop) * inv_n;
+        // a wait that gave up ends the loop for the whole block (below): the flag is read between this iteration's barrier
+        // and the next one, and written before the one or behind the other
+        live = live && stop == 0u;
         // behind that barrier every thread is done with the iteration before this one: its stage is free
-        if (threadIdx.x == 0 && it > 0) {
-            const int64_t rr = r0 + (depth - 1) * step;
-            if (rr < a.M) issue(rr, s == 0 ? depth - 1 : s - 1);
+        if (threadIdx.x == 0 && it > 0 && stop == 0u) {
+            const uint32_t rr = r0 + (depth - 1) * step;
+            if (rr < M) issue(rr, s == 0 ? depth - 1 : s - 1);
         }
         const uint64_t nc = pk(-c, -c), rr2 = pk(rstd, rstd);
 #pragma unroll
@@ -325,12 +337,13 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
                 upk(kRes ? fma2(d, rr2, res) : mul2(d, rr2), lo, hi);
                 o[e] = bf16x2(lo, hi);
             }
-            *reinterpret_cast<uint4*>(a.dx + r * N + col[j]) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(a.dx + (int64_t)r * N + col[j]) = make_uint4(o[0], o[1], o[2], o[3]);
         }
+        if (stop != 0u) break;
         if (++s == depth) { s = 0; ph ^= 1u; }
     }
     dependents_may_start();
-    float* part = a.partial + (first + team) * N;
+    float* part = a.partial + (int64_t)(first + team) * N;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
         if (in_row[j]) {
@@ -338,6 +351,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
             p[0] = make_ulonglong2(dw[j][0], dw[j][1]);
             p[1] = make_ulonglong2(dw[j][2], dw[j][3]);
         }
+    // stopped early: the copies on their way have to land before the block may leave its shared memory
+    if (r0 < M && threadIdx.x == 0)
+        ring_drain(it, (M - first + step - 1) / step, depth,
+                   [&](int stage, uint32_t parity) { mbar_wait(bar0 + 8u * (uint32_t)stage, parity, nullptr); });
 }
 
 // kCols columns of one of two sums per block, 1024 / kCols rows of the partial sums side by side and four more on their
