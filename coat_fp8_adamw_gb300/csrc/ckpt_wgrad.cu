@@ -181,15 +181,25 @@ __device__ __forceinline__ uint32_t elect_one() {
 }
 
 // whether the phase is over, without a wait (a try may hold the warp until its phase ends)
+template <bool kRelaxed = false>
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (kRelaxed)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0u;
 }
 
@@ -337,19 +347,19 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
             bool ready = false;
             for (int64_t i = cid; ok && i < items; i += nclusters, aph ^= 1u) {
                 const Item it = item_at(i, plan);
-                ok = __all_sync(kFull, mbar_wait_fast(acc_empty, aph ^ 1u, abort));
+                ok = __all_sync(kFull, mbar_wait_relaxed(acc_empty, aph ^ 1u, abort));
                 if (!ok) break;
                 tc_fence_after();
                 for (int32_t st = it.from; st < it.to; ++st) {
                     if (!ready) {
-                        ok = __all_sync(kFull, mbar_wait_fast(y_full(s), ph, abort) && mbar_wait_fast(x_full(s), ph, abort));
+                        ok = __all_sync(kFull, mbar_wait_fast(y_full(s), ph, abort) && mbar_wait_relaxed(x_full(s), ph, abort));
                         if (!ok) break;
                     }
                     tc_fence_after();
                     const uint64_t yd = ydesc0 + (uint64_t)(s * (kStageBytes >> 4));
                     const uint32_t xd = xmem + (uint32_t)s * kXCols, freed = empty(s);
                     if (++s == kStages) { s = 0; ph ^= 1u; }
-                    const bool y_in = mbar_test(y_full(s), ph), x_in = mbar_test(x_full(s), ph);
+                    const bool y_in = mbar_test(y_full(s), ph), x_in = mbar_test<true>(x_full(s), ph);
                     if (elected) {
 #pragma unroll
                         for (int kk = 0; kk < kTok / kMmaTok; ++kk)
@@ -410,7 +420,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
         auto release = [&]() {                     // the accumulator has been read
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(ae);
+            if (lane == 0) mbar_arrive_relaxed(ae);
         };
         uint32_t aph = 0;
         for (int64_t i = cid; i < items; i += nclusters, aph ^= 1u) {
@@ -516,7 +526,7 @@ wgrad_kernel(const __grid_constant__ CUtensorMap tmy, const __grid_constant__ CU
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_at(xb0 + 8u * (uint32_t)s);
+                if (lane == 0) mbar_arrive_relaxed(xb0 + 8u * (uint32_t)s);
                 if (++s == kStages) { s = 0; ph ^= 1u; }
             }
         }

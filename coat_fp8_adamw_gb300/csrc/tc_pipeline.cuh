@@ -26,22 +26,34 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// kRelaxed: at cluster scope and without an acquire, the other side of mbar_arrive_relaxed
+template <bool kRelaxed = false>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (kRelaxed)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0u;
 }
 // Wait for the phase of parity `parity` to complete, at most kSpinLimit
 // polls; give up early once another role has aborted (when `abort` is given).
+template <bool kRelaxed = false>
 __device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
     for (uint32_t i = 0; i < kSpinLimit; ++i) {
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<kRelaxed>(bar, parity)) return true;
         if (abort && (i & 255u) == 255u && *abort) return false;
     }
     atomicAdd(&g_wait_timeouts, 1ull);
@@ -52,6 +64,9 @@ __device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile u
 __device__ __forceinline__ bool mbar_wait_fast(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
     return mbar_try(bar, parity) || mbar_wait(bar, parity, abort);
 }
+__device__ __forceinline__ bool mbar_wait_relaxed(uint32_t bar, uint32_t parity, volatile uint32_t* abort) {
+    return mbar_try<true>(bar, parity) || mbar_wait<true>(bar, parity, abort);
+}
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -60,13 +75,14 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
-// The same in the instruction's default form (release at CTA scope).  For a
-// signal whose data stays in the arriving CTA's shared memory and is read there
-// by the pair's MMA: the writes are ordered before that asynchronous read by
-// each writer's fence.proxy.async, not by the arrival, which only has to come
-// after it.  (A release to the cluster holds the arriving warp for about 0.6 us.)
-__device__ __forceinline__ void mbar_arrive_at(uint32_t cbar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
+// The same without a release, for a signal about tensor memory alone: what this thread's CTA wrote to tensor memory (or
+// read from it) before the arrival, the waiting thread's MMAs read (or overwrite) behind it.  tcgen05.wait has completed
+// those accesses, tcgen05.fence::before_thread_sync here and ::after_thread_sync behind the wait (mbar_wait_relaxed) order
+// them around the barrier, and the scope of both has to take in both CTAs; no ordinary memory is passed on, so there is
+// nothing for a release to make visible.  (A release to the cluster holds the arriving warp for about 0.6 us: the weight
+// gradient of 8192 tokens x 11008 x 4096 takes 1200 us with it, 430 so.)
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cbar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
 
 // ---- clusters ----
