@@ -346,7 +346,6 @@ template <int kLanes, bool kInter>
 __global__ void __launch_bounds__(kBlock, kPerSm) qk_bwd_kernel(const QkArgs a, const Task tk) {
     constexpr int kHeads = 32 / kLanes;
     __shared__ BwdShared sh;
-    __shared__ float part_sum[kWarps][16 * kLanes];
     const int lane = threadIdx.x & 31, l = lane & (kLanes - 1), sub = lane / kLanes, warp = threadIdx.x >> 5;
     const bool is_q = blockIdx.x < tk.blocks_q;
     const HeadSide sd = is_q ? a.q : a.k;
@@ -491,7 +490,10 @@ __global__ void __launch_bounds__(kBlock, kPerSm) qk_bwd_kernel(const QkArgs a, 
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     dependents_may_start();
-    // the block's sums: the warp's heads by shuffles, then its warps in order
+    // the block's sums: the warp's heads by shuffles, then its warps in order, where the rings were (beside them they would
+    // take a block of D = 256 past the 48 KB of static shared memory)
+    float(*part_sum)[16 * kLanes] = reinterpret_cast<float(*)[16 * kLanes]>(&sh);
+    static_assert(sizeof(float) * kWarps * 16 * kLanes <= sizeof(sh) && sizeof(sh) <= 48 << 10, "shared memory");
     float dw[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) upk(dw2[e], dw[2 * e], dw[2 * e + 1]);
@@ -500,6 +502,7 @@ __global__ void __launch_bounds__(kBlock, kPerSm) qk_bwd_kernel(const QkArgs a, 
 #pragma unroll
         for (int off = 16; off >= kLanes; off >>= 1) dw[e] += __shfl_xor_sync(kFull, dw[e], off);
     }
+    __syncthreads();                           // every warp is done with its ring
     if (sub == 0 && in_head) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
