@@ -25,6 +25,7 @@
 
 #include "ckpt_device.cuh"
 #include "ckpt_kernels.h"
+#include "divide.h"
 
 namespace coat {
 
@@ -33,23 +34,6 @@ namespace {
 using namespace ckpt;
 
 constexpr int kBlock = 256;
-
-// n / d for n < 2^31, d >= 1: (n mul) >> (32 + shift) with mul = ceil(2^(32 + shift) / d), shift = ceil(log2 d) - 1
-// (the error of mul is below 2^-shift of its unit times n < 2^31: it never reaches the next quotient).
-struct Divider {
-    uint32_t d, mul;
-    int shift;
-};
-Divider divider(uint32_t d) {
-    Divider v{d, 0u, 0};
-    if (d == 1) return v;
-    while ((1ull << (v.shift + 1)) < d) ++v.shift;
-    v.mul = (uint32_t)(((1ull << (32 + v.shift)) + d - 1) / d);
-    return v;
-}
-__device__ __forceinline__ uint32_t divide(uint32_t n, const Divider& v) {
-    return v.d == 1 ? n : __umulhi(n, v.mul) >> v.shift;
-}
 
 // Chunk i of the rows of nc chunks: its first element in a tensor whose rows are ld apart.
 __device__ __forceinline__ int64_t strided_at(uint32_t i, const Divider& nc, int64_t ld) {
