@@ -279,7 +279,8 @@ def coat_ckpt_weight_grad_workspace_bytes(M: int, N: int, K: int, device=None) -
 def coat_ckpt_weight_grad(dy, q, scale, G: int, dw, workspace, row_scale=None, col_scale=None,
                           stream=None) -> None:
     """Weight gradient of a linear layer from the checkpoint of its input:
-    dw bf16 [N, K] = (dy^T X) col_scale, X = row_scale scale E4M3(q), for dy bf16
+    dw bf16 [N, K] = (dy^T X) col_scale, X = row_scale scale E4M3(q) rounded to
+    bf16 (the operand of the tensor cores; sums are float32), for dy bf16
     [M, N] (rows at any distance), q uint8 [M, K], scale float32 [M, K/G],
     row_scale float32 [M] and col_scale float32 [K] (1 when not given).  With a
     norm's rstd and weight the checkpoint of the norm's input stands for its

@@ -307,19 +307,20 @@ coat_status coat_kernel_wait_timeouts(uint64_t *count, int32_t reset);
  * group of zeros has scale 0 and zero codes.  It stands for scale E4M3(q).
  *
  * For all of them: bf16 tensors are raw 16-bit patterns; everything between
- * input and output is float32, rounded once where an output is bf16; G is a
- * power of two in [8, 128] (COAT_ERR_UNSUPPORTED_G otherwise); widths are
- * multiples of 16 and of G; row counts are at least 1; row strides (`ld`, in
- * elements) are at least the row's width and multiples of 8; every pointer is
- * 16-byte aligned; outputs overlap neither inputs nor each other, except that
- * two outputs with row strides may be column ranges of one tensor.  Gradients
- * of weights come as bf16, the type that coat_fp8_adamw_step reads, and norm
- * weights as fp32, the type of its master weights.  Results do not depend on
- * the order in which blocks run.  `workspace` is scratch of the caller's (its
- * content before the call does not matter, and two calls that may run at once
- * need one each); the *_workspace_bytes functions say how much a call on the
- * current device needs (0: bad sizes), and a smaller one is
- * COAT_ERR_INVALID_ARG.
+ * input and output is float32, rounded once where an output is bf16 (but for
+ * the weight gradient's operand, which goes to the tensor cores as bf16: see
+ * there); G is a power of two in [8, 128] (COAT_ERR_UNSUPPORTED_G otherwise);
+ * widths are multiples of 16 and of G; row counts are at least 1; row strides
+ * (`ld`, in elements) are at least the row's width and multiples of 8; every
+ * pointer is 16-byte aligned; outputs overlap neither inputs nor each other,
+ * except that two outputs with row strides may be column ranges of one tensor.
+ * Gradients of weights come as bf16, the type that coat_fp8_adamw_step reads,
+ * and norm weights as fp32, the type of its master weights.  Results do not
+ * depend on the order in which blocks run.  `workspace` is scratch of the
+ * caller's (its content before the call does not matter, and two calls that
+ * may run at once need one each); the *_workspace_bytes functions say how much
+ * a call on the current device needs (0: bad sizes, or, for the weight
+ * gradient, none), and a smaller one is COAT_ERR_INVALID_ARG.
  * ---------------------------------------------------------------------------
  */
 
@@ -352,6 +353,9 @@ size_t coat_rmsnorm_ckpt_backward_workspace_bytes(int64_t M, int64_t N);
 
 /*
  * h = silu(gate) up with checkpoints of gate and up, silu(g) = g / (1 + e^-g).
+ * Here and backward, s(g) = 1 / (1 + e^-g) is formed by the hardware's
+ * approximations of 2^x and 1 / x: within (|g| + 8) 2^-23 of itself, relatively,
+ * and 0 where 1 + e^-g is 2^126 or more (g below about -87.3).
  *   gate, up  M rows of N bf16, ld apart (column ranges of one tensor, or two
  *             tensors), in;
  *   h [M x N] bf16 out;  gate_q, up_q [M x N] uint8 out;
@@ -422,7 +426,13 @@ size_t coat_qk_norm_rope_ckpt_backward_workspace_bytes(int64_t M, int32_t D);
 
 /*
  * Weight gradient of a linear layer y = x W^T from the checkpoint of x:
- *   dw[n, k] = col_scale[k] sum over m of dy[m, n] row_scale[m] scale[m, k/G] E4M3(q[m, k]).
+ *   dw[n, k] = col_scale[k] sum over m of dy[m, n] X[m, k],
+ *   X[m, k] = row_scale[m] scale[m, k/G] E4M3(q[m, k]) rounded to bf16.
+ * A scale belongs to one token and G columns and the sum runs over tokens, so X
+ * is formed before the product, as the type that dy has and the tensor cores
+ * multiply; products are added in float32, times col_scale, and rounded to bf16.
+ * So dw is within 2^-8 |dw| + (2^-8 + (M + 8) 2^-22) |col_scale| sum |dy X| of the
+ * sum of exact X: an entry whose terms cancel has an error of the terms' size.
  *   dy  M rows of N bf16, dy_ld apart, in;  q [M x K] uint8, scale [M x K/G] in;
  *   row_scale [M], col_scale [K] in, or NULL: factors of 1.  With a norm's rstd
  *   and weight, the checkpoint of the norm's INPUT stands for its output, so
