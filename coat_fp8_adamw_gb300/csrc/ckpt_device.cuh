@@ -1,6 +1,7 @@
 // ckpt_device.cuh -- what the operators with 8-bit activation checkpoints share
-// on the device: eight bf16 values per 16-byte access, a group's scale and
-// E4M3 codes, and codes back to values.
+// on the device: sixteen bf16 values per thread in one 256-bit access (two of
+// 128 bits where the address is a multiple of 16 bytes alone), a group's scale
+// and E4M3 codes, and codes back to values.
 //
 // A checkpoint of a row is the one coat_act_quantize_fp8 writes: per group of G
 // consecutive elements S = RN(max|x| / 448) and q = E4M3(x / S), rounded to
@@ -49,13 +50,6 @@ __device__ __forceinline__ void store_words8(void* p, bool wide, const uint32_t 
         reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
         reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
-}
-
-// 32 bytes of shared memory
-__device__ __forceinline__ void read8(const void* p, uint32_t (&w)[8]) {
-    const uint4 lo = reinterpret_cast<const uint4*>(p)[0], hi = reinterpret_cast<const uint4*>(p)[1];
-    w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
-    w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
 }
 
 // ---- programmatic dependent launch ----

@@ -26,6 +26,9 @@ cudaError_t launch_next(void (*kernel)(P...), dim3 blocks, int threads, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// whether a 256-bit access may start there
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 struct NormFwdArgs {
     const uint16_t* x;         // M x N bf16
     const uint16_t* residual;  // M x N bf16, or null

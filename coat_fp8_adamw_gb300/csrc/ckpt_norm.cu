@@ -18,8 +18,8 @@
 // Bound by memory.  8192 x 4096, G = 128, with a residual: forward 46.3 us, 98 %
 // of the copy rate (without a residual 31.5 us, 80 %); backward 43.6 us, of which 8 to 9 do not depend on the rows
 // (two kernels, the ring's first rows, the sum over the blocks' dw: 4099 x 5120
-// takes 27.0 us, 60 % of the copy rate).  Forward one row per block and no loop,
-// so that blocks in different phases keep loads on their way; backward persistent
+// takes 27.0 us, 60 % of the copy rate).  Forward a block has its rows (one
+// team each) once, without a loop, so that blocks in different phases keep loads on their way; backward persistent
 // blocks, since each keeps its sums for dw in registers, fed by a ring of rows in
 // shared memory.
 #include <cstdint>
@@ -425,8 +425,6 @@ int64_t bwd_blocks(int64_t M, int64_t N, bool res, int sms) {
     const Shape sh = bwd_shape(N, res);
     return blocks_of(M, sh, sh.T <= 320 ? 96 : sh.T <= 512 ? 128 : 64, sms);
 }
-
-bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // more than the 48 KB that every kernel may have, its static part (under 1 KB) included
 template <typename F>

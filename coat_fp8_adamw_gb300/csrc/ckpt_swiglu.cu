@@ -128,8 +128,6 @@ __global__ void __launch_bounds__(kBlock) swiglu_bwd_kernel(const SwigluBwdArgs 
     }
 }
 
-bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
-
 // rows per launch: its chunks are counted in 31 bits
 int64_t slab_rows(int64_t N) {
     const int64_t rows = (((int64_t)1 << 31) - kBlock) / (N / 16);
