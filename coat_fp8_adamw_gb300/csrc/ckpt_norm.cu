@@ -23,6 +23,7 @@
 // blocks, since each keeps its sums for dw in registers, fed by a ring of rows in
 // shared memory.
 #include <cstdint>
+#include <type_traits>
 
 #include "ckpt_device.cuh"
 #include "ckpt_kernels.h"
@@ -222,10 +223,14 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
     const float inv_n = 1.0f / (float)N;
     const int64_t ngr = N >> gshift;
     const uint32_t bar0 = smem_u32(bars), ring0 = smem_u32(ring);
-    // rows as 32-bit numbers: M < 2^31, and a ring's rows beyond the last one stay far below 2^32
-    const uint32_t M = (uint32_t)a.M, step = gridDim.x * (uint32_t)teams, first = blockIdx.x * (uint32_t)teams;
-    auto issue = [&](uint32_t r0, int s) {
-        const uint32_t n = min(M - r0, (uint32_t)teams) * (uint32_t)N;
+    // Rows as 32-bit numbers (M < 2^31, and a ring's rows beyond the last one stay far below 2^32): 64-bit ones take 98
+    // registers where 96 are there for two blocks (8192 x 5120 58.6 us instead of 43.0), and are slower without a residual
+    // (8192 x 12288 and 16384 104 and 130 us instead of 99 and 123).  But with one, in the widest rows, they are not:
+    // 152 and 181 us instead of 156 and 182.
+    using Row = typename std::conditional<kRes && kThreads == 1024, int64_t, uint32_t>::type;
+    const Row M = (Row)a.M, step = (Row)gridDim.x * (Row)teams, first = (Row)blockIdx.x * (Row)teams;
+    auto issue = [&](Row r0, int s) {
+        const uint32_t n = (uint32_t)min(M - r0, (Row)teams) * (uint32_t)N;
         const uint32_t d = ring0 + (uint32_t)s * sh.stage, bar = bar0 + 8u * (uint32_t)s;
         mbar_expect_tx(bar, n * (kRes ? 5u : 3u));
         const int64_t at = (int64_t)r0 * N;
@@ -256,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
 #pragma unroll
         for (int e = 0; e < 4; ++e) dw[j][e] = 0ull;
     }
-    auto fetch_scales = [&](uint32_t r) {   // one iteration ahead
+    auto fetch_scales = [&](Row r) {   // one iteration ahead
         if (r < M) {
             rn = a.rstd[r];
 #pragma unroll
@@ -267,9 +272,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
     fetch_scales(first + team);
     int s = 0;
     uint32_t ph = 0;
-    uint32_t r0 = first, it = 0;
+    Row r0 = first;
+    uint32_t it = 0;
     for (; r0 < M; r0 += step, ++it) {
-        const uint32_t r = r0 + team;
+        const Row r = r0 + team;
         bool live = r < M;                 // a team past the last row only keeps step
         const float rstd = rn, S[2] = {Sn[0] * rn, Sn[1] * rn};
         fetch_scales(r + step);
@@ -312,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_ke
         live = live && stop == 0u;
         // behind that barrier every thread is done with the iteration before this one: its stage is free
         if (threadIdx.x == 0 && it > 0 && stop == 0u) {
-            const uint32_t rr = r0 + (depth - 1) * step;
+            const Row rr = r0 + (depth - 1) * step;
             if (rr < M) issue(rr, s == 0 ? depth - 1 : s - 1);
         }
         const uint64_t nc = pk(-c, -c), rr2 = pk(rstd, rstd);
