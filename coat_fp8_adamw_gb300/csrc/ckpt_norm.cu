@@ -15,13 +15,14 @@
 // access of a bf16 tensor and one 128-bit access of codes; every tensor is read
 // and written once.
 //
-// Bound by memory.  8192 x 4096, G = 128, with a residual: forward 46.3 us, 98 %
-// of the copy rate (without a residual 31.5 us, 80 %); backward 43.6 us, of which 8 to 9 do not depend on the rows
-// (two kernels, the ring's first rows, the sum over the blocks' dw: 4099 x 5120
-// takes 27.0 us, 60 % of the copy rate).  Forward a block has its rows (one
-// team each) once, without a loop, so that blocks in different phases keep loads on their way; backward persistent
-// blocks, since each keeps its sums for dw in registers, fed by a ring of rows in
-// shared memory.
+// Bound by memory.  8192 x 4096, G = 128, with a residual: forward 46.1 us, 98 %
+// of the copy rate (without a residual 31.4 us, 80 %); backward 43.5 us, 81 %, of
+// which about 10 do not grow with the rows once there are some thousands (two
+// kernels, the ring's first rows, the sum over the blocks' dw; a single row takes
+// 5): 4099 x 5120 takes 26.7 us, 60 %.  Forward a block has its rows (one team
+// each) once, without a loop, so that blocks in different phases keep loads on
+// their way; backward persistent blocks, since each keeps its sums for dw in
+// registers, fed by a ring of rows in shared memory.
 #include <cstdint>
 #include <type_traits>
 
@@ -89,7 +90,7 @@ __device__ __forceinline__ void weights_of(const float4* sw, int items, int i, f
 }
 
 // Eight weights, in pairs: one 256-bit access where `wide`, which L1 serves in half the passes of two (a lane's sixteen
-// lie 64 bytes from the next lane's; 8192 x 4096 without a residual 35.4 us with 128-bit accesses, 31.5 so)
+// lie 64 bytes from the next lane's; 8192 x 4096 without a residual 35.4 us with 128-bit accesses, 31.4 so)
 __device__ __forceinline__ void load_weights8(const float* p, bool wide, uint64_t (&w)[4]) {
     if (wide) {
         asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(w[0]), "=l"(w[1]), "=l"(w[2]), "=l"(w[3]) : "l"(p));
@@ -129,7 +130,7 @@ __device__ __noinline__ void far_row(const NormFwdArgs& a, const Shape& sh) {
 
 // Forward: a block has its rows once, a thread sixteen consecutive elements (so that a
 // group of G >= 16 is G / 16 lanes).  What keeps the memory busy are many small
-// blocks per SM in different phases: at 8192 x 4096 with a residual 46.3 us with
+// blocks per SM in different phases: at 8192 x 4096 with a residual 46.1 us with
 // 40 registers (six blocks of 256 threads per SM), 51.0 with 50 (four); blocks
 // that walk the rows through a ring of bulk copies, as backward, took 53.3.
 template <bool kRes, int kThreads, int kBlocks>
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_fwd_kernel(const __gri
 // 67 us, a second wave); 320, bound to 96, is for them (52 us; where both fit, 2 %
 // slower).  1024 (N > 8192): 64 registers, so a row's elements are formed again
 // from shared memory after its sum instead of being held over it (8192 x 12288
-// and 16384 103 and 128 us; held, in local memory, 164 and 222; at N <= 5120 forming
+// and 16384 99 and 123 us; held, in local memory, 164 and 222; at N <= 5120 forming
 // them again for three or more blocks per SM costs 4 to 8 us).
 template <bool kRes, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 320 ? 2 : 1) norm_bwd_kernel(const NormBwdArgs a, const Shape sh) {
@@ -450,7 +451,7 @@ cudaError_t launch_fwd(const NormFwdArgs& a, cudaStream_t s) {
         return launch_next(norm_fwd_kernel<kRes, 256, 6>, blocks, threads, 0, s, a, sh, wide, wide_w);
     if (threads <= 512)
         return launch_next(norm_fwd_kernel<kRes, 512, 3>, blocks, threads, 0, s, a, sh, wide, wide_w);
-    // two blocks per SM up to N = 12288 (8192 x 12288 without a residual: 169 us with one, 117 with two; 103 now)
+    // two blocks per SM up to N = 12288 (8192 x 12288 without a residual: 169 us with one, 117 with two; 102 now)
     if (threads <= 768) return launch_next(norm_fwd_kernel<kRes, 768, 2>, blocks, threads, 0, s, a, sh, wide, wide_w);
     return launch_next(norm_fwd_kernel<kRes, 1024, 1>, blocks, threads, 0, s, a, sh, wide, wide_w);
 }

@@ -25,12 +25,12 @@
 // tokens' heads go to the warps in equal ranges.
 //
 // Both directions are bound by memory in the long run (time per further token:
-// 95 % of the copy rate forward, 84 to 92 % backward) and are sensitive to two
+// the copy rate forward, 85 to 93 % of it backward) and are sensitive to two
 // things.  Registers: three blocks of 256 threads with 80 registers, some of
 // them in local memory, took 61.6 us forward at 8192 tokens x 64 heads x 128
-// where nine of 64 threads take 55.0.  And the balance of the warps' work: equal
+// where nine of 64 threads take 54.8.  And the balance of the warps' work: equal
 // ranges of passes instead of tokens brought 4101 tokens x 50 heads x 128
-// backward from 35.9 to 31.1 us (30.5 now), of which about 7 are the start of two kernels.
+// backward from 35.9 to 31.1 us (30.5 now), of which 7 to 8 do not grow with the tokens (two kernels, first passes).
 #include <cstdint>
 
 #include "ckpt_device.cuh"

@@ -17,7 +17,7 @@
 // walk the flat element range; gate and up (and their gradients) may be column
 // ranges of a wider tensor.
 //
-// Bound by memory: 8192 x 11008, G = 128, halves of one tensor, 108.3 us forward
+// Bound by memory: 8192 x 11008, G = 128, halves of one tensor, 107.7 us forward
 // and 121.0 us backward with the product's checkpoint, both at the copy rate
 // (every tensor is read and written once).  Eight elements per thread took
 // 197 and 160 us: what the threads issue per element was the bound then.
