@@ -401,8 +401,20 @@ def coat_dre_dequantize(q, scale, k, G: int, x, stream=None) -> None:
         raise CoatError(st, "coat_dre_dequantize")
 
 
-from .ckpt import (  # noqa: E402  (uses the helpers above)
-    coat_ckpt_weight_grad, coat_ckpt_weight_grad_workspace_bytes, coat_qk_norm_rope_ckpt,
-    coat_qk_norm_rope_ckpt_backward, coat_qk_norm_rope_ckpt_backward_workspace_bytes,
-    coat_rmsnorm_ckpt, coat_rmsnorm_ckpt_backward, coat_rmsnorm_ckpt_backward_workspace_bytes,
-    coat_swiglu_ckpt, coat_swiglu_ckpt_backward)
+
+# The operators of ckpt.py, whose checks hold torch's types, are imported with the first use of one of them, so that
+# importing the package still needs no torch.
+_CKPT = tuple(n for n in __all__ if "_ckpt" in n)
+
+
+def __getattr__(name):
+    if name != "ckpt" and name not in _CKPT:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    ckpt = importlib.import_module(".ckpt", __name__)
+    globals().update((n, getattr(ckpt, n)) for n in _CKPT)
+    return globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_CKPT, "ckpt"})
