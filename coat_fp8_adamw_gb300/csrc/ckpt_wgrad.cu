@@ -34,7 +34,7 @@
 // tensor memory, so there is one accumulator, and the MMAs of a tile wait until
 // the last one's is read.
 //
-// Measured (8192 tokens, G = 128): N x K = 11008 x 4096 0.41 to 0.44 ms alone (1.68 to 1.79 PFLOP/s) and 0.48 to 0.50 ms when
+// Measured (8192 tokens, G = 128): N x K = 11008 x 4096 0.41 to 0.44 ms alone (1.68 to 1.79 PFLOP/s) and 0.48 to 0.51 ms when
 // repeated for seconds, where the GPU stands at its power limit; 4096 x 4096
 // 0.157 ms, 2048 x 2048 0.046 ms; the smallest calls 8 us (launch, tensor
 // memory, first tiles, join).  11008 x 4096 at G = 16 0.46 ms, at G = 8 0.63 ms.
