@@ -27,6 +27,8 @@ __all__ = ["CoatError", "coat_fp8_adamw_step", "coat_fp8_adamw_step_host",
            "coat_swiglu_ckpt_backward", "coat_qk_norm_rope_ckpt",
            "coat_qk_norm_rope_ckpt_backward", "coat_qk_norm_rope_ckpt_backward_workspace_bytes",
            "coat_ckpt_weight_grad", "coat_ckpt_weight_grad_workspace_bytes",
+           "coat_embedding", "coat_embedding_backward",
+           "coat_embedding_backward_workspace_bytes", "coat_dropout", "coat_dropout_backward",
            "coat_dre_dequantize", "coat_exact_recompute_counts", "coat_kernel_wait_timeouts",
            "coat_status_string",
            "coat_r_e4m3", "coat_version", "lib",
@@ -53,6 +55,8 @@ EXPORTS = ("coat_fp8_adamw_step", "coat_fp8_adamw_step_host",
            "coat_swiglu_ckpt_backward", "coat_qk_norm_rope_ckpt",
            "coat_qk_norm_rope_ckpt_backward", "coat_qk_norm_rope_ckpt_backward_workspace_bytes",
            "coat_ckpt_weight_grad", "coat_ckpt_weight_grad_workspace_bytes",
+           "coat_embedding", "coat_embedding_backward",
+           "coat_embedding_backward_workspace_bytes", "coat_dropout", "coat_dropout_backward",
            "coat_dre_dequantize", "coat_exact_recompute_counts", "coat_kernel_wait_timeouts",
            "coat_status_string",
            "coat_r_e4m3", "coat_version")
@@ -137,6 +141,17 @@ def lib() -> ctypes.CDLL:
         L.coat_ckpt_weight_grad.restype = ctypes.c_int
         L.coat_ckpt_weight_grad_workspace_bytes.argtypes = [i64, i64, i64]
         L.coat_ckpt_weight_grad_workspace_bytes.restype = ctypes.c_size_t
+        L.coat_embedding.argtypes = [vp, vp, i32, f32, i64, i64, i64, vp, vp]
+        L.coat_embedding.restype = ctypes.c_int
+        L.coat_embedding_backward.argtypes = [vp, vp, i32, f32, i64, i64, i64, i32, vp, vp,
+                                              ctypes.c_size_t, vp]
+        L.coat_embedding_backward.restype = ctypes.c_int
+        L.coat_embedding_backward_workspace_bytes.argtypes = [i64, i64]
+        L.coat_embedding_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.coat_dropout.argtypes = [vp, vp, f32, vp, i64, vp, vp]
+        L.coat_dropout.restype = ctypes.c_int
+        L.coat_dropout_backward.argtypes = [vp, f32, vp, i64, vp, vp]
+        L.coat_dropout_backward.restype = ctypes.c_int
         L.coat_status_string.argtypes = [ctypes.c_int]
         L.coat_status_string.restype = ctypes.c_char_p
         L.coat_r_e4m3.argtypes = []
@@ -402,19 +417,21 @@ def coat_dre_dequantize(q, scale, k, G: int, x, stream=None) -> None:
 
 
 
-# The operators of ckpt.py, whose checks hold torch's types, are imported with the first use of one of them, so that
-# importing the package still needs no torch.
-_CKPT = tuple(n for n in __all__ if "_ckpt" in n)
+# The operators of ckpt.py and lm.py, whose checks hold torch's types, are imported with the first use of one of them, so
+# that importing the package still needs no torch.
+_LAZY = {n: "ckpt" for n in __all__ if "_ckpt" in n}
+_LAZY.update((n, "lm") for n in __all__ if n.startswith(("coat_embedding", "coat_dropout", "coat_linear_cross")))
 
 
 def __getattr__(name):
-    if name != "ckpt" and name not in _CKPT:
+    module = name if name in ("ckpt", "lm") else _LAZY.get(name)
+    if module is None:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     import importlib
-    ckpt = importlib.import_module(".ckpt", __name__)
-    globals().update((n, getattr(ckpt, n)) for n in _CKPT)
+    mod = importlib.import_module(f".{module}", __name__)
+    globals().update((n, getattr(mod, n)) for n, m in _LAZY.items() if m == module)
     return globals()[name]
 
 
 def __dir__():
-    return sorted({*globals(), *_CKPT, "ckpt"})
+    return sorted({*globals(), *_LAZY, "ckpt", "lm"})

@@ -4,7 +4,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
-#include <initializer_list>
 
 #include "abi_checks.h"
 #include "ckpt_kernels.h"
@@ -14,39 +13,9 @@ namespace {
 
 using namespace coat::abi;
 
-// A buffer of a call.  A null pointer: not there.
-enum Kind { kIn, kOut, kOutRows };
-struct Buf {
-    const void* p;
-    size_t bytes;
-    Kind kind;
-};
-
-// Alignment, then overlap, then where the memory is.  Outputs overlap nothing,
-// except that two outputs of rows (kOutRows) may interleave: rows_apart has
-// looked at those.
-coat_status check_buffers(std::initializer_list<Buf> bufs) {
-    for (const Buf& b : bufs)
-        if (b.p && !aligned16(b.p)) return COAT_ERR_MISALIGNED;
-    for (const Buf* b = bufs.begin(); b != bufs.end(); ++b)
-        for (const Buf* c = b + 1; c != bufs.end(); ++c) {
-            if (!b->p || !c->p || (b->kind == kIn && c->kind == kIn)) continue;
-            if (b->kind == kOutRows && c->kind == kOutRows) continue;
-            if (overlaps(b->p, b->bytes, c->p, c->bytes)) return COAT_ERR_INVALID_ARG;
-        }
-    for (const Buf& b : bufs)
-        if (b.p && !is_device(b.p)) return COAT_ERR_NOT_DEVICE;
-    return COAT_OK;
-}
-
 // 1 x G groups of rows of N: G a power of two in [8, 128], N a multiple of it and of 16
 bool group_ok(int32_t G) { return G >= 8 && G <= 128 && (G & (G - 1)) == 0; }
-bool shape_ok(int64_t M, int64_t N) { return M >= 1 && N >= 1 && M < (1LL << 31) && N < (1LL << 31); }
 bool width_ok(int64_t N, int32_t G) { return N % 16 == 0 && N % G == 0; }
-bool stride_ok(int64_t ld, int64_t N) { return ld >= N && ld % 8 == 0 && ld < (1LL << 31); }
-// bytes from the first to the last element of M rows of n elements, ld apart
-size_t span(int64_t M, int64_t n, int64_t ld, size_t elem) { return ((size_t)(M - 1) * (size_t)ld + (size_t)n) * elem; }
-
 // Two sets of M rows of n elements with row stride ld that share no element:
 // apart in memory, or column ranges of one tensor.
 bool rows_apart(const uint16_t* a, int64_t na, const uint16_t* b, int64_t nb, int64_t M, int64_t ld) {

@@ -446,6 +446,62 @@ coat_status coat_ckpt_weight_grad(const uint16_t *dy, int64_t dy_ld, const uint8
                                   size_t workspace_bytes, void *stream);
 size_t coat_ckpt_weight_grad_workspace_bytes(int64_t M, int64_t N, int64_t K);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators at the two ends of a language model's training step, and dropout.
+ * The COAT review page has no counterpart of its own for them: they are what a
+ * step that keeps its activations in 8 bits (above) otherwise keeps most of,
+ * the logits, the dropout masks and a dense float32 gradient of the embedding.
+ *
+ * As above: bf16 tensors are raw 16-bit patterns, everything between input and
+ * output is float32, rounded once where an output is bf16 (but for the gradient
+ * of the logits, which goes to the tensor cores as bf16: see there); widths (C)
+ * are multiples of 16; row counts are at least 1 and below 2^31; every pointer is
+ * 16-byte aligned; outputs overlap neither inputs nor each other.  Results do not
+ * depend on the order in which blocks run.  `workspace` and *_workspace_bytes as
+ * above.  Lists of indexes are int32, or int64 where `wide_*` is not 0.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Embedding lookup: out[m] = scale table[ids[m]].
+ *   table [V x C] bf16, ids [M] in;  out [M x C] bf16 out.  A negative id
+ *   (padding) gives a row of zeros, one of V or more a row of NaN.  scale finite.
+ */
+coat_status coat_embedding(const uint16_t *table, const void *ids, int32_t wide_ids, float scale, int64_t M,
+                           int64_t V, int64_t C, uint16_t *out, void *stream);
+
+/*
+ * Its gradient: dtable[v] = scale sum over m with ids[m] = v of dout[m], plus what
+ * dtable[v] held where `accumulate` is not 0 (a table that is the output layer's
+ * weight too: rows without a token are then not touched; otherwise they become
+ * zeros).  Ids outside [0, V) have no gradient.
+ *   dout [M x C] bf16, ids [M] in;  dtable [V x C] bf16 out (and in).
+ * The sum is taken in float32 in the order of the tokens, in chunks of up to 32.
+ */
+coat_status coat_embedding_backward(const uint16_t *dout, const void *ids, int32_t wide_ids, float scale,
+                                    int64_t M, int64_t V, int64_t C, int32_t accumulate, uint16_t *dtable,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t C);
+
+/*
+ * Dropout: y = keep x 65536 / (65536 - T) (+ residual), T = round(65536 p), p in
+ * [0, 1) with T < 65536.  An element is kept where its 16 random bits are T or
+ * more: of counter (i / 8, rng[1]) and key rng[0], Philox4x32-10 (Salmon et al.,
+ * SC 2011) gives four 32-bit words, whose halves, the low one first, belong to
+ * elements i = 8 (i / 8) .. + 7.  A dropped element does not count, whatever it holds.
+ *   x [n] bf16, residual [n] bf16 or NULL, rng [2] uint64 in device memory, in;
+ *   y [n] bf16 out.
+ * Calls that may not share their masks differ in rng[0] or rng[1].  rng is read
+ * when the kernel runs: a captured graph draws new bits once rng has changed.
+ */
+coat_status coat_dropout(const uint16_t *x, const uint16_t *residual, float p, const uint64_t *rng, int64_t n,
+                         uint16_t *y, void *stream);
+
+/* Its gradient with the same p and rng: dx = keep dy 65536 / (65536 - T); the residual's is dy. */
+coat_status coat_dropout_backward(const uint16_t *dy, float p, const uint64_t *rng, int64_t n, uint16_t *dx,
+                                  void *stream);
+
 /* Static description of a status code (never NULL). */
 const char *coat_status_string(coat_status status);
 
