@@ -29,6 +29,9 @@ __all__ = ["CoatError", "coat_fp8_adamw_step", "coat_fp8_adamw_step_host",
            "coat_ckpt_weight_grad", "coat_ckpt_weight_grad_workspace_bytes",
            "coat_embedding", "coat_embedding_backward",
            "coat_embedding_backward_workspace_bytes", "coat_dropout", "coat_dropout_backward",
+           "coat_linear_cross_entropy", "coat_linear_cross_entropy_workspace_bytes",
+           "coat_linear_cross_entropy_backward",
+           "coat_linear_cross_entropy_backward_workspace_bytes",
            "coat_dre_dequantize", "coat_exact_recompute_counts", "coat_kernel_wait_timeouts",
            "coat_status_string",
            "coat_r_e4m3", "coat_version", "lib",
@@ -57,6 +60,9 @@ EXPORTS = ("coat_fp8_adamw_step", "coat_fp8_adamw_step_host",
            "coat_ckpt_weight_grad", "coat_ckpt_weight_grad_workspace_bytes",
            "coat_embedding", "coat_embedding_backward",
            "coat_embedding_backward_workspace_bytes", "coat_dropout", "coat_dropout_backward",
+           "coat_linear_cross_entropy", "coat_linear_cross_entropy_workspace_bytes",
+           "coat_linear_cross_entropy_backward",
+           "coat_linear_cross_entropy_backward_workspace_bytes",
            "coat_dre_dequantize", "coat_exact_recompute_counts", "coat_kernel_wait_timeouts",
            "coat_status_string",
            "coat_r_e4m3", "coat_version")
@@ -148,6 +154,16 @@ def lib() -> ctypes.CDLL:
         L.coat_embedding_backward.restype = ctypes.c_int
         L.coat_embedding_backward_workspace_bytes.argtypes = [i64, i64]
         L.coat_embedding_backward_workspace_bytes.restype = ctypes.c_size_t
+        L.coat_linear_cross_entropy.argtypes = [vp, i64, vp, vp, i32, i64, i64, i64, vp, vp, vp,
+                                                ctypes.c_size_t, vp]
+        L.coat_linear_cross_entropy.restype = ctypes.c_int
+        L.coat_linear_cross_entropy_workspace_bytes.argtypes = [i64, i64]
+        L.coat_linear_cross_entropy_workspace_bytes.restype = ctypes.c_size_t
+        L.coat_linear_cross_entropy_backward.argtypes = [vp, i64, vp, vp, i32, vp, vp, vp, i64, i64, i64, i64,
+                                                         vp, vp, vp, ctypes.c_size_t, vp]
+        L.coat_linear_cross_entropy_backward.restype = ctypes.c_int
+        L.coat_linear_cross_entropy_backward_workspace_bytes.argtypes = [i64, i64, i64, i64]
+        L.coat_linear_cross_entropy_backward_workspace_bytes.restype = ctypes.c_size_t
         L.coat_dropout.argtypes = [vp, vp, f32, vp, i64, vp, vp]
         L.coat_dropout.restype = ctypes.c_int
         L.coat_dropout_backward.argtypes = [vp, f32, vp, i64, vp, vp]

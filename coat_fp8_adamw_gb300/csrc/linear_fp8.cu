@@ -33,6 +33,7 @@
 #include "ckpt_kernels.h"
 #include "coat_device.cuh"
 #include "coat_kernels.h"
+#include "lm_kernels.h"
 #include "tc_pipeline.cuh"
 
 namespace coat {
@@ -461,11 +462,12 @@ cudaError_t launch_linear_fp8(const LinArgs& a, int G, cudaStream_t s) {
 }
 
 cudaError_t read_wait_timeouts(unsigned long long* out, bool reset) {
-    unsigned long long n[3] = {0ull, 0ull, 0ull};
+    unsigned long long n[4] = {0ull, 0ull, 0ull, 0ull};
     cudaError_t e = read_own_wait_timeouts(&n[0], reset);
     if (e == cudaSuccess) e = read_wgrad_wait_timeouts(&n[1], reset);
     if (e == cudaSuccess) e = read_norm_wait_timeouts(&n[2], reset);
-    *out = n[0] + n[1] + n[2];
+    if (e == cudaSuccess) e = read_lce_wait_timeouts(&n[3], reset);
+    *out = n[0] + n[1] + n[2] + n[3];
     return e;
 }
 

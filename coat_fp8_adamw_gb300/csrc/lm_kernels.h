@@ -44,6 +44,42 @@ struct DropoutArgs {
     uint16_t* y;               // n bf16
 };
 
+struct LceFwdArgs {
+    const uint16_t* x;         // M rows of C bf16, x_ld apart
+    int64_t x_ld;
+    const uint16_t* weight;    // V x C bf16
+    const void* targets;       // M indexes of 4 or 8 bytes
+    int32_t wide;              // 8 bytes
+    int64_t M, V, C;
+    float* loss;               // M
+    float* lse;                // M
+    void* stats;               // lce_stats_bytes(M, V)
+};
+struct LceBwdArgs {
+    const uint16_t* x;
+    int64_t x_ld;
+    const uint16_t* weight;
+    const void* targets;
+    int32_t wide;
+    const float* lse;          // M
+    const float* dloss;        // M
+    const float* dlse;         // M, or null
+    int64_t M, V, C;
+    int64_t piece;             // rows of the weight at once
+    uint16_t* dx;              // M x C bf16
+    uint16_t* dweight;         // V x C bf16
+    uint16_t* dz;              // M x lce_piece_ld(piece, V) bf16
+    float* sums;               // M x C, where there are several pieces
+};
+constexpr int64_t kLceDzBytes = 256 << 20;   // of a piece's gradient of the logits, unless the caller says how wide a piece is
+int64_t lce_piece(int64_t M, int64_t V, int64_t piece);
+int64_t lce_piece_ld(int64_t piece, int64_t V);
+size_t lce_stats_bytes(int64_t M, int64_t V);
+
+cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s);
+cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s);
+// bounded waits that gave up in the kernels of lm_lce.cu, on the current device
+cudaError_t read_lce_wait_timeouts(unsigned long long* out, bool reset);
 cudaError_t launch_embed_fwd(const EmbedFwdArgs& a, cudaStream_t s);
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, cudaStream_t s);
 cudaError_t launch_dropout(const DropoutArgs& a, cudaStream_t s);

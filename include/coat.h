@@ -485,6 +485,42 @@ coat_status coat_embedding_backward(const uint16_t *dout, const void *ids, int32
 size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t C);
 
 /*
+ * Softmax cross entropy of a linear layer, whose logits z = x W^T are not kept:
+ *   lse[m] = log sum over v of e^z[m, v];  loss[m] = lse[m] - z[m, targets[m]].
+ *   x  M rows of C bf16, x_ld apart (a multiple of 8), in;  weight [V x C] bf16 in;
+ *   targets [M] in: a negative one (a token without a target) gives loss 0, one
+ *   of V or more NaN;  loss, lse [M] float32 out.
+ * Products are added in float32 by the tensor cores; the logits have to be finite
+ * or -inf there.  M V at most COAT_MAX_N, here and below.
+ */
+coat_status coat_linear_cross_entropy(const uint16_t *x, int64_t x_ld, const uint16_t *weight,
+                                      const void *targets, int32_t wide_targets, int64_t M, int64_t V, int64_t C,
+                                      float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+size_t coat_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V);
+
+/*
+ * Its gradients, with dloss and dlse the gradients of loss and lse:
+ *   dz[m, v] = e^(z[m, v] - lse[m]) (dloss[m] + dlse[m]) - [v = targets[m]] dloss[m],
+ *   rounded to bf16;  dx = dz W;  dweight = dz^T x.
+ *   x, weight, targets as above;  lse [M] as the forward pass left it;  dloss [M]
+ *   float32 in (of a token without a target it does not count);  dlse [M] float32
+ *   in, or NULL: zeros;  dx [M x C], dweight [V x C] bf16 out.
+ * The logits are formed again, `piece` rows of the weight at a time (rounded up to
+ * a multiple of 256; 0: as few pieces as leave 256 MiB for one's dz).  dz is an
+ * operand of the tensor cores, so it is bf16, the type of a layer's gradient; sums
+ * are float32, dx's over the pieces too, so that dx may differ in its last bits
+ * with another `piece`.  Of sums of exact terms, dx and dweight are within
+ * 2^-8 of themselves and (2^-8 + (n + 32) 2^-22) sum |terms|, n = V or M terms.
+ */
+coat_status coat_linear_cross_entropy_backward(const uint16_t *x, int64_t x_ld, const uint16_t *weight,
+                                               const void *targets, int32_t wide_targets, const float *lse,
+                                               const float *dloss, const float *dlse, int64_t M, int64_t V,
+                                               int64_t C, int64_t piece, uint16_t *dx, uint16_t *dweight,
+                                               void *workspace, size_t workspace_bytes, void *stream);
+size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t C, int64_t piece);
+
+/*
  * Dropout: y = keep x 65536 / (65536 - T) (+ residual), T = round(65536 p), p in
  * [0, 1) with T < 65536.  An element is kept where its 16 random bits are T or
  * more: of counter (i / 8, rng[1]) and key rng[0], Philox4x32-10 (Salmon et al.,

@@ -82,3 +82,27 @@ def draws(rng, start, n):
 
 def threshold(p):
     return round(float(np.float32(p)) * 65536)
+
+
+def linear_cross_entropy(x, w, targets):
+    """loss, lse, logits and the sums of the logits' terms' sizes at their largest of every row."""
+    z = x.double() @ w.double().T
+    size = (x.double().abs() @ w.double().abs().T).amax(1)
+    t = targets.long()
+    lse = torch.logsumexp(z, 1)
+    zt = z.gather(1, t.clamp(0, w.shape[0] - 1)[:, None]).squeeze(1)
+    loss = torch.where(t < 0, 0.0, lse - zt)
+    return torch.where(t >= w.shape[0], float("nan"), loss), lse, z, size
+
+
+def linear_cross_entropy_backward(x, w, targets, lse, dloss, dlse=None):
+    """dx, dw, and per element the sums of the sizes of what is added up: of dz itself, and of its two terms, in which the
+    errors of the logits (relative ones of e^(z - lse)) count."""
+    x, w, t = x.double(), w.double(), targets.long()
+    z, size = x @ w.T, x.abs() @ w.abs().T
+    g = torch.where(t >= 0, dloss.double(), 0.0)
+    p = (z - lse.double()[:, None]).exp() * (g if dlse is None else g + dlse.double())[:, None]
+    dz = p.clone()
+    has = (t >= 0).nonzero().squeeze(1)
+    dz[has, t[has]] -= g[has]
+    return dz @ w, dz.T @ x, dz.abs() @ w.abs(), dz.abs().T @ x.abs(), p, size, z

@@ -103,3 +103,46 @@ def test_binding_refuses_what_is_not_on_a_gpu():
         coat.coat_embedding(table.flatten(), ids, 1.0, out)
     with pytest.raises(TypeError, match="int32"):
         coat.coat_embedding(table, ids.float(), 1.0, out)
+
+
+def _lce(L, x=at(0), ld=64, w=at(1), t=at(2), wide=0, M=64, V=100, C=64, loss=at(3), lse=at(4), ws=at(5), n=1 << 20):
+    return L.coat_linear_cross_entropy(x, ld, w, t, wide, M, V, C, loss, lse, ws, n, None)
+
+
+def test_linear_cross_entropy(L):
+    assert _lce(L) == 5 and _lce(L, wide=1, ld=72, V=1, M=1) == 5
+    for k in ("x", "w", "t", "loss", "lse", "ws"):
+        assert _lce(L, **{k: 0}) == 1
+    for k in ("M", "V", "C"):
+        assert _lce(L, **{k: 0}) == 1 and _lce(L, **{k: 1 << 31}) == 1
+    assert _lce(L, C=24, ld=24) == 1 and _lce(L, ld=56) == 1 and _lce(L, ld=68) == 1
+    assert _lce(L, M=1 << 20, V=(1 << 20) + 1, C=16, ld=16) == 1        # more logits than any entry point takes elements
+    assert _lce(L, x=at(0, 8)) == 2 and _lce(L, lse=at(4, 4)) == 2
+    assert _lce(L, loss=at(0)) == 1 and _lce(L, lse=at(3)) == 1 and _lce(L, ws=at(4)) == 1 and _lce(L, ws=at(1)) == 1
+
+
+def _lce_b(L, x=at(0), ld=64, w=at(1), t=at(2), wide=0, lse=at(3), g=at(4), h=None, M=64, V=1000, C=64, piece=0, dx=at(5), dw=at(6),
+           ws=at(7), n=1 << 20):
+    return L.coat_linear_cross_entropy_backward(x, ld, w, t, wide, lse, g, h, M, V, C, piece, dx, dw, ws, n, None)
+
+
+def test_linear_cross_entropy_backward(L):
+    assert _lce_b(L) == 5 and _lce_b(L, h=at(8), wide=1) == 5 and _lce_b(L, piece=300) == 5
+    for k in ("x", "w", "t", "lse", "g", "dx", "dw", "ws"):
+        assert _lce_b(L, **{k: 0}) == 1
+    for k in ("M", "V", "C"):
+        assert _lce_b(L, **{k: 0}) == 1
+    assert _lce_b(L, piece=-1) == 1 and _lce_b(L, ld=60) == 1 and _lce_b(L, h=at(8, 8)) == 2
+    assert _lce_b(L, piece=(1 << 63) - 1) == 5
+    assert _lce_b(L, dx=at(0)) == 1 and _lce_b(L, dw=at(1)) == 1 and _lce_b(L, dx=at(6)) == 1 and _lce_b(L, h=at(6)) == 1
+
+
+def test_linear_cross_entropy_workspaces(L):
+    f, b = L.coat_linear_cross_entropy_workspace_bytes, L.coat_linear_cross_entropy_backward_workspace_bytes
+    assert f(0, 10) == 0 and f(1 << 20, (1 << 20) + 1) == 0 and f(1, 1) > 0
+    assert b(10, 100, 24, 0) == 0 and b(10, 100, 64, -1) == 0
+    assert b(10, 100, 64, 0) == b(10, 100, 64, 1) == b(10, 100, 64, (1 << 63) - 1) == 2 * 10 * 256    # one piece
+    assert b(10, 1000, 64, 300) == 2 * 10 * 512 + 4 * 10 * 64            # two: and dx's sums between them
+    M, V, C = 8192, 32000, 4096
+    assert b(M, V, C, 0) == 2 * M * 16128 + 4 * M * C                     # two pieces of about the same width
+    assert 2 * M * 16128 <= 256 << 20
