@@ -152,7 +152,7 @@ def lib() -> ctypes.CDLL:
         L.coat_embedding_backward.argtypes = [vp, vp, i32, f32, i64, i64, i64, i32, vp, vp,
                                               ctypes.c_size_t, vp]
         L.coat_embedding_backward.restype = ctypes.c_int
-        L.coat_embedding_backward_workspace_bytes.argtypes = [i64, i64]
+        L.coat_embedding_backward_workspace_bytes.argtypes = [i64, i64, i64]
         L.coat_embedding_backward_workspace_bytes.restype = ctypes.c_size_t
         L.coat_linear_cross_entropy.argtypes = [vp, i64, vp, vp, i32, i64, i64, i64, vp, vp, vp,
                                                 ctypes.c_size_t, vp]

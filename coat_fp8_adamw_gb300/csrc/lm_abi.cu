@@ -15,6 +15,9 @@ using namespace coat::abi;
 
 // rows x C elements: C a multiple of 16, and no more elements than any entry point takes
 bool rows_ok(int64_t rows, int64_t C) { return shape_ok(rows, C) && C % 16 == 0 && rows * C <= COAT_MAX_N; }
+// the parts of the embedding gradient's workspace: the sorted tokens, the chunks' shares, and a flag per row of the table
+size_t sorted_bytes(int64_t M) { return (sizeof(coat::Entry) * (size_t)M + 15) / 16 * 16; }
+size_t partial_bytes(int64_t M, int64_t C) { return 8 * (size_t)coat::embed_chunks(M) * (size_t)C; }
 bool lce_ok(int64_t M, int64_t V, int64_t C, int64_t x_ld) {
     return rows_ok(M, C) && rows_ok(V, C) && stride_ok(x_ld, C) && M * V <= COAT_MAX_N;
 }
@@ -48,9 +51,9 @@ coat_status coat_embedding(const uint16_t* table, const void* ids, int32_t wide_
     return from_cuda(coat::launch_embed_fwd(a, static_cast<cudaStream_t>(stream)));
 }
 
-size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t C) {
-    if (!rows_ok(M, C)) return 0;
-    return (sizeof(coat::Entry) * (size_t)M + 15) / 16 * 16 + 4 * (size_t)coat::embed_chunks(M) * (size_t)C;
+size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t V, int64_t C) {
+    if (!rows_ok(M, C) || !rows_ok(V, C)) return 0;
+    return sorted_bytes(M) + partial_bytes(M, C) + (size_t)coat::embed_flags(V);
 }
 
 coat_status coat_embedding_backward(const uint16_t* dout, const void* ids, int32_t wide_ids, float scale, int64_t M, int64_t V,
@@ -61,10 +64,10 @@ coat_status coat_embedding_backward(const uint16_t* dout, const void* ids, int32
     const coat_status st = check_buffers({{dout, 2 * (size_t)M * (size_t)C, kIn}, {ids, index_bytes(M, wide_ids), kIn},
                                           {dtable, 2 * (size_t)V * (size_t)C, kOut}, {workspace, workspace_bytes, kOut}});
     if (st != COAT_OK) return st;
-    if (workspace_bytes < coat_embedding_backward_workspace_bytes(M, C)) return COAT_ERR_INVALID_ARG;
-    char* partial = static_cast<char*>(workspace) + (sizeof(coat::Entry) * (size_t)M + 15) / 16 * 16;
+    if (workspace_bytes < coat_embedding_backward_workspace_bytes(M, V, C)) return COAT_ERR_INVALID_ARG;
+    char* partial = static_cast<char*>(workspace) + sorted_bytes(M);
     const coat::EmbedBwdArgs a{dout, ids, wide_ids, scale, M, V, C, accumulate, dtable, static_cast<coat::Entry*>(workspace),
-                               reinterpret_cast<float*>(partial)};
+                               reinterpret_cast<float*>(partial), reinterpret_cast<uint8_t*>(partial) + partial_bytes(M, C)};
     return from_cuda(coat::launch_embed_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -4,13 +4,14 @@
 //   backward  dtable[v] = RN(scale sum over m with ids[m] = v of dout[m] (+ dtable[v]))
 //
 // Backward in three kernels, sums in float32 and in a fixed order (that of the tokens, chunk by chunk):
-//   sort    the tokens by their row of the table, stably: block b has a range of rows of its own, walks all M ids (they
-//           are few bytes) and counts what lies below its range, which is where its part of the sorted order begins, so
-//           that no block waits for another.  Rows without a token are written as zeros here, unless the gradient is
+//   sort    the tokens by their row of the table, stably: block b has rows of its own (every B-th), walks all M ids (they
+//           are few bytes) and counts those of the blocks before it, which is where its part of the sorted order begins, so
+//           that no block waits for another;
+//   chunks  the sorted order in chunks of 32 tokens, a warp for each and 256 columns: rows that begin and end in the chunk
+//           are finished; of one that goes on the chunk's share goes to the workspace, so that the work of a row with
+//           many tokens (text has some that are a tenth of all) goes to many warps;
+//   join    the rows that go on: their shares are added up; and rows without a token become zeros, unless the gradient is
 //           added to what is there.
-//   chunks  the sorted order in chunks of 32 tokens: those of one row alone are summed into the workspace, so that the
-//           work of a row with many tokens (text has some that are a tenth of all) goes to many warps;
-//   rows    a warp for each sorted token and 512 columns: the first token of a row adds up the row's tokens and chunks.
 #include <cstdint>
 
 #include "ckpt_kernels.h"
@@ -27,11 +28,18 @@ using lm::index_at;
 
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
-constexpr int kChunk = 32;            // tokens of a chunk: a warp's lanes hold one's entries
-constexpr int kSlice = 512;           // columns of a warp: 16 per lane
+constexpr int kChunk = 32;            // tokens of a chunk, one of a warp's lanes each
+constexpr int kSlice = 256;           // columns of a warp: 8 per lane
+// Tokens whose loads are on their way at once: with 4, and registers for four blocks per SM, all warps of 16411 x 2048 are
+// resident together (41 us; 8 and two blocks 45, 8 and three 47, 4 and three 49; chunks of 16 tokens 46).
+constexpr int kDeep = 4;
 constexpr int kSortBlock = 1024;
 constexpr int kSortWarps = kSortBlock / 32;
-constexpr int kMaxRange = 1024;       // rows of a sorting block: their counts take 128 KB of shared memory
+constexpr int kIds = 8;
+constexpr int kMaxRange = 768;        // rows of a sorting block: they take 256 bytes of shared memory each
+constexpr int kTeams = 2;              // ranges of 256 columns of a joining block
+constexpr int kZeroBytes = 8192;
+constexpr int kFill = 64;             // rows of a filling block
 
 // ---- forward ----
 __global__ void __launch_bounds__(kBlock) embed_fwd_kernel(const EmbedFwdArgs a, const Divider nc, bool wide) {
@@ -56,84 +64,116 @@ __global__ void __launch_bounds__(kBlock) embed_fwd_kernel(const EmbedFwdArgs a,
 }
 
 // ---- backward: sort ----
-// dynamic shared memory: counts[kSortWarps][R], then totals[R]
-__global__ void __launch_bounds__(kSortBlock) embed_sort_kernel(const EmbedBwdArgs a, int R, bool wide) {
-    extern __shared__ int counts[];
+// An id as a row of the table: itself, or -1 where it is none's.
+__device__ __forceinline__ int row_of(int id) { return id; }
+__device__ __forceinline__ int row_of(long long id) { return id < 0 || id > 0x7FFFFFFF ? -1 : (int)id; }
+// f(token, id's row) for the tokens m0 + lane, m0 + lane + 32, ... below m1, kIds loads on their way at once; the whole
+// warp calls f together, with a row of -1 behind the last token.
+template <typename T, typename F>
+__device__ __forceinline__ void for_ids(const void* ids, int64_t m0, int64_t m1, int lane, F f) {
+    int64_t m = m0;
+    for (; m + 32 * kIds <= m1; m += 32 * kIds) {
+        const volatile T* p = static_cast<const volatile T*>(ids) + m + lane;
+        T v[kIds];
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) v[k] = p[32 * k];
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) f((int)m + 32 * k + lane, row_of(v[k]));
+    }
+    if (m >= m1) return;
+    T v[kIds];
+#pragma unroll
+    for (int k = 0; k < kIds; ++k) {   // (a load without a condition: behind a branch every load would wait for the one before it)
+        const int64_t at = m + 32 * k + lane;
+        v[k] = static_cast<const volatile T*>(ids)[at < m1 ? at : m1 - 1];
+    }
+#pragma unroll
+    for (int k = 0; k < kIds; ++k)
+        if (m + 32 * k < m1) f((int)m + 32 * k + lane, m + 32 * k + lane < m1 ? row_of(v[k]) : -1);
+}
+
+// A block's rows are every B-th row of the table (B a power of two), so that rows that lie together, as frequent tokens' rows
+// do, go to different blocks; the sorted order is that of (row mod B, row / B).
+struct Ranges {
+    int32_t shift;     // B = 1 << shift blocks
+    int32_t R;         // most rows of a block
+};
+struct Slot {
+    int32_t next;      // where the warp's next token of the row goes
+    uint32_t lanes;    // of this step: those with a token of the row
+};
+// dynamic shared memory: slots[kSortWarps][R]
+template <typename T>
+__global__ void __launch_bounds__(kSortBlock) embed_sort_kernel(const EmbedBwdArgs a, const Ranges by) {
+    extern __shared__ __align__(8) Slot slots[];
     __shared__ int scan[kSortWarps];
     __shared__ int below_all;
-    int* totals = counts + kSortWarps * R;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int64_t v0 = (int64_t)blockIdx.x * R, v1 = v0 + R < a.V ? v0 + R : a.V;
-    const int rows = (int)(v1 - v0);
-    for (int i = t; i < kSortWarps * R; i += kSortBlock) counts[i] = 0;
+    const int R = by.R, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const unsigned b = blockIdx.x, mask = (1u << by.shift) - 1u, V = (unsigned)a.V;
+    for (int i = t; i < kSortWarps * R; i += kSortBlock) slots[i] = Slot{0, 0u};
     if (t == 0) below_all = 0;
     __syncthreads();
     wait_for_primary();
     // a warp has tokens m0 .. m1 - 1, so that the order of the warps is the order of the tokens
     const int64_t per = (a.M + kSortWarps - 1) / kSortWarps, m0 = per * warp, m1 = m0 + per < a.M ? m0 + per : a.M;
-    int* mine = counts + warp * R;
+    Slot* mine = slots + warp * R;
     int below = 0;
-    for (int64_t m = m0 + lane; m < m1; m += 32) {
-        const int64_t id = index_at(a.ids, a.wide, m);
-        below += id >= 0 && id < v0;
-        if (id >= v0 && id < v1) atomicAdd(mine + (id - v0), 1);
-    }
-    for (int off = 16; off > 0; off >>= 1) below += __shfl_xor_sync(kFull, below, off);
+    for_ids<T>(a.ids, m0, m1, lane, [&](int, int id) {
+        const unsigned at = (unsigned)id & mask;
+        if ((unsigned)id < V) {
+            below += at < b;
+            if (at == b) atomicAdd(&mine[id >> by.shift].next, 1);
+        }
+    });
+    below = __reduce_add_sync(kFull, below);
     if (lane == 0) atomicAdd(&below_all, below);   // whole numbers: any order gives the same sum
     __syncthreads();
-    // counts -> where the warp's first token of the row goes, from the row's start; totals: tokens of the row
-    for (int r = t; r < rows; r += kSortBlock) {
-        int sum = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int n = counts[w * R + r];
-            counts[w * R + r] = sum;
-            sum += n;
-        }
-        totals[r] = sum;
+    // counts -> places in the sorted order; a row per thread (R <= kSortBlock)
+    int own = 0;
+    if (t < R) {
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) own += slots[w * R + t].next;
     }
-    __syncthreads();
-    // rows' starts: R <= kSortBlock, a row per thread
-    const int own = t < rows ? totals[t] : 0;
     int incl = own;
+#pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int up = __shfl_up_sync(kFull, incl, off);
         if (lane >= off) incl += up;
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    int start = below_all + incl - own;
-    for (int w = 0; w < warp; ++w) start += scan[w];
-    if (t < rows) {
-        for (int w = 0; w < kSortWarps; ++w) counts[w * R + t] += start;
+    const int all = scan[lane];
+    int next = below_all + incl - own + __reduce_add_sync(kFull, lane < warp ? all : 0);
+    if (t < R) {
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int n = slots[w * R + t].next;
+            slots[w * R + t].next = next;
+            next += n;
+        }
+        if (!a.accumulate) a.empty[(int64_t)b * R + t] = own == 0;
     }
-    if (blockIdx.x == gridDim.x - 1) {   // behind the last row: the tokens without one
-        int64_t end = below_all;
-        for (int w = 0; w < kSortWarps; ++w) end += scan[w];
+    if (b == gridDim.x - 1) {   // behind the last row: the tokens without one
+        const int64_t end = (int64_t)below_all + __reduce_add_sync(kFull, all);
         for (int64_t j = end + t; j < a.M; j += kSortBlock) a.sorted[j] = Entry{-1, -1};
     }
     __syncthreads();
-    for (int64_t m = m0; m < m1; m += 32) {
-        const int64_t id = m + lane < m1 ? index_at(a.ids, a.wide, m + lane) : -1;
-        const bool in = id >= v0 && id < v1;
-        const uint32_t some = __ballot_sync(kFull, in);
+    for_ids<T>(a.ids, m0, m1, lane, [&](int m, int id) {
+        const bool in = (unsigned)id < V && ((unsigned)id & mask) == b;
+        if (!__any_sync(kFull, in)) return;
+        // the lanes with the same row, in a word of the row (__match_any_sync takes longer the more rows there are)
+        Slot* s = mine + (in ? id >> by.shift : 0);
+        if (in) atomicOr(&s->lanes, 1u << lane);
+        __syncwarp();
+        const Slot v = *s;
+        const uint32_t before = v.lanes & ((1u << lane) - 1u);
+        __syncwarp();
         if (in) {
-            const int r = (int)(id - v0);
-            const uint32_t same = __match_any_sync(some, r), before = same & ((1u << lane) - 1u);
-            const int at = mine[r] + __popc(before);
-            __syncwarp(some);
-            if (before == 0) mine[r] += __popc(same);
-            a.sorted[at] = Entry{(int32_t)(m + lane), (int32_t)id};
+            if (before == 0u) *s = Slot{v.next + __popc(v.lanes), 0u};
+            a.sorted[v.next + __popc(before)] = Entry{m, id};
         }
         __syncwarp();
-    }
-    if (!a.accumulate) {
-        const uint32_t zero[8] = {};
-        for (int r = warp; r < rows; r += kSortWarps) {
-            if (totals[r] != 0) continue;
-            uint16_t* p = a.dtable + (v0 + r) * a.C;
-            for (int64_t c = 16 * lane; c < a.C; c += kSlice) store_words8(p + c, wide, zero);
-        }
-    }
+    });
 }
 
 // ---- backward: sums ----
@@ -142,104 +182,176 @@ __device__ __forceinline__ Entry entry_at(const EmbedBwdArgs& a, int64_t j) {
     const int2 e = *reinterpret_cast<const int2*>(a.sorted + j);
     return Entry{e.x, e.y};
 }
-// adds 16 columns from col of the tokens that the first n lanes hold
-__device__ __forceinline__ void add_tokens(const EmbedBwdArgs& a, int token, int n, int64_t col, bool wide, float (&sum)[16]) {
-#pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-        const int m = __shfl_sync(kFull, token, k);
-        uint32_t w[8];
-        float x[16];
-        load_words8(a.dout + (int64_t)m * a.C + col, wide, w);
-        unpack(w, x);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] += x[e];
-    }
+// a chunk's float32 row in the workspace: 0 of the row that the chunk before it has begun, 1 of one that goes on behind it
+__device__ __forceinline__ float* partial_at(const EmbedBwdArgs& a, int64_t chunk, int which) {
+    return a.partial + (2 * chunk + which) * a.C;
 }
-__device__ __forceinline__ void add_partial(const float* p, float (&sum)[16]) {
+__device__ __forceinline__ void add_row(const float* p, float (&sum)[8]) {
+    const float4 f = reinterpret_cast<const float4*>(p)[0], g = reinterpret_cast<const float4*>(p)[1];
+    sum[0] += f.x; sum[1] += f.y; sum[2] += f.z; sum[3] += f.w;
+    sum[4] += g.x; sum[5] += g.y; sum[6] += g.z; sum[7] += g.w;
+}
+__device__ __forceinline__ void store_row(float* p, const float (&sum)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+}
+// 16 bytes, or zeros where not `there`.  A predicated load, not a load in a branch: behind a branch the compiler copies the
+// loaded words, and every load of a batch waits for the one before it.
+__device__ __forceinline__ void load_words_if(uint32_t there, const void* p, uint32_t (&w)[4]) {
+    w[0] = w[1] = w[2] = w[3] = 0u;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3])
+        : "l"(p), "r"(there));
+}
+// the table's row from the sum of its tokens; old: what it held
+template <bool kAdd>
+__device__ __forceinline__ void store_table(const EmbedBwdArgs& a, int row, int64_t col, const float (&sum)[8], const uint32_t (&old)[4]) {
+    float x[8];
+    uint32_t w[4];
+    if constexpr (kAdd) unpack(old, x);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float4 f = reinterpret_cast<const float4*>(p)[q];
-        sum[4 * q] += f.x;
-        sum[4 * q + 1] += f.y;
-        sum[4 * q + 2] += f.z;
-        sum[4 * q + 3] += f.w;
-    }
+    for (int i = 0; i < 8; ++i) x[i] = kAdd ? fmaf(sum[i], a.scale, x[i]) : sum[i] * a.scale;
+    pack(x, w);
+    *reinterpret_cast<uint4*>(a.dtable + (int64_t)row * a.C + col) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kBlock) embed_chunks_kernel(const EmbedBwdArgs a, int slices, bool wide) {
+template <bool kAdd>
+__global__ void __launch_bounds__(kBlock, 4) embed_chunks_kernel(const EmbedBwdArgs a, int slices) {
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), chunk = unit / slices;
     const int lane = threadIdx.x & 31;
     wait_for_primary();
-    if ((chunk + 1) * kChunk > a.M) return;
+    if (chunk * kChunk >= a.M) return;
     const Entry e = entry_at(a, chunk * kChunk + lane);
-    if (__shfl_sync(kFull, e.row, 0) != __shfl_sync(kFull, e.row, 31) || __shfl_sync(kFull, e.row, 31) < 0) return;
-    const int64_t col = (unit - chunk * slices) * kSlice + 16 * lane;
+    const int before = entry_at(a, chunk * kChunk - 1).row, behind = entry_at(a, (chunk + 1) * kChunk).row;
+    int next = __shfl_down_sync(kFull, e.row, 1);
+    if (lane == 31) next = behind;
+    const uint32_t here = __ballot_sync(kFull, e.row >= 0), ends = __ballot_sync(kFull, e.row >= 0 && e.row != next);
+    const int64_t col = (unit - chunk * slices) * kSlice + 8 * lane;
     const bool ok = col < a.C;
-    float sum[16] = {};
-    add_tokens(a, e.token, kChunk, ok ? col : 0, wide, sum);
-    if (!ok) return;
-    float4* p = reinterpret_cast<float4*>(a.partial + chunk * a.C + col);
+    const int64_t from = ok ? col : 0;
+    const bool begun = before >= 0 && before == __shfl_sync(kFull, e.row, 0);
+    uint32_t mine = ends;                      // the tokens whose rows begin and end in this chunk
+    if (begun) mine &= mine - 1u;
+    float sum[8] = {};
+#pragma unroll 1
+    for (int k0 = 0; k0 < kChunk; k0 += kDeep) {
+        if ((here >> k0 & 1u) == 0u) break;    // behind the last token
+        uint32_t w[kDeep][4], old[kAdd ? kDeep : 1][4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) p[q] = make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]);
-}
-
-__global__ void __launch_bounds__(kBlock) embed_rows_kernel(const EmbedBwdArgs a, int slices, bool wide) {
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), j = unit / slices;
-    const int lane = threadIdx.x & 31;
-    wait_for_primary();
-    if (j >= a.M) return;
-    Entry e = entry_at(a, j + lane);
-    const int row = __shfl_sync(kFull, e.row, 0);
-    if (row < 0 || entry_at(a, j - 1).row == row) return;   // the same for the whole warp
-    const int64_t col = (unit - j * slices) * kSlice + 16 * lane;
-    const bool ok = col < a.C;
-    float sum[16] = {};
-    // the tokens up to the end of the chunk that the row begins in, unless it begins with the chunk and fills it
-    int64_t at = j;
-    const int rest = kChunk - (int)(j % kChunk);
-    int run = __ffs(~__ballot_sync(kFull, e.row == row));   // 1 + the tokens of the row from j on, 0: all 32
-    run = run == 0 ? 32 : run - 1;
-    bool more = run >= rest;
-    if (rest < kChunk || run < kChunk) {
-        add_tokens(a, e.token, run < rest ? run : rest, ok ? col : 0, wide, sum);
-        at = j + rest;
-    }
-    // whole chunks
-    while (more) {
-        const int64_t chunk = at / kChunk;
-        const uint32_t whole = __ballot_sync(kFull, entry_at(a, at + (int64_t)kChunk * lane + kChunk - 1).row == row);
-        int n = __ffs(~whole);
-        n = n == 0 ? 32 : n - 1;
-        if (ok)
-            for (int k = 0; k < n; ++k) add_partial(a.partial + (chunk + k) * a.C + col, sum);
-        at += (int64_t)n * kChunk;
-        more = n == 32;
-        if (!more) {   // the tokens of the chunk that the row ends in
-            e = entry_at(a, at + lane);
-            const uint32_t here = __ballot_sync(kFull, e.row == row);
-            add_tokens(a, e.token, __popc(here), ok ? col : 0, wide, sum);
+        for (int k = 0; k < kDeep; ++k) {
+            const int m = __shfl_sync(kFull, e.token, k0 + k);
+            load_words_if(here >> (k0 + k) & 1u, a.dout + (int64_t)m * a.C + from, w[k]);
+        }
+        if constexpr (kAdd) {
+#pragma unroll
+            for (int k = 0; k < kDeep; ++k) {
+                const int row = __shfl_sync(kFull, e.row, k0 + k);
+                load_words_if(mine >> (k0 + k) & 1u, a.dtable + (int64_t)row * a.C + from, old[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int row = __shfl_sync(kFull, e.row, k0 + k);
+            if ((here >> (k0 + k) & 1u) == 0u) break;
+            float x[8];
+            unpack(w[k], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += x[i];
+            if (ends >> (k0 + k) & 1u) {
+                if (ok) {
+                    if (mine >> (k0 + k) & 1u) store_table<kAdd>(a, row, col, sum, old[kAdd ? k : 0]);
+                    else store_row(partial_at(a, chunk, 0) + col, sum);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+            }
         }
     }
-    if (!ok) return;
-    uint16_t* p = a.dtable + (int64_t)row * a.C + col;
-    uint32_t w[8];
-    if (a.accumulate) {
-        float x[16];
-        load_words8(p, wide, w);
-        unpack(w, x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = fmaf(sum[i], a.scale, x[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] *= a.scale;
+    // a row that goes on: the whole chunk of one that the chunk before has begun, or the beginning of one
+    if (here == kFull && (ends >> 31) == 0u && ok) store_row(partial_at(a, chunk, begun && ends == 0u ? 0 : 1) + col, sum);
+}
+
+// Of the chunks behind `chunk`, how many begin with a token of `row` (they are consecutive), if the first 64 do; the whole
+// warp.
+__device__ __noinline__ int64_t chunks_of_row(const EmbedBwdArgs& a, int row, int64_t chunk, int lane) {
+    int64_t n = 64, step = 1;
+    uint32_t in;
+    auto probe = [&] { return __ballot_sync(kFull, entry_at(a, (chunk + n + step * (lane + 1)) * kChunk).row == row); };
+    // in steps that grow 32 times each, as far as all 32 probes are in the row
+    while ((in = probe()) == kFull) {
+        n += 32 * step;
+        step *= 32;
     }
-    pack(sum, w);
-    store_words8(p, wide, w);
+    n += step * (__ffs(~in) - 1);
+    while (step > 1) {   // the first chunk that is not lies within `step` of chunk + n
+        step /= 32;
+        in = probe();
+        n += step * (in == kFull ? 32 : __ffs(~in) - 1);
+    }
+    return n;
+}
+
+// Zeros over the rows without a token: kFill rows per block, one thread for each, whose copies read
+// the same zeros in shared memory (8192 x 4096 of 32000 rows: 28 us for 205 MB; by stores of the warps 31 us).
+__device__ __forceinline__ void fill_rows(const EmbedBwdArgs& a, const Ranges& by, int64_t block, float* zeros) {
+    for (int i = threadIdx.x; i < kZeroBytes / 4; i += kBlock) zeros[i] = 0.0f;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies read them
+    __syncthreads();
+    const int64_t row = block * kFill + threadIdx.x;
+    if (threadIdx.x >= kFill || row >= a.V || a.empty[(row & ((1 << by.shift) - 1)) * by.R + (row >> by.shift)] == 0) return;
+    char* p = reinterpret_cast<char*>(a.dtable + row * a.C);
+    for (int64_t n = 2 * a.C; n > 0; n -= kZeroBytes, p += kZeroBytes)
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p),
+                     "r"((uint32_t)__cvta_generic_to_shared(zeros)), "r"((uint32_t)(n < kZeroBytes ? n : kZeroBytes))
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// The first `fills` blocks fill.  Of the others each has a chunk and 2 times 256 columns; four warps add up a row's shares for
+// the same columns.
+template <bool kAdd>
+__global__ void __launch_bounds__(kBlock) embed_join_kernel(const EmbedBwdArgs a, int groups, const Ranges by, unsigned fills) {
+    __shared__ __align__(16) float part[kWarps][kSlice];
+    wait_for_primary();
+    if (!kAdd && blockIdx.x < fills) {
+        fill_rows(a, by, blockIdx.x, &part[0][0]);
+        return;
+    }
+    const int64_t block = blockIdx.x - fills, chunk = block / groups;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / kTeams;
+    // a row that begins in this chunk and goes on behind it: in n chunks (all of these loads at once)
+    const int64_t last = chunk * kChunk + kChunk - 1;
+    const int near = entry_at(a, last + 1 + kChunk * lane).row, far = entry_at(a, last + 1 + kChunk * (32 + lane)).row;
+    const int row = entry_at(a, last).row, first = entry_at(a, last - kChunk + 1).row, before = entry_at(a, last - kChunk).row;
+    if (row < 0 || (first == row && before == row)) return;   // the same for the whole block
+    const uint32_t in = __ballot_sync(kFull, near == row), more = __ballot_sync(kFull, far == row);
+    if (in == 0u) return;
+    const int64_t n = in != kFull ? __popc(in) : more != kFull ? 32 + __popc(more) : chunks_of_row(a, row, chunk, lane);
+    const int64_t col = ((block - chunk * groups) * kTeams + warp % kTeams) * kSlice + 8 * lane;
+    const bool ok = col < a.C;
+    uint32_t old[4];
+    load_words_if(kAdd && ok && team == 0, a.dtable + (int64_t)row * a.C + (ok ? col : 0), old);
+    float sum[8] = {};
+    if (ok) {
+        if (team == 0) add_row(partial_at(a, chunk, 1) + col, sum);
+#pragma unroll 8
+        for (int64_t i = 1 + team; i <= n; i += kWarps / kTeams) add_row(partial_at(a, chunk + i, 0) + col, sum);
+    }
+    if (team > 0) store_row(part[warp] + 8 * lane, sum);
+    __syncthreads();
+    if (team > 0 || !ok) return;
+#pragma unroll
+    for (int w = kTeams; w < kWarps; w += kTeams) add_row(part[warp + w] + 8 * lane, sum);
+    store_table<kAdd>(a, row, col, sum, old);
 }
 
 }  // namespace
 
-int64_t embed_chunks(int64_t M) { return M / kChunk; }
+int64_t embed_chunks(int64_t M) { return (M + kChunk - 1) / kChunk; }
 
 cudaError_t launch_embed_fwd(const EmbedFwdArgs& all, cudaStream_t s) {
     const int64_t nc = all.C / 16, slab = (((int64_t)1 << 31) - kBlock) / nc;   // a launch's chunks are counted in 31 bits
@@ -256,23 +368,38 @@ cudaError_t launch_embed_fwd(const EmbedFwdArgs& all, cudaStream_t s) {
     return cudaSuccess;
 }
 
+namespace {
+Ranges ranges_of(int64_t V) {
+    Ranges by{7, 0};
+    while (((V - 1) >> by.shift) + 1 > kMaxRange) ++by.shift;
+    by.R = (int32_t)(((V - 1) >> by.shift) + 1);
+    return by;
+}
+}  // namespace
+
+int64_t embed_flags(int64_t V) {
+    const Ranges by = ranges_of(V);
+    return (int64_t)by.R << by.shift;
+}
+
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
-    const int sms = device_sms();
-    if (sms < 1) return cudaErrorInvalidConfiguration;
-    const bool wide = aligned32(a.dout) && aligned32(a.dtable);
-    int64_t R = (a.V + sms - 1) / sms;
-    R = R > kMaxRange ? kMaxRange : R;
-    const size_t smem = (size_t)(kSortWarps + 1) * (size_t)R * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const Ranges by = ranges_of(a.V);
+    const size_t smem = (size_t)kSortWarps * (size_t)by.R * sizeof(Slot);
+    auto* const sort = a.wide ? embed_sort_kernel<long long> : embed_sort_kernel<int>;
+    cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    e = launch_next(embed_sort_kernel, (unsigned)((a.V + R - 1) / R), kSortBlock, smem, s, a, (int)R, wide);
+    e = launch_next(sort, 1u << by.shift, kSortBlock, smem, s, a, by);
     if (e != cudaSuccess) return e;
-    const int slices = (int)((a.C + kSlice - 1) / kSlice);
-    if (embed_chunks(a.M) > 0) {
-        e = launch_next(embed_chunks_kernel, (unsigned)((embed_chunks(a.M) * slices + kWarps - 1) / kWarps), kBlock, 0, s, a, slices, wide);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_next(embed_rows_kernel, (unsigned)((a.M * slices + kWarps - 1) / kWarps), kBlock, 0, s, a, slices, wide);
+    const int slices = (int)((a.C + kSlice - 1) / kSlice), groups = (slices + kTeams - 1) / kTeams;
+    const int64_t chunks = embed_chunks(a.M);
+    e = launch_next(a.accumulate ? embed_chunks_kernel<true> : embed_chunks_kernel<false>,
+                    (unsigned)((chunks * slices + kWarps - 1) / kWarps), kBlock, 0, s, a, slices);
+    if (e != cudaSuccess) return e;
+    const unsigned fills = a.accumulate ? 0u : (unsigned)((a.V + kFill - 1) / kFill);
+    const int64_t joins = chunks > 1 ? chunks * groups : 0;   // one chunk: no row goes on behind it
+    if (fills + joins == 0) return cudaSuccess;
+    return launch_next(a.accumulate ? embed_join_kernel<true> : embed_join_kernel<false>, (unsigned)(fills + joins), kBlock, 0, s, a, groups,
+                       by, fills);
 }
 
 }  // namespace coat

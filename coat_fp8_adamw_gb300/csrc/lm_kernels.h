@@ -30,9 +30,11 @@ struct EmbedBwdArgs {
     int32_t accumulate;
     uint16_t* dtable;          // V x C bf16
     Entry* sorted;             // M
-    float* partial;            // embed_chunks(M) x C
+    float* partial;            // embed_chunks(M) x 2 x C
+    uint8_t* empty;            // embed_flags(V): rows without a token
 };
 int64_t embed_chunks(int64_t M);
+int64_t embed_flags(int64_t V);
 
 struct DropoutArgs {
     const uint16_t* x;         // n bf16

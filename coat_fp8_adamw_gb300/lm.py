@@ -37,9 +37,9 @@ def coat_embedding(table, ids, scale: float, out, stream=None) -> None:
           float(scale), M, V, C, _ptr(out, _BF16, M * C, "out", dev))
 
 
-def coat_embedding_backward_workspace_bytes(M: int, C: int, device=None) -> int:
-    """Bytes of workspace that coat_embedding_backward needs for M tokens."""
-    return _size("coat_embedding_backward_workspace_bytes", device, M, C)
+def coat_embedding_backward_workspace_bytes(M: int, V: int, C: int, device=None) -> int:
+    """Bytes of workspace that coat_embedding_backward needs for M tokens and a table [V, C]."""
+    return _size("coat_embedding_backward_workspace_bytes", device, M, V, C)
 
 
 def coat_embedding_backward(dout, ids, scale: float, dtable, workspace, accumulate: bool = False,

@@ -482,7 +482,7 @@ coat_status coat_embedding(const uint16_t *table, const void *ids, int32_t wide_
 coat_status coat_embedding_backward(const uint16_t *dout, const void *ids, int32_t wide_ids, float scale,
                                     int64_t M, int64_t V, int64_t C, int32_t accumulate, uint16_t *dtable,
                                     void *workspace, size_t workspace_bytes, void *stream);
-size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t C);
+size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t V, int64_t C);
 
 /*
  * Softmax cross entropy of a linear layer, whose logits z = x W^T are not kept:

@@ -30,7 +30,7 @@ def text(M, V, seed):
 def backward(dout, ids, scale, V, old=None, ws=None, stream=None):
     M, C = dout.shape
     d = unwritten(V, C) if old is None else old.clone()
-    ws = workspace(coat.coat_embedding_backward_workspace_bytes(M, C)) if ws is None else ws
+    ws = workspace(coat.coat_embedding_backward_workspace_bytes(M, V, C)) if ws is None else ws
     coat.coat_embedding_backward(dout, ids, scale, d, ws, accumulate=old is not None, stream=stream)
     return d
 
@@ -140,7 +140,7 @@ def test_pointers_of_16_bytes(shift):
     out, d = view(unwritten(M, C)), view(unwritten(V, C))
     coat.coat_embedding(table, ids, 1.0, out)
     assert torch.equal(out[ids >= 0], table[ids[ids >= 0]])
-    ws = workspace(coat.coat_embedding_backward_workspace_bytes(M, C))
+    ws = workspace(coat.coat_embedding_backward_workspace_bytes(M, V, C))
     coat.coat_embedding_backward(dout, ids, 1.0, d, ws)
     assert torch.equal(d, backward(dout.clone(), ids, 1.0, V))
 
@@ -169,7 +169,7 @@ def test_offsets_past_2_31_elements():
     assert torch.equal(out, table[ids])
     before = table[ids].clone()
     dout = torch.ones(5, C, dtype=BF, device="cuda")
-    ws = workspace(coat.coat_embedding_backward_workspace_bytes(5, C))
+    ws = workspace(coat.coat_embedding_backward_workspace_bytes(5, V, C))
     coat.coat_embedding_backward(dout, ids, 2.0, table, ws)
     want = torch.tensor([4.0, 2.0, 4.0, 2.0, 2.0], device="cuda")
     assert torch.equal(table[ids], want[:, None].expand(5, C).to(BF)) and before.isfinite().all()
@@ -182,7 +182,7 @@ def test_captured_and_replayed_on_another_stream():
     M, V, C = 600, 90, 128
     ids, dout = text(M, V, 1).int(), randn(M, C, seed=1).to(BF)
     table, out, d = randn(V, C, seed=2).to(BF), unwritten(M, C), unwritten(V, C)
-    ws = workspace(coat.coat_embedding_backward_workspace_bytes(M, C))
+    ws = workspace(coat.coat_embedding_backward_workspace_bytes(M, V, C))
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):

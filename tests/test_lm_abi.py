@@ -57,9 +57,10 @@ def test_embedding_backward(L):
 
 def test_embedding_backward_workspace(L):
     f = L.coat_embedding_backward_workspace_bytes
-    assert f(1, 16) == 16 and f(2, 16) == 16 and f(3, 16) == 32         # eight bytes a token, in multiples of 16
-    assert f(32, 16) == 256 + 64 and f(63, 64) == 512 + 256             # and a float32 row for every whole chunk of 32
-    assert f(0, 16) == 0 and f(16, 24) == 0 and f(1 << 31, 16) == 0
+    # eight bytes a token, in multiples of 16; two float32 rows for every chunk of 32; a flag for 128 k >= V rows
+    assert f(1, 1, 16) == 16 + 128 + 128 and f(3, 129, 16) == 32 + 128 + 256
+    assert f(32, 128, 16) == 256 + 128 + 128 and f(63, 1, 64) == 512 + 1024 + 128
+    assert f(0, 1, 16) == 0 and f(16, 1, 24) == 0 and f(1 << 31, 1, 16) == 0 and f(16, 0, 16) == 0
 
 
 def _drop(L, x=at(0), res=None, p=0.1, rng=at(1), n=1000, y=at(2)):
