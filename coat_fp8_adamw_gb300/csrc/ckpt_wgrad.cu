@@ -170,39 +170,6 @@ __device__ __forceinline__ Item item_at(int64_t i, const Plan& p) {
     return it;
 }
 
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p;
-}
-
-// whether the phase is over, without a wait (a try may hold the warp until its phase ends)
-template <bool kRelaxed = false>
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    if constexpr (kRelaxed)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-    return ok != 0u;
-}
-
 // Two 16 x 16 blocks of bytes, transposed: lane's address = row `lane` of the two
 // blocks (16 bytes each); r[2 b + h] = bytes 4 (lane % 4) .. + 3 of the
 // transposed block b's row lane / 4 + 8 h.

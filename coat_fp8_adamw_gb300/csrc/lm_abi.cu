@@ -22,6 +22,7 @@ bool lce_ok(int64_t M, int64_t V, int64_t C, int64_t x_ld) {
     return rows_ok(M, C) && rows_ok(V, C) && stride_ok(x_ld, C) && M * V <= COAT_MAX_N;
 }
 size_t dz_bytes(int64_t M, int64_t V, int64_t piece) { return 2 * (size_t)M * (size_t)coat::lce_piece_ld(piece, V); }
+size_t xt_bytes(int64_t M, int64_t C) { return 2 * (size_t)C * (size_t)coat::lce_xt_ld(M); }
 size_t index_bytes(int64_t M, int32_t wide) { return (size_t)M * (wide ? 8 : 4); }
 
 coat_status dropout(const uint16_t* x, const uint16_t* residual, float p, const uint64_t* rng, int64_t n, uint16_t* y, void* stream) {
@@ -92,7 +93,7 @@ coat_status coat_linear_cross_entropy(const uint16_t* x, int64_t x_ld, const uin
 size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t C, int64_t piece) {
     if (!lce_ok(M, V, C, C) || piece < 0) return 0;
     const int64_t p = coat::lce_piece(M, V, piece);
-    return dz_bytes(M, V, p) + (p < V ? 4 * (size_t)M * (size_t)C : 0);
+    return dz_bytes(M, V, p) + xt_bytes(M, C) + 4 * (size_t)coat::lce_sums(M, V, C, p);
 }
 
 coat_status coat_linear_cross_entropy_backward(const uint16_t* x, int64_t x_ld, const uint16_t* weight, const void* targets,
@@ -109,9 +110,10 @@ coat_status coat_linear_cross_entropy_backward(const uint16_t* x, int64_t x_ld, 
     if (st != COAT_OK) return st;
     if (workspace_bytes < coat_linear_cross_entropy_backward_workspace_bytes(M, V, C, piece)) return COAT_ERR_INVALID_ARG;
     const int64_t p = coat::lce_piece(M, V, piece);
-    float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(M, V, p));
+    char* xt = static_cast<char*>(workspace) + dz_bytes(M, V, p);
     const coat::LceBwdArgs a{x, x_ld, weight, targets, wide_targets, lse, dloss, dlse, M, V, C, p, dx, dweight,
-                             static_cast<uint16_t*>(workspace), sums};
+                             static_cast<uint16_t*>(workspace), reinterpret_cast<uint16_t*>(xt),
+                             reinterpret_cast<float*>(xt + xt_bytes(M, C))};
     return from_cuda(coat::launch_lce_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -71,11 +71,15 @@ struct LceBwdArgs {
     uint16_t* dx;              // M x C bf16
     uint16_t* dweight;         // V x C bf16
     uint16_t* dz;              // M x lce_piece_ld(piece, V) bf16
-    float* sums;               // M x C, where there are several pieces
+    uint16_t* xt;              // C x lce_xt_ld(M) bf16: x transposed
+    float* sums;               // lce_sums(...): of products in several parts or pieces
 };
 constexpr int64_t kLceDzBytes = 256 << 20;   // of a piece's gradient of the logits, unless the caller says how wide a piece is
 int64_t lce_piece(int64_t M, int64_t V, int64_t piece);
 int64_t lce_piece_ld(int64_t piece, int64_t V);
+int64_t lce_xt_ld(int64_t M);
+int64_t lce_dx_sums(int64_t M, int64_t V, int64_t C, int64_t piece);
+int64_t lce_sums(int64_t M, int64_t V, int64_t C, int64_t piece);
 size_t lce_stats_bytes(int64_t M, int64_t V);
 
 cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s);

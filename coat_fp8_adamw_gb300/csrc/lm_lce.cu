@@ -11,12 +11,13 @@
 //             dx (added up over the pieces in float32) and the piece's rows of dW in one launch.
 // dz is rounded to bf16, since it is an operand of the tensor cores, like a layer's gradient that a step keeps as bf16.
 //
-// One kernel for all four: persistent CTA pairs (clusters of two, one CTA per SM) walk tiles of 256 rows x BN columns,
+// One kernel for all four: persistent CTA pairs (clusters of two, one CTA per SM) walk tiles of 256 rows x up to 256 columns,
 // 64 of the summed index per stage, as in linear_fp8.cu: each CTA has its 128 rows of A and half of the columns of B in
 // a ring of stages filled by TMA (128-byte swizzle), one thread of the even CTA issues tcgen05.mma.cta_group::2
 // kind::f16, and eight epilogue warps per CTA read one of two accumulators in tensor memory while the other one fills.
-// An operand lies as it is in memory, with its summed index along the row (K-major: x and W for z, dz for dx) or across
-// it (MN-major: W for dx, dz and x for dW): the MMA takes both, and nothing is transposed.
+// B has its summed index along the row (K-major); A has it so too (x for z) or across the row (MN-major), which the MMA
+// takes at the same rate (8192^3: 1.79 PFLOP/s both; with B MN-major 1.46).  So dx is formed as its transpose, of W
+// (MN-major) and dz, and dW of dz (MN-major) and x's transpose, which a kernel lays out before.
 // Every wait on an mbarrier is bounded, as in linear_fp8.cu.
 #include <cstdint>
 
@@ -40,36 +41,42 @@ constexpr int kBoxBytes = kBK * 128;           // MN-major: 64 of the summed ind
 constexpr int kEpiWarps = 8;                   // two per SM sub-partition, each half the columns
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kChunk = 32;                     // columns that an epilogue thread holds at once
+constexpr int64_t kPairs = 76;                  // that the division of the work goes by, on every device
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int BN>
-struct Shape {
-    static constexpr int kBBytes = (BN / 2) * kBK * 2;
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = BN == 256 ? 7 : 9;
-    static constexpr int kBarOff = kStages * kStageBytes;
-    static constexpr int kNumBars = 2 * kStages + 5;   // full, empty, acc full x2, acc empty x2, done
-    static constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 1024-B alignment
-    static_assert(kSmemBytes <= 232448, "shared memory of an SM");
-};
+constexpr int kBN = 256;                       // most columns of a tile
+constexpr int kBBytes = (kBN / 2) * kBK * 2;   // 16 KB
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 7;
+constexpr int kBarOff = kStages * kStageBytes;
+constexpr int kNumBars = 2 * kStages + 5;      // full, empty, acc full x2, acc empty x2, done
+constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 1024-B alignment
+static_assert(kSmemBytes <= 232448, "shared memory of an SM");
 
 // What a launch does with a tile's sums.
 enum Mode : int32_t { kStats, kDz, kDx, kDw };
 
+// A product: its tiles, each summed in `parts` parts of the summed index.
 struct Job {
     int32_t mode;
-    int32_t a_mn, b_mn;      // the operands are MN-major
+    int32_t a_mn;            // A is MN-major
     int32_t steps;           // 64 of the summed index each
+    int32_t bn;              // columns of a tile: a multiple of 32
+    int32_t parts;
     int64_t tm, tn;          // tiles
     int64_t rows, cols;      // of the product
     uint16_t* out;           // kDz, kDx (last piece), kDw: bf16, ld apart
     int64_t ld;
-    float* sums;             // kDx in several pieces: the float32 sums so far, rows x cols
-    int32_t first, last;     // kDx: the first and last piece
+    float* sums;             // [parts][out's shape] float32: of parts, or of the pieces so far
+    int32_t first, last;     // sums: the first piece, which writes them; the last one of a product in one part, which ends in out
 };
+// The jobs of a launch, the one with the longer items first.  Of its items every pair has one in turn; `ahead` pairs have one
+// more of them than the others, and those have `extra` items of the second job for it.  Everything else goes in turn again.
 struct Work {
     Job job[2];
     int32_t jobs;
+    int32_t pairs, ahead;
+    int64_t items[2], extra;
     // rows of the logits
     const void* targets;
     int32_t wide, V;
@@ -77,7 +84,7 @@ struct Work {
     const float* lse;
     const float* dloss;
     const float* dlse;
-    float2* stats;           // kStats: [column half tile][row], rows padded
+    float2* stats;           // kStats: [half tile's columns][row], rows padded
     int64_t stats_ld;
     float* target_logit;
 };
@@ -87,12 +94,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, bool mn) {
     return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn ? kBoxBytes >> 4 : 1) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
-// D in f32 (bits 4-5 = 1), A and B bf16 (bits 7-9 and 10-12 = 1), MN-major operands (bits 15, 16), N / 8 in bits 17-22,
-// M / 16 in bits 24-28 (M = 256 over the two CTAs).
-template <int BN>
+// D in f32 (bits 4-5 = 1), A and B bf16 (bits 7-9 and 10-12 = 1), A MN-major (bit 15) or not, N / 8 in bits 17-22, M / 16 in
+// bits 24-28 (M = 256 over the two CTAs).
 __device__ __forceinline__ uint32_t instr_desc(const Job& j) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)j.a_mn << 15) | ((uint32_t)j.b_mn << 16) | ((uint32_t)(BN >> 3) << 17) |
-           ((uint32_t)((2 * kBM) >> 4) << 24);
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)j.a_mn << 15) | ((uint32_t)(j.bn >> 3) << 17) | ((uint32_t)((2 * kBM) >> 4) << 24);
 }
 __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -107,39 +112,60 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
 // A and walk B together.
 constexpr int64_t kBand = 16;
 struct Item {
-    int32_t job;
-    int64_t m, n;
+    int32_t job, part;
+    int32_t from, to;        // steps
+    int64_t m, n;            // tile
 };
-__device__ __forceinline__ Item item_at(int64_t t, const Work& w) {
-    Item it;
-    const int64_t first = w.job[0].tm * w.job[0].tn;
-    it.job = t >= first;
-    if (it.job) t -= first;
-    const int64_t tm = w.job[it.job].tm, tn = w.job[it.job].tn;
-    const int64_t band = t / (kBand * tn), top = band * kBand;
-    const int64_t rows = tm - top < kBand ? tm - top : kBand;
-    const int64_t r = t - band * kBand * tn;
+// the k-th item of pair `pair`; false: it has none left
+__device__ __forceinline__ bool item_of(int64_t k, int64_t pair, const Work& w, Item& it) {
+    const int64_t P = w.pairs, own = (w.items[0] - pair + P - 1) / P;   // of the first job
+    int64_t t;
+    it.job = k >= own;
+    if (it.job == 0) {
+        t = pair + k * P;
+    } else {
+        k -= own;
+        const int64_t behind = pair - w.ahead;
+        if (behind >= 0) {
+            const int64_t lot = P - w.ahead, mine = behind < w.extra ? (w.extra - behind + lot - 1) / lot : 0;
+            if (k < mine) {
+                t = behind + k * lot;
+                k = -1;
+            } else {
+                k -= mine;
+            }
+        }
+        if (k >= 0) t = w.extra + k * P + pair;
+        if (t >= w.items[1]) return false;
+    }
+    const Job& j = w.job[it.job];
+    const int64_t tiles = j.tm * j.tn;
+    it.part = (int32_t)(t / tiles);
+    t -= it.part * tiles;
+    it.from = (int32_t)((int64_t)j.steps * it.part / j.parts);
+    it.to = (int32_t)((int64_t)j.steps * (it.part + 1) / j.parts);
+    const int64_t band = t / (kBand * j.tn), top = band * kBand;
+    const int64_t rows = j.tm - top < kBand ? j.tm - top : kBand;
+    const int64_t r = t - band * kBand * j.tn;
     it.m = top + r % rows;
     it.n = r / rows;
-    return it;
+    return true;
 }
 
-// ---- epilogues: one row of the tile, BN / 2 columns from n0, per thread ----
-template <int BN>
-__device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t part) {
+// ---- epilogues: one row of the tile, columns n0 .. end - 1 (at most 128, a multiple of 16 but for the matrix's end), per
+// thread; where a chunk of 32 goes past them, it reads columns of the other half, which do not count ----
+__device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int64_t part) {
     float top = -INFINITY, sum = 0.0f;
     const int64_t target = row < j.rows ? index_at(w.targets, w.wide, row) : -1;
 #pragma unroll 1
-    for (int c = 0; c < BN / 2; c += kChunk) {
-        const int64_t col = n0 + c;
-        if (col >= j.cols) break;   // the same for the whole warp
+    for (int64_t col = n0; col < end; col += kChunk) {   // the same for the whole warp
         uint32_t v[kChunk];
         __syncwarp();   // tcgen05.ld is warp-collective
-        tmem_ld<kChunk>(taddr + (uint32_t)c, v);
-        if (col + kChunk > j.cols) {
+        tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
+        if (col + kChunk > end) {
 #pragma unroll
             for (int e = 0; e < kChunk; ++e)
-                if (col + e >= j.cols) v[e] = 0xFF800000u;   // -inf: not a column
+                if (col + e >= end) v[e] = 0xFF800000u;   // -inf: not a column
         }
         const bool has = target >= col && target < col + kChunk;
         if (__any_sync(kFull, has)) {
@@ -147,7 +173,7 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, uint32
 #pragma unroll
             for (int e = 0; e < kChunk; ++e)
                 if (col + e == target) z = __uint_as_float(v[e]);
-            if (has && target < j.cols) w.target_logit[row] = z;
+            if (has && target < end) w.target_logit[row] = z;
         }
         float mx = top;
 #pragma unroll
@@ -160,7 +186,7 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, uint32
         for (int e = 0; e < kChunk; ++e) s[e & 3] += ex2_ftz((__uint_as_float(v[e]) - ref) * kLog2e);
         sum += (s[0] + s[1]) + (s[2] + s[3]);
     }
-    if (row < j.rows && n0 < j.cols) w.stats[part * w.stats_ld + row] = make_float2(top, sum);
+    if (row < j.rows && n0 < end) w.stats[part * w.stats_ld + row] = make_float2(top, sum);
 }
 
 // 32 bf16 columns of a row; n of them (a multiple of 16) are there
@@ -173,8 +199,7 @@ __device__ __forceinline__ void store_row(uint16_t* p, int64_t n, bool wide, con
     }
 }
 
-template <int BN>
-__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, uint32_t taddr, int64_t row, int64_t n0, bool wide) {
+__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, bool wide) {
     const bool ok = row < j.rows;
     float lse = 0.0f, g = 0.0f, p = 0.0f;   // dz = p e^(z - lse) - [v = t] g
     int64_t target = -1;
@@ -186,12 +211,10 @@ __device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, uint32_t 
     }
     target -= w.v0;
 #pragma unroll 1
-    for (int c = 0; c < BN / 2; c += kChunk) {
-        const int64_t col = n0 + c;
-        if (col >= j.cols) break;
+    for (int64_t col = n0; col < end; col += kChunk) {
         uint32_t v[kChunk], o[kChunk / 2];
         __syncwarp();
-        tmem_ld<kChunk>(taddr + (uint32_t)c, v);
+        tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
 #pragma unroll
         for (int e = 0; e < kChunk; ++e) v[e] = __float_as_uint(p * ex2_ftz((__uint_as_float(v[e]) - lse) * kLog2e));
         if (__any_sync(kFull, target >= col && target < col + kChunk)) {
@@ -201,48 +224,82 @@ __device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, uint32_t 
         }
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        // the buffer's rows are whole tiles, and what lies behind the piece's columns is not read
-        if (ok) store_row(j.out + row * j.ld + col, kChunk, wide, o);
+        // what lies behind the piece's columns is there, but not read
+        if (ok) store_row(j.out + row * j.ld + col, end - col, wide, o);
     }
 }
 
-template <int BN>
-__device__ __forceinline__ void sums_of_row(const Job& j, uint32_t taddr, int64_t row, int64_t n0, bool wide) {
+// Where there are sums of other parts or pieces: those of the pieces before are added; true: more will be added to these, here
+// or behind the last piece, and they are stored, so nothing else is to do.  `left` of the 32 sums are there, one column each
+// (p: float32, a multiple of 16 of them) or one row each, `stride` apart.
+__device__ __forceinline__ bool with_sums_of_row(const Job& j, float* p, int64_t left, uint32_t (&v)[kChunk]) {
+    float4* q = reinterpret_cast<float4*>(p);
+#pragma unroll
+    for (int i = 0; i < kChunk / 4; ++i) {
+        if (j.first || 4 * i >= left) break;
+        const float4 f = q[i];
+        v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + f.x);
+        v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + f.y);
+        v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + f.z);
+        v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + f.w);
+    }
+    if (j.last) return false;
+#pragma unroll
+    for (int i = 0; i < kChunk / 4; ++i)
+        if (4 * i < left)
+            q[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                               __uint_as_float(v[4 * i + 3]));
+    return true;
+}
+__device__ __forceinline__ bool with_sums_of_column(const Job& j, float* p, int64_t stride, int64_t left, uint32_t (&v)[kChunk]) {
+    if (!j.first) {
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e)
+            if (e < left) v[e] = __float_as_uint(__uint_as_float(v[e]) + p[e * stride]);
+    }
+    if (j.last) return false;
+#pragma unroll
+    for (int e = 0; e < kChunk; ++e)
+        if (e < left) p[e * stride] = __uint_as_float(v[e]);
+    return true;
+}
+
+// kDw: rows of the weight's gradient
+__device__ __forceinline__ void dw_of_row(const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int part, bool wide) {
     const bool ok = row < j.rows;
 #pragma unroll 1
-    for (int c = 0; c < BN / 2; c += kChunk) {
-        const int64_t col = n0 + c, left = j.cols - col;
-        if (left <= 0) break;
+    for (int64_t col = n0; col < end; col += kChunk) {
         uint32_t v[kChunk];
-        __syncwarp();   // tcgen05.ld is warp-collective
-        tmem_ld<kChunk>(taddr + (uint32_t)c, v);
-        if (!ok) continue;
-        if (j.sums) {
-            float4* p = reinterpret_cast<float4*>(j.sums + row * j.cols + col);
-            if (!j.first) {
-#pragma unroll
-                for (int q = 0; q < kChunk / 4; ++q) {
-                    if (4 * q >= left) break;
-                    const float4 f = p[q];
-                    v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) + f.x);
-                    v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) + f.y);
-                    v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) + f.z);
-                    v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) + f.w);
-                }
-            }
-            if (!j.last) {
-#pragma unroll
-                for (int q = 0; q < kChunk / 4; ++q)
-                    if (4 * q < left)
-                        p[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
-                                           __uint_as_float(v[4 * q + 3]));
-                continue;
-            }
-        }
+        __syncwarp();
+        tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
+        if (!ok || (j.sums && with_sums_of_row(j, j.sums + (part * j.rows + row) * j.cols + col, end - col, v))) continue;
         uint32_t o[kChunk / 2];
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        store_row(j.out + row * j.ld + col, left, wide, o);
+        store_row(j.out + row * j.ld + col, end - col, wide, o);
+    }
+}
+
+// kDx: the product's rows are the columns of dx, its columns the tokens, so the lanes of a warp have neighbours of one token
+__device__ __forceinline__ void dx_of_column(const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int part, int lane) {
+    const bool ok = row < j.rows;
+    const int odd = lane & 1;
+#pragma unroll 1
+    for (int64_t col = n0; col < end; col += kChunk) {
+        uint32_t v[kChunk];
+        __syncwarp();
+        tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
+        const int64_t left = ok ? end - col : 0;
+        if (j.sums && with_sums_of_column(j, j.sums + (part * j.cols + col) * j.rows + row, j.rows, left, v)) continue;   // not j.last: all lanes
+        __syncwarp();
+        // two lanes exchange, so that each has two neighbours of one token: the even lane of token e, the odd one of e + 1
+        uint16_t* p = j.out + (col + odd) * j.ld + (row - odd);
+#pragma unroll
+        for (int e = 0; e < kChunk; e += 2) {
+            const uint32_t own = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), got = __shfl_xor_sync(kFull, own, 1);
+            const uint32_t out = odd ? __byte_perm(got, own, 0x7632) : __byte_perm(own, got, 0x5410);
+            if (e + odd < left) *reinterpret_cast<uint32_t*>(p + e * j.ld) = out;
+        }
     }
 }
 
@@ -251,21 +308,18 @@ struct Maps {
     CUtensorMap a[2], b[2];
 };
 
-template <int BN>
 __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w, const bool wide) {
-    using S = Shape<BN>;
-    constexpr int kStages = S::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);   // the same offset in both CTAs
     const uint32_t sb = smem_u32(smem);
-    const uint32_t bar0 = sb + S::kBarOff;
+    const uint32_t bar0 = sb + kBarOff;
     auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
     auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(kStages + s); };
     auto acc_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kStages + b); };
     auto acc_empty = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kStages + 2 + b); };
     const uint32_t done = bar0 + 8u * (uint32_t)(2 * kStages + 4);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kBarOff + 8 * S::kNumBars);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * kNumBars);
     volatile uint32_t* abort = tmem_slot + 1;
 
     const int warp = __shfl_sync(kFull, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -283,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         }
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(2 * BN)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(2 * kBN)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -293,99 +347,115 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     wait_for_primary();
     const uint32_t tmem = *tmem_slot;
 
-    const int64_t items = w.job[0].tm * w.job[0].tn + (w.jobs > 1 ? w.job[1].tm * w.job[1].tn : 0);
-    const int64_t cid = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+    const int64_t pair = blockIdx.x >> 1;
+    Item it;
 
-    if (warp == 0 && lane == 0) {
-        // ---- TMA producer (both CTAs): this CTA's 128 rows of A and BN / 2 columns of B ----
+    // The producer's and the issuer's warps walk together and one elected lane issues, so that addresses and descriptors stay
+    // in uniform registers, and ask for the next stage's barrier before they issue for this one: a single thread that waits,
+    // issues and turns takes 550 clocks a step, more than the 512 of a 256 x 256 tile's MMAs.
+    if (warp == 0) {
+        // ---- TMA producer (both CTAs): this CTA's 128 rows of A and half of the columns of B ----
         int s = 0;
         uint32_t ph = 0, issued = 0, last_ph = 0;   // per stage: issued at all, parity of the last issue
-        bool ok = true;
+        bool ok = true, ready = false;
+        const uint32_t elected = elect_one();
         const uint32_t fb0 = map_to_rank(full(0), 0);   // the leader's barriers, contiguous like ours
-        for (int64_t i = cid; ok && i < items; i += nclusters) {
-            const Item it = item_at(i, w);
+        for (int64_t i = 0; ok && item_of(i, pair, w, it); ++i) {
             const Job& j = w.job[it.job];
             const CUtensorMap *ma = &maps.a[it.job], *mb = &maps.b[it.job];
-            const int32_t m0 = (int32_t)(it.m * (2 * kBM) + rank * kBM), n0 = (int32_t)(it.n * BN + rank * (BN / 2));
-            const int steps = j.steps;
-            const bool a_mn = j.a_mn, b_mn = j.b_mn;
-            for (int k = 0; k < steps; ++k) {
-                if (!mbar_wait_fast(empty(s), ph ^ 1u, abort)) { ok = false; break; }
-                if (leader) mbar_expect_tx(full(s), (uint32_t)(2 * S::kStageBytes));   // the bytes of both CTAs
-                const uint32_t fb = fb0 + 8u * (uint32_t)s, sa = sb + (uint32_t)(s * S::kStageBytes), sbb = sa + kABytes;
-                const int32_t k0 = k * kBK;
-                if (a_mn) {
-                    tma_load_2d_pair(sa, ma, m0, k0, fb);
-                    tma_load_2d_pair(sa + kBoxBytes, ma, m0 + 64, k0, fb);
-                } else {
-                    tma_load_2d_pair(sa, ma, k0, m0, fb);
-                }
-                if (b_mn) {
-#pragma unroll
-                    for (int q = 0; q < BN / 128; ++q) tma_load_2d_pair(sbb + (uint32_t)(q * kBoxBytes), mb, n0 + 64 * q, k0, fb);
-                } else {
-                    tma_load_2d_pair(sbb, mb, k0, n0, fb);
-                }
+            const int32_t m0 = (int32_t)(it.m * (2 * kBM) + rank * kBM), n0 = (int32_t)(it.n * j.bn + rank * (j.bn / 2));
+            const uint32_t bytes = 2u * (uint32_t)(kABytes + j.bn / 2 * kBK * 2);   // of both CTAs
+            const bool a_mn = j.a_mn;
+            for (int k = it.from; k < it.to; ++k) {
+                if (!ready) ok = __all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort));
+                if (!ok) break;
+                const uint32_t fb = fb0 + 8u * (uint32_t)s, own = full(s), sa = sb + (uint32_t)(s * kStageBytes), sbb = sa + kABytes;
                 issued |= 1u << s;
                 last_ph = (last_ph & ~(1u << s)) | (ph << s);
                 if (++s == kStages) { s = 0; ph ^= 1u; }
+                const bool next = mbar_test(empty(s), ph ^ 1u);
+                const int32_t k0 = k * kBK;
+                if (elected) {
+                    if (leader) mbar_expect_tx(own, bytes);
+                    if (a_mn) {
+                        tma_load_2d_pair(sa, ma, m0, k0, fb);
+                        tma_load_2d_pair(sa + kBoxBytes, ma, m0 + 64, k0, fb);
+                    } else {
+                        tma_load_2d_pair(sa, ma, k0, m0, fb);
+                    }
+                    tma_load_2d_pair(sbb, mb, k0, n0, fb);
+                }
+                ready = __all_sync(kFull, next);
             }
         }
         // every stage issued has been read by the MMAs before the CTA may exit
         for (int i = 0; i < kStages; ++i)
             if (issued & (1u << i)) mbar_wait(empty(i), (last_ph >> i) & 1u, nullptr);
-    } else if (warp == 1 && lane == 0) {
+        __syncwarp();
+    } else if (warp == 1) {
         if (leader) {
             // ---- MMA issuer (even CTA) ----
             int s = 0, acc = 0;
             uint32_t ph = 0, aph = 0;
-            bool ok = true;
-            for (int64_t i = cid; ok && i < items; i += nclusters) {
-                const Job& j = w.job[item_at(i, w).job];
-                const uint32_t idesc = instr_desc<BN>(j);
-                const uint64_t adesc0 = smem_desc(sb, j.a_mn), bdesc0 = smem_desc(sb + kABytes, j.b_mn);
+            bool ok = true, ready = false;
+            const uint32_t elected = elect_one();
+            const uint64_t bdesc0 = smem_desc(sb + kABytes, false);
+            for (int64_t i = 0; ok && item_of(i, pair, w, it); ++i) {
+                if (it.from == it.to) continue;
+                const Job& j = w.job[it.job];
+                const uint32_t idesc = instr_desc(j);
+                const uint64_t adesc0 = smem_desc(sb, j.a_mn);
                 // 16 of the summed index: 32 bytes along a row, or 16 rows of 128 bytes
-                const uint64_t ka = j.a_mn ? (kMmaK * 128) >> 4 : (kMmaK * 2) >> 4, kb = j.b_mn ? (kMmaK * 128) >> 4 : (kMmaK * 2) >> 4;
-                const int steps = j.steps;
-                if (!mbar_wait_relaxed(acc_empty(acc), aph ^ 1u, abort)) break;   // see mbar_arrive_relaxed
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * BN);
-                for (int k = 0; k < steps; ++k) {
-                    if (!mbar_wait_fast(full(s), ph, abort)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint64_t so = (uint64_t)(s * (S::kStageBytes >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < kBK / kMmaK; ++kk)
-                        mma_bf16_pair(d, adesc0 + so + kk * ka, bdesc0 + so + kk * kb, idesc, (k | kk) != 0);
-                    mma_commit_pair(empty(s), 0x3);   // both CTAs' stage s is free once read
-                    if (++s == kStages) { s = 0; ph ^= 1u; }
-                }
+                const uint64_t ka = j.a_mn ? (kMmaK * 128) >> 4 : (kMmaK * 2) >> 4;
+                ok = __all_sync(kFull, mbar_wait_relaxed(acc_empty(acc), aph ^ 1u, abort));   // see mbar_arrive_relaxed
                 if (!ok) break;
-                mma_commit_pair(acc_full(acc), 0x3);
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * kBN), af = acc_full(acc);
+                for (int k = it.from; k < it.to; ++k) {
+                    if (!ready) ok = __all_sync(kFull, mbar_wait_fast(full(s), ph, abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t so = (uint64_t)(s * (kStageBytes >> 4)), ad = adesc0 + so, bd = bdesc0 + so;
+                    const uint32_t freed = empty(s);
+                    if (++s == kStages) { s = 0; ph ^= 1u; }
+                    const bool next = mbar_test(full(s), ph);
+                    if (elected) {
+#pragma unroll
+                        for (int kk = 0; kk < kBK / kMmaK; ++kk)
+                            mma_bf16_pair(d, ad + kk * ka, bd + (uint64_t)(kk * ((kMmaK * 2) >> 4)), idesc, k != it.from || kk != 0);
+                        mma_commit_pair(freed, 0x3);   // both CTAs' stage is free once read
+                        if (k + 1 == it.to) mma_commit_pair(af, 0x3);
+                    }
+                    ready = __all_sync(kFull, next);
+                }
                 acc ^= 1;
                 if (acc == 0) aph ^= 1u;
             }
-            mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
+            if (elected) mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
         }
-        mbar_wait(done, 0u, nullptr);
+        if (lane == 0) mbar_wait(done, 0u, nullptr);
+        __syncwarp();
     } else if (warp >= 4) {
-        // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31, columns BN / 2 ((w - 4) / 4) onwards ----
+        // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31, half (w - 4) / 4 of the columns ----
         const int q4 = warp & 3, half = (warp - 4) >> 2;
         int acc = 0;
         uint32_t aph = 0;
-        for (int64_t i = cid; i < items; i += nclusters) {
+        for (int64_t i = 0; item_of(i, pair, w, it); ++i) {
+            if (it.from == it.to) continue;
             if (!__all_sync(kFull, mbar_wait_fast(acc_full(acc), aph, abort))) break;
             tc_fence_after();
-            const Item it = item_at(i, w);
             const Job& j = w.job[it.job];
-            const int64_t row = it.m * (2 * kBM) + rank * kBM + 32 * q4 + lane, n0 = it.n * BN + half * (BN / 2);
-            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * BN + half * (BN / 2));
+            const int64_t row = it.m * (2 * kBM) + rank * kBM + 32 * q4 + lane, n0 = it.n * j.bn + half * (j.bn / 2);
+            const int64_t end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN + half * (j.bn / 2));
             if (j.mode == kStats)
-                stats_of_row<BN>(w, j, taddr, row, n0, 2 * it.n + half);
+                stats_of_row(w, j, taddr, row, n0, end, 2 * it.n + half);
             else if (j.mode == kDz)
-                dz_of_row<BN>(w, j, taddr, row, n0, wide);
+                dz_of_row(w, j, taddr, row, n0, end, wide);
+            else if (j.mode == kDw)
+                dw_of_row(j, taddr, row, n0, end, it.part, wide);
             else
-                sums_of_row<BN>(j, taddr, row, n0, wide);
+                dx_of_column(j, taddr, row, n0, end, it.part, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(map_to_rank(acc_empty(acc), 0));
@@ -399,15 +469,16 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     tc_fence_after();
     __syncwarp();
     if (warp == 2)
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kBN) : "memory");
 }
 
-// loss and lse from the tiles' maxima and sums: 32 rows per block, a warp for every eighth part
-__global__ void __launch_bounds__(256) lce_join_kernel(const float2* stats, int64_t ld, int64_t parts, const void* targets, int32_t wide,
-                                                       int64_t M, int64_t V, float* loss, float* lse) {
-    __shared__ float2 part[8][32];
+// loss and lse from the half tiles' maxima and sums: 32 rows per block, each warp every 32nd of them
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2* stats, int64_t ld, int64_t parts, const void* targets,
+                                                                   int32_t wide, int64_t M, int64_t V, float* loss, float* lse) {
+    __shared__ float2 part[kJoinWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t row0 = (int64_t)blockIdx.x * 32;
     wait_for_primary();
     float top = -INFINITY, sum = 0.0f;
     auto join = [&](float2 f) {
@@ -415,17 +486,71 @@ __global__ void __launch_bounds__(256) lce_join_kernel(const float2* stats, int6
         sum = sum * ex2_ftz((top - ref) * kLog2e) + f.y * ex2_ftz((f.x - ref) * kLog2e);
         top = mx;
     };
-    if (row < M)
-        for (int64_t p = warp; p < parts; p += 8) join(stats[p * ld + row]);
+    // stats_ld is a multiple of 32: the rows behind the last one are there, whatever they hold
+    const float2* p = stats + row0 + lane;
+#pragma unroll 4
+    for (int64_t i = warp; i < parts; i += kJoinWarps) join(p[i * ld]);
     part[warp][lane] = make_float2(top, sum);
     __syncthreads();
-    if (warp != 0 || row >= M) return;
-    for (int k = 1; k < 8; ++k) join(part[k][lane]);
+    // a warp for each row: its 32 lanes hold the warps' results
+    const int64_t row = row0 + warp;
+    if (row >= M) return;
+    float2 f = part[lane][warp];
+    for (int off = 16; off > 0; off >>= 1) {
+        top = f.x;
+        sum = f.y;
+        join(make_float2(__shfl_xor_sync(kFull, f.x, off), __shfl_xor_sync(kFull, f.y, off)));
+        f = make_float2(top, sum);
+    }
+    if (lane != 0) return;
     const float low = logf(sum);
     const int64_t t = index_at(targets, wide, row);
     lse[row] = top + low;
     // (top - z) + log(sum): nothing cancels where the target's logit is the largest
     loss[row] = t < 0 ? 0.0f : t >= V ? NAN : (top - loss[row]) + low;
+}
+
+// xt[c][m] = x[m][c]: tiles of 64 x 64 through shared memory.  (xt's rows are whole 16-byte units; what lies behind their M
+// elements is not read.)
+__global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, int64_t x_ld, int64_t M, int64_t C, uint16_t* xt, int64_t ld) {
+    __shared__ uint16_t tile[64][66];
+    const int64_t across = (M + 63) / 64, m0 = blockIdx.x % across * 64, c0 = blockIdx.x / across * 64;
+    wait_for_primary();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = threadIdx.x + 256 * h, r = i >> 3, c = (i & 7) * 8;
+        uint32_t w[4] = {};
+        if (m0 + r < M && c0 + c < C) load_words<4>(x + (m0 + r) * x_ld + c0 + c, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(&tile[r][c + 2 * k]) = w[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = threadIdx.x + 256 * h, c = i >> 3, r = (i & 7) * 8;
+        if (c0 + c >= C || m0 + r >= M) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = (uint32_t)tile[r + 2 * k][c] | (uint32_t)tile[r + 2 * k + 1][c] << 16;
+        *reinterpret_cast<uint4*>(xt + (c0 + c) * ld + m0 + r) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// out[i] = bf16(sum over parts of sums[part][i]): products summed in parts; eight elements per thread
+__global__ void __launch_bounds__(256) lce_parts_kernel(const float* sums, int parts, int64_t n, uint16_t* out) {
+    const int64_t at = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    wait_for_primary();
+    if (at >= n) return;
+    float x[8] = {};
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float4 f = *reinterpret_cast<const float4*>(sums + p * n + at), g = *reinterpret_cast<const float4*>(sums + p * n + at + 4);
+        x[0] += f.x; x[1] += f.y; x[2] += f.z; x[3] += f.w;
+        x[4] += g.x; x[5] += g.y; x[6] += g.z; x[7] += g.w;
+    }
+    uint32_t w[4];
+    pack(x, w);
+    *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // rows x cols bf16, row-major, ld elements apart; boxes of 64 columns x box_rows rows, zeros outside
@@ -441,7 +566,7 @@ bool encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A matrix as an operand: along its rows or across them.  The box of a K-major one is all of a CTA's rows.
+// A matrix as an operand: with the summed index along its rows, or (A alone) across them.
 struct Operand {
     const uint16_t* p;
     int64_t rows, cols, ld;
@@ -449,34 +574,59 @@ struct Operand {
 };
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-template <int BN>
+// Columns of a tile: of the multiples of 32 the one with which the pairs that have most tiles take least time for them, where
+// a tile counts as its columns and kTileCost for what does not grow with them (its rows, the steps' barriers).
+constexpr int kTileCost = 64;
+int tile_columns(int64_t rows, int64_t cols) {
+    int64_t best = 0;
+    int bn = kBN;
+    for (int n = kBN; n >= 32; n -= 32) {
+        const int64_t cost = up(up(rows, 2 * kBM) * up(cols, n), kPairs) * (n + kTileCost);
+        if (best == 0 || cost < best) {
+            best = cost;
+            bn = n;
+        }
+    }
+    return bn;
+}
+
 bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand& b, uint16_t* out, int64_t ld) {
     Job& j = w.job[w.jobs];
     const int64_t K = a.mn ? a.rows : a.cols;
     j.mode = mode;
     j.a_mn = a.mn;
-    j.b_mn = b.mn;
     j.rows = a.mn ? a.cols : a.rows;
-    j.cols = b.mn ? b.cols : b.rows;
+    j.cols = b.rows;
     j.steps = (int32_t)up(K, kBK);
+    j.bn = tile_columns(j.rows, j.cols);
+    j.parts = 1;
     j.tm = up(j.rows, 2 * kBM);
-    j.tn = up(j.cols, BN);
+    j.tn = up(j.cols, j.bn);
     j.out = out;
     j.ld = ld;
     j.sums = nullptr;
     j.first = j.last = 1;
     if (!encode(&maps.a[w.jobs], a.p, a.rows, a.cols, a.ld, a.mn ? kBK : kBM) ||
-        !encode(&maps.b[w.jobs], b.p, b.rows, b.cols, b.ld, b.mn ? kBK : BN / 2))
+        !encode(&maps.b[w.jobs], b.p, b.rows, b.cols, b.ld, j.bn / 2))
         return false;
     ++w.jobs;
     return true;
 }
 
-template <int BN>
-cudaError_t launch_work(const Work& w, const Maps& maps, bool wide, cudaStream_t s) {
+cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
     const int64_t pairs = device_sms() / 2;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    cudaError_t e = cudaFuncSetAttribute(lce_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<BN>::kSmemBytes);
+    for (int i = 0; i < 2; ++i) w.items[i] = i < w.jobs ? w.job[i].tm * w.job[i].tn * w.job[i].parts : 0;
+    const int64_t items = w.items[0] + w.items[1];
+    w.pairs = (int32_t)(items < pairs ? items : pairs);
+    w.ahead = (int32_t)(w.items[0] % w.pairs);
+    w.extra = 0;
+    if (w.ahead > 0 && w.jobs > 1) {
+        const int64_t long_steps = up(w.job[0].steps, w.job[0].parts), steps = up(w.job[1].steps, w.job[1].parts);
+        w.extra = (w.pairs - w.ahead) * ((long_steps + steps / 2) / steps);
+        if (w.extra > w.items[1]) w.extra = w.items[1];
+    }
+    cudaError_t e = cudaFuncSetAttribute(lce_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -487,21 +637,34 @@ cudaError_t launch_work(const Work& w, const Maps& maps, bool wide, cudaStream_t
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Shape<BN>::kSmemBytes;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    int64_t items = 0;
-    for (int i = 0; i < w.jobs; ++i) items += w.job[i].tm * w.job[i].tn;
-    cfg.gridDim = dim3(2u * (unsigned)(items < pairs ? items : pairs));
-    return cudaLaunchKernelEx(&cfg, lce_kernel<BN>, maps, w, wide);
+    cfg.gridDim = dim3(2u * (unsigned)w.pairs);
+    return cudaLaunchKernelEx(&cfg, lce_kernel, maps, (const Work&)w, wide);
 }
 
-template <int BN>
-cudaError_t forward(const LceFwdArgs& a, cudaStream_t s) {
+// Parts of the two products behind a piece of n columns: their items are at most half of a pair's share of all steps, and at
+// least kMinSteps long.
+struct Parts {
+    int dx, dw;
+};
+constexpr int64_t kMinSteps = 4;
+Parts parts_of(int64_t M, int64_t n, int64_t C) {
+    const int64_t dx = up(n, kBK), dw = up(M, kBK);   // steps
+    const int64_t dx_tiles = up(C, 2 * kBM) * up(M, tile_columns(C, M)), dw_tiles = up(n, 2 * kBM) * up(C, tile_columns(n, C));
+    int64_t most = (dx_tiles * dx + dw_tiles * dw) / (2 * kPairs);
+    if (most < kMinSteps) most = kMinSteps;
+    return Parts{(int)up(dx, most), (int)up(dw, most)};
+}
+
+}  // namespace
+
+cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s) {
     Work w = {};
     alignas(64) Maps maps;
-    if (!add_job<BN>(w, maps, kStats, Operand{a.x, a.M, a.C, a.x_ld, false}, Operand{a.weight, a.V, a.C, a.C, false}, nullptr, 0))
+    if (!add_job(w, maps, kStats, Operand{a.x, a.M, a.C, a.x_ld, false}, Operand{a.weight, a.V, a.C, a.C, false}, nullptr, 0))
         return cudaErrorInvalidValue;
     w.targets = a.targets;
     w.wide = a.wide;
@@ -509,22 +672,28 @@ cudaError_t forward(const LceFwdArgs& a, cudaStream_t s) {
     w.stats = reinterpret_cast<float2*>(a.stats);
     w.stats_ld = up(a.M, 32) * 32;
     w.target_logit = a.loss;
-    cudaError_t e = launch_work<BN>(w, maps, true, s);
+    cudaError_t e = launch_work(w, maps, true, s);
     if (e != cudaSuccess) return e;
-    return launch_next(lce_join_kernel, (unsigned)up(a.M, 32), 256, 0, s, (const float2*)w.stats, w.stats_ld, up(a.V, BN / 2),
-                       a.targets, a.wide, a.M, a.V, a.loss, a.lse);
+    // the halves of the last tile: the second one only where it has columns
+    return launch_next(lce_join_kernel, (unsigned)up(a.M, 32), 32 * kJoinWarps, 0, s, (const float2*)w.stats, w.stats_ld,
+                       up(a.V, w.job[0].bn / 2), a.targets, a.wide, a.M, a.V, a.loss, a.lse);
 }
 
-template <int BN>
-cudaError_t backward(const LceBwdArgs& a, cudaStream_t s) {
+cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
     const bool wide = aligned32(a.dx) && aligned32(a.dweight);
     const int64_t ld = lce_piece_ld(a.piece, a.V);
+    const Parts parts = parts_of(a.M, a.piece, a.C);
+    float* const dw_sums = a.sums + lce_dx_sums(a.M, a.V, a.C, a.piece);
+    const bool dx_sums = parts.dx > 1 || a.piece < a.V;
+    cudaError_t e = launch_next(lce_transpose_kernel, (unsigned)(up(a.M, 64) * up(a.C, 64)), 256, 0, s, a.x, a.x_ld, a.M, a.C,
+                                a.xt, lce_xt_ld(a.M));
+    if (e != cudaSuccess) return e;
     for (int64_t v0 = 0; v0 < a.V; v0 += a.piece) {
         const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
         const uint16_t* W = a.weight + v0 * a.C;
         Work w = {};
         alignas(64) Maps maps;
-        if (!add_job<BN>(w, maps, kDz, Operand{a.x, a.M, a.C, a.x_ld, false}, Operand{W, n, a.C, a.C, false}, a.dz, ld))
+        if (!add_job(w, maps, kDz, Operand{a.x, a.M, a.C, a.x_ld, false}, Operand{W, n, a.C, a.C, false}, a.dz, ld))
             return cudaErrorInvalidValue;
         w.targets = a.targets;
         w.wide = a.wide;
@@ -533,22 +702,38 @@ cudaError_t backward(const LceBwdArgs& a, cudaStream_t s) {
         w.lse = a.lse;
         w.dloss = a.dloss;
         w.dlse = a.dlse;
-        cudaError_t e = launch_work<BN>(w, maps, aligned32(a.dz), s);
+        e = launch_work(w, maps, aligned32(a.dz), s);
         if (e != cudaSuccess) return e;
         w.jobs = 0;
-        if (!add_job<BN>(w, maps, kDw, Operand{a.dz, a.M, n, ld, true}, Operand{a.x, a.M, a.C, a.x_ld, true}, a.dweight + v0 * a.C, a.C) ||
-            !add_job<BN>(w, maps, kDx, Operand{a.dz, a.M, n, ld, false}, Operand{W, n, a.C, a.C, true}, a.dx, a.C))
-            return cudaErrorInvalidValue;
-        w.job[1].sums = a.piece < a.V ? a.sums : nullptr;
-        w.job[1].first = v0 == 0;
-        w.job[1].last = v0 + n == a.V;
-        e = launch_work<BN>(w, maps, wide, s);
+        // the product with the longer items first
+        const bool dx_first = up(up(n, kBK), parts.dx) >= up(up(a.M, kBK), parts.dw);
+        for (int i = 0; i < 2; ++i) {
+            Job& j = w.job[i];
+            if (dx_first == (i == 0)) {
+                if (!add_job(w, maps, kDx, Operand{W, n, a.C, a.C, true}, Operand{a.dz, a.M, n, ld, false}, a.dx, a.C))
+                    return cudaErrorInvalidValue;
+                j.parts = parts.dx;
+                j.sums = dx_sums ? a.sums : nullptr;
+                j.first = v0 == 0;
+                j.last = parts.dx == 1 && v0 + n == a.V;
+            } else {
+                if (!add_job(w, maps, kDw, Operand{a.dz, a.M, n, ld, true}, Operand{a.xt, a.C, a.M, lce_xt_ld(a.M), false},
+                             a.dweight + v0 * a.C, a.C))
+                    return cudaErrorInvalidValue;
+                j.parts = parts.dw;
+                j.sums = parts.dw > 1 ? dw_sums : nullptr;
+                j.last = parts.dw == 1;
+            }
+        }
+        e = launch_work(w, maps, wide, s);
+        if (e == cudaSuccess && parts.dw > 1)
+            e = launch_next(lce_parts_kernel, (unsigned)up(n * a.C, 8 * 256), 256, 0, s, (const float*)dw_sums, parts.dw, n * a.C,
+                            a.dweight + v0 * a.C);
         if (e != cudaSuccess) return e;
     }
-    return cudaSuccess;
+    if (parts.dx == 1) return cudaSuccess;
+    return launch_next(lce_parts_kernel, (unsigned)up(a.M * a.C, 8 * 256), 256, 0, s, (const float*)a.sums, parts.dx, a.M * a.C, a.dx);
 }
-
-}  // namespace
 
 int64_t lce_piece(int64_t M, int64_t V, int64_t piece) {
     if (piece < 1) {   // as few pieces, of about the same width, as leave dz within kLceDzBytes
@@ -559,10 +744,16 @@ int64_t lce_piece(int64_t M, int64_t V, int64_t piece) {
     return piece < V ? up(piece, 256) * 256 < V ? up(piece, 256) * 256 : V : V;
 }
 int64_t lce_piece_ld(int64_t piece, int64_t V) { return up(piece < V ? piece : V, 256) * 256; }
-size_t lce_stats_bytes(int64_t M, int64_t V) { return 8 * (size_t)(up(M, 32) * 32) * (size_t)up(V, 64); }
-
-cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s) { return forward<256>(a, s); }
-cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) { return backward<256>(a, s); }
+int64_t lce_xt_ld(int64_t M) { return up(M, 8) * 8; }
+int64_t lce_dx_sums(int64_t M, int64_t V, int64_t C, int64_t piece) {
+    const Parts p = parts_of(M, piece, C);
+    return p.dx > 1 || piece < V ? p.dx * M * C : 0;
+}
+int64_t lce_sums(int64_t M, int64_t V, int64_t C, int64_t piece) {
+    const Parts p = parts_of(M, piece, C);
+    return lce_dx_sums(M, V, C, piece) + (p.dw > 1 ? p.dw * piece * C : 0);
+}
+size_t lce_stats_bytes(int64_t M, int64_t V) { return 8 * (size_t)(up(M, 32) * 32) * (size_t)up(V, tile_columns(M, V) / 2); }
 
 cudaError_t read_lce_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }
 

@@ -1,4 +1,5 @@
-// tc_pipeline.cuh -- what the tensor-core kernels (linear_fp8.cu, ckpt_wgrad.cu)
+// tc_pipeline.cuh -- what the tensor-core kernels (linear_fp8.cu, ckpt_wgrad.cu,
+// lm_lce.cu)
 // share: bounded waits on mbarriers, clusters of two CTAs, TMA loads, tensor
 // memory, and the tensor-map encoder.
 //
@@ -69,6 +70,39 @@ __device__ __forceinline__ bool mbar_wait_relaxed(uint32_t bar, uint32_t parity,
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p;
+}
+
+// whether the phase is over, without a wait (a try may hold the warp until its phase ends)
+template <bool kRelaxed = false>
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    if constexpr (kRelaxed)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    return ok != 0u;
 }
 
 // arrive on an mbarrier of either CTA of the cluster (a shared::cluster address)
