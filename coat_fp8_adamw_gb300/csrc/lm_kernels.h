@@ -74,7 +74,7 @@ struct LceBwdArgs {
     uint16_t* xt;              // C x lce_xt_ld(M) bf16: x transposed
     float* sums;               // lce_sums(...): of products in several parts or pieces
 };
-constexpr int64_t kLceDzBytes = 256 << 20;   // of a piece's gradient of the logits, unless the caller says how wide a piece is
+constexpr int64_t kLceDzBytes = 512 << 20;   // of a piece's gradient of the logits, unless the caller says how wide a piece is
 int64_t lce_piece(int64_t M, int64_t V, int64_t piece);
 int64_t lce_piece_ld(int64_t piece, int64_t V);
 int64_t lce_xt_ld(int64_t M);

@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
     };
     // stats_ld is a multiple of 32: the rows behind the last one are there, whatever they hold
     const float2* p = stats + row0 + lane;
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t i = warp; i < parts; i += kJoinWarps) join(p[i * ld]);
     part[warp][lane] = make_float2(top, sum);
     __syncthreads();
@@ -574,14 +574,20 @@ struct Operand {
 };
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
-// Columns of a tile: of the multiples of 32 the one with which the pairs that have most tiles take least time for them, where
-// a tile counts as its columns and kTileCost for what does not grow with them (its rows, the steps' barriers).
-constexpr int kTileCost = 64;
-int tile_columns(int64_t rows, int64_t cols) {
+// What a step of a tile of n columns takes, as the columns that its MMAs alone would take: they and the rows of A are loaded
+// in 64 columns' time more, and the steps' barriers take as long as 208 (8192 rows, 64 x 64 of the summed index: 309 ns a
+// step with 256 columns, 276 with 224, 245 with 192, 220 with 160, 207 with 128, 198 with 64).
+int64_t step_cost(int64_t n) { return n + 64 > 208 ? n + 64 : 208; }
+constexpr int64_t kWholeStep = kBN + 64;
+
+// Columns of a tile, of the multiples of 32.  Of a product alone: those with which the pairs that have most tiles take least
+// time (33 x 50304 x 2048 forward: 225 tiles of 224 for 76 pairs, instead of 197 of 256).  Of one of two products, which make up
+// for each other's last tiles: those that cover it in the least time.
+int tile_columns(int64_t rows, int64_t cols, bool alone) {
     int64_t best = 0;
     int bn = kBN;
     for (int n = kBN; n >= 32; n -= 32) {
-        const int64_t cost = up(up(rows, 2 * kBM) * up(cols, n), kPairs) * (n + kTileCost);
+        const int64_t tiles = up(rows, 2 * kBM) * up(cols, n), cost = (alone ? up(tiles, kPairs) : tiles) * step_cost(n);
         if (best == 0 || cost < best) {
             best = cost;
             bn = n;
@@ -598,7 +604,7 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     j.rows = a.mn ? a.cols : a.rows;
     j.cols = b.rows;
     j.steps = (int32_t)up(K, kBK);
-    j.bn = tile_columns(j.rows, j.cols);
+    j.bn = tile_columns(j.rows, j.cols, mode == kStats || mode == kDz);
     j.parts = 1;
     j.tm = up(j.rows, 2 * kBM);
     j.tn = up(j.cols, j.bn);
@@ -613,19 +619,35 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     return true;
 }
 
+// How the items of a launch go to the pairs: see Work.
+struct Split {
+    int64_t pairs, ahead, extra;
+};
+Split split_of(int64_t first, int64_t first_steps, int64_t second, int64_t second_steps, int64_t pairs) {
+    Split s;
+    s.pairs = first + second < pairs ? first + second : pairs;
+    s.ahead = first % s.pairs;
+    s.extra = 0;
+    if (s.ahead > 0 && second > 0) {
+        s.extra = (s.pairs - s.ahead) * ((first_steps + second_steps / 2) / second_steps);
+        if (s.extra > second) s.extra = second;
+    }
+    return s;
+}
+
 cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
     const int64_t pairs = device_sms() / 2;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    for (int i = 0; i < 2; ++i) w.items[i] = i < w.jobs ? w.job[i].tm * w.job[i].tn * w.job[i].parts : 0;
-    const int64_t items = w.items[0] + w.items[1];
-    w.pairs = (int32_t)(items < pairs ? items : pairs);
-    w.ahead = (int32_t)(w.items[0] % w.pairs);
-    w.extra = 0;
-    if (w.ahead > 0 && w.jobs > 1) {
-        const int64_t long_steps = up(w.job[0].steps, w.job[0].parts), steps = up(w.job[1].steps, w.job[1].parts);
-        w.extra = (w.pairs - w.ahead) * ((long_steps + steps / 2) / steps);
-        if (w.extra > w.items[1]) w.extra = w.items[1];
+    int64_t steps[2] = {0, 0};
+    for (int i = 0; i < w.jobs; ++i) {
+        w.items[i] = w.job[i].tm * w.job[i].tn * w.job[i].parts;
+        steps[i] = up(w.job[i].steps, w.job[i].parts);
     }
+    if (w.jobs < 2) w.items[1] = 0;
+    const Split sp = split_of(w.items[0], steps[0], w.items[1], steps[1], pairs);
+    w.pairs = (int32_t)sp.pairs;
+    w.ahead = (int32_t)sp.ahead;
+    w.extra = sp.extra;
     cudaError_t e = cudaFuncSetAttribute(lce_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
@@ -645,18 +667,38 @@ cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, lce_kernel, maps, (const Work&)w, wide);
 }
 
-// Parts of the two products behind a piece of n columns: their items are at most half of a pair's share of all steps, and at
-// least kMinSteps long.
+// Parts of the two products behind a piece of n columns.  Few tiles with many steps leave pairs idle; parts of them cost
+// float32 sums that are written, read and added by a kernel of their own.  The parts with which the busiest pair and that
+// together take least, in steps of whole tiles (0.31 us; 2 MB of memory traffic; 8 for the kernel, 2 for an item's ends).
 struct Parts {
     int dx, dw;
 };
-constexpr int64_t kMinSteps = 4;
+int64_t busiest(int64_t first, int64_t first_steps, int64_t second, int64_t second_steps) {
+    const Split s = split_of(first, first_steps, second, second_steps, kPairs);
+    const int64_t whole = first / s.pairs * first_steps, with = s.ahead > 0 ? first_steps : 0;
+    const int64_t lot = s.pairs - s.ahead, without = s.extra > 0 ? up(s.extra, lot) * second_steps : 0;
+    return whole + (with > without ? with : without) + up(second - s.extra, s.pairs) * second_steps;
+}
 Parts parts_of(int64_t M, int64_t n, int64_t C) {
     const int64_t dx = up(n, kBK), dw = up(M, kBK);   // steps
-    const int64_t dx_tiles = up(C, 2 * kBM) * up(M, tile_columns(C, M)), dw_tiles = up(n, 2 * kBM) * up(C, tile_columns(n, C));
-    int64_t most = (dx_tiles * dx + dw_tiles * dw) / (2 * kPairs);
-    if (most < kMinSteps) most = kMinSteps;
-    return Parts{(int)up(dx, most), (int)up(dw, most)};
+    const int dx_bn = tile_columns(C, M, false), dw_bn = tile_columns(n, C, false);
+    const int64_t dx_tiles = up(C, 2 * kBM) * up(M, dx_bn), dw_tiles = up(n, 2 * kBM) * up(C, dw_bn);
+    constexpr int kTry[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    Parts best{1, 1};
+    int64_t least = -1;
+    for (const int px : kTry)
+        for (const int pw : kTry) {
+            if (px > dx || pw > dw) continue;
+            const int64_t lx = (up(dx, px) + 2) * step_cost(dx_bn), lw = (up(dw, pw) + 2) * step_cost(dw_bn);
+            int64_t cost = lx >= lw ? busiest(dx_tiles * px, lx, dw_tiles * pw, lw) : busiest(dw_tiles * pw, lw, dx_tiles * px, lx);
+            if (px > 1) cost += (8 + (px * M * C * 8 >> 21)) * kWholeStep;
+            if (pw > 1) cost += (8 + (pw * n * C * 8 >> 21)) * kWholeStep;
+            if (least < 0 || cost < least) {
+                least = cost;
+                best = Parts{px, pw};
+            }
+        }
+    return best;
 }
 
 }  // namespace
@@ -753,7 +795,7 @@ int64_t lce_sums(int64_t M, int64_t V, int64_t C, int64_t piece) {
     const Parts p = parts_of(M, piece, C);
     return lce_dx_sums(M, V, C, piece) + (p.dw > 1 ? p.dw * piece * C : 0);
 }
-size_t lce_stats_bytes(int64_t M, int64_t V) { return 8 * (size_t)(up(M, 32) * 32) * (size_t)up(V, tile_columns(M, V) / 2); }
+size_t lce_stats_bytes(int64_t M, int64_t V) { return 8 * (size_t)(up(M, 32) * 32) * (size_t)up(V, tile_columns(M, V, true) / 2); }
 
 cudaError_t read_lce_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }
 

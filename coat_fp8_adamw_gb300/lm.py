@@ -76,7 +76,7 @@ def coat_linear_cross_entropy(x, weight, targets, loss, lse, workspace, stream=N
 
 def coat_linear_cross_entropy_backward_workspace_bytes(M: int, V: int, C: int, piece: int = 0, device=None) -> int:
     """Bytes of workspace that coat_linear_cross_entropy_backward needs with pieces of
-    ``piece`` rows of the weight (0: as few as leave 256 MiB for a piece)."""
+    ``piece`` rows of the weight (0: as few as leave 512 MiB for a piece)."""
     return _size("coat_linear_cross_entropy_backward_workspace_bytes", device, M, V, C, piece)
 
 
@@ -87,7 +87,7 @@ def coat_linear_cross_entropy_backward(x, weight, targets, lse, dloss, dx, dweig
     dx bf16 [M, C] = dz weight and dweight bf16 [V, C] = dz^T x.  lse as the forward
     pass left it; dloss and dlse float32 [M], dlse 0 when not given; dloss of a
     token without a target does not count.  The logits are formed again, ``piece`` rows of the weight at a
-    time (0: as few pieces as leave 256 MiB for one; rounded up to a multiple of
+    time (0: as few pieces as leave 512 MiB for one; rounded up to a multiple of
     256)."""
     (M, C), (V, _), dev = _matrix(x, "x"), _matrix(weight, "weight"), x.device
     px, ld = _rows(x, M, C, "x", dev)

@@ -507,7 +507,7 @@ size_t coat_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V);
  *   float32 in (of a token without a target it does not count);  dlse [M] float32
  *   in, or NULL: zeros;  dx [M x C], dweight [V x C] bf16 out.
  * The logits are formed again, `piece` rows of the weight at a time (rounded up to
- * a multiple of 256; 0: as few pieces as leave 256 MiB for one's dz).  dz is an
+ * a multiple of 256; 0: as few pieces as leave 512 MiB for one's dz).  dz is an
  * operand of the tensor cores, so it is bf16, the type of a layer's gradient; sums
  * are float32, dx's over the pieces too, so that dx may differ in its last bits
  * with another `piece`.  Of sums of exact terms, dx and dweight are within

@@ -144,7 +144,8 @@ def test_linear_cross_entropy_workspaces(L):
     assert b(10, 100, 24, 0) == 0 and b(10, 100, 64, -1) == 0
     xt = 2 * 64 * 16                                                     # x transposed, its rows in multiples of eight
     assert b(10, 100, 64, 0) == b(10, 100, 64, 1) == b(10, 100, 64, (1 << 63) - 1) == 2 * 10 * 256 + xt    # one piece
-    assert b(10, 1000, 64, 300) == 2 * 10 * 512 + xt + 4 * 2 * 10 * 64   # two: and dx's sums between them, in two parts
+    assert b(10, 1000, 64, 300) == 2 * 10 * 512 + xt + 4 * 10 * 64       # two: and dx's sums between them
     M, V, C = 8192, 32000, 4096
-    assert b(M, V, C, 0) == 2 * M * 16128 + 2 * M * C + 4 * M * C         # two pieces of about the same width
-    assert 2 * M * 16128 <= 256 << 20
+    assert b(M, V, C, 0) == 2 * M * V + 2 * M * C                         # one piece: its dz is within 512 MiB
+    M = 16384                                                             # two of about the same width
+    assert b(M, V, C, 0) == 2 * M * 16128 + 2 * M * C + 4 * M * C and 2 * M * 16128 <= 512 << 20
