@@ -154,9 +154,36 @@ __device__ __forceinline__ bool item_of(int64_t k, int64_t pair, const Work& w, 
 
 // ---- epilogues: one row of the tile, columns n0 .. end - 1 (at most 128, a multiple of 16 but for the matrix's end), per
 // thread; where a chunk of 32 goes past them, it reads columns of the other half, which do not count ----
-__device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int64_t part) {
-    float top = -INFINITY, sum = 0.0f;
-    const int64_t target = row < j.rows ? index_at(w.targets, w.wide, row) : -1;
+// What a row of the logits needs of its token, loaded while the tile's MMAs still run.
+struct RowValues {
+    int64_t target;
+    float lse, g, p;         // dz = p e^(z - lse) - [v = target] g
+};
+__device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int64_t row) {
+    RowValues r{-1, 0.0f, 0.0f, 0.0f};
+    if (j.mode > kDz || row >= j.rows) return r;
+    r.target = index_at(w.targets, w.wide, row);
+    if (j.mode == kStats) return r;
+    const float g = static_cast<const volatile float*>(w.dloss)[row], h = w.dlse ? static_cast<const volatile float*>(w.dlse)[row] : 0.0f;
+    r.lse = static_cast<const volatile float*>(w.lse)[row];
+    r.g = r.target < 0 ? 0.0f : r.target < w.V ? g : NAN;
+    r.p = r.g + h;
+    return r;
+}
+
+// e^(z - ref) of two logits (the difference first: with one fused multiply-add of z log2(e) and ref's, the largest logit's
+// share would be 1 to float32's last bits only, and so would the loss of a certain token)
+__device__ __forceinline__ void exp2_of(uint32_t z0, uint32_t z1, uint64_t minus_ref, float& a, float& b) {
+    upk(mul2(add2(pk(__uint_as_float(z0), __uint_as_float(z1)), minus_ref), pk(kLog2e, kLog2e)), a, b);
+    a = ex2_ftz(a);
+    b = ex2_ftz(b);
+}
+
+__device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, int64_t row, int64_t n0,
+                                             int64_t end, int64_t part) {
+    float top = -INFINITY;
+    uint64_t sums = pk(0.0f, 0.0f);
+    const int64_t target = r.target;
 #pragma unroll 1
     for (int64_t col = n0; col < end; col += kChunk) {   // the same for the whole warp
         uint32_t v[kChunk];
@@ -177,16 +204,19 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, uint32
         }
         float mx = top;
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
+        for (int e = 0; e < kChunk; e += 2) mx = max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
         const float ref = mx == -INFINITY ? 0.0f : mx;   // a row of -inf so far
-        sum *= ex2_ftz((top - ref) * kLog2e);
+        const float f = ex2_ftz((top - ref) * kLog2e);
         top = mx;
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        sums = mul2(sums, pk(f, f));
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) s[e & 3] += ex2_ftz((__uint_as_float(v[e]) - ref) * kLog2e);
-        sum += (s[0] + s[1]) + (s[2] + s[3]);
+        for (int e = 0; e < kChunk; e += 2) {
+            float a, b;
+            exp2_of(v[e], v[e + 1], pk(-ref, -ref), a, b);
+            sums = add2(sums, pk(a, b));
+        }
     }
-    if (row < j.rows && n0 < end) w.stats[part * w.stats_ld + row] = make_float2(top, sum);
+    if (row < j.rows && n0 < end) w.stats[part * w.stats_ld + row] = make_float2(top, sum2(sums));
 }
 
 // 32 bf16 columns of a row; n of them (a multiple of 16) are there
@@ -199,28 +229,28 @@ __device__ __forceinline__ void store_row(uint16_t* p, int64_t n, bool wide, con
     }
 }
 
-__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, bool wide) {
+__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, int64_t row, int64_t n0,
+                                          int64_t end, bool wide) {
     const bool ok = row < j.rows;
-    float lse = 0.0f, g = 0.0f, p = 0.0f;   // dz = p e^(z - lse) - [v = t] g
-    int64_t target = -1;
-    if (ok) {
-        target = index_at(w.targets, w.wide, row);
-        lse = static_cast<const volatile float*>(w.lse)[row];
-        if (target >= 0) g = target < w.V ? static_cast<const volatile float*>(w.dloss)[row] : NAN;
-        p = w.dlse ? g + static_cast<const volatile float*>(w.dlse)[row] : g;
-    }
-    target -= w.v0;
+    const float lse = r.lse, p = r.p;
+    const int64_t target = r.target - w.v0;
 #pragma unroll 1
     for (int64_t col = n0; col < end; col += kChunk) {
         uint32_t v[kChunk], o[kChunk / 2];
         __syncwarp();
         tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
 #pragma unroll
-        for (int e = 0; e < kChunk; ++e) v[e] = __float_as_uint(p * ex2_ftz((__uint_as_float(v[e]) - lse) * kLog2e));
+        for (int e = 0; e < kChunk; e += 2) {
+            float a, b;
+            exp2_of(v[e], v[e + 1], pk(-lse, -lse), a, b);
+            upk(mul2(pk(a, b), pk(p, p)), a, b);
+            v[e] = __float_as_uint(a);
+            v[e + 1] = __float_as_uint(b);
+        }
         if (__any_sync(kFull, target >= col && target < col + kChunk)) {
 #pragma unroll
             for (int e = 0; e < kChunk; ++e)
-                if (col + e == target) v[e] = __float_as_uint(__uint_as_float(v[e]) - g);
+                if (col + e == target) v[e] = __float_as_uint(__uint_as_float(v[e]) - r.g);
         }
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
@@ -442,16 +472,18 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         uint32_t aph = 0;
         for (int64_t i = 0; item_of(i, pair, w, it); ++i) {
             if (it.from == it.to) continue;
+            const Job& j = w.job[it.job];
+            const int64_t row = it.m * (2 * kBM) + rank * kBM + 32 * q4 + lane;
+            const RowValues r = row_values(w, j, row);
             if (!__all_sync(kFull, mbar_wait_fast(acc_full(acc), aph, abort))) break;
             tc_fence_after();
-            const Job& j = w.job[it.job];
-            const int64_t row = it.m * (2 * kBM) + rank * kBM + 32 * q4 + lane, n0 = it.n * j.bn + half * (j.bn / 2);
+            const int64_t n0 = it.n * j.bn + half * (j.bn / 2);
             const int64_t end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
             const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN + half * (j.bn / 2));
             if (j.mode == kStats)
-                stats_of_row(w, j, taddr, row, n0, end, 2 * it.n + half);
+                stats_of_row(w, j, r, taddr, row, n0, end, 2 * it.n + half);
             else if (j.mode == kDz)
-                dz_of_row(w, j, taddr, row, n0, end, wide);
+                dz_of_row(w, j, r, taddr, row, n0, end, wide);
             else if (j.mode == kDw)
                 dw_of_row(j, taddr, row, n0, end, it.part, wide);
             else
@@ -619,17 +651,24 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     return true;
 }
 
+// What an item takes, in the unit of step_cost: its steps, or its epilogue where that is longer (a tile's 128 KB of bf16 at a
+// pair's share of the memory take as long as five steps), and one for its ends.
+int64_t item_cost(int64_t steps, int64_t parts, int bn) {
+    const int64_t n = up(steps, parts);
+    return (n > 5 ? n : 5) * step_cost(bn) + step_cost(bn);
+}
+
 // How the items of a launch go to the pairs: see Work.
 struct Split {
     int64_t pairs, ahead, extra;
 };
-Split split_of(int64_t first, int64_t first_steps, int64_t second, int64_t second_steps, int64_t pairs) {
+Split split_of(int64_t first, int64_t first_cost, int64_t second, int64_t second_cost, int64_t pairs) {
     Split s;
     s.pairs = first + second < pairs ? first + second : pairs;
     s.ahead = first % s.pairs;
     s.extra = 0;
     if (s.ahead > 0 && second > 0) {
-        s.extra = (s.pairs - s.ahead) * ((first_steps + second_steps / 2) / second_steps);
+        s.extra = (s.pairs - s.ahead) * ((first_cost + second_cost / 2) / second_cost);
         if (s.extra > second) s.extra = second;
     }
     return s;
@@ -638,13 +677,13 @@ Split split_of(int64_t first, int64_t first_steps, int64_t second, int64_t secon
 cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
     const int64_t pairs = device_sms() / 2;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    int64_t steps[2] = {0, 0};
+    int64_t cost[2] = {0, 0};
     for (int i = 0; i < w.jobs; ++i) {
         w.items[i] = w.job[i].tm * w.job[i].tn * w.job[i].parts;
-        steps[i] = up(w.job[i].steps, w.job[i].parts);
+        cost[i] = item_cost(w.job[i].steps, w.job[i].parts, w.job[i].bn);
     }
     if (w.jobs < 2) w.items[1] = 0;
-    const Split sp = split_of(w.items[0], steps[0], w.items[1], steps[1], pairs);
+    const Split sp = split_of(w.items[0], cost[0], w.items[1], cost[1], pairs);
     w.pairs = (int32_t)sp.pairs;
     w.ahead = (int32_t)sp.ahead;
     w.extra = sp.extra;
@@ -667,35 +706,37 @@ cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, lce_kernel, maps, (const Work&)w, wide);
 }
 
-// Parts of the two products behind a piece of n columns.  Few tiles with many steps leave pairs idle; parts of them cost
-// float32 sums that are written, read and added by a kernel of their own.  The parts with which the busiest pair and that
-// together take least, in steps of whole tiles (0.31 us; 2 MB of memory traffic; 8 for the kernel, 2 for an item's ends).
+// The two products behind a piece of n columns: their parts, and which has the longer items.  Few tiles with many steps leave
+// pairs idle; parts of them cost float32 sums that are written, read and added by a kernel of their own.  The parts with which
+// the busiest pair and that together take least (a whole tile's step is 0.31 us or 2 MB of memory traffic; the kernel 8).
 struct Parts {
     int dx, dw;
+    bool dx_first;
 };
-int64_t busiest(int64_t first, int64_t first_steps, int64_t second, int64_t second_steps) {
-    const Split s = split_of(first, first_steps, second, second_steps, kPairs);
-    const int64_t whole = first / s.pairs * first_steps, with = s.ahead > 0 ? first_steps : 0;
-    const int64_t lot = s.pairs - s.ahead, without = s.extra > 0 ? up(s.extra, lot) * second_steps : 0;
-    return whole + (with > without ? with : without) + up(second - s.extra, s.pairs) * second_steps;
+int64_t busiest(int64_t first, int64_t first_cost, int64_t second, int64_t second_cost) {
+    const Split s = split_of(first, first_cost, second, second_cost, kPairs);
+    const int64_t whole = first / s.pairs * first_cost, with = s.ahead > 0 ? first_cost : 0;
+    const int64_t lot = s.pairs - s.ahead, without = s.extra > 0 ? up(s.extra, lot) * second_cost : 0;
+    return whole + (with > without ? with : without) + up(second - s.extra, s.pairs) * second_cost;
 }
 Parts parts_of(int64_t M, int64_t n, int64_t C) {
     const int64_t dx = up(n, kBK), dw = up(M, kBK);   // steps
     const int dx_bn = tile_columns(C, M, false), dw_bn = tile_columns(n, C, false);
     const int64_t dx_tiles = up(C, 2 * kBM) * up(M, dx_bn), dw_tiles = up(n, 2 * kBM) * up(C, dw_bn);
     constexpr int kTry[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-    Parts best{1, 1};
+    Parts best{1, 1, true};
     int64_t least = -1;
     for (const int px : kTry)
         for (const int pw : kTry) {
             if (px > dx || pw > dw) continue;
-            const int64_t lx = (up(dx, px) + 2) * step_cost(dx_bn), lw = (up(dw, pw) + 2) * step_cost(dw_bn);
-            int64_t cost = lx >= lw ? busiest(dx_tiles * px, lx, dw_tiles * pw, lw) : busiest(dw_tiles * pw, lw, dx_tiles * px, lx);
+            const int64_t lx = item_cost(dx, px, dx_bn), lw = item_cost(dw, pw, dw_bn);
+            const bool dx_first = lx >= lw;
+            int64_t cost = dx_first ? busiest(dx_tiles * px, lx, dw_tiles * pw, lw) : busiest(dw_tiles * pw, lw, dx_tiles * px, lx);
             if (px > 1) cost += (8 + (px * M * C * 8 >> 21)) * kWholeStep;
             if (pw > 1) cost += (8 + (pw * n * C * 8 >> 21)) * kWholeStep;
             if (least < 0 || cost < least) {
                 least = cost;
-                best = Parts{px, pw};
+                best = Parts{px, pw, dx_first};
             }
         }
     return best;
@@ -747,11 +788,9 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
         e = launch_work(w, maps, aligned32(a.dz), s);
         if (e != cudaSuccess) return e;
         w.jobs = 0;
-        // the product with the longer items first
-        const bool dx_first = up(up(n, kBK), parts.dx) >= up(up(a.M, kBK), parts.dw);
         for (int i = 0; i < 2; ++i) {
             Job& j = w.job[i];
-            if (dx_first == (i == 0)) {
+            if (parts.dx_first == (i == 0)) {   // the product with the longer items first
                 if (!add_job(w, maps, kDx, Operand{W, n, a.C, a.C, true}, Operand{a.dz, a.M, n, ld, false}, a.dx, a.C))
                     return cudaErrorInvalidValue;
                 j.parts = parts.dx;
