@@ -45,16 +45,22 @@ constexpr int64_t kPairs = 76;                  // that the division of the work
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int kBN = 256;                       // most columns of a tile
-constexpr int kBBytes = (kBN / 2) * kBK * 2;   // 16 KB
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 7;
-constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kNumBars = 2 * kStages + 5;      // full, empty, acc full x2, acc empty x2, done
+// Shared memory: the ring of stages (A's 16 KB and B's columns each, as many as fit), then 4 KB for every epilogue warp
+// (which kFewStats uses as 32 rows of 33 floats), then the barriers.
+constexpr int kStageArea = 6 * 32768;
+constexpr int kMaxStages = 10;
+constexpr int kStagingBytes = 32 * 33 * 4;
+constexpr int kBarOff = kStageArea + 8 * kStagingBytes;
+constexpr int kNumBars = 2 * kMaxStages + 5;   // full, empty, acc full x2, acc empty x2, done
 constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 1024-B alignment
-static_assert(kSmemBytes <= 232448, "shared memory of an SM");
+constexpr int slot_bytes(int bn) { return kABytes + bn / 2 * kBK * 2; }
+constexpr int stages_of(int bn) { return kStageArea / slot_bytes(bn) < kMaxStages ? kStageArea / slot_bytes(bn) : kMaxStages; }
+static_assert(kSmemBytes <= 232448 && stages_of(256) == 6 && stages_of(32) == 10, "shared memory of an SM");
+constexpr int64_t kFewTokens = 64;             // up to so many, the logits are formed with the tokens as columns
 
 // What a launch does with a tile's sums.
-enum Mode : int32_t { kStats, kDz, kDx, kDw };
+// Of few tokens, the logits' rows are those of the weight and their columns the tokens (kFewStats, kFewDz).
+enum Mode : int32_t { kStats, kDz, kFewStats, kFewDz, kDx, kDw };
 
 // A product: its tiles, each summed in `parts` parts of the summed index.
 struct Job {
@@ -65,7 +71,7 @@ struct Job {
     int32_t parts;
     int64_t tm, tn;          // tiles
     int64_t rows, cols;      // of the product
-    uint16_t* out;           // kDz, kDx (last piece), kDw: bf16, ld apart
+    uint16_t* out;           // kFewDz, kDx (last piece): bf16, rows ld apart (kDz and kDw store by their tensor map)
     int64_t ld;
     float* sums;             // [parts][out's shape] float32: of parts, or of the pieces so far
     int32_t first, last;     // sums: the first piece, which writes them; the last one of a product in one part, which ends in out
@@ -75,6 +81,7 @@ struct Job {
 struct Work {
     Job job[2];
     int32_t jobs;
+    int32_t slot, stages;    // bytes of a stage, and their number
     int32_t pairs, ahead;
     int64_t items[2], extra;
     // rows of the logits
@@ -84,7 +91,7 @@ struct Work {
     const float* lse;
     const float* dloss;
     const float* dlse;
-    float2* stats;           // kStats: [half tile's columns][row], rows padded
+    float2* stats;           // [half tile's columns, or, of few tokens, epilogue warp][token], tokens padded
     int64_t stats_ld;
     float* target_logit;
 };
@@ -154,18 +161,18 @@ __device__ __forceinline__ bool item_of(int64_t k, int64_t pair, const Work& w, 
 
 // ---- epilogues: one row of the tile, columns n0 .. end - 1 (at most 128, a multiple of 16 but for the matrix's end), per
 // thread; where a chunk of 32 goes past them, it reads columns of the other half, which do not count ----
-// What a row of the logits needs of its token, loaded while the tile's MMAs still run.
+// What is needed of a token (a lane's row of the logits, or its column of 32), loaded while the tile's MMAs still run.
 struct RowValues {
     int64_t target;
     float lse, g, p;         // dz = p e^(z - lse) - [v = target] g
 };
-__device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int64_t row) {
+__device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int64_t token, int64_t tokens) {
     RowValues r{-1, 0.0f, 0.0f, 0.0f};
-    if (j.mode > kDz || row >= j.rows) return r;
-    r.target = index_at(w.targets, w.wide, row);
-    if (j.mode == kStats) return r;
-    const float g = static_cast<const volatile float*>(w.dloss)[row], h = w.dlse ? static_cast<const volatile float*>(w.dlse)[row] : 0.0f;
-    r.lse = static_cast<const volatile float*>(w.lse)[row];
+    if (j.mode > kFewDz || token >= tokens) return r;
+    r.target = index_at(w.targets, w.wide, token);
+    if (j.mode == kStats || j.mode == kFewStats) return r;
+    const float g = static_cast<const volatile float*>(w.dloss)[token], h = w.dlse ? static_cast<const volatile float*>(w.dlse)[token] : 0.0f;
+    r.lse = static_cast<const volatile float*>(w.lse)[token];
     r.g = r.target < 0 ? 0.0f : r.target < w.V ? g : NAN;
     r.p = r.g + h;
     return r;
@@ -219,68 +226,176 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const 
     if (row < j.rows && n0 < end) w.stats[part * w.stats_ld + row] = make_float2(top, sum2(sums));
 }
 
-// 32 bf16 columns of a row; n of them (a multiple of 16) are there
-__device__ __forceinline__ void store_row(uint16_t* p, int64_t n, bool wide, const uint32_t (&o)[kChunk / 2]) {
+// The same of few tokens: a warp has 32 rows of the weight and up to 32 tokens n0 .. end - 1, which it turns over in shared
+// memory, so that a lane has one token; top and sum go on from tile to tile.
+__device__ __forceinline__ void few_stats(const Work& w, const Job& j, int64_t target, uint32_t taddr, uint32_t buf, int64_t row0, int lane,
+                                          int64_t n0, int64_t end, float& top, float& sum) {
+    uint32_t v[kChunk];
+    __syncwarp();
+    tmem_ld<kChunk>(taddr, v);
+    const bool in = row0 + lane < j.rows;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (16 * h >= n) return;
-        const uint32_t w8[8] = {o[8 * h], o[8 * h + 1], o[8 * h + 2], o[8 * h + 3], o[8 * h + 4], o[8 * h + 5], o[8 * h + 6], o[8 * h + 7]};
-        store_words8(p + 16 * h, wide, w8);
+    for (int e = 0; e < kChunk; ++e)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(4 * (33 * lane + e))), "r"(in ? v[e] : 0xFF800000u) : "memory");
+    __syncwarp();
+    float mx = top;
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[k]) : "r"(buf + (uint32_t)(4 * (33 * k + lane))));
+        mx = fmaxf(mx, __uint_as_float(v[k]));
+    }
+    const int64_t at = target - row0;
+    if (at >= 0 && at < kChunk && target < j.rows && n0 + lane < end) {
+        float z;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=f"(z) : "r"(buf + (uint32_t)(4 * (33 * (int)at + lane))));
+        w.target_logit[n0 + lane] = z;
+    }
+    __syncwarp();   // the next tile's rows may be written
+    const float ref = mx == -INFINITY ? 0.0f : mx, f = ex2_ftz((top - ref) * kLog2e);
+    uint64_t sums = pk(sum * f, 0.0f);
+    top = mx;
+#pragma unroll
+    for (int k = 0; k < kChunk; k += 2) {
+        float a, b;
+        exp2_of(v[k], v[k + 1], pk(-ref, -ref), a, b);
+        sums = add2(sums, pk(a, b));
+    }
+    sum = sum2(sums);
+}
+
+// ---- stores of bf16 by TMA: 64 columns of a warp's 32 rows through its 4 KB of shared memory, 128-byte swizzle ----
+__device__ __forceinline__ void staging_free(int lane) {   // the copy before has read its values
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+// columns 32 h .. + 31 of the lane's row
+__device__ __forceinline__ void stage_row(uint32_t buf, int lane, int h, const uint32_t (&o)[kChunk / 2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + (uint32_t)(128 * lane + (((4 * h + i) ^ (lane & 7)) << 4))),
+                     "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                     : "memory");
+}
+// (columns and rows that the tensor does not have are left out)
+__device__ __forceinline__ void store_staged(const CUtensorMap* map, uint32_t buf, int64_t col, int64_t row0, int64_t rows, int lane) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0 && row0 < rows) {
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                     "r"((int32_t)col), "r"((int32_t)row0), "r"(buf)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
 }
 
-__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, int64_t row, int64_t n0,
-                                          int64_t end, bool wide) {
-    const bool ok = row < j.rows;
-    const float lse = r.lse, p = r.p;
+// kDz: boxes of 64 columns, every second one from `half` on
+__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, uint32_t buf, const CUtensorMap* map,
+                                          int64_t row0, int64_t col0, int half, int lane) {
+    const uint64_t minus_lse = pk(-r.lse, -r.lse), p2 = pk(r.p, r.p);
     const int64_t target = r.target - w.v0;
 #pragma unroll 1
-    for (int64_t col = n0; col < end; col += kChunk) {
-        uint32_t v[kChunk], o[kChunk / 2];
-        __syncwarp();
-        tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
+    for (int b = 64 * half; b < j.bn && col0 + b < j.cols; b += 128) {
+        staging_free(lane);
 #pragma unroll
-        for (int e = 0; e < kChunk; e += 2) {
-            float a, b;
-            exp2_of(v[e], v[e + 1], pk(-lse, -lse), a, b);
-            upk(mul2(pk(a, b), pk(p, p)), a, b);
-            v[e] = __float_as_uint(a);
-            v[e + 1] = __float_as_uint(b);
+        for (int h = 0; h < 2; ++h) {
+            const int64_t col = col0 + b + 32 * h;
+            uint32_t v[kChunk], o[kChunk / 2];
+            tmem_ld<kChunk>(taddr + (uint32_t)(b + 32 * h), v);
+#pragma unroll
+            for (int e = 0; e < kChunk; e += 2) {
+                float x, y;
+                exp2_of(v[e], v[e + 1], minus_lse, x, y);
+                upk(mul2(pk(x, y), p2), x, y);
+                v[e] = __float_as_uint(x);
+                v[e + 1] = __float_as_uint(y);
+            }
+            if (__any_sync(kFull, target >= col && target < col + kChunk)) {
+#pragma unroll
+                for (int e = 0; e < kChunk; ++e)
+                    if (col + e == target) v[e] = __float_as_uint(__uint_as_float(v[e]) - r.g);
+            }
+#pragma unroll
+            for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            __syncwarp();
+            stage_row(buf, lane, h, o);
         }
-        if (__any_sync(kFull, target >= col && target < col + kChunk)) {
-#pragma unroll
-            for (int e = 0; e < kChunk; ++e)
-                if (col + e == target) v[e] = __float_as_uint(__uint_as_float(v[e]) - r.g);
-        }
-#pragma unroll
-        for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        // what lies behind the piece's columns is there, but not read
-        if (ok) store_row(j.out + row * j.ld + col, end - col, wide, o);
+        store_staged(map, buf, col0 + b, row0, j.rows, lane);
     }
 }
 
-// Where there are sums of other parts or pieces: those of the pieces before are added; true: more will be added to these, here
-// or behind the last piece, and they are stored, so nothing else is to do.  `left` of the 32 sums are there, one column each
-// (p: float32, a multiple of 16 of them) or one row each, `stride` apart.
-__device__ __forceinline__ bool with_sums_of_row(const Job& j, float* p, int64_t left, uint32_t (&v)[kChunk]) {
-    float4* q = reinterpret_cast<float4*>(p);
+// kDw in one part: likewise
+__device__ __forceinline__ void dw_of_row(const Job& j, uint32_t taddr, uint32_t buf, const CUtensorMap* map, int64_t row0, int64_t col0,
+                                          int half, int lane) {
+#pragma unroll 1
+    for (int b = 64 * half; b < j.bn && col0 + b < j.cols; b += 128) {
+        staging_free(lane);
 #pragma unroll
-    for (int i = 0; i < kChunk / 4; ++i) {
-        if (j.first || 4 * i >= left) break;
-        const float4 f = q[i];
-        v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + f.x);
-        v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + f.y);
-        v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + f.z);
-        v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + f.w);
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v[kChunk], o[kChunk / 2];
+            tmem_ld<kChunk>(taddr + (uint32_t)(b + 32 * h), v);
+#pragma unroll
+            for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            stage_row(buf, lane, h, o);
+        }
+        store_staged(map, buf, col0 + b, row0, j.rows, lane);
     }
-    if (j.last) return false;
+}
+
+// 32 columns of the product, rows of `out`, whose columns `row` are the lanes' (the first `left` of them; 0: not a row):
+// two lanes exchange, so that each has two neighbours of one of them: the even lane of column e, the odd one of e + 1
+__device__ __forceinline__ void store_columns(uint16_t* out, int64_t ld, int64_t row, int64_t col, int64_t left, int lane,
+                                              const uint32_t (&v)[kChunk]) {
+    const int odd = lane & 1;
+    uint16_t* p = out + (col + odd) * ld + (row - odd);
+#pragma unroll
+    for (int e = 0; e < kChunk; e += 2) {
+        const uint32_t own = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), got = __shfl_xor_sync(kFull, own, 1);
+        const uint32_t x = odd ? __byte_perm(got, own, 0x7632) : __byte_perm(own, got, 0x5410);
+        if (e + odd < left) *reinterpret_cast<uint32_t*>(p + e * ld) = x;
+    }
+}
+
+// kFewDz: r is that of token n0 + lane.  (A last column without a neighbour takes one of the row's padding with it.)
+__device__ __forceinline__ void few_dz(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, int64_t row0, int lane, int64_t n0,
+                                       int64_t end) {
+    uint32_t v[kChunk];
+    __syncwarp();
+    tmem_ld<kChunk>(taddr, v);
+#pragma unroll
+    for (int e = 0; e < kChunk; e += 2) {
+        const float s0 = __shfl_sync(kFull, r.lse, e), s1 = __shfl_sync(kFull, r.lse, e + 1);
+        const float p0 = __shfl_sync(kFull, r.p, e), p1 = __shfl_sync(kFull, r.p, e + 1);
+        float x, y;
+        exp2_of(v[e], v[e + 1], pk(-s0, -s1), x, y);
+        upk(mul2(pk(x, y), pk(p0, p1)), x, y);
+        v[e] = __float_as_uint(x);
+        v[e + 1] = __float_as_uint(y);
+    }
+    const int64_t at = r.target - w.v0 - row0;
+    if (__any_sync(kFull, at >= 0 && at < 32)) {
+        const int mine = at >= 0 && at < 32 ? (int)at : -1;
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) {
+            const int t = __shfl_sync(kFull, mine, e);
+            const float g = __shfl_sync(kFull, r.g, e);
+            if (t == lane) v[e] = __float_as_uint(__uint_as_float(v[e]) - g);
+        }
+    }
+    const int64_t row = row0 + lane;
+    store_columns(j.out, j.ld, row, n0, row - (lane & 1) < j.rows ? end - n0 : 0, lane, v);
+}
+
+// `left` of 32 sums of a row (a multiple of 16)
+__device__ __forceinline__ void store_sums(float* p, int64_t left, const uint32_t (&v)[kChunk]) {
+    float4* q = reinterpret_cast<float4*>(p);
 #pragma unroll
     for (int i = 0; i < kChunk / 4; ++i)
         if (4 * i < left)
             q[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
                                __uint_as_float(v[4 * i + 3]));
-    return true;
 }
+// Where there are sums of other parts or pieces: those of the pieces before are added; true: more will be added to these, here
+// or behind the last piece, and they are stored, so nothing else is to do.  `left` of the 32 sums are there, `stride` apart.
 __device__ __forceinline__ bool with_sums_of_column(const Job& j, float* p, int64_t stride, int64_t left, uint32_t (&v)[kChunk]) {
     if (!j.first) {
 #pragma unroll
@@ -294,26 +409,20 @@ __device__ __forceinline__ bool with_sums_of_column(const Job& j, float* p, int6
     return true;
 }
 
-// kDw: rows of the weight's gradient
-__device__ __forceinline__ void dw_of_row(const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int part, bool wide) {
-    const bool ok = row < j.rows;
+// kDw in several parts
+__device__ __forceinline__ void dw_sums_of_row(const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int part) {
 #pragma unroll 1
     for (int64_t col = n0; col < end; col += kChunk) {
         uint32_t v[kChunk];
         __syncwarp();
         tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
-        if (!ok || (j.sums && with_sums_of_row(j, j.sums + (part * j.rows + row) * j.cols + col, end - col, v))) continue;
-        uint32_t o[kChunk / 2];
-#pragma unroll
-        for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-        store_row(j.out + row * j.ld + col, end - col, wide, o);
+        if (row < j.rows) store_sums(j.sums + (part * j.rows + row) * j.cols + col, end - col, v);
     }
 }
 
 // kDx: the product's rows are the columns of dx, its columns the tokens, so the lanes of a warp have neighbours of one token
 __device__ __forceinline__ void dx_of_column(const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int part, int lane) {
     const bool ok = row < j.rows;
-    const int odd = lane & 1;
 #pragma unroll 1
     for (int64_t col = n0; col < end; col += kChunk) {
         uint32_t v[kChunk];
@@ -322,33 +431,26 @@ __device__ __forceinline__ void dx_of_column(const Job& j, uint32_t taddr, int64
         const int64_t left = ok ? end - col : 0;
         if (j.sums && with_sums_of_column(j, j.sums + (part * j.cols + col) * j.rows + row, j.rows, left, v)) continue;   // not j.last: all lanes
         __syncwarp();
-        // two lanes exchange, so that each has two neighbours of one token: the even lane of token e, the odd one of e + 1
-        uint16_t* p = j.out + (col + odd) * j.ld + (row - odd);
-#pragma unroll
-        for (int e = 0; e < kChunk; e += 2) {
-            const uint32_t own = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), got = __shfl_xor_sync(kFull, own, 1);
-            const uint32_t out = odd ? __byte_perm(got, own, 0x7632) : __byte_perm(own, got, 0x5410);
-            if (e + odd < left) *reinterpret_cast<uint32_t*>(p + e * j.ld) = out;
-        }
+        store_columns(j.out, j.ld, row, col, left, lane, v);
     }
 }
 
-// The maps: A and B of the two jobs.
+// The maps of the two jobs: A, B, and the output of kDz and kDw.
 struct Maps {
-    CUtensorMap a[2], b[2];
+    CUtensorMap a[2], b[2], o[2];
 };
 
-__global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w, const bool wide) {
+__global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     unsigned char* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);   // the same offset in both CTAs
     const uint32_t sb = smem_u32(smem);
     const uint32_t bar0 = sb + kBarOff;
     auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
-    auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(kStages + s); };
-    auto acc_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kStages + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kStages + 2 + b); };
-    const uint32_t done = bar0 + 8u * (uint32_t)(2 * kStages + 4);
+    auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(kMaxStages + s); };
+    auto acc_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kMaxStages + b); };
+    auto acc_empty = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kMaxStages + 2 + b); };
+    const uint32_t done = bar0 + 8u * (uint32_t)(2 * kMaxStages + 4);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * kNumBars);
     volatile uint32_t* abort = tmem_slot + 1;
 
@@ -356,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     const uint32_t rank = cluster_rank();   // 0: the CTA that issues the pair's MMAs
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
+        for (int s = 0; s < kMaxStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
         for (int b = 0; b < 2; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 2 * kEpiWarps); }
         mbar_init(done, 1);
         *abort = 0u;
@@ -378,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     const uint32_t tmem = *tmem_slot;
 
     const int64_t pair = blockIdx.x >> 1;
+    const int stages = w.stages, slot = w.slot;
     Item it;
 
     // The producer's and the issuer's warps walk together and one elected lane issues, so that addresses and descriptors stay
@@ -399,10 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             for (int k = it.from; k < it.to; ++k) {
                 if (!ready) ok = __all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort));
                 if (!ok) break;
-                const uint32_t fb = fb0 + 8u * (uint32_t)s, own = full(s), sa = sb + (uint32_t)(s * kStageBytes), sbb = sa + kABytes;
+                const uint32_t fb = fb0 + 8u * (uint32_t)s, own = full(s), sa = sb + (uint32_t)(s * slot), sbb = sa + kABytes;
                 issued |= 1u << s;
                 last_ph = (last_ph & ~(1u << s)) | (ph << s);
-                if (++s == kStages) { s = 0; ph ^= 1u; }
+                if (++s == stages) { s = 0; ph ^= 1u; }
                 const bool next = mbar_test(empty(s), ph ^ 1u);
                 const int32_t k0 = k * kBK;
                 if (elected) {
@@ -419,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             }
         }
         // every stage issued has been read by the MMAs before the CTA may exit
-        for (int i = 0; i < kStages; ++i)
+        for (int i = 0; i < kMaxStages; ++i)
             if (issued & (1u << i)) mbar_wait(empty(i), (last_ph >> i) & 1u, nullptr);
         __syncwarp();
     } else if (warp == 1) {
@@ -445,9 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                     if (!ready) ok = __all_sync(kFull, mbar_wait_fast(full(s), ph, abort));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t so = (uint64_t)(s * (kStageBytes >> 4)), ad = adesc0 + so, bd = bdesc0 + so;
+                    const uint64_t so = (uint64_t)(s * (slot >> 4)), ad = adesc0 + so, bd = bdesc0 + so;
                     const uint32_t freed = empty(s);
-                    if (++s == kStages) { s = 0; ph ^= 1u; }
+                    if (++s == stages) { s = 0; ph ^= 1u; }
                     const bool next = mbar_test(full(s), ph);
                     if (elected) {
 #pragma unroll
@@ -468,32 +571,49 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     } else if (warp >= 4) {
         // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31, half (w - 4) / 4 of the columns ----
         const int q4 = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t staging = sb + kStageArea + (uint32_t)((warp - 4) * kStagingBytes);   // of kFewStats
+        const uint32_t box = sb + kStageArea + (uint32_t)((warp - 4) * 4096);                // of TMA stores: 1024-byte aligned
+        float top = -INFINITY, sum = 0.0f;   // kFewStats: of the lane's token
         int acc = 0;
         uint32_t aph = 0;
         for (int64_t i = 0; item_of(i, pair, w, it); ++i) {
             if (it.from == it.to) continue;
             const Job& j = w.job[it.job];
-            const int64_t row = it.m * (2 * kBM) + rank * kBM + 32 * q4 + lane;
-            const RowValues r = row_values(w, j, row);
+            const int64_t row0 = it.m * (2 * kBM) + rank * kBM + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
+            const int64_t n0 = col0 + half * (j.bn / 2), end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
+            const bool few = j.mode == kFewStats || j.mode == kFewDz;
+            const RowValues r = row_values(w, j, few ? n0 + lane : row, few ? end : j.rows);
             if (!__all_sync(kFull, mbar_wait_fast(acc_full(acc), aph, abort))) break;
             tc_fence_after();
-            const int64_t n0 = it.n * j.bn + half * (j.bn / 2);
-            const int64_t end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
-            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN + half * (j.bn / 2));
+            const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN), taddr = acc0 + (uint32_t)(half * (j.bn / 2));
             if (j.mode == kStats)
                 stats_of_row(w, j, r, taddr, row, n0, end, 2 * it.n + half);
             else if (j.mode == kDz)
-                dz_of_row(w, j, r, taddr, row, n0, end, wide);
-            else if (j.mode == kDw)
-                dw_of_row(j, taddr, row, n0, end, it.part, wide);
-            else
+                dz_of_row(w, j, r, acc0, box, &maps.o[it.job], row0, col0, half, lane);
+            else if (j.mode == kFewStats)
+                few_stats(w, j, r.target, taddr, staging, row0, lane, n0, end, top, sum);
+            else if (j.mode == kFewDz)
+                few_dz(w, j, r, taddr, row0, lane, n0, end);
+            else if (j.mode == kDx)
                 dx_of_column(j, taddr, row, n0, end, it.part, lane);
+            else if (j.sums)
+                dw_sums_of_row(j, taddr, row, n0, end, it.part);
+            else
+                dw_of_row(j, acc0, box, &maps.o[it.job], row0, col0, half, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(map_to_rank(acc_empty(acc), 0));
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
         }
+        if (w.job[0].mode == kFewStats) {
+            const int bn = w.job[0].bn;
+            const int64_t token = half * (bn / 2) + lane;
+            if (lane < bn / 2 && token < w.job[0].cols)
+                w.stats[((2 * pair + rank) * 4 + q4) * w.stats_ld + token] = make_float2(top, sum);
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the stores by TMA are done
+        __syncwarp();
     }
     dependents_may_start();
     tc_fence_before();
@@ -615,16 +735,19 @@ constexpr int64_t kWholeStep = kBN + 64;
 // Columns of a tile, of the multiples of 32.  Of a product alone: those with which the pairs that have most tiles take least
 // time (33 x 50304 x 2048 forward: 225 tiles of 224 for 76 pairs, instead of 197 of 256).  Of one of two products, which make up
 // for each other's last tiles: those that cover it in the least time.
-int tile_columns(int64_t rows, int64_t cols, bool alone) {
+int tile_columns(int64_t rows, int64_t cols, int32_t mode) {
+    const bool alone = mode < kDx;
+    const int step = mode == kDz || mode == kDw ? 64 : 32;   // a store by TMA has 64 columns
     int64_t best = 0;
     int bn = kBN;
-    for (int n = kBN; n >= 32; n -= 32) {
+    for (int n = kBN; n >= step; n -= step) {
         const int64_t tiles = up(rows, 2 * kBM) * up(cols, n), cost = (alone ? up(tiles, kPairs) : tiles) * step_cost(n);
         if (best == 0 || cost < best) {
             best = cost;
             bn = n;
         }
     }
+    if (mode == kFewStats || mode == kFewDz) bn = cols <= 32 ? 32 : 64;   // all tokens
     return bn;
 }
 
@@ -636,7 +759,7 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     j.rows = a.mn ? a.cols : a.rows;
     j.cols = b.rows;
     j.steps = (int32_t)up(K, kBK);
-    j.bn = tile_columns(j.rows, j.cols, mode == kStats || mode == kDz);
+    j.bn = tile_columns(j.rows, j.cols, mode);
     j.parts = 1;
     j.tm = up(j.rows, 2 * kBM);
     j.tn = up(j.cols, j.bn);
@@ -645,7 +768,8 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     j.sums = nullptr;
     j.first = j.last = 1;
     if (!encode(&maps.a[w.jobs], a.p, a.rows, a.cols, a.ld, a.mn ? kBK : kBM) ||
-        !encode(&maps.b[w.jobs], b.p, b.rows, b.cols, b.ld, j.bn / 2))
+        !encode(&maps.b[w.jobs], b.p, b.rows, b.cols, b.ld, j.bn / 2) ||
+        ((mode == kDz || mode == kDw) && !encode(&maps.o[w.jobs], out, j.rows, j.cols, ld, 32)))
         return false;
     ++w.jobs;
     return true;
@@ -674,8 +798,8 @@ Split split_of(int64_t first, int64_t first_cost, int64_t second, int64_t second
     return s;
 }
 
-cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
-    const int64_t pairs = device_sms() / 2;
+cudaError_t launch_work(Work& w, const Maps& maps, cudaStream_t s) {
+    const int64_t sms = device_sms(), pairs = sms / 2 < kPairs ? sms / 2 : kPairs;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     int64_t cost[2] = {0, 0};
     for (int i = 0; i < w.jobs; ++i) {
@@ -687,6 +811,10 @@ cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
     w.pairs = (int32_t)sp.pairs;
     w.ahead = (int32_t)sp.ahead;
     w.extra = sp.extra;
+    int bn = 0;
+    for (int i = 0; i < w.jobs; ++i) bn = w.job[i].bn > bn ? w.job[i].bn : bn;
+    w.slot = slot_bytes(bn);
+    w.stages = stages_of(bn);
     cudaError_t e = cudaFuncSetAttribute(lce_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
@@ -703,7 +831,7 @@ cudaError_t launch_work(Work& w, const Maps& maps, bool wide, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(2u * (unsigned)w.pairs);
-    return cudaLaunchKernelEx(&cfg, lce_kernel, maps, (const Work&)w, wide);
+    return cudaLaunchKernelEx(&cfg, lce_kernel, maps, (const Work&)w);
 }
 
 // The two products behind a piece of n columns: their parts, and which has the longer items.  Few tiles with many steps leave
@@ -721,7 +849,7 @@ int64_t busiest(int64_t first, int64_t first_cost, int64_t second, int64_t secon
 }
 Parts parts_of(int64_t M, int64_t n, int64_t C) {
     const int64_t dx = up(n, kBK), dw = up(M, kBK);   // steps
-    const int dx_bn = tile_columns(C, M, false), dw_bn = tile_columns(n, C, false);
+    const int dx_bn = tile_columns(C, M, kDx), dw_bn = tile_columns(n, C, kDw);
     const int64_t dx_tiles = up(C, 2 * kBM) * up(M, dx_bn), dw_tiles = up(n, 2 * kBM) * up(C, dw_bn);
     constexpr int kTry[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
     Parts best{1, 1, true};
@@ -747,23 +875,24 @@ Parts parts_of(int64_t M, int64_t n, int64_t C) {
 cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s) {
     Work w = {};
     alignas(64) Maps maps;
-    if (!add_job(w, maps, kStats, Operand{a.x, a.M, a.C, a.x_ld, false}, Operand{a.weight, a.V, a.C, a.C, false}, nullptr, 0))
-        return cudaErrorInvalidValue;
+    const Operand x{a.x, a.M, a.C, a.x_ld, false}, W{a.weight, a.V, a.C, a.C, false};
+    const bool few = a.M <= kFewTokens;
+    if (!(few ? add_job(w, maps, kFewStats, W, x, nullptr, 0) : add_job(w, maps, kStats, x, W, nullptr, 0))) return cudaErrorInvalidValue;
     w.targets = a.targets;
     w.wide = a.wide;
     w.V = (int32_t)a.V;
     w.stats = reinterpret_cast<float2*>(a.stats);
     w.stats_ld = up(a.M, 32) * 32;
     w.target_logit = a.loss;
-    cudaError_t e = launch_work(w, maps, true, s);
+    cudaError_t e = launch_work(w, maps, s);
     if (e != cudaSuccess) return e;
-    // the halves of the last tile: the second one only where it has columns
+    // the epilogue warps; or halves of tiles, the last one's second half only where it has columns
+    const int64_t parts = few ? 8 * (int64_t)w.pairs : up(a.V, w.job[0].bn / 2);
     return launch_next(lce_join_kernel, (unsigned)up(a.M, 32), 32 * kJoinWarps, 0, s, (const float2*)w.stats, w.stats_ld,
-                       up(a.V, w.job[0].bn / 2), a.targets, a.wide, a.M, a.V, a.loss, a.lse);
+                       parts, a.targets, a.wide, a.M, a.V, a.loss, a.lse);
 }
 
 cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
-    const bool wide = aligned32(a.dx) && aligned32(a.dweight);
     const int64_t ld = lce_piece_ld(a.piece, a.V);
     const Parts parts = parts_of(a.M, a.piece, a.C);
     float* const dw_sums = a.sums + lce_dx_sums(a.M, a.V, a.C, a.piece);
@@ -776,7 +905,8 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
         const uint16_t* W = a.weight + v0 * a.C;
         Work w = {};
         alignas(64) Maps maps;
-        if (!add_job(w, maps, kDz, Operand{a.x, a.M, a.C, a.x_ld, false}, Operand{W, n, a.C, a.C, false}, a.dz, ld))
+        const Operand x{a.x, a.M, a.C, a.x_ld, false}, Wz{W, n, a.C, a.C, false};
+        if (!(a.M <= kFewTokens ? add_job(w, maps, kFewDz, Wz, x, a.dz, ld) : add_job(w, maps, kDz, x, Wz, a.dz, ld)))
             return cudaErrorInvalidValue;
         w.targets = a.targets;
         w.wide = a.wide;
@@ -785,7 +915,7 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
         w.lse = a.lse;
         w.dloss = a.dloss;
         w.dlse = a.dlse;
-        e = launch_work(w, maps, aligned32(a.dz), s);
+        e = launch_work(w, maps, s);
         if (e != cudaSuccess) return e;
         w.jobs = 0;
         for (int i = 0; i < 2; ++i) {
@@ -806,7 +936,7 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
                 j.last = parts.dw == 1;
             }
         }
-        e = launch_work(w, maps, wide, s);
+        e = launch_work(w, maps, s);
         if (e == cudaSuccess && parts.dw > 1)
             e = launch_next(lce_parts_kernel, (unsigned)up(n * a.C, 8 * 256), 256, 0, s, (const float*)dw_sums, parts.dw, n * a.C,
                             a.dweight + v0 * a.C);
@@ -834,7 +964,10 @@ int64_t lce_sums(int64_t M, int64_t V, int64_t C, int64_t piece) {
     const Parts p = parts_of(M, piece, C);
     return lce_dx_sums(M, V, C, piece) + (p.dw > 1 ? p.dw * piece * C : 0);
 }
-size_t lce_stats_bytes(int64_t M, int64_t V) { return 8 * (size_t)(up(M, 32) * 32) * (size_t)up(V, tile_columns(M, V, true) / 2); }
+size_t lce_stats_bytes(int64_t M, int64_t V) {
+    const int64_t parts = M <= kFewTokens ? 8 * kPairs : up(V, tile_columns(M, V, kStats) / 2);
+    return 8 * (size_t)(up(M, 32) * 32) * (size_t)parts;
+}
 
 cudaError_t read_lce_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }
 
