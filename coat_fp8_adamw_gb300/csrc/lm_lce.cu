@@ -117,47 +117,54 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
 
 // Tile order: bands of kBand tiles of rows, column-major inside a band, so that the pairs that run at once share a band of
 // A and walk B together.
-constexpr int64_t kBand = 16;
+constexpr uint32_t kBand = 16;
 struct Item {
     int32_t job, part;
     int32_t from, to;        // steps
     int64_t m, n;            // tile
 };
-// the k-th item of pair `pair`; false: it has none left
-__device__ __forceinline__ bool item_of(int64_t k, int64_t pair, const Work& w, Item& it) {
-    const int64_t P = w.pairs, own = (w.items[0] - pair + P - 1) / P;   // of the first job
-    int64_t t;
-    it.job = k >= own;
-    if (it.job == 0) {
-        t = pair + k * P;
-    } else {
-        k -= own;
-        const int64_t behind = pair - w.ahead;
-        if (behind >= 0) {
-            const int64_t lot = P - w.ahead, mine = behind < w.extra ? (w.extra - behind + lot - 1) / lot : 0;
-            if (k < mine) {
-                t = behind + k * lot;
-                k = -1;
-            } else {
-                k -= mine;
-            }
-        }
-        if (k >= 0) t = w.extra + k * P + pair;
-        if (t >= w.items[1]) return false;
+// A pair's way through the items: the first job's in turn, those that make up for one less of them, and the rest.  In 32 bits
+// and with what does not change taken once: 64-bit divisions took 1500 clocks an item, in every role.
+struct Walk {
+    uint32_t pair, own, behind, lot, mine;
+    __device__ __forceinline__ Walk(const Work& w, uint32_t p) {
+        const uint32_t P = (uint32_t)w.pairs, ahead = (uint32_t)w.ahead;
+        pair = p;
+        own = ((uint32_t)w.items[0] - p + P - 1u) / P;   // of the first job
+        behind = p - ahead;
+        lot = P - ahead;
+        mine = p >= ahead && behind < (uint32_t)w.extra ? ((uint32_t)w.extra - behind + lot - 1u) / lot : 0u;
     }
-    const Job& j = w.job[it.job];
-    const int64_t tiles = j.tm * j.tn;
-    it.part = (int32_t)(t / tiles);
-    t -= it.part * tiles;
-    it.from = (int32_t)((int64_t)j.steps * it.part / j.parts);
-    it.to = (int32_t)((int64_t)j.steps * (it.part + 1) / j.parts);
-    const int64_t band = t / (kBand * j.tn), top = band * kBand;
-    const int64_t rows = j.tm - top < kBand ? j.tm - top : kBand;
-    const int64_t r = t - band * kBand * j.tn;
-    it.m = top + r % rows;
-    it.n = r / rows;
-    return true;
-}
+    // the k-th item; false: there is none
+    __device__ __forceinline__ bool item(uint32_t k, const Work& w, Item& it) const {
+        const uint32_t P = (uint32_t)w.pairs;
+        uint32_t t;
+        it.job = k >= own;
+        if (it.job == 0) {
+            t = pair + k * P;
+        } else {
+            k -= own;
+            t = k < mine ? behind + k * lot : (uint32_t)w.extra + (k - mine) * P + pair;
+            if (t >= (uint32_t)w.items[1]) return false;
+        }
+        const Job& j = w.job[it.job];
+        const uint32_t tm = (uint32_t)j.tm, tn = (uint32_t)j.tn, tiles = tm * tn;
+        it.part = 0;
+        it.from = 0;
+        it.to = j.steps;
+        if (j.parts > 1) {
+            it.part = (int32_t)(t / tiles);
+            t -= (uint32_t)it.part * tiles;
+            it.from = (int32_t)((int64_t)j.steps * it.part / j.parts);
+            it.to = (int32_t)((int64_t)j.steps * (it.part + 1) / j.parts);
+        }
+        const uint32_t band = t / (kBand * tn), top = band * kBand;
+        const uint32_t rows = tm - top < kBand ? tm - top : kBand, r = t - top * tn, n = r / rows;
+        it.m = top + (r - n * rows);
+        it.n = n;
+        return true;
+    }
+};
 
 // ---- epilogues: one row of the tile, columns n0 .. end - 1 (at most 128, a multiple of 16 but for the matrix's end), per
 // thread; where a chunk of 32 goes past them, it reads columns of the other half, which do not count ----
@@ -480,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     const uint32_t tmem = *tmem_slot;
 
     const int64_t pair = blockIdx.x >> 1;
+    const Walk walk(w, blockIdx.x >> 1);
     const int stages = w.stages, slot = w.slot;
     Item it;
 
@@ -493,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         bool ok = true, ready = false;
         const uint32_t elected = elect_one();
         const uint32_t fb0 = map_to_rank(full(0), 0);   // the leader's barriers, contiguous like ours
-        for (int64_t i = 0; ok && item_of(i, pair, w, it); ++i) {
+        for (uint32_t i = 0; ok && walk.item(i, w, it); ++i) {
             const Job& j = w.job[it.job];
             const CUtensorMap *ma = &maps.a[it.job], *mb = &maps.b[it.job];
             const int32_t m0 = (int32_t)(it.m * (2 * kBM) + rank * kBM), n0 = (int32_t)(it.n * j.bn + rank * (j.bn / 2));
@@ -533,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             bool ok = true, ready = false;
             const uint32_t elected = elect_one();
             const uint64_t bdesc0 = smem_desc(sb + kABytes, false);
-            for (int64_t i = 0; ok && item_of(i, pair, w, it); ++i) {
+            for (uint32_t i = 0; ok && walk.item(i, w, it); ++i) {
                 if (it.from == it.to) continue;
                 const Job& j = w.job[it.job];
                 const uint32_t idesc = instr_desc(j);
@@ -576,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         float top = -INFINITY, sum = 0.0f;   // kFewStats: of the lane's token
         int acc = 0;
         uint32_t aph = 0;
-        for (int64_t i = 0; item_of(i, pair, w, it); ++i) {
+        for (uint32_t i = 0; walk.item(i, w, it); ++i) {
             if (it.from == it.to) continue;
             const Job& j = w.job[it.job];
             const int64_t row0 = it.m * (2 * kBM) + rank * kBM + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
@@ -807,6 +815,7 @@ cudaError_t launch_work(Work& w, const Maps& maps, cudaStream_t s) {
         cost[i] = item_cost(w.job[i].steps, w.job[i].parts, w.job[i].bn);
     }
     if (w.jobs < 2) w.items[1] = 0;
+    if (w.items[0] + w.items[1] >= (int64_t)1 << 31) return cudaErrorInvalidValue;   // (2^40 logits are 2^27 tiles)
     const Split sp = split_of(w.items[0], cost[0], w.items[1], cost[1], pairs);
     w.pairs = (int32_t)sp.pairs;
     w.ahead = (int32_t)sp.ahead;
