@@ -8,9 +8,20 @@
 namespace coat {
 namespace lm {
 
-// index i of a list of 4- or 8-byte integers (a volatile load: the kernels start before the one ahead of them has ended)
+// Indexes of 4 or 8 bytes.  (volatile: the kernels start before the one ahead of them has ended, so no load may move ahead of
+// the wait for it; through L1, since many threads read the same ones)
+__device__ __forceinline__ int32_t load_index(const int32_t* p) {
+    int32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int64_t load_index(const int64_t* p) {
+    int64_t v;
+    asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(p));
+    return v;
+}
 __device__ __forceinline__ int64_t index_at(const void* p, int32_t wide, int64_t i) {
-    return wide ? static_cast<const volatile long long*>(p)[i] : (long long)static_cast<const volatile int*>(p)[i];
+    return wide ? load_index(static_cast<const int64_t*>(p) + i) : (int64_t)load_index(static_cast<const int32_t*>(p) + i);
 }
 
 }  // namespace lm

@@ -25,21 +25,27 @@ namespace {
 
 using namespace ckpt;
 using lm::index_at;
+using lm::load_index;
 
 constexpr int kBlock = 256;
 constexpr int kWarps = kBlock / 32;
 constexpr int kChunk = 32;            // tokens of a chunk, one of a warp's lanes each
 constexpr int kSlice = 256;           // columns of a warp: 8 per lane
-// Tokens whose loads are on their way at once: with 4, and registers for four blocks per SM, all warps of 16411 x 2048 are
-// resident together (41 us; 8 and two blocks 45, 8 and three 47, 4 and three 49; chunks of 16 tokens 46).
-constexpr int kDeep = 4;
+// Tokens whose loads are on their way at once.  Many chunks: 4, and registers for four blocks per SM, with which all warps of
+// 16411 x 2048 are resident together (41 us; 8 and two blocks 45, 8 and three 47, 4 and three 49; chunks of 16 tokens 46).
+// Up to kFewUnits warps, which find room one block per SM: 16 (300 x 4096, added: 14.6 us, with 4 18.3).
+constexpr int kDeep = 4, kDeepest = 16;
+constexpr int64_t kFewUnits = 152 * 8;
 constexpr int kSortBlock = 1024;
 constexpr int kSortWarps = kSortBlock / 32;
 constexpr int kIds = 8;
 constexpr int kMaxRange = 768;        // rows of a sorting block: they take 256 bytes of shared memory each
-constexpr int kTeams = 2;              // ranges of 256 columns of a joining block
+constexpr int kJoinBlock = 128;
+constexpr int kTeams = kJoinBlock / 32;
+// Rows of a filling block.  More copies at once per SM are slower: 8192 tokens, 32000 x 4096, all three kernels: 60 us with 4
+// and 8, 62 with 16 and 32, 66 with 64, 67 with 128.
+constexpr int kFill = 8;
 constexpr int kZeroBytes = 8192;
-constexpr int kFill = 64;             // rows of a filling block
 
 // ---- forward ----
 __global__ void __launch_bounds__(kBlock) embed_fwd_kernel(const EmbedFwdArgs a, const Divider nc, bool wide) {
@@ -65,18 +71,18 @@ __global__ void __launch_bounds__(kBlock) embed_fwd_kernel(const EmbedFwdArgs a,
 
 // ---- backward: sort ----
 // An id as a row of the table: itself, or -1 where it is none's.
-__device__ __forceinline__ int row_of(int id) { return id; }
-__device__ __forceinline__ int row_of(long long id) { return id < 0 || id > 0x7FFFFFFF ? -1 : (int)id; }
+__device__ __forceinline__ int row_of(int32_t id) { return id; }
+__device__ __forceinline__ int row_of(int64_t id) { return id < 0 || id > 0x7FFFFFFF ? -1 : (int)id; }
 // f(token, id's row) for the tokens m0 + lane, m0 + lane + 32, ... below m1, kIds loads on their way at once; the whole
 // warp calls f together, with a row of -1 behind the last token.
 template <typename T, typename F>
 __device__ __forceinline__ void for_ids(const void* ids, int64_t m0, int64_t m1, int lane, F f) {
     int64_t m = m0;
     for (; m + 32 * kIds <= m1; m += 32 * kIds) {
-        const volatile T* p = static_cast<const volatile T*>(ids) + m + lane;
+        const T* p = static_cast<const T*>(ids) + m + lane;
         T v[kIds];
 #pragma unroll
-        for (int k = 0; k < kIds; ++k) v[k] = p[32 * k];
+        for (int k = 0; k < kIds; ++k) v[k] = load_index(p + 32 * k);
 #pragma unroll
         for (int k = 0; k < kIds; ++k) f((int)m + 32 * k + lane, row_of(v[k]));
     }
@@ -85,7 +91,7 @@ __device__ __forceinline__ void for_ids(const void* ids, int64_t m0, int64_t m1,
 #pragma unroll
     for (int k = 0; k < kIds; ++k) {   // (a load without a condition: behind a branch every load would wait for the one before it)
         const int64_t at = m + 32 * k + lane;
-        v[k] = static_cast<const volatile T*>(ids)[at < m1 ? at : m1 - 1];
+        v[k] = load_index(static_cast<const T*>(ids) + (at < m1 ? at : m1 - 1));
     }
 #pragma unroll
     for (int k = 0; k < kIds; ++k)
@@ -218,8 +224,8 @@ __device__ __forceinline__ void store_table(const EmbedBwdArgs& a, int row, int6
     *reinterpret_cast<uint4*>(a.dtable + (int64_t)row * a.C + col) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool kAdd>
-__global__ void __launch_bounds__(kBlock, 4) embed_chunks_kernel(const EmbedBwdArgs a, int slices) {
+template <bool kAdd, int kDeep>
+__global__ void __launch_bounds__(kBlock, kDeep == kDeepest ? 1 : 4) embed_chunks_kernel(const EmbedBwdArgs a, int slices) {
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), chunk = unit / slices;
     const int lane = threadIdx.x & 31;
     wait_for_primary();
@@ -295,9 +301,9 @@ __device__ __noinline__ int64_t chunks_of_row(const EmbedBwdArgs& a, int row, in
 }
 
 // Zeros over the rows without a token: kFill rows per block, one thread for each, whose copies read
-// the same zeros in shared memory (8192 x 4096 of 32000 rows: 28 us for 205 MB; by stores of the warps 31 us).
+// the same zeros in shared memory.
 __device__ __forceinline__ void fill_rows(const EmbedBwdArgs& a, const Ranges& by, int64_t block, float* zeros) {
-    for (int i = threadIdx.x; i < kZeroBytes / 4; i += kBlock) zeros[i] = 0.0f;
+    for (int i = threadIdx.x; i < kZeroBytes / 4; i += kJoinBlock) zeros[i] = 0.0f;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies read them
     __syncthreads();
     const int64_t row = block * kFill + threadIdx.x;
@@ -311,18 +317,17 @@ __device__ __forceinline__ void fill_rows(const EmbedBwdArgs& a, const Ranges& b
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// The first `fills` blocks fill.  Of the others each has a chunk and 2 times 256 columns; four warps add up a row's shares for
-// the same columns.
+// The first `fills` blocks fill.  Of the others each has a chunk and 256 columns, and its warps add up a row's shares.
 template <bool kAdd>
-__global__ void __launch_bounds__(kBlock) embed_join_kernel(const EmbedBwdArgs a, int groups, const Ranges by, unsigned fills) {
-    __shared__ __align__(16) float part[kWarps][kSlice];
+__global__ void __launch_bounds__(kJoinBlock) embed_join_kernel(const EmbedBwdArgs a, int slices, const Ranges by, unsigned fills) {
+    __shared__ __align__(16) float part[kAdd ? (kTeams - 1) * kSlice : kZeroBytes / 4];
     wait_for_primary();
     if (!kAdd && blockIdx.x < fills) {
-        fill_rows(a, by, blockIdx.x, &part[0][0]);
+        fill_rows(a, by, blockIdx.x, part);
         return;
     }
-    const int64_t block = blockIdx.x - fills, chunk = block / groups;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / kTeams;
+    const int64_t block = blockIdx.x - fills, chunk = block / slices;
+    const int lane = threadIdx.x & 31, team = threadIdx.x >> 5;
     // a row that begins in this chunk and goes on behind it: in n chunks (all of these loads at once)
     const int64_t last = chunk * kChunk + kChunk - 1;
     const int near = entry_at(a, last + 1 + kChunk * lane).row, far = entry_at(a, last + 1 + kChunk * (32 + lane)).row;
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kBlock) embed_join_kernel(const EmbedBwdArgs a
     const uint32_t in = __ballot_sync(kFull, near == row), more = __ballot_sync(kFull, far == row);
     if (in == 0u) return;
     const int64_t n = in != kFull ? __popc(in) : more != kFull ? 32 + __popc(more) : chunks_of_row(a, row, chunk, lane);
-    const int64_t col = ((block - chunk * groups) * kTeams + warp % kTeams) * kSlice + 8 * lane;
+    const int64_t col = (block - chunk * slices) * kSlice + 8 * lane;
     const bool ok = col < a.C;
     uint32_t old[4];
     load_words_if(kAdd && ok && team == 0, a.dtable + (int64_t)row * a.C + (ok ? col : 0), old);
@@ -339,13 +344,13 @@ __global__ void __launch_bounds__(kBlock) embed_join_kernel(const EmbedBwdArgs a
     if (ok) {
         if (team == 0) add_row(partial_at(a, chunk, 1) + col, sum);
 #pragma unroll 8
-        for (int64_t i = 1 + team; i <= n; i += kWarps / kTeams) add_row(partial_at(a, chunk + i, 0) + col, sum);
+        for (int64_t i = 1 + team; i <= n; i += kTeams) add_row(partial_at(a, chunk + i, 0) + col, sum);
     }
-    if (team > 0) store_row(part[warp] + 8 * lane, sum);
+    if (team > 0) store_row(part + (team - 1) * kSlice + 8 * lane, sum);
     __syncthreads();
     if (team > 0 || !ok) return;
 #pragma unroll
-    for (int w = kTeams; w < kWarps; w += kTeams) add_row(part[warp + w] + 8 * lane, sum);
+    for (int t = 0; t < kTeams - 1; ++t) add_row(part + t * kSlice + 8 * lane, sum);
     store_table<kAdd>(a, row, col, sum, old);
 }
 
@@ -385,21 +390,23 @@ int64_t embed_flags(int64_t V) {
 cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
     const Ranges by = ranges_of(a.V);
     const size_t smem = (size_t)kSortWarps * (size_t)by.R * sizeof(Slot);
-    auto* const sort = a.wide ? embed_sort_kernel<long long> : embed_sort_kernel<int>;
+    auto* const sort = a.wide ? embed_sort_kernel<int64_t> : embed_sort_kernel<int32_t>;
     cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_next(sort, 1u << by.shift, kSortBlock, smem, s, a, by);
     if (e != cudaSuccess) return e;
-    const int slices = (int)((a.C + kSlice - 1) / kSlice), groups = (slices + kTeams - 1) / kTeams;
+    const int slices = (int)((a.C + kSlice - 1) / kSlice);
     const int64_t chunks = embed_chunks(a.M);
-    e = launch_next(a.accumulate ? embed_chunks_kernel<true> : embed_chunks_kernel<false>,
-                    (unsigned)((chunks * slices + kWarps - 1) / kWarps), kBlock, 0, s, a, slices);
+    auto* const sums = chunks * slices <= kFewUnits
+                           ? (a.accumulate ? embed_chunks_kernel<true, kDeepest> : embed_chunks_kernel<false, kDeepest>)
+                           : (a.accumulate ? embed_chunks_kernel<true, kDeep> : embed_chunks_kernel<false, kDeep>);
+    e = launch_next(sums, (unsigned)((chunks * slices + kWarps - 1) / kWarps), kBlock, 0, s, a, slices);
     if (e != cudaSuccess) return e;
     const unsigned fills = a.accumulate ? 0u : (unsigned)((a.V + kFill - 1) / kFill);
-    const int64_t joins = chunks > 1 ? chunks * groups : 0;   // one chunk: no row goes on behind it
+    const int64_t joins = chunks > 1 ? chunks * slices : 0;   // one chunk: no row goes on behind it
     if (fills + joins == 0) return cudaSuccess;
-    return launch_next(a.accumulate ? embed_join_kernel<true> : embed_join_kernel<false>, (unsigned)(fills + joins), kBlock, 0, s, a, groups,
-                       by, fills);
+    return launch_next(a.accumulate ? embed_join_kernel<true> : embed_join_kernel<false>, (unsigned)(fills + joins), kJoinBlock, 0, s, a,
+                       slices, by, fills);
 }
 
 }  // namespace coat
