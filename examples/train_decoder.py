@@ -5,10 +5,13 @@ the heads' norm with its rotation and the gated unit leave an 8-bit checkpoint o
 what went into them; the backward pass reads the checkpoints alone, writes the
 weight gradients (coat_ckpt_weight_grad) and the norms' gradients into one flat
 bf16 gradient, and coat_fp8_adamw_step updates all parameters from it in one
-call.  Projections' outputs and input gradients are torch matrix products, and
-attention is torch's, which keeps its own inputs (q, k, v) in bf16.
+call.  At the ends, the embedding's gradient is summed by sorted tokens, and the
+cross entropy keeps no logits; dropout behind the projections into the residual
+stream keeps no masks.  Projections' outputs and input gradients are torch
+matrix products, and attention is torch's, which keeps its own inputs (q, k, v)
+in bf16.
 
-    python examples/train_decoder.py [--layers 4] [--width 1024] [--tokens 2048] [--steps 20]
+    python examples/train_decoder.py [--layers 4] [--width 1024] [--tokens 2048] [--steps 20] [--dropout 0.1] [--tied]
 """
 from __future__ import annotations
 
@@ -27,9 +30,11 @@ BF, F32, U8 = torch.bfloat16, torch.float32, torch.uint8
 
 
 class Config:
-    def __init__(self, layers=4, width=1024, heads=8, kv_heads=2, hidden=2816, vocab=512, seq=256, group=128, eps=1e-5):
+    def __init__(self, layers=4, width=1024, heads=8, kv_heads=2, hidden=2816, vocab=512, seq=256, group=128, eps=1e-5,
+                 dropout=0.0, tied=False):
         self.layers, self.width, self.heads, self.kv_heads, self.hidden = layers, width, heads, kv_heads, hidden
         self.vocab, self.seq, self.group, self.eps = vocab, seq, group, eps
+        self.dropout, self.tied = dropout, tied     # tied: the embedding's table is the output layer's weight
         self.head_dim = width // heads
         self.head_group = min(group, self.head_dim)
 
@@ -38,7 +43,11 @@ class Config:
         block = [("norm1", (C,)), ("qkv", (qkv, C)), ("q_norm", (D,)), ("k_norm", (D,)), ("out", (C, self.heads * D)),
                  ("norm2", (C,)), ("gate_up", (2 * self.hidden, C)), ("down", (C, self.hidden))]
         return ([("embed", (self.vocab, C))] + [(f"{n}.{i}", s) for i in range(self.layers) for n, s in block]
-                + [("norm", (C,)), ("head", (self.vocab, C))])
+                + [("norm", (C,))] + ([] if self.tied else [("head", (self.vocab, C))]))
+
+    @property
+    def head(self):
+        return "embed" if self.tied else "head"
 
 
 def views(flat, shapes):
@@ -86,13 +95,25 @@ class Decoder:
         angle = torch.arange(cfg.seq, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, D, 2, device="cuda") / D)
         self.cos, self.sin = angle.cos().contiguous(), angle.sin().contiguous()
         self.positions = (torch.arange(tokens, device="cuda") % cfg.seq).to(torch.int32)
-        need = max([coat.coat_rmsnorm_ckpt_backward_workspace_bytes(tokens, cfg.width),
+        # dropout's key and counters: one row for each place it is used at, moved on by the step
+        self.rng = torch.stack((torch.full((2 * cfg.layers,), seed), torch.arange(2 * cfg.layers)), 1).cuda()
+        need = max([coat.coat_linear_cross_entropy_workspace_bytes(tokens, cfg.vocab),
+                    coat.coat_linear_cross_entropy_backward_workspace_bytes(tokens, cfg.vocab, cfg.width),
+                    coat.coat_embedding_backward_workspace_bytes(tokens, cfg.vocab, cfg.width)]
+                   + [coat.coat_rmsnorm_ckpt_backward_workspace_bytes(tokens, cfg.width),
                     coat.coat_qk_norm_rope_ckpt_backward_workspace_bytes(tokens, D)]
                    + [coat.coat_ckpt_weight_grad_workspace_bytes(tokens, *s) for _, s in shapes if len(s) == 2])
         self.workspace = torch.empty(max(need, 16), dtype=U8, device="cuda")
 
     def new(self, *shape):
         return torch.empty(shape, dtype=BF, device="cuda")
+
+    def drop(self, x, place, backward=False):
+        if self.cfg.dropout == 0.0:
+            return x
+        y = torch.empty_like(x)
+        (coat.coat_dropout_backward if backward else coat.coat_dropout)(x, self.cfg.dropout, self.rng[place], y)
+        return y
 
     def norm(self, x, residual, weight):
         """y, h = x + residual, and h's checkpoint."""
@@ -108,10 +129,12 @@ class Decoder:
         k, v = (t.repeat_interleave(cfg.heads // cfg.kv_heads, 1) for t in (k, v))
         return F.scaled_dot_product_attention(q, k, v, is_causal=True).transpose(1, 2).reshape(self.M, -1)
 
-    def forward(self, ids):
+    def forward(self, ids, targets):
+        """Every token's loss and log of the softmax's sum, and what the backward pass reads."""
         cfg, w, M, D = self.cfg, self.w16, self.M, self.cfg.head_dim
         Hq, Hk = cfg.heads, cfg.kv_heads
-        x, delta, kept = w["embed"][ids], None, []
+        x, delta, kept = self.new(M, cfg.width), None, []
+        coat.coat_embedding(w["embed"], ids, 1.0, x)
         for i in range(cfg.layers):
             y, h, c1 = self.norm(x, delta, self.w[f"norm1.{i}"])
             qkv = (y @ w[f"qkv.{i}"].T).view(M, Hq + 2 * Hk, D)
@@ -125,15 +148,17 @@ class Decoder:
             co = Checkpoint(padded.shape, cfg.group)
             coat.coat_act_quantize_fp8(padded, co.G, co.q, co.scale)
             co.q, co.scale = co.q[:M], co.scale[:M]
-            y, h, c2 = self.norm(o @ w[f"out.{i}"].T, h, self.w[f"norm2.{i}"])
+            y, h, c2 = self.norm(self.drop(o @ w[f"out.{i}"].T, 2 * i), h, self.w[f"norm2.{i}"])
             both = y @ w[f"gate_up.{i}"].T
             a = self.new(M, cfg.hidden)
             cg, cu = (Checkpoint(a.shape, cfg.group) for _ in range(2))
             coat.coat_swiglu_ckpt(both[:, :cfg.hidden], both[:, cfg.hidden:], cg.G, a, cg.q, cg.scale, cu.q, cu.scale)
-            x, delta = h, a @ w[f"down.{i}"].T
+            x, delta = h, self.drop(a @ w[f"down.{i}"].T, 2 * i + 1)
             kept.append((c1, cq, ck, (qr, kr, v), co, c2, cg, cu))
         y, _, c = self.norm(x, delta, self.w["norm"])
-        return y @ w["head"].T, kept, c
+        loss, lse = (torch.empty(M, dtype=F32, device="cuda") for _ in range(2))
+        coat.coat_linear_cross_entropy(y, w[cfg.head], targets, loss, lse, self.workspace)
+        return loss, lse, y, kept, c
 
     def weight_grad(self, name, dy, c, norm_weight=None):
         """Behind a norm the checkpoint is of the norm's input: 1/rms and the weight make it its output."""
@@ -146,22 +171,25 @@ class Decoder:
                                         dresidual=dresidual)
         return dx
 
-    def backward(self, ids, dlogits, kept, last):
+    def backward(self, ids, targets, dloss, lse, y, kept, last):
         cfg, w, M, D = self.cfg, self.w16, self.M, self.cfg.head_dim
         Hq, Hk = cfg.heads, cfg.kv_heads
-        self.weight_grad("head", dlogits, last, self.w["norm"])
-        d = self.norm_backward("norm", dlogits @ w["head"], last)
+        dy = torch.empty_like(y)
+        coat.coat_linear_cross_entropy_backward(y, w[cfg.head], targets, lse, dloss, dy, self.g[cfg.head], self.workspace)
+        d = self.norm_backward("norm", dy, last)
         for i in reversed(range(cfg.layers)):
             c1, cq, ck, qkv, co, c2, cg, cu = kept.pop()
-            da = d @ w[f"down.{i}"]
+            dd = self.drop(d, 2 * i + 1, backward=True)
+            da = dd @ w[f"down.{i}"]
             dboth, ca = self.new(M, 2 * cfg.hidden), Checkpoint(da.shape, cfg.group)
             coat.coat_swiglu_ckpt_backward(da, cg.q, cg.scale, cu.q, cu.scale, cg.G, dboth[:, :cfg.hidden],
                                            dboth[:, cfg.hidden:], h_q=ca.q, h_scale=ca.scale)
-            self.weight_grad(f"down.{i}", d, ca)
+            self.weight_grad(f"down.{i}", dd, ca)
             self.weight_grad(f"gate_up.{i}", dboth, c2, self.w[f"norm2.{i}"])
             d = self.norm_backward(f"norm2.{i}", dboth @ w[f"gate_up.{i}"], c2, d)
-            self.weight_grad(f"out.{i}", d, co)
-            do = d @ w[f"out.{i}"]
+            dd = self.drop(d, 2 * i, backward=True)
+            self.weight_grad(f"out.{i}", dd, co)
+            do = dd @ w[f"out.{i}"]
             with torch.enable_grad():
                 leaves = [t.detach().requires_grad_() for t in qkv]
                 dqr, dkr, dv = torch.autograd.grad(self.attention(*leaves), leaves, do)
@@ -174,24 +202,25 @@ class Decoder:
             dqkv = dqkv.view(M, -1)
             self.weight_grad(f"qkv.{i}", dqkv, c1, self.w[f"norm1.{i}"])
             d = self.norm_backward(f"norm1.{i}", dqkv @ w[f"qkv.{i}"], c1, d)
-        self.g["embed"].copy_(torch.zeros(cfg.vocab, cfg.width, device="cuda").index_add_(0, ids, d.float()))
+        # of a tied table: added to what the output layer has left there
+        coat.coat_embedding_backward(d, ids, 1.0, self.g["embed"], self.workspace, accumulate=cfg.tied)
 
     @torch.no_grad()
     def loss_and_gradients(self, ids, targets):
-        logits, kept, last = self.forward(ids)
-        logp = F.log_softmax(logits.float(), -1)
-        loss = F.nll_loss(logp, targets)
+        """The mean loss of the tokens with a target (the others' is negative), and all gradients in self.grad."""
+        loss, lse, y, kept, last = self.forward(ids, targets)
         self.kept_bytes = sum(c.bytes() for block in kept for c in block if isinstance(c, Checkpoint)) + last.bytes()
-        dlogits = logp.exp()
-        dlogits[torch.arange(self.M, device="cuda"), targets] -= 1
-        self.backward(ids, (dlogits / self.M).to(BF), kept, last)
-        return loss
+        dloss = (targets >= 0).float()
+        dloss /= dloss.sum()
+        self.backward(ids, targets, dloss, lse, y, kept, last)
+        return (loss * dloss).sum()
 
     def step(self, ids, targets, lr=1e-3):
         loss = self.loss_and_gradients(ids, targets)
         self.steps += 1
         coat.coat_fp8_adamw_step(self.flat, self.grad, self.m_q, self.v_q, self.meta, 128, 0.9, 0.95, lr, 1e-8, 0.1, self.steps)
         self.flat16.copy_(self.flat)
+        self.rng[:, 1] += len(self.rng)
         return loss
 
 
@@ -211,8 +240,10 @@ def main():
     ap.add_argument("--width", type=int, default=1024)
     ap.add_argument("--tokens", type=int, default=2048)
     ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--dropout", type=float, default=0.0)
+    ap.add_argument("--tied", action="store_true")
     a = ap.parse_args()
-    cfg = Config(layers=a.layers, width=a.width)
+    cfg = Config(layers=a.layers, width=a.width, dropout=a.dropout, tied=a.tied)
     model = Decoder(cfg, a.tokens)
     begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     for i in range(a.steps):
