@@ -56,7 +56,11 @@ constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 
 constexpr int slot_bytes(int bn) { return kABytes + bn / 2 * kBK * 2; }
 constexpr int stages_of(int bn) { return kStageArea / slot_bytes(bn) < kMaxStages ? kStageArea / slot_bytes(bn) : kMaxStages; }
 static_assert(kSmemBytes <= 232448 && stages_of(256) == 6 && stages_of(32) == 10, "shared memory of an SM");
-constexpr int64_t kFewTokens = 64;             // up to so many, the logits are formed with the tokens as columns
+// Up to so many tokens, the logits are formed with the tokens as the only tile's columns, so that the product has no rows
+// without a token (50304 x 2048 forward, 1 / 33 / 100 tokens: 40 / 41 / 43 us, with the tokens as rows 62 / 46 / 46; 200 / 256
+// tokens 46 / 48, as rows 46 / 47).
+constexpr int64_t kFewTokens = 128;
+constexpr int kFewChunks = (int)kFewTokens / 2 / kChunk;   // of an epilogue warp
 
 // What a launch does with a tile's sums.
 // Of few tokens, the logits' rows are those of the weight and their columns the tokens (kFewStats, kFewDz).
@@ -233,41 +237,58 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const 
     if (row < j.rows && n0 < end) w.stats[part * w.stats_ld + row] = make_float2(top, sum2(sums));
 }
 
-// The same of few tokens: a warp has 32 rows of the weight and up to 32 tokens n0 .. end - 1, which it turns over in shared
-// memory, so that a lane has one token; top and sum go on from tile to tile.
-__device__ __forceinline__ void few_stats(const Work& w, const Job& j, int64_t target, uint32_t taddr, uint32_t buf, int64_t row0, int lane,
-                                          int64_t n0, int64_t end, float& top, float& sum) {
-    uint32_t v[kChunk];
-    __syncwarp();
-    tmem_ld<kChunk>(taddr, v);
+// What an epilogue warp keeps of its few tokens from tile to tile: the lane's one of every 32.
+struct FewTokens {
+    RowValues r[kFewChunks];
+    float top[kFewChunks], sum[kFewChunks];
+};
+__device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t n0, int64_t end, int lane, FewTokens& f) {
+#pragma unroll
+    for (int c = 0; c < kFewChunks; ++c) {
+        f.r[c] = row_values(w, j, n0 + kChunk * c + lane, end);
+        f.top[c] = -INFINITY;
+        f.sum[c] = 0.0f;
+    }
+}
+
+// The statistics of few tokens: a warp has 32 rows of the weight and its tokens n0 .. end - 1, 32 of which at a time it turns
+// over in shared memory, so that a lane has one token.
+__device__ __forceinline__ void few_stats(const Work& w, const Job& j, uint32_t taddr, uint32_t buf, int64_t row0, int lane, int64_t n0,
+                                          int64_t end, FewTokens& f) {
     const bool in = row0 + lane < j.rows;
 #pragma unroll
-    for (int e = 0; e < kChunk; ++e)
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(4 * (33 * lane + e))), "r"(in ? v[e] : 0xFF800000u) : "memory");
-    __syncwarp();
-    float mx = top;
+    for (int c = 0; c < kFewChunks; ++c) {
+        if (n0 + kChunk * c >= end) break;   // the same for the whole warp
+        uint32_t v[kChunk];
+        __syncwarp();   // also: the chunk before has been read
+        tmem_ld<kChunk>(taddr + (uint32_t)(kChunk * c), v);
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) {
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[k]) : "r"(buf + (uint32_t)(4 * (33 * k + lane))));
-        mx = fmaxf(mx, __uint_as_float(v[k]));
-    }
-    const int64_t at = target - row0;
-    if (at >= 0 && at < kChunk && target < j.rows && n0 + lane < end) {
-        float z;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=f"(z) : "r"(buf + (uint32_t)(4 * (33 * (int)at + lane))));
-        w.target_logit[n0 + lane] = z;
-    }
-    __syncwarp();   // the next tile's rows may be written
-    const float ref = mx == -INFINITY ? 0.0f : mx, f = ex2_ftz((top - ref) * kLog2e);
-    uint64_t sums = pk(sum * f, 0.0f);
-    top = mx;
+        for (int e = 0; e < kChunk; ++e)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(4 * (33 * lane + e))), "r"(in ? v[e] : 0xFF800000u) : "memory");
+        __syncwarp();
+        float mx = f.top[c];
 #pragma unroll
-    for (int k = 0; k < kChunk; k += 2) {
-        float a, b;
-        exp2_of(v[k], v[k + 1], pk(-ref, -ref), a, b);
-        sums = add2(sums, pk(a, b));
+        for (int k = 0; k < kChunk; ++k) {
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[k]) : "r"(buf + (uint32_t)(4 * (33 * k + lane))));
+            mx = fmaxf(mx, __uint_as_float(v[k]));
+        }
+        const int64_t token = n0 + kChunk * c + lane, at = f.r[c].target - row0;
+        if (at >= 0 && at < kChunk && f.r[c].target < j.rows && token < end) {
+            float z;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=f"(z) : "r"(buf + (uint32_t)(4 * (33 * (int)at + lane))));
+            w.target_logit[token] = z;
+        }
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        uint64_t sums = pk(f.sum[c] * ex2_ftz((f.top[c] - ref) * kLog2e), 0.0f);
+        f.top[c] = mx;
+#pragma unroll
+        for (int k = 0; k < kChunk; k += 2) {
+            float x, y;
+            exp2_of(v[k], v[k + 1], pk(-ref, -ref), x, y);
+            sums = add2(sums, pk(x, y));
+        }
+        f.sum[c] = sum2(sums);
     }
-    sum = sum2(sums);
 }
 
 // ---- stores of bf16 by TMA: 64 columns of a warp's 32 rows through its 4 KB of shared memory, 128-byte swizzle ----
@@ -362,34 +383,41 @@ __device__ __forceinline__ void store_columns(uint16_t* out, int64_t ld, int64_t
     }
 }
 
-// kFewDz: r is that of token n0 + lane.  (A last column without a neighbour takes one of the row's padding with it.)
-__device__ __forceinline__ void few_dz(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, int64_t row0, int lane, int64_t n0,
-                                       int64_t end) {
-    uint32_t v[kChunk];
-    __syncwarp();
-    tmem_ld<kChunk>(taddr, v);
-#pragma unroll
-    for (int e = 0; e < kChunk; e += 2) {
-        const float s0 = __shfl_sync(kFull, r.lse, e), s1 = __shfl_sync(kFull, r.lse, e + 1);
-        const float p0 = __shfl_sync(kFull, r.p, e), p1 = __shfl_sync(kFull, r.p, e + 1);
-        float x, y;
-        exp2_of(v[e], v[e + 1], pk(-s0, -s1), x, y);
-        upk(mul2(pk(x, y), pk(p0, p1)), x, y);
-        v[e] = __float_as_uint(x);
-        v[e + 1] = __float_as_uint(y);
-    }
-    const int64_t at = r.target - w.v0 - row0;
-    if (__any_sync(kFull, at >= 0 && at < 32)) {
-        const int mine = at >= 0 && at < 32 ? (int)at : -1;
-#pragma unroll
-        for (int e = 0; e < kChunk; ++e) {
-            const int t = __shfl_sync(kFull, mine, e);
-            const float g = __shfl_sync(kFull, r.g, e);
-            if (t == lane) v[e] = __float_as_uint(__uint_as_float(v[e]) - g);
-        }
-    }
+// kFewDz.  (A last column without a neighbour takes one of the row's padding with it.)
+__device__ __forceinline__ void few_dz(const Work& w, const Job& j, uint32_t taddr, int64_t row0, int lane, int64_t n0, int64_t end,
+                                       const FewTokens& f) {
     const int64_t row = row0 + lane;
-    store_columns(j.out, j.ld, row, n0, row - (lane & 1) < j.rows ? end - n0 : 0, lane, v);
+    const bool ok = row - (lane & 1) < j.rows;
+#pragma unroll
+    for (int c = 0; c < kFewChunks; ++c) {
+        const int64_t col = n0 + kChunk * c;
+        if (col >= end) break;
+        const RowValues& r = f.r[c];
+        uint32_t v[kChunk];
+        __syncwarp();
+        tmem_ld<kChunk>(taddr + (uint32_t)(kChunk * c), v);
+#pragma unroll
+        for (int e = 0; e < kChunk; e += 2) {
+            const float s0 = __shfl_sync(kFull, r.lse, e), s1 = __shfl_sync(kFull, r.lse, e + 1);
+            const float p0 = __shfl_sync(kFull, r.p, e), p1 = __shfl_sync(kFull, r.p, e + 1);
+            float x, y;
+            exp2_of(v[e], v[e + 1], pk(-s0, -s1), x, y);
+            upk(mul2(pk(x, y), pk(p0, p1)), x, y);
+            v[e] = __float_as_uint(x);
+            v[e + 1] = __float_as_uint(y);
+        }
+        const int64_t at = r.target - w.v0 - row0;
+        if (__any_sync(kFull, at >= 0 && at < 32)) {
+            const int mine = at >= 0 && at < 32 ? (int)at : -1;
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e) {
+                const int t = __shfl_sync(kFull, mine, e);
+                const float g = __shfl_sync(kFull, r.g, e);
+                if (t == lane) v[e] = __float_as_uint(__uint_as_float(v[e]) - g);
+            }
+        }
+        store_columns(j.out, j.ld, row, col, ok ? end - col : 0, lane, v);
+    }
 }
 
 // `left` of 32 sums of a row (a multiple of 16)
@@ -581,7 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         const int q4 = warp & 3, half = (warp - 4) >> 2;
         const uint32_t staging = sb + kStageArea + (uint32_t)((warp - 4) * kStagingBytes);   // of kFewStats
         const uint32_t box = sb + kStageArea + (uint32_t)((warp - 4) * 4096);                // of TMA stores: 1024-byte aligned
-        float top = -INFINITY, sum = 0.0f;   // kFewStats: of the lane's token
+        const bool few = w.job[0].mode == kFewStats || w.job[0].mode == kFewDz;
+        const int64_t few_n0 = half * (w.job[0].bn / 2), few_end = few_n0 + w.job[0].bn / 2 < w.job[0].cols ? few_n0 + w.job[0].bn / 2 : w.job[0].cols;
+        FewTokens tokens;
+        if (few) few_tokens(w, w.job[0], few_n0, few_end, lane, tokens);
         int acc = 0;
         uint32_t aph = 0;
         for (uint32_t i = 0; walk.item(i, w, it); ++i) {
@@ -589,8 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             const Job& j = w.job[it.job];
             const int64_t row0 = it.m * (2 * kBM) + rank * kBM + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
             const int64_t n0 = col0 + half * (j.bn / 2), end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
-            const bool few = j.mode == kFewStats || j.mode == kFewDz;
-            const RowValues r = row_values(w, j, few ? n0 + lane : row, few ? end : j.rows);
+            const RowValues r = row_values(w, j, row, few ? 0 : j.rows);
             if (!__all_sync(kFull, mbar_wait_fast(acc_full(acc), aph, abort))) break;
             tc_fence_after();
             const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN), taddr = acc0 + (uint32_t)(half * (j.bn / 2));
@@ -599,9 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             else if (j.mode == kDz)
                 dz_of_row(w, j, r, acc0, box, &maps.o[it.job], row0, col0, half, lane);
             else if (j.mode == kFewStats)
-                few_stats(w, j, r.target, taddr, staging, row0, lane, n0, end, top, sum);
+                few_stats(w, j, taddr, staging, row0, lane, n0, end, tokens);
             else if (j.mode == kFewDz)
-                few_dz(w, j, r, taddr, row0, lane, n0, end);
+                few_dz(w, j, taddr, row0, lane, n0, end, tokens);
             else if (j.mode == kDx)
                 dx_of_column(j, taddr, row, n0, end, it.part, lane);
             else if (j.sums)
@@ -615,10 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             if (acc == 0) aph ^= 1u;
         }
         if (w.job[0].mode == kFewStats) {
-            const int bn = w.job[0].bn;
-            const int64_t token = half * (bn / 2) + lane;
-            if (lane < bn / 2 && token < w.job[0].cols)
-                w.stats[((2 * pair + rank) * 4 + q4) * w.stats_ld + token] = make_float2(top, sum);
+#pragma unroll
+            for (int c = 0; c < kFewChunks; ++c) {
+                const int64_t token = few_n0 + kChunk * c + lane;
+                if (token < few_end) w.stats[((2 * pair + rank) * 4 + q4) * w.stats_ld + token] = make_float2(tokens.top[c], tokens.sum[c]);
+            }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the stores by TMA are done
         __syncwarp();
@@ -755,7 +786,7 @@ int tile_columns(int64_t rows, int64_t cols, int32_t mode) {
             bn = n;
         }
     }
-    if (mode == kFewStats || mode == kFewDz) bn = cols <= 32 ? 32 : 64;   // all tokens
+    if (mode == kFewStats || mode == kFewDz) bn = (int)up(cols, 32) * 32;   // all tokens
     return bn;
 }
 
