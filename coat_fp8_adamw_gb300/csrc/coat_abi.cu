@@ -220,6 +220,6 @@ const char* coat_status_string(coat_status s) {
 
 double coat_r_e4m3(void) { return 448.0 * 512.0; }
 
-int32_t coat_version(void) { return 200; }
+int32_t coat_version(void) { return 300; }
 
 }  // extern "C"

@@ -288,7 +288,8 @@ coat_status coat_exact_recompute_counts(uint64_t counts[2], int32_t reset);
  * How many bounded waits inside the library's kernels gave up on the current
  * device since the library was loaded there (or since the last reset).  The
  * pipelined kernels (coat_fp8_linear_group_quantize, coat_ckpt_weight_grad,
- * coat_rmsnorm_ckpt_backward) wait on their own
+ * coat_rmsnorm_ckpt_backward, coat_linear_cross_entropy and its backward
+ * pass) wait on their own
  * producers with an iteration limit instead of forever; a non-zero count
  * means a launch returned without finishing its work.  reset != 0 clears the
  * counter after reading it.  Synchronizes with the current device.
@@ -490,8 +491,10 @@ size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t V, int64_t C);
  *   x  M rows of C bf16, x_ld apart (a multiple of 8), in;  weight [V x C] bf16 in;
  *   targets [M] in: a negative one (a token without a target) gives loss 0, one
  *   of V or more NaN;  loss, lse [M] float32 out.
- * Products are added in float32 by the tensor cores; the logits have to be finite
- * or -inf there.  M V at most COAT_MAX_N, here and below.
+ * Products are added in float32 by the tensor cores, which truncate: a logit is
+ * within (C + 8) 2^-22 sum |x W| of the sum, and so are lse and loss of theirs,
+ * with float32's roundings of what they are formed of.  The logits have to be
+ * finite or -inf.  M V at most COAT_MAX_N, here and below.
  */
 coat_status coat_linear_cross_entropy(const uint16_t *x, int64_t x_ld, const uint16_t *weight,
                                       const void *targets, int32_t wide_targets, int64_t M, int64_t V, int64_t C,
