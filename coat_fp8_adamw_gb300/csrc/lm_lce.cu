@@ -334,8 +334,8 @@ __device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, const Row
                 float x, y;
                 exp2_of(v[e], v[e + 1], minus_lse, x, y);
                 upk(mul2(pk(x, y), p2), x, y);
-                v[e] = __float_as_uint(x);
-                v[e + 1] = __float_as_uint(y);
+                v[e] = r.p == 0.0f ? 0u : __float_as_uint(x);   // without a gradient, whatever the logits are
+                v[e + 1] = r.p == 0.0f ? 0u : __float_as_uint(y);
             }
             if (__any_sync(kFull, target >= col && target < col + kChunk)) {
 #pragma unroll
@@ -403,8 +403,8 @@ __device__ __forceinline__ void few_dz(const Work& w, const Job& j, uint32_t tad
             float x, y;
             exp2_of(v[e], v[e + 1], pk(-s0, -s1), x, y);
             upk(mul2(pk(x, y), pk(p0, p1)), x, y);
-            v[e] = __float_as_uint(x);
-            v[e + 1] = __float_as_uint(y);
+            v[e] = p0 == 0.0f ? 0u : __float_as_uint(x);
+            v[e + 1] = p1 == 0.0f ? 0u : __float_as_uint(y);
         }
         const int64_t at = r.target - w.v0 - row0;
         if (__any_sync(kFull, at >= 0 && at < 32)) {

@@ -494,7 +494,7 @@ size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t V, int64_t C);
  * Products are added in float32 by the tensor cores, which truncate: a logit is
  * within (C + 8) 2^-22 sum |x W| of the sum, and so are lse and loss of theirs,
  * with float32's roundings of what they are formed of.  The logits have to be
- * finite or -inf.  M V at most COAT_MAX_N, here and below.
+ * finite or -inf (a token whose logits all are -inf has lse -inf and loss NaN).  M V at most COAT_MAX_N, here and below.
  */
 coat_status coat_linear_cross_entropy(const uint16_t *x, int64_t x_ld, const uint16_t *weight,
                                       const void *targets, int32_t wide_targets, int64_t M, int64_t V, int64_t C,
@@ -509,6 +509,8 @@ size_t coat_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V);
  *   x, weight, targets as above;  lse [M] as the forward pass left it;  dloss [M]
  *   float32 in (of a token without a target it does not count);  dlse [M] float32
  *   in, or NULL: zeros;  dx [M x C], dweight [V x C] bf16 out.
+ * Where dloss[m] + dlse[m] is 0, e^... does not count, whatever the logits are: a
+ * padded token leaves zeros in dx (its row of x is a factor of dweight all the same).
  * The logits are formed again, `piece` rows of the weight at a time (rounded up to
  * a multiple of 256; 0: as few pieces as leave 512 MiB for one's dz).  dz is an
  * operand of the tensor cores, so it is bf16, the type of a layer's gradient; sums

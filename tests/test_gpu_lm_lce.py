@@ -79,7 +79,7 @@ def check_backward(x, w, t, lse, dloss, dlse=None, piece=0):
     return dx, dw
 
 
-SIZES = [(1, 1, 16), (1, 5000, 64), (2, 33, 48), (17, 257, 2048), (33, 1000, 528), (130, 128, 80), (255, 129, 256), (256, 256, 64),
+SIZES = [(97, 700, 64), (128, 129, 1024), (129, 640, 96), (1, 1, 16), (1, 5000, 64), (2, 33, 48), (17, 257, 2048), (33, 1000, 528), (130, 128, 80), (255, 129, 256), (256, 256, 64),
          (257, 513, 144), (300, 4099, 1024), (513, 777, 5120), (1000, 20001, 128), (2048, 512, 1024), (64, 130001, 32)]
 
 
@@ -100,12 +100,12 @@ def test_backward(M, V, C, zloss, piece):
     check_backward(x, w, t, lse, dloss, 1e-3 * randn(M, seed=6) if zloss else None, piece)
 
 
-def test_every_operand_in_whole_numbers():
+@pytest.mark.parametrize("M,V,C", [(700, 1300, 272), (100, 1300, 272), (20, 30000, 64), (5000, 100, 64), (257, 513, 1040)])
+def test_every_operand_in_whole_numbers(M, V, C):
     """dz of 0, +-1 by choice of lse and gradients, whole numbers elsewhere: sums are exact in every order, so an element
-    that is missed, doubled or misplaced in any tile, piece or split shows.
+    that is missed, doubled or misplaced in any tile, piece or part shows.
 
     x = 0: every logit is 0; lse = 0: e^0 = 1 for every column; dloss = 1: dz = 1 - [v = t]."""
-    M, V, C = 700, 1300, 272
     x = torch.zeros(M, C, dtype=BF, device="cuda")
     w = torch.randint(-1, 2, (V, C), generator=gen(1), device="cuda").to(BF)
     t = torch.randint(0, V, (M,), generator=gen(2), device="cuda")
@@ -121,6 +121,28 @@ def test_every_operand_in_whole_numbers():
     for piece in (0, 256, 768):
         dx, dw = backward(x, w, t, lse, dloss, piece=piece)
         assert torch.equal(dw, want) and not dx.any()
+
+
+@pytest.mark.parametrize("M", [100, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
+def test_what_a_padded_token_holds_does_not_count(M, bad):
+    """Rows without a target and without gradients, whose logits are NaN or infinite: loss 0, zeros in dx, and every other row
+    as it is without them."""
+    V, C = 400, 64
+    x, w, t = inputs(M, V, C, 1)
+    rest = t >= 0
+    loss, lse = forward(x, w, t)
+    padded = x.clone()
+    padded[~rest] = bad
+    loss2, lse2 = forward(padded, w, t)
+    assert not loss2[~rest].any() and torch.equal(loss2, loss) and torch.equal(lse2[rest], lse[rest])
+    dloss = torch.full((M,), 1 / M, device="cuda")
+    dx, _ = backward(x, w, t, lse, dloss)
+    dx2, _ = backward(padded, w, t, lse2, dloss)
+    assert torch.equal(dx2, dx) and not dx2[~rest].any()
+    weights = torch.where(torch.arange(M, device="cuda") % 3 == 0, 0.0, dloss)      # tokens with a target and no weight
+    dx3, _ = backward(x, w, t, lse, weights)
+    assert not dx3[::3].any()
 
 
 def test_logits_of_one_hot_rows_are_the_weights():
