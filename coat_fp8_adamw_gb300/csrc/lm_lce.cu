@@ -43,6 +43,14 @@ constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kChunk = 32;                     // columns that an epilogue thread holds at once
 constexpr int64_t kPairs = 76;                  // that the division of the work goes by, on every device
 constexpr float kLog2e = 1.4426950408889634f;
+// The tensor cores truncate when they add to an accumulator, so that a sum falls short by up to 2^-24 of its size at every
+// addition.  Logits are therefore added up by them over 512 of the summed index at a time, and the epilogue adds those sums
+// in its registers, with float32's rounding (lse of C = 4096: 4.6e-6 off without, XX so; the plain float32 form 8.5e-7).
+constexpr int kSegment = 8;                    // steps
+// Registers: the epilogue warps hold their logits, 128 a thread, and take what the other four warps give up.  Every one of
+// 384 threads is launched with kLaunchRegs.
+constexpr int kLaunchRegs = 168, kOtherRegs = 72, kEpiRegs = 216;
+static_assert(128 * kOtherRegs + 256 * kEpiRegs <= 384 * kLaunchRegs, "setmaxnreg.inc would wait for ever");
 
 constexpr int kBN = 256;                       // most columns of a tile
 // Shared memory: the ring of stages (A's 16 KB and B's columns each, as many as fit), then 4 KB for every epilogue warp
@@ -65,12 +73,16 @@ constexpr int kFewChunks = (int)kFewTokens / 2 / kChunk;   // of an epilogue war
 // What a launch does with a tile's sums.
 // Of few tokens, the logits' rows are those of the weight and their columns the tokens (kFewStats, kFewDz).
 enum Mode : int32_t { kStats, kDz, kFewStats, kFewDz, kDx, kDw };
+// The kernels: by what their epilogue warps hold.
+enum Kind { kLogits, kFewLogits, kProducts };
+constexpr Kind kind_of(int32_t mode) { return mode <= kDz ? kLogits : mode <= kFewDz ? kFewLogits : kProducts; }
 
 // A product: its tiles, each summed in `parts` parts of the summed index.
 struct Job {
     int32_t mode;
     int32_t a_mn;            // A is MN-major
     int32_t steps;           // 64 of the summed index each
+    int32_t segment;         // steps that the tensor cores add up by themselves
     int32_t bn;              // columns of a tile: a multiple of 32
     int32_t parts;
     int64_t tm, tn;          // tiles
@@ -95,7 +107,7 @@ struct Work {
     const float* lse;
     const float* dloss;
     const float* dlse;
-    float2* stats;           // [half tile's columns, or, of few tokens, epilogue warp][token], tokens padded
+    float2* stats;           // [half of a tile's columns, or, of few tokens, epilogue warp][token], tokens padded
     int64_t stats_ld;
     float* target_logit;
 };
@@ -174,13 +186,14 @@ struct Walk {
 // thread; where a chunk of 32 goes past them, it reads columns of the other half, which do not count ----
 // What is needed of a token (a lane's row of the logits, or its column of 32), loaded while the tile's MMAs still run.
 struct RowValues {
-    int64_t target;
+    int32_t target;          // -1: none; V: past the vocabulary
     float lse, g, p;         // dz = p e^(z - lse) - [v = target] g
 };
 __device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int64_t token, int64_t tokens) {
     RowValues r{-1, 0.0f, 0.0f, 0.0f};
     if (j.mode > kFewDz || token >= tokens) return r;
-    r.target = index_at(w.targets, w.wide, token);
+    const int64_t t = index_at(w.targets, w.wide, token);
+    r.target = t < 0 ? -1 : t < w.V ? (int32_t)t : w.V;
     if (j.mode == kStats || j.mode == kFewStats) return r;
     const float g = static_cast<const volatile float*>(w.dloss)[token], h = w.dlse ? static_cast<const volatile float*>(w.dlse)[token] : 0.0f;
     r.lse = static_cast<const volatile float*>(w.lse)[token];
@@ -197,28 +210,66 @@ __device__ __forceinline__ void exp2_of(uint32_t z0, uint32_t z1, uint64_t minus
     b = ex2_ftz(b);
 }
 
-__device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, int64_t row, int64_t n0,
-                                             int64_t end, int64_t part) {
+// The logits that an epilogue thread holds: four times 32 columns of its row, or, of few tokens, of which there are two times
+// 32, a row of the weight's.  Columns 32 c .. + 31 begin at column off(c) of the tile: every second 64 columns, so that a
+// store by TMA has 64 neighbours.
+constexpr int kChunks = 4;
+template <int kN>
+struct Logits {
+    uint32_t z[kN][kChunk];
+};
+__device__ __forceinline__ int chunk_off(int half, int c) { return 64 * half + 128 * (c >> 1) + kChunk * (c & 1); }
+// one segment's sums of them; the chunks that have columns below `cols` of the tile, the same for the whole warp
+template <bool kFirst, int kN>
+__device__ __forceinline__ void add_segment(uint32_t acc0, int half, int bn, int cols, Logits<kN>& l) {
+#pragma unroll
+    for (int c = 0; c < kN; ++c) {
+        const int off = kN == kFewChunks ? half * (bn / 2) + kChunk * c : chunk_off(half, c);
+        if (off >= cols) continue;
+        __syncwarp();   // tcgen05.ld is warp-collective
+        if constexpr (kFirst) {
+            tmem_ld<kChunk>(acc0 + (uint32_t)off, l.z[c]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < kChunk; h += 16) {
+                uint32_t v[16];
+                tmem_ld<16>(acc0 + (uint32_t)(off + h), v);
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    float x, y;
+                    upk(add2(pk(__uint_as_float(l.z[c][h + e]), __uint_as_float(l.z[c][h + e + 1])),
+                             pk(__uint_as_float(v[e]), __uint_as_float(v[e + 1]))), x, y);
+                    l.z[c][h + e] = __float_as_uint(x);
+                    l.z[c][h + e + 1] = __float_as_uint(y);
+                }
+            }
+        }
+    }
+}
+
+// columns col0 .. end - 1 of the tile are logits
+__device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const RowValues& r, Logits<kChunks>& l, int64_t row, int64_t col0, int64_t end,
+                                             int half, int64_t part) {
     float top = -INFINITY;
     uint64_t sums = pk(0.0f, 0.0f);
-    const int64_t target = r.target;
-#pragma unroll 1
-    for (int64_t col = n0; col < end; col += kChunk) {   // the same for the whole warp
-        uint32_t v[kChunk];
-        __syncwarp();   // tcgen05.ld is warp-collective
-        tmem_ld<kChunk>(taddr + (uint32_t)(col - n0), v);
-        if (col + kChunk > end) {
+    const int cols = (int)(end - col0), target = r.target - (int)col0;   // in the tile
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int off = chunk_off(half, c);
+        if (off >= cols) continue;
+        uint32_t (&v)[kChunk] = l.z[c];
+        if (off + kChunk > cols) {
 #pragma unroll
             for (int e = 0; e < kChunk; ++e)
-                if (col + e >= end) v[e] = 0xFF800000u;   // -inf: not a column
+                if (off + e >= cols) v[e] = 0xFF800000u;   // -inf: not a column
         }
-        const bool has = target >= col && target < col + kChunk;
+        const bool has = target >= off && target < off + kChunk;
         if (__any_sync(kFull, has)) {
             float z = 0.0f;
 #pragma unroll
             for (int e = 0; e < kChunk; ++e)
-                if (col + e == target) z = __uint_as_float(v[e]);
-            if (has && target < end) w.target_logit[row] = z;
+                if (off + e == target) z = __uint_as_float(v[e]);
+            if (has && target < cols && row < j.rows) w.target_logit[row] = z;
         }
         float mx = top;
 #pragma unroll
@@ -229,12 +280,12 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const 
         sums = mul2(sums, pk(f, f));
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) {
-            float a, b;
-            exp2_of(v[e], v[e + 1], pk(-ref, -ref), a, b);
-            sums = add2(sums, pk(a, b));
+            float x, y;
+            exp2_of(v[e], v[e + 1], pk(-ref, -ref), x, y);
+            sums = add2(sums, pk(x, y));
         }
     }
-    if (row < j.rows && n0 < end) w.stats[part * w.stats_ld + row] = make_float2(top, sum2(sums));
+    if (row < j.rows) w.stats[part * w.stats_ld + row] = make_float2(top, sum2(sums));   // of no columns: -inf and 0
 }
 
 // What an epilogue warp keeps of its few tokens from tile to tile: the lane's one of every 32.
@@ -253,29 +304,29 @@ __device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t 
 
 // The statistics of few tokens: a warp has 32 rows of the weight and its tokens n0 .. end - 1, 32 of which at a time it turns
 // over in shared memory, so that a lane has one token.
-__device__ __forceinline__ void few_stats(const Work& w, const Job& j, uint32_t taddr, uint32_t buf, int64_t row0, int lane, int64_t n0,
+__device__ __forceinline__ void few_stats(const Work& w, const Job& j, const Logits<kFewChunks>& l, uint32_t buf, int64_t row0, int lane, int64_t n0,
                                           int64_t end, FewTokens& f) {
     const bool in = row0 + lane < j.rows;
 #pragma unroll
     for (int c = 0; c < kFewChunks; ++c) {
         if (n0 + kChunk * c >= end) break;   // the same for the whole warp
-        uint32_t v[kChunk];
-        __syncwarp();   // also: the chunk before has been read
-        tmem_ld<kChunk>(taddr + (uint32_t)(kChunk * c), v);
+        __syncwarp();   // the chunk before has been read
 #pragma unroll
         for (int e = 0; e < kChunk; ++e)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(4 * (33 * lane + e))), "r"(in ? v[e] : 0xFF800000u) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + (uint32_t)(4 * (33 * lane + e))), "r"(in ? l.z[c][e] : 0xFF800000u) : "memory");
         __syncwarp();
+        uint32_t v[kChunk];
         float mx = f.top[c];
 #pragma unroll
         for (int k = 0; k < kChunk; ++k) {
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[k]) : "r"(buf + (uint32_t)(4 * (33 * k + lane))));
             mx = fmaxf(mx, __uint_as_float(v[k]));
         }
-        const int64_t token = n0 + kChunk * c + lane, at = f.r[c].target - row0;
+        const int64_t token = n0 + kChunk * c + lane;
+        const int at = f.r[c].target - (int)row0;
         if (at >= 0 && at < kChunk && f.r[c].target < j.rows && token < end) {
             float z;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=f"(z) : "r"(buf + (uint32_t)(4 * (33 * (int)at + lane))));
+            asm volatile("ld.shared.b32 %0, [%1];" : "=f"(z) : "r"(buf + (uint32_t)(4 * (33 * at + lane))));
             w.target_logit[token] = z;
         }
         const float ref = mx == -INFINITY ? 0.0f : mx;
@@ -316,38 +367,35 @@ __device__ __forceinline__ void store_staged(const CUtensorMap* map, uint32_t bu
     }
 }
 
-// kDz: boxes of 64 columns, every second one from `half` on
-__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, const RowValues& r, uint32_t taddr, uint32_t buf, const CUtensorMap* map,
+// kDz: boxes of 64 columns
+__device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, const RowValues& r, Logits<kChunks>& l, uint32_t buf, const CUtensorMap* map,
                                           int64_t row0, int64_t col0, int half, int lane) {
     const uint64_t minus_lse = pk(-r.lse, -r.lse), p2 = pk(r.p, r.p);
-    const int64_t target = r.target - w.v0;
-#pragma unroll 1
-    for (int b = 64 * half; b < j.bn && col0 + b < j.cols; b += 128) {
-        staging_free(lane);
+    const int target = r.target - (int)w.v0 - (int)col0;         // in the tile
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t col = col0 + b + 32 * h;
-            uint32_t v[kChunk], o[kChunk / 2];
-            tmem_ld<kChunk>(taddr + (uint32_t)(b + 32 * h), v);
+    for (int c = 0; c < kChunks; ++c) {
+        const int off = chunk_off(half, c & ~1), at = chunk_off(half, c);   // of the box, and of its columns
+        if (off >= j.bn || col0 + off >= j.cols) continue;      // the same for the whole warp
+        if ((c & 1) == 0) staging_free(lane);
+        uint32_t (&v)[kChunk] = l.z[c];
+        uint32_t o[kChunk / 2];
 #pragma unroll
-            for (int e = 0; e < kChunk; e += 2) {
-                float x, y;
-                exp2_of(v[e], v[e + 1], minus_lse, x, y);
-                upk(mul2(pk(x, y), p2), x, y);
-                v[e] = r.p == 0.0f ? 0u : __float_as_uint(x);   // without a gradient, whatever the logits are
-                v[e + 1] = r.p == 0.0f ? 0u : __float_as_uint(y);
-            }
-            if (__any_sync(kFull, target >= col && target < col + kChunk)) {
-#pragma unroll
-                for (int e = 0; e < kChunk; ++e)
-                    if (col + e == target) v[e] = __float_as_uint(__uint_as_float(v[e]) - r.g);
-            }
-#pragma unroll
-            for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-            __syncwarp();
-            stage_row(buf, lane, h, o);
+        for (int e = 0; e < kChunk; e += 2) {
+            float x, y;
+            exp2_of(v[e], v[e + 1], minus_lse, x, y);
+            upk(mul2(pk(x, y), p2), x, y);
+            v[e] = r.p == 0.0f ? 0u : __float_as_uint(x);   // without a gradient, whatever the logits are
+            v[e + 1] = r.p == 0.0f ? 0u : __float_as_uint(y);
         }
-        store_staged(map, buf, col0 + b, row0, j.rows, lane);
+        if (__any_sync(kFull, target >= at && target < at + kChunk)) {
+#pragma unroll
+            for (int e = 0; e < kChunk; ++e)
+                if (at + e == target) v[e] = __float_as_uint(__uint_as_float(v[e]) - r.g);
+        }
+#pragma unroll
+        for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+        stage_row(buf, lane, c & 1, o);
+        if ((c & 1) == 1) store_staged(map, buf, col0 + off, row0, j.rows, lane);
     }
 }
 
@@ -384,7 +432,7 @@ __device__ __forceinline__ void store_columns(uint16_t* out, int64_t ld, int64_t
 }
 
 // kFewDz.  (A last column without a neighbour takes one of the row's padding with it.)
-__device__ __forceinline__ void few_dz(const Work& w, const Job& j, uint32_t taddr, int64_t row0, int lane, int64_t n0, int64_t end,
+__device__ __forceinline__ void few_dz(const Work& w, const Job& j, Logits<kFewChunks>& l, int64_t row0, int lane, int64_t n0, int64_t end,
                                        const FewTokens& f) {
     const int64_t row = row0 + lane;
     const bool ok = row - (lane & 1) < j.rows;
@@ -393,9 +441,8 @@ __device__ __forceinline__ void few_dz(const Work& w, const Job& j, uint32_t tad
         const int64_t col = n0 + kChunk * c;
         if (col >= end) break;
         const RowValues& r = f.r[c];
-        uint32_t v[kChunk];
+        uint32_t (&v)[kChunk] = l.z[c];
         __syncwarp();
-        tmem_ld<kChunk>(taddr + (uint32_t)(kChunk * c), v);
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) {
             const float s0 = __shfl_sync(kFull, r.lse, e), s1 = __shfl_sync(kFull, r.lse, e + 1);
@@ -406,9 +453,9 @@ __device__ __forceinline__ void few_dz(const Work& w, const Job& j, uint32_t tad
             v[e] = p0 == 0.0f ? 0u : __float_as_uint(x);
             v[e + 1] = p1 == 0.0f ? 0u : __float_as_uint(y);
         }
-        const int64_t at = r.target - w.v0 - row0;
+        const int at = r.target - (int)w.v0 - (int)row0;
         if (__any_sync(kFull, at >= 0 && at < 32)) {
-            const int mine = at >= 0 && at < 32 ? (int)at : -1;
+            const int mine = at >= 0 && at < 32 ? at : -1;
 #pragma unroll
             for (int e = 0; e < kChunk; ++e) {
                 const int t = __shfl_sync(kFull, mine, e);
@@ -475,6 +522,7 @@ struct Maps {
     CUtensorMap a[2], b[2], o[2];
 };
 
+template <Kind kKind>
 __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Work w) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -522,6 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     // The producer's and the issuer's warps walk together and one elected lane issues, so that addresses and descriptors stay
     // in uniform registers, and ask for the next stage's barrier before they issue for this one: a single thread that waits,
     // issues and turns takes 550 clocks a step, more than the 512 of a 256 x 256 tile's MMAs.
+    if constexpr (kKind == kLogits) {
+        if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    }
     if (warp == 0) {
         // ---- TMA producer (both CTAs): this CTA's 128 rows of A and half of the columns of B ----
         int s = 0;
@@ -570,81 +621,104 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             const uint32_t elected = elect_one();
             const uint64_t bdesc0 = smem_desc(sb + kABytes, false);
             for (uint32_t i = 0; ok && walk.item(i, w, it); ++i) {
-                if (it.from == it.to) continue;
                 const Job& j = w.job[it.job];
                 const uint32_t idesc = instr_desc(j);
                 const uint64_t adesc0 = smem_desc(sb, j.a_mn);
                 // 16 of the summed index: 32 bytes along a row, or 16 rows of 128 bytes
                 const uint64_t ka = j.a_mn ? (kMmaK * 128) >> 4 : (kMmaK * 2) >> 4;
-                ok = __all_sync(kFull, mbar_wait_relaxed(acc_empty(acc), aph ^ 1u, abort));   // see mbar_arrive_relaxed
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(acc * kBN), af = acc_full(acc);
-                for (int k = it.from; k < it.to; ++k) {
-                    if (!ready) ok = __all_sync(kFull, mbar_wait_fast(full(s), ph, abort));
+                for (int from = it.from; ok && from < it.to; from += j.segment) {
+                    const int to = it.to - from < j.segment ? it.to : from + j.segment;
+                    ok = __all_sync(kFull, mbar_wait_relaxed(acc_empty(acc), aph ^ 1u, abort));   // see mbar_arrive_relaxed
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t so = (uint64_t)(s * (slot >> 4)), ad = adesc0 + so, bd = bdesc0 + so;
-                    const uint32_t freed = empty(s);
-                    if (++s == stages) { s = 0; ph ^= 1u; }
-                    const bool next = mbar_test(full(s), ph);
-                    if (elected) {
+                    const uint32_t d = tmem + (uint32_t)(acc * kBN), af = acc_full(acc);
+                    for (int k = from; k < to; ++k) {
+                        if (!ready) ok = __all_sync(kFull, mbar_wait_fast(full(s), ph, abort));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t so = (uint64_t)(s * (slot >> 4)), ad = adesc0 + so, bd = bdesc0 + so;
+                        const uint32_t freed = empty(s);
+                        if (++s == stages) { s = 0; ph ^= 1u; }
+                        const bool next = mbar_test(full(s), ph);
+                        if (elected) {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / kMmaK; ++kk)
-                            mma_bf16_pair(d, ad + kk * ka, bd + (uint64_t)(kk * ((kMmaK * 2) >> 4)), idesc, k != it.from || kk != 0);
-                        mma_commit_pair(freed, 0x3);   // both CTAs' stage is free once read
-                        if (k + 1 == it.to) mma_commit_pair(af, 0x3);
+                            for (int kk = 0; kk < kBK / kMmaK; ++kk)
+                                mma_bf16_pair(d, ad + kk * ka, bd + (uint64_t)(kk * ((kMmaK * 2) >> 4)), idesc, k != from || kk != 0);
+                            mma_commit_pair(freed, 0x3);   // both CTAs' stage is free once read
+                            if (k + 1 == to) mma_commit_pair(af, 0x3);
+                        }
+                        ready = __all_sync(kFull, next);
                     }
-                    ready = __all_sync(kFull, next);
+                    acc ^= 1;
+                    if (acc == 0) aph ^= 1u;
                 }
-                acc ^= 1;
-                if (acc == 0) aph ^= 1u;
             }
             if (elected) mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
         }
         if (lane == 0) mbar_wait(done, 0u, nullptr);
         __syncwarp();
     } else if (warp >= 4) {
+        if constexpr (kKind == kLogits) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31, half (w - 4) / 4 of the columns ----
         const int q4 = warp & 3, half = (warp - 4) >> 2;
         const uint32_t staging = sb + kStageArea + (uint32_t)((warp - 4) * kStagingBytes);   // of kFewStats
         const uint32_t box = sb + kStageArea + (uint32_t)((warp - 4) * 4096);                // of TMA stores: 1024-byte aligned
-        const bool few = w.job[0].mode == kFewStats || w.job[0].mode == kFewDz;
         const int64_t few_n0 = half * (w.job[0].bn / 2), few_end = few_n0 + w.job[0].bn / 2 < w.job[0].cols ? few_n0 + w.job[0].bn / 2 : w.job[0].cols;
         FewTokens tokens;
-        if (few) few_tokens(w, w.job[0], few_n0, few_end, lane, tokens);
+        if constexpr (kKind == kFewLogits) few_tokens(w, w.job[0], few_n0, few_end, lane, tokens);
         int acc = 0;
         uint32_t aph = 0;
-        for (uint32_t i = 0; walk.item(i, w, it); ++i) {
-            if (it.from == it.to) continue;
-            const Job& j = w.job[it.job];
-            const int64_t row0 = it.m * (2 * kBM) + rank * kBM + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
-            const int64_t n0 = col0 + half * (j.bn / 2), end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
-            const RowValues r = row_values(w, j, row, few ? 0 : j.rows);
-            if (!__all_sync(kFull, mbar_wait_fast(acc_full(acc), aph, abort))) break;
-            tc_fence_after();
-            const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN), taddr = acc0 + (uint32_t)(half * (j.bn / 2));
-            if (j.mode == kStats)
-                stats_of_row(w, j, r, taddr, row, n0, end, 2 * it.n + half);
-            else if (j.mode == kDz)
-                dz_of_row(w, j, r, acc0, box, &maps.o[it.job], row0, col0, half, lane);
-            else if (j.mode == kFewStats)
-                few_stats(w, j, taddr, staging, row0, lane, n0, end, tokens);
-            else if (j.mode == kFewDz)
-                few_dz(w, j, taddr, row0, lane, n0, end, tokens);
-            else if (j.mode == kDx)
-                dx_of_column(j, taddr, row, n0, end, it.part, lane);
-            else if (j.sums)
-                dw_sums_of_row(j, taddr, row, n0, end, it.part);
-            else
-                dw_of_row(j, acc0, box, &maps.o[it.job], row0, col0, half, lane);
+        auto release = [&] {   // the accumulator has been read
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(map_to_rank(acc_empty(acc), 0));
             acc ^= 1;
             if (acc == 0) aph ^= 1u;
+        };
+        for (uint32_t i = 0; walk.item(i, w, it); ++i) {
+            if (it.from == it.to) continue;
+            const Job& j = w.job[it.job];
+            const int64_t row0 = it.m * (2 * kBM) + rank * kBM + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
+            if constexpr (kKind != kProducts) {
+                constexpr bool few = kKind == kFewLogits;
+                const RowValues r = row_values(w, j, row, few ? 0 : j.rows);
+                const int64_t end = col0 + j.bn < j.cols ? col0 + j.bn : j.cols;
+                Logits<few ? kFewChunks : kChunks> l;
+                bool ok = true;
+                for (int from = it.from; from < it.to; from += j.segment) {
+                    ok = __all_sync(kFull, mbar_wait_inline(acc_full(acc), aph, abort));   // the sums so far stay in registers
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN);
+                    if (from == it.from)
+                        add_segment<true>(acc0, half, j.bn, (int)(end - col0), l);
+                    else
+                        add_segment<false>(acc0, half, j.bn, (int)(end - col0), l);
+                    release();
+                }
+                if (!ok) break;
+                if constexpr (few) {
+                    if (j.mode == kFewStats) few_stats(w, j, l, staging, row0, lane, few_n0, few_end, tokens);
+                    else few_dz(w, j, l, row0, lane, few_n0, few_end, tokens);
+                } else {
+                    if (j.mode == kStats) stats_of_row(w, j, r, l, row, col0, end, half, 2 * it.n + half);
+                    else dz_of_row(w, j, r, l, box, &maps.o[it.job], row0, col0, half, lane);
+                }
+            } else {
+                if (!__all_sync(kFull, mbar_wait_fast(acc_full(acc), aph, abort))) break;
+                tc_fence_after();
+                const int64_t n0 = col0 + half * (j.bn / 2), end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
+                const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN), taddr = acc0 + (uint32_t)(half * (j.bn / 2));
+                if (j.mode == kDx)
+                    dx_of_column(j, taddr, row, n0, end, it.part, lane);
+                else if (j.sums)
+                    dw_sums_of_row(j, taddr, row, n0, end, it.part);
+                else
+                    dw_of_row(j, acc0, box, &maps.o[it.job], row0, col0, half, lane);
+                release();
+            }
         }
-        if (w.job[0].mode == kFewStats) {
+        if (kKind == kFewLogits && w.job[0].mode == kFewStats) {
 #pragma unroll
             for (int c = 0; c < kFewChunks; ++c) {
                 const int64_t token = few_n0 + kChunk * c + lane;
@@ -819,6 +893,7 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     j.rows = a.mn ? a.cols : a.rows;
     j.cols = b.rows;
     j.steps = (int32_t)up(K, kBK);
+    j.segment = mode <= kFewDz ? kSegment : j.steps;
     j.bn = tile_columns(j.rows, j.cols, mode);
     j.parts = 1;
     j.tm = up(j.rows, 2 * kBM);
@@ -876,7 +951,16 @@ cudaError_t launch_work(Work& w, const Maps& maps, cudaStream_t s) {
     for (int i = 0; i < w.jobs; ++i) bn = w.job[i].bn > bn ? w.job[i].bn : bn;
     w.slot = slot_bytes(bn);
     w.stages = stages_of(bn);
-    cudaError_t e = cudaFuncSetAttribute(lce_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    const Kind kind = kind_of(w.job[0].mode);
+    auto* const kernel = kind == kLogits ? lce_kernel<kLogits> : kind == kFewLogits ? lce_kernel<kFewLogits> : lce_kernel<kProducts>;
+    cudaError_t e = cudaSuccess;
+    if (kind == kLogits) {
+        // with fewer registers than the roles divide among them setmaxnreg would wait for ever: such a build is not launched
+        cudaFuncAttributes built;
+        if ((e = cudaFuncGetAttributes(&built, kernel)) != cudaSuccess) return e;
+        if (built.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -892,7 +976,7 @@ cudaError_t launch_work(Work& w, const Maps& maps, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(2u * (unsigned)w.pairs);
-    return cudaLaunchKernelEx(&cfg, lce_kernel, maps, (const Work&)w);
+    return cudaLaunchKernelEx(&cfg, kernel, maps, (const Work&)w);
 }
 
 // The two products behind a piece of n columns: their parts, and which has the longer items.  Few tiles with many steps leave
@@ -947,8 +1031,7 @@ cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s) {
     w.target_logit = a.loss;
     cudaError_t e = launch_work(w, maps, s);
     if (e != cudaSuccess) return e;
-    // the epilogue warps; or halves of tiles, the last one's second half only where it has columns
-    const int64_t parts = few ? 8 * (int64_t)w.pairs : up(a.V, w.job[0].bn / 2);
+    const int64_t parts = few ? 8 * (int64_t)w.pairs : 2 * w.job[0].tn;   // the epilogue warps, or two of each tile
     return launch_next(lce_join_kernel, (unsigned)up(a.M, 32), 32 * kJoinWarps, 0, s, (const float2*)w.stats, w.stats_ld,
                        parts, a.targets, a.wide, a.M, a.V, a.loss, a.lse);
 }
@@ -1025,7 +1108,7 @@ int64_t lce_sums(int64_t M, int64_t V, int64_t C, int64_t piece) {
     return lce_dx_sums(M, V, C, piece) + (p.dw > 1 ? p.dw * piece * C : 0);
 }
 size_t lce_stats_bytes(int64_t M, int64_t V) {
-    const int64_t parts = M <= kFewTokens ? 8 * kPairs : up(V, tile_columns(M, V, kStats) / 2);
+    const int64_t parts = M <= kFewTokens ? 8 * kPairs : 2 * up(V, tile_columns(M, V, kStats));
     return 8 * (size_t)(up(M, 32) * 32) * (size_t)parts;
 }
 
