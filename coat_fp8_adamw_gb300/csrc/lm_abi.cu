@@ -93,7 +93,7 @@ coat_status coat_linear_cross_entropy(const uint16_t* x, int64_t x_ld, const uin
 size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t C, int64_t piece) {
     if (!lce_ok(M, V, C, C) || piece < 0) return 0;
     const int64_t p = coat::lce_piece(M, V, piece);
-    return dz_bytes(M, V, p) + xt_bytes(M, C) + 4 * (size_t)coat::lce_sums(M, V, C, p);
+    return dz_bytes(M, V, p) + xt_bytes(M, C) + 16 + 4 * (size_t)coat::lce_sums(M, V, C, p);
 }
 
 coat_status coat_linear_cross_entropy_backward(const uint16_t* x, int64_t x_ld, const uint16_t* weight, const void* targets,
@@ -113,7 +113,7 @@ coat_status coat_linear_cross_entropy_backward(const uint16_t* x, int64_t x_ld, 
     char* xt = static_cast<char*>(workspace) + dz_bytes(M, V, p);
     const coat::LceBwdArgs a{x, x_ld, weight, targets, wide_targets, lse, dloss, dlse, M, V, C, p, dx, dweight,
                              static_cast<uint16_t*>(workspace), reinterpret_cast<uint16_t*>(xt),
-                             reinterpret_cast<float*>(xt + xt_bytes(M, C))};
+                             reinterpret_cast<float*>(xt + xt_bytes(M, C)), reinterpret_cast<float*>(xt + xt_bytes(M, C) + 16)};
     return from_cuda(coat::launch_lce_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -72,6 +72,7 @@ struct LceBwdArgs {
     uint16_t* dweight;         // V x C bf16
     uint16_t* dz;              // M x lce_piece_ld(piece, V) bf16
     uint16_t* xt;              // C x lce_xt_ld(M) bf16: x transposed
+    float* unit;               // 4 floats
     float* sums;               // lce_sums(...): of products in several parts or pieces
 };
 constexpr int64_t kLceDzBytes = 512 << 20;   // of a piece's gradient of the logits, unless the caller says how wide a piece is

@@ -45,7 +45,7 @@ constexpr int64_t kPairs = 76;                  // that the division of the work
 constexpr float kLog2e = 1.4426950408889634f;
 // The tensor cores truncate when they add to an accumulator, so that a sum falls short by up to 2^-24 of its size at every
 // addition.  Logits are therefore added up by them over 512 of the summed index at a time, and the epilogue adds those sums
-// in its registers, with float32's rounding (lse of C = 4096: 4.6e-6 off without, XX so; the plain float32 form 8.5e-7).
+// in its registers, with float32's rounding (lse of C = 4096: 4.6e-6 off in one go, 5.2e-7 so; the plain float32 form 8.6e-7).
 constexpr int kSegment = 8;                    // steps
 // Registers: the epilogue warps hold their logits, 128 a thread, and take what the other four warps give up.  Every one of
 // 384 threads is launched with kLaunchRegs.
@@ -107,6 +107,7 @@ struct Work {
     const float* lse;
     const float* dloss;
     const float* dlse;
+    const float* unit;       // backward: what dz is stored times, and its reciprocal (see unit_of)
     float2* stats;           // [half of a tile's columns, or, of few tokens, epilogue warp][token], tokens padded
     int64_t stats_ld;
     float* target_logit;
@@ -189,7 +190,7 @@ struct RowValues {
     int32_t target;          // -1: none; V: past the vocabulary
     float lse, g, p;         // dz = p e^(z - lse) - [v = target] g
 };
-__device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int64_t token, int64_t tokens) {
+__device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int64_t token, int64_t tokens, float unit) {
     RowValues r{-1, 0.0f, 0.0f, 0.0f};
     if (j.mode > kFewDz || token >= tokens) return r;
     const int64_t t = index_at(w.targets, w.wide, token);
@@ -198,7 +199,8 @@ __device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int
     const float g = static_cast<const volatile float*>(w.dloss)[token], h = w.dlse ? static_cast<const volatile float*>(w.dlse)[token] : 0.0f;
     r.lse = static_cast<const volatile float*>(w.lse)[token];
     r.g = r.target < 0 ? 0.0f : r.target < w.V ? g : NAN;
-    r.p = r.g + h;
+    r.p = (r.g + h) * unit;
+    r.g *= unit;
     return r;
 }
 
@@ -293,10 +295,10 @@ struct FewTokens {
     RowValues r[kFewChunks];
     float top[kFewChunks], sum[kFewChunks];
 };
-__device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t n0, int64_t end, int lane, FewTokens& f) {
+__device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t n0, int64_t end, int lane, float unit, FewTokens& f) {
 #pragma unroll
     for (int c = 0; c < kFewChunks; ++c) {
-        f.r[c] = row_values(w, j, n0 + kChunk * c + lane, end);
+        f.r[c] = row_values(w, j, n0 + kChunk * c + lane, end, unit);
         f.top[c] = -INFINITY;
         f.sum[c] = 0.0f;
     }
@@ -401,7 +403,7 @@ __device__ __forceinline__ void dz_of_row(const Work& w, const Job& j, const Row
 
 // kDw in one part: likewise
 __device__ __forceinline__ void dw_of_row(const Job& j, uint32_t taddr, uint32_t buf, const CUtensorMap* map, int64_t row0, int64_t col0,
-                                          int half, int lane) {
+                                          int half, int lane, float unit) {
 #pragma unroll 1
     for (int b = 64 * half; b < j.bn && col0 + b < j.cols; b += 128) {
         staging_free(lane);
@@ -410,7 +412,7 @@ __device__ __forceinline__ void dw_of_row(const Job& j, uint32_t taddr, uint32_t
             uint32_t v[kChunk], o[kChunk / 2];
             tmem_ld<kChunk>(taddr + (uint32_t)(b + 32 * h), v);
 #pragma unroll
-            for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+            for (int e = 0; e < kChunk; e += 2) o[e / 2] = bf16x2(__uint_as_float(v[e]) * unit, __uint_as_float(v[e + 1]) * unit);
             stage_row(buf, lane, h, o);
         }
         store_staged(map, buf, col0 + b, row0, j.rows, lane);
@@ -503,7 +505,8 @@ __device__ __forceinline__ void dw_sums_of_row(const Job& j, uint32_t taddr, int
 }
 
 // kDx: the product's rows are the columns of dx, its columns the tokens, so the lanes of a warp have neighbours of one token
-__device__ __forceinline__ void dx_of_column(const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int part, int lane) {
+__device__ __forceinline__ void dx_of_column(const Job& j, uint32_t taddr, int64_t row, int64_t n0, int64_t end, int part, int lane,
+                                             float unit) {
     const bool ok = row < j.rows;
 #pragma unroll 1
     for (int64_t col = n0; col < end; col += kChunk) {
@@ -513,6 +516,8 @@ __device__ __forceinline__ void dx_of_column(const Job& j, uint32_t taddr, int64
         const int64_t left = ok ? end - col : 0;
         if (j.sums && with_sums_of_column(j, j.sums + (part * j.cols + col) * j.rows + row, j.rows, left, v)) continue;   // not j.last: all lanes
         __syncwarp();
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * unit);
         store_columns(j.out, j.ld, row, col, left, lane, v);
     }
 }
@@ -664,8 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         const uint32_t staging = sb + kStageArea + (uint32_t)((warp - 4) * kStagingBytes);   // of kFewStats
         const uint32_t box = sb + kStageArea + (uint32_t)((warp - 4) * 4096);                // of TMA stores: 1024-byte aligned
         const int64_t few_n0 = half * (w.job[0].bn / 2), few_end = few_n0 + w.job[0].bn / 2 < w.job[0].cols ? few_n0 + w.job[0].bn / 2 : w.job[0].cols;
+        const float unit = w.unit ? static_cast<const volatile float*>(w.unit)[kKind == kProducts] : 1.0f;
         FewTokens tokens;
-        if constexpr (kKind == kFewLogits) few_tokens(w, w.job[0], few_n0, few_end, lane, tokens);
+        if constexpr (kKind == kFewLogits) few_tokens(w, w.job[0], few_n0, few_end, lane, unit, tokens);
         int acc = 0;
         uint32_t aph = 0;
         auto release = [&] {   // the accumulator has been read
@@ -681,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             const int64_t row0 = it.m * (2 * kBM) + rank * kBM + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
             if constexpr (kKind != kProducts) {
                 constexpr bool few = kKind == kFewLogits;
-                const RowValues r = row_values(w, j, row, few ? 0 : j.rows);
+                const RowValues r = row_values(w, j, row, few ? 0 : j.rows, unit);
                 const int64_t end = col0 + j.bn < j.cols ? col0 + j.bn : j.cols;
                 Logits<few ? kFewChunks : kChunks> l;
                 bool ok = true;
@@ -710,11 +716,11 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                 const int64_t n0 = col0 + half * (j.bn / 2), end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
                 const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN), taddr = acc0 + (uint32_t)(half * (j.bn / 2));
                 if (j.mode == kDx)
-                    dx_of_column(j, taddr, row, n0, end, it.part, lane);
+                    dx_of_column(j, taddr, row, n0, end, it.part, lane, unit);
                 else if (j.sums)
                     dw_sums_of_row(j, taddr, row, n0, end, it.part);
                 else
-                    dw_of_row(j, acc0, box, &maps.o[it.job], row0, col0, half, lane);
+                    dw_of_row(j, acc0, box, &maps.o[it.job], row0, col0, half, lane, unit);
                 release();
             }
         }
@@ -775,12 +781,38 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
     loss[row] = t < 0 ? 0.0f : t >= V ? NAN : (top - loss[row]) + low;
 }
 
+// The gradient of a target's logit is -g (1 - e^(z - lse)), which is -g for most tokens, and with a mean over the tokens g is
+// the same for all of them: rounded to bf16, they would all be off by the same share of themselves, up to 2^-8, and dx and dW
+// with them (8192 x 32000 x 4096, a mean over the tokens: 2.0e-3 to 2.9e-3 off by the number of tokens, so 2.0e-3).  So dz is
+// stored times a factor within 1 +- 2^-8, with which the g of the first token that has one is a bf16 value, and the products
+// are multiplied by its reciprocal.  (Of the first 1024 tokens; without one, or if
+// it is not a number to divide by, 1.)
+__device__ __forceinline__ void unit_of(const void* targets, int32_t wide, const float* dloss, int64_t M, int lane, float* unit) {
+    float f = 1.0f;
+    for (int64_t m = lane; m - lane < M && m < 1024; m += 32) {
+        float g = 0.0f;
+        if (m < M && index_at(targets, wide, m) >= 0) g = static_cast<const volatile float*>(dloss)[m];
+        const uint32_t some = __ballot_sync(kFull, fabsf(g) > 0x1p-100f && fabsf(g) < 0x1p100f);
+        if (some != 0u) {
+            g = __shfl_sync(kFull, g, __ffs(some) - 1);
+            f = __uint_as_float(bf16x2(g, 0.0f) << 16) / g;
+            break;
+        }
+    }
+    if (lane == 0) {
+        unit[0] = f;
+        unit[1] = 1.0f / f;
+    }
+}
+
 // xt[c][m] = x[m][c]: tiles of 64 x 64 through shared memory.  (xt's rows are whole 16-byte units; what lies behind their M
 // elements is not read.)
-__global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, int64_t x_ld, int64_t M, int64_t C, uint16_t* xt, int64_t ld) {
+__global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, int64_t x_ld, int64_t M, int64_t C, uint16_t* xt, int64_t ld,
+                                                            const void* targets, int32_t wide, const float* dloss, float* unit) {
     __shared__ uint16_t tile[64][66];
     const int64_t across = (M + 63) / 64, m0 = blockIdx.x % across * 64, c0 = blockIdx.x / across * 64;
     wait_for_primary();
+    if (blockIdx.x == 0 && threadIdx.x < 32) unit_of(targets, wide, dloss, M, (int)threadIdx.x, unit);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = threadIdx.x + 256 * h, r = i >> 3, c = (i & 7) * 8;
@@ -801,11 +833,11 @@ __global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, i
     }
 }
 
-// out[i] = bf16(sum over parts of sums[part][i]): products summed in parts.  A warp has 256 elements, and where there are
+// out[i] = bf16(unit[1] sum over parts of sums[part][i]): products summed in parts.  A warp has 256 elements, and where there are
 // several parts several warps of the block share them, every one some of the parts (200 x 30000 x 256, 32 parts: 4.5 us; all
 // parts in one thread 11 us).
 constexpr int kPartWarps = 8;
-__global__ void __launch_bounds__(32 * kPartWarps) lce_parts_kernel(const float* sums, int parts, int teams, int64_t n, uint16_t* out) {
+__global__ void __launch_bounds__(32 * kPartWarps) lce_parts_kernel(const float* sums, int parts, int teams, int64_t n, const float* unit, uint16_t* out) {
     __shared__ __align__(16) float part[kPartWarps][256];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp % teams;
     const int64_t at = ((int64_t)blockIdx.x * (kPartWarps / teams) + warp / teams) * 256 + 8 * lane;
@@ -829,14 +861,18 @@ __global__ void __launch_bounds__(32 * kPartWarps) lce_parts_kernel(const float*
         for (int t = 1; t < teams; ++t) add(&part[warp + t][8 * lane]);
     }
     if (at >= n) return;
+    const float u = static_cast<const volatile float*>(unit)[1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= u;
     uint32_t w[4];
     pack(x, w);
     *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-cudaError_t launch_parts(const float* sums, int parts, int64_t n, uint16_t* out, cudaStream_t s) {
+cudaError_t launch_parts(const float* sums, int parts, int64_t n, const float* unit, uint16_t* out, cudaStream_t s) {
     const int teams = parts >= 8 ? 8 : parts >= 4 ? 4 : parts >= 2 ? 2 : 1;
     const int64_t per = 256 * (kPartWarps / teams);
-    return launch_next(lce_parts_kernel, (unsigned)((n + per - 1) / per), 32 * kPartWarps, 0, s, sums, parts, teams, n, out);
+    return launch_next(lce_parts_kernel, (unsigned)((n + per - 1) / per), 32 * kPartWarps, 0, s, sums, parts, teams, n, unit,
+                       out);
 }
 
 // rows x cols bf16, row-major, ld elements apart; boxes of 64 columns x box_rows rows, zeros outside
@@ -1042,7 +1078,7 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
     float* const dw_sums = a.sums + lce_dx_sums(a.M, a.V, a.C, a.piece);
     const bool dx_sums = parts.dx > 1 || a.piece < a.V;
     cudaError_t e = launch_next(lce_transpose_kernel, (unsigned)(up(a.M, 64) * up(a.C, 64)), 256, 0, s, a.x, a.x_ld, a.M, a.C,
-                                a.xt, lce_xt_ld(a.M));
+                                a.xt, lce_xt_ld(a.M), a.targets, a.wide, a.dloss, a.unit);
     if (e != cudaSuccess) return e;
     for (int64_t v0 = 0; v0 < a.V; v0 += a.piece) {
         const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
@@ -1059,6 +1095,7 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
         w.lse = a.lse;
         w.dloss = a.dloss;
         w.dlse = a.dlse;
+        w.unit = a.unit;
         e = launch_work(w, maps, s);
         if (e != cudaSuccess) return e;
         w.jobs = 0;
@@ -1082,11 +1119,11 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
         }
         e = launch_work(w, maps, s);
         if (e == cudaSuccess && parts.dw > 1)
-            e = launch_parts(dw_sums, parts.dw, n * a.C, a.dweight + v0 * a.C, s);
+            e = launch_parts(dw_sums, parts.dw, n * a.C, a.unit, a.dweight + v0 * a.C, s);
         if (e != cudaSuccess) return e;
     }
     if (parts.dx == 1) return cudaSuccess;
-    return launch_parts(a.sums, parts.dx, a.M * a.C, a.dx, s);
+    return launch_parts(a.sums, parts.dx, a.M * a.C, a.unit, a.dx, s);
 }
 
 int64_t lce_piece(int64_t M, int64_t V, int64_t piece) {

@@ -491,9 +491,9 @@ size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t V, int64_t C);
  *   x  M rows of C bf16, x_ld apart (a multiple of 8), in;  weight [V x C] bf16 in;
  *   targets [M] in: a negative one (a token without a target) gives loss 0, one
  *   of V or more NaN;  loss, lse [M] float32 out.
- * Products are added in float32 by the tensor cores, which truncate: a logit is
- * within (C + 8) 2^-22 sum |x W| of the sum, and so are lse and loss of theirs,
- * with float32's roundings of what they are formed of.  The logits have to be
+ * Products are added in float32, by the tensor cores, which truncate, over 512 of C
+ * at a time: a logit is within (C + 8) 2^-22 sum |x W| of the sum at worst, and lse
+ * and loss of theirs, with float32's roundings of what they are formed of.  The logits have to be
  * finite or -inf (a token whose logits all are -inf has lse -inf and loss NaN).  M V at most COAT_MAX_N, here and below.
  */
 coat_status coat_linear_cross_entropy(const uint16_t *x, int64_t x_ld, const uint16_t *weight,
@@ -505,7 +505,8 @@ size_t coat_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V);
 /*
  * Its gradients, with dloss and dlse the gradients of loss and lse:
  *   dz[m, v] = e^(z[m, v] - lse[m]) (dloss[m] + dlse[m]) - [v = targets[m]] dloss[m],
- *   rounded to bf16;  dx = dz W;  dweight = dz^T x.
+ *   rounded to bf16 (in units of the first non-zero dloss, so that a dloss that is
+ *   the same for all tokens is not rounded);  dx = dz W;  dweight = dz^T x.
  *   x, weight, targets as above;  lse [M] as the forward pass left it;  dloss [M]
  *   float32 in (of a token without a target it does not count);  dlse [M] float32
  *   in, or NULL: zeros;  dx [M x C], dweight [V x C] bf16 out.

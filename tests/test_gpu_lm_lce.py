@@ -353,3 +353,42 @@ def test_refusals():
         coat.coat_linear_cross_entropy_backward(x, w, t, lse, loss, x, unwritten(50, 32), ws)
     with pytest.raises(coat.CoatError, match="INVALID_ARG"):
         coat.coat_linear_cross_entropy_backward(x, w, t, lse, loss, unwritten(20, 32), unwritten(50, 32), ws, piece=-1)
+
+
+@pytest.mark.parametrize("M,V,C", [(100, 3000, 256), (700, 3000, 256)])
+@pytest.mark.parametrize("first", [0, 40])
+def test_a_mean_over_the_tokens_is_not_off_by_the_rounding_of_its_factor(M, V, C, first):
+    """The targets' dz are all but -g: with one g for all tokens, halfway between two bf16 values, its rounding (2^-8 of it)
+    would be that of dx and dw.  Errors that do not line up are, for values spread over a binade, 2^-8 sqrt(0.541 / 3) = 0.00166
+    of themselves in the mean square at each rounding; dz and the output are two: 0.00235, and a tenth for the spread."""
+    x, w, t = inputs(M, V, C, 21, gain=1.0)
+    t = torch.randint(0, V, (M,), generator=gen(5), device="cuda")
+    t[:first] = -1                                         # the first tokens have no target
+    g = torch.full((M,), (1 + 2.0 ** -8 + 2.0 ** -20) * 2.0 ** -13, device="cuda")
+    lse = linear_cross_entropy(x, w, t)[1].float()
+    for piece in (0, 512):
+        dx, dw = check_backward(x, w, t, lse, g, piece=piece)
+        rx, rw = linear_cross_entropy_backward(x, w, t, lse, g)[:2]
+        for got, ref in ((dx, rx), (dw, rw)):
+            assert (got.double() - ref).norm() / ref.norm() <= 0.0026
+
+
+def test_gradients_that_are_no_numbers_to_divide_by():
+    """Gradients below any scale, zeros, and one that is infinite or NaN: each stays what it is, in its own row."""
+    M, V, C = 70, 300, 64
+    x, w, t = inputs(M, V, C, 22)
+    t = t.clamp_min(0)
+    lse = linear_cross_entropy(x, w, t)[1].float()
+    zero = torch.zeros(M, device="cuda")
+    assert not any(d.any() for d in backward(x, w, t, lse, zero))
+    tiny = torch.full((M,), 2.0 ** -120, device="cuda")
+    dx, dw = backward(x, w, t, lse, tiny)
+    assert dx.isfinite().all() and dw.isfinite().all()
+    check_backward(x, w, t, lse, torch.where(torch.arange(M, device="cuda") < 5, 0.0, 0.3).float())
+    for bad in (float("inf"), float("nan")):
+        g = torch.full((M,), 0.3, device="cuda")
+        g[0] = bad
+        dx, _ = backward(x, w, t, lse, g)
+        g[0] = 0.0
+        ref, _ = backward(x, w, t, lse, g)
+        assert not dx[0].isfinite().all() and torch.equal(dx[1:], ref[1:])

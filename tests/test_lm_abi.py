@@ -142,10 +142,10 @@ def test_linear_cross_entropy_workspaces(L):
     f, b = L.coat_linear_cross_entropy_workspace_bytes, L.coat_linear_cross_entropy_backward_workspace_bytes
     assert f(0, 10) == 0 and f(1 << 20, (1 << 20) + 1) == 0 and f(1, 1) > 0
     assert b(10, 100, 24, 0) == 0 and b(10, 100, 64, -1) == 0
-    xt = 2 * 64 * 16                                                     # x transposed, its rows in multiples of eight
+    xt = 2 * 64 * 16 + 16                                                # x transposed, its rows in multiples of eight, and a factor
     assert b(10, 100, 64, 0) == b(10, 100, 64, 1) == b(10, 100, 64, (1 << 63) - 1) == 2 * 10 * 256 + xt    # one piece
     assert b(10, 1000, 64, 300) == 2 * 10 * 512 + xt + 4 * 10 * 64       # two: and dx's sums between them
     M, V, C = 8192, 32000, 4096
-    assert b(M, V, C, 0) == 2 * M * V + 2 * M * C                         # one piece: its dz is within 512 MiB
+    assert b(M, V, C, 0) == 2 * M * V + 2 * M * C + 16                         # one piece: its dz is within 512 MiB
     M = 16384                                                             # two of about the same width
-    assert b(M, V, C, 0) == 2 * M * 16128 + 2 * M * C + 4 * M * C and 2 * M * 16128 <= 512 << 20
+    assert b(M, V, C, 0) == 2 * M * 16128 + 2 * M * C + 16 + 4 * M * C and 2 * M * 16128 <= 512 << 20
