@@ -14,7 +14,7 @@
 // One kernel for all four: persistent CTA pairs (clusters of two, one CTA per SM) walk tiles of 256 rows x up to 256 columns,
 // 64 of the summed index per stage, as in linear_fp8.cu: each CTA has its 128 rows of A and half of the columns of B in
 // a ring of stages filled by TMA (128-byte swizzle), one thread of the even CTA issues tcgen05.mma.cta_group::2
-// kind::f16, and eight epilogue warps per CTA read one of two accumulators in tensor memory while the other one fills.
+// kind::f16, and eight epilogue warps per CTA read one of several accumulators in tensor memory while another one fills.
 // B has its summed index along the row (K-major); A has it so too (x for z) or across the row (MN-major), which the MMA
 // takes at the same rate (8192^3: 1.79 PFLOP/s both; with B MN-major 1.46).  So dx is formed as its transpose, of W
 // (MN-major) and dz, and dW of dz (MN-major) and x's transpose, which a kernel lays out before.
@@ -47,6 +47,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // addition.  Logits are therefore added up by them over 512 of the summed index at a time, and the epilogue adds those sums
 // in its registers, with float32's rounding (lse of C = 4096: 4.6e-6 off in one go, 5.2e-7 so; the plain float32 form 8.6e-7).
 constexpr int kSegment = 8;                    // steps
+// of few tokens, whose time goes to the weight's bytes, 128 (33 x 50304 x 2048 forward, of 64 / 128 / 256 / 512: 50.4 / 43.6 / 42.5 / 42.3 us)
+constexpr int kFewSegment = 2;
 // Registers: the epilogue warps hold their logits, 128 a thread, and take what the other four warps give up.  Every one of
 // 384 threads is launched with kLaunchRegs.
 constexpr int kLaunchRegs = 168, kOtherRegs = 72, kEpiRegs = 216;
@@ -57,9 +59,10 @@ constexpr int kBN = 256;                       // most columns of a tile
 // (which kFewStats uses as 32 rows of 33 floats), then the barriers.
 constexpr int kStageArea = 6 * 32768;
 constexpr int kMaxStages = 10;
+constexpr int kMaxAccs = 4;
 constexpr int kStagingBytes = 32 * 33 * 4;
 constexpr int kBarOff = kStageArea + 8 * kStagingBytes;
-constexpr int kNumBars = 2 * kMaxStages + 5;   // full, empty, acc full x2, acc empty x2, done
+constexpr int kNumBars = 2 * kMaxStages + 2 * kMaxAccs + 1;   // full, empty, acc full, acc empty, done
 constexpr int kSmemBytes = kBarOff + 8 * kNumBars + 16 + 1024;   // + slack for 1024-B alignment
 constexpr int slot_bytes(int bn) { return kABytes + bn / 2 * kBK * 2; }
 constexpr int stages_of(int bn) { return kStageArea / slot_bytes(bn) < kMaxStages ? kStageArea / slot_bytes(bn) : kMaxStages; }
@@ -76,6 +79,10 @@ enum Mode : int32_t { kStats, kDz, kFewStats, kFewDz, kDx, kDw };
 // The kernels: by what their epilogue warps hold.
 enum Kind { kLogits, kFewLogits, kProducts };
 constexpr Kind kind_of(int32_t mode) { return mode <= kDz ? kLogits : mode <= kFewDz ? kFewLogits : kProducts; }
+// Accumulators in tensor memory, of at most 512 / accs_of columns each.  Few tokens leave room for four: segments are short, and
+// while the epilogue works on a tile's logits the next one's are formed.
+constexpr int accs_of(Kind kind) { return kind == kFewLogits ? 4 : 2; }
+static_assert(kFewTokens <= 512 / accs_of(kFewLogits) && kBN <= 512 / accs_of(kLogits) && accs_of(kFewLogits) <= kMaxAccs, "tensor memory");
 
 // A product: its tiles, each summed in `parts` parts of the summed index.
 struct Job {
@@ -108,7 +115,7 @@ struct Work {
     const float* dloss;
     const float* dlse;
     const float* unit;       // backward: what dz is stored times, and its reciprocal (see unit_of)
-    float2* stats;           // [half of a tile's columns, or, of few tokens, epilogue warp][token], tokens padded
+    float2* stats;           // {maximum, rest} (see Rest), [half of a tile's columns, or, of few tokens, epilogue warp][token], tokens padded
     int64_t stats_ld;
     float* target_logit;
 };
@@ -224,6 +231,7 @@ __device__ __forceinline__ int chunk_off(int half, int c) { return 64 * half + 1
 // one segment's sums of them; the chunks that have columns below `cols` of the tile, the same for the whole warp
 template <bool kFirst, int kN>
 __device__ __forceinline__ void add_segment(uint32_t acc0, int half, int bn, int cols, Logits<kN>& l) {
+    constexpr int kLoad = kN == kFewChunks ? 32 : 16;   // columns: with 32 beside 128 logits, a thread's registers do not suffice
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
         const int off = kN == kFewChunks ? half * (bn / 2) + kChunk * c : chunk_off(half, c);
@@ -233,11 +241,11 @@ __device__ __forceinline__ void add_segment(uint32_t acc0, int half, int bn, int
             tmem_ld<kChunk>(acc0 + (uint32_t)off, l.z[c]);
         } else {
 #pragma unroll
-            for (int h = 0; h < kChunk; h += 16) {
-                uint32_t v[16];
-                tmem_ld<16>(acc0 + (uint32_t)(off + h), v);
+            for (int h = 0; h < kChunk; h += kLoad) {
+                uint32_t v[kLoad];
+                tmem_ld<kLoad>(acc0 + (uint32_t)(off + h), v);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
+                for (int e = 0; e < kLoad; e += 2) {
                     float x, y;
                     upk(add2(pk(__uint_as_float(l.z[c][h + e]), __uint_as_float(l.z[c][h + e + 1])),
                              pk(__uint_as_float(v[e]), __uint_as_float(v[e + 1]))), x, y);
@@ -249,11 +257,27 @@ __device__ __forceinline__ void add_segment(uint32_t acc0, int half, int bn, int
     }
 }
 
+// Of a sum of e^(z - top), with top the largest z, a float32 keeps the terms but the largest only in units of 2^-23 of it, and the
+// loss of a certain token is the sum of those.  So what is kept is the rest: the sum without the largest one's 1 (of no logits,
+// or of -inf alone, -1).
+constexpr float kNoRest = -1.0f;
+// joined with the rest of others
+__device__ __forceinline__ void join_rest(float& top, float& rest, float top1, float rest1) {
+    const float mx = fmaxf(top, top1), ref = mx == -INFINITY ? 0.0f : mx;
+    const float f = ex2_ftz((fminf(top, top1) - ref) * kLog2e);
+    rest = top1 > top ? rest1 + (1.0f + rest) * f : rest + (1.0f + rest1) * f;
+    top = mx;
+}
+// joined with a sum of e^(z - mx) of more logits, mx the largest of all; before: e^(top - mx)
+__device__ __forceinline__ void add_to_rest(float& top, float& rest, float mx, float before, float sum) {
+    rest = mx > top ? (sum - 1.0f) + (1.0f + rest) * before : rest + sum;
+    top = mx;
+}
+
 // columns col0 .. end - 1 of the tile are logits
 __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const RowValues& r, Logits<kChunks>& l, int64_t row, int64_t col0, int64_t end,
                                              int half, int64_t part) {
-    float top = -INFINITY;
-    uint64_t sums = pk(0.0f, 0.0f);
+    float top = -INFINITY, rest = kNoRest;
     const int cols = (int)(end - col0), target = r.target - (int)col0;   // in the tile
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
@@ -277,30 +301,29 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const 
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) mx = max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
         const float ref = mx == -INFINITY ? 0.0f : mx;   // a row of -inf so far
-        const float f = ex2_ftz((top - ref) * kLog2e);
-        top = mx;
-        sums = mul2(sums, pk(f, f));
+        uint64_t sums = pk(0.0f, 0.0f);
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) {
             float x, y;
             exp2_of(v[e], v[e + 1], pk(-ref, -ref), x, y);
             sums = add2(sums, pk(x, y));
         }
+        add_to_rest(top, rest, mx, ex2_ftz((top - ref) * kLog2e), sum2(sums));
     }
-    if (row < j.rows) w.stats[part * w.stats_ld + row] = make_float2(top, sum2(sums));   // of no columns: -inf and 0
+    if (row < j.rows) w.stats[part * w.stats_ld + row] = make_float2(top, rest);
 }
 
 // What an epilogue warp keeps of its few tokens from tile to tile: the lane's one of every 32.
 struct FewTokens {
     RowValues r[kFewChunks];
-    float top[kFewChunks], sum[kFewChunks];
+    float top[kFewChunks], rest[kFewChunks];
 };
 __device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t n0, int64_t end, int lane, float unit, FewTokens& f) {
 #pragma unroll
     for (int c = 0; c < kFewChunks; ++c) {
         f.r[c] = row_values(w, j, n0 + kChunk * c + lane, end, unit);
         f.top[c] = -INFINITY;
-        f.sum[c] = 0.0f;
+        f.rest[c] = kNoRest;
     }
 }
 
@@ -332,15 +355,14 @@ __device__ __forceinline__ void few_stats(const Work& w, const Job& j, const Log
             w.target_logit[token] = z;
         }
         const float ref = mx == -INFINITY ? 0.0f : mx;
-        uint64_t sums = pk(f.sum[c] * ex2_ftz((f.top[c] - ref) * kLog2e), 0.0f);
-        f.top[c] = mx;
+        uint64_t sums = pk(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < kChunk; k += 2) {
             float x, y;
             exp2_of(v[k], v[k + 1], pk(-ref, -ref), x, y);
             sums = add2(sums, pk(x, y));
         }
-        f.sum[c] = sum2(sums);
+        add_to_rest(f.top[c], f.rest[c], mx, ex2_ftz((f.top[c] - ref) * kLog2e), sum2(sums));
     }
 }
 
@@ -537,8 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     auto full = [&](int s) { return bar0 + 8u * (uint32_t)s; };
     auto empty = [&](int s) { return bar0 + 8u * (uint32_t)(kMaxStages + s); };
     auto acc_full = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kMaxStages + b); };
-    auto acc_empty = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kMaxStages + 2 + b); };
-    const uint32_t done = bar0 + 8u * (uint32_t)(2 * kMaxStages + 4);
+    auto acc_empty = [&](int b) { return bar0 + 8u * (uint32_t)(2 * kMaxStages + kMaxAccs + b); };
+    const uint32_t done = bar0 + 8u * (uint32_t)(2 * kMaxStages + 2 * kMaxAccs);
+    constexpr int kAccs = accs_of(kKind), kAccStride = 2 * kBN / kAccs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + 8 * kNumBars);
     volatile uint32_t* abort = tmem_slot + 1;
 
@@ -547,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kMaxStages; ++s) { mbar_init(full(s), 1); mbar_init(empty(s), 1); }
-        for (int b = 0; b < 2; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 2 * kEpiWarps); }
+        for (int b = 0; b < kAccs; ++b) { mbar_init(acc_full(b), 1); mbar_init(acc_empty(b), 2 * kEpiWarps); }
         mbar_init(done, 1);
         *abort = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -636,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                     ok = __all_sync(kFull, mbar_wait_relaxed(acc_empty(acc), aph ^ 1u, abort));   // see mbar_arrive_relaxed
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + (uint32_t)(acc * kBN), af = acc_full(acc);
+                    const uint32_t d = tmem + (uint32_t)(acc * kAccStride), af = acc_full(acc);
                     for (int k = from; k < to; ++k) {
                         if (!ready) ok = __all_sync(kFull, mbar_wait_fast(full(s), ph, abort));
                         if (!ok) break;
@@ -654,8 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                         }
                         ready = __all_sync(kFull, next);
                     }
-                    acc ^= 1;
-                    if (acc == 0) aph ^= 1u;
+                    if (++acc == kAccs) { acc = 0; aph ^= 1u; }
                 }
             }
             if (elected) mma_commit_pair(done, 0x3);   // every MMA issued has completed before either CTA frees tensor memory
@@ -678,8 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(map_to_rank(acc_empty(acc), 0));
-            acc ^= 1;
-            if (acc == 0) aph ^= 1u;
+            if (++acc == kAccs) { acc = 0; aph ^= 1u; }
         };
         for (uint32_t i = 0; walk.item(i, w, it); ++i) {
             if (it.from == it.to) continue;
@@ -695,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                     ok = __all_sync(kFull, mbar_wait_inline(acc_full(acc), aph, abort));   // the sums so far stay in registers
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN);
+                    const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kAccStride);
                     if (from == it.from)
                         add_segment<true>(acc0, half, j.bn, (int)(end - col0), l);
                     else
@@ -714,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                 if (!__all_sync(kFull, mbar_wait_fast(acc_full(acc), aph, abort))) break;
                 tc_fence_after();
                 const int64_t n0 = col0 + half * (j.bn / 2), end = n0 + j.bn / 2 < j.cols ? n0 + j.bn / 2 : j.cols;
-                const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kBN), taddr = acc0 + (uint32_t)(half * (j.bn / 2));
+                const uint32_t acc0 = tmem + ((uint32_t)(32 * q4) << 16) + (uint32_t)(acc * kAccStride), taddr = acc0 + (uint32_t)(half * (j.bn / 2));
                 if (j.mode == kDx)
                     dx_of_column(j, taddr, row, n0, end, it.part, lane, unit);
                 else if (j.sums)
@@ -728,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
 #pragma unroll
             for (int c = 0; c < kFewChunks; ++c) {
                 const int64_t token = few_n0 + kChunk * c + lane;
-                if (token < few_end) w.stats[((2 * pair + rank) * 4 + q4) * w.stats_ld + token] = make_float2(tokens.top[c], tokens.sum[c]);
+                if (token < few_end) w.stats[((2 * pair + rank) * 4 + q4) * w.stats_ld + token] = make_float2(tokens.top[c], tokens.rest[c]);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the stores by TMA are done
@@ -743,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kBN) : "memory");
 }
 
-// loss and lse from the half tiles' maxima and sums: 32 rows per block, each warp every 32nd of them
+// loss and lse from the half tiles' maxima and rests: 32 rows per block, each warp every 32nd of them
 constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2* stats, int64_t ld, int64_t parts, const void* targets,
                                                                    int32_t wide, int64_t M, int64_t V, float* loss, float* lse) {
@@ -751,30 +772,27 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row0 = (int64_t)blockIdx.x * 32;
     wait_for_primary();
-    float top = -INFINITY, sum = 0.0f;
-    auto join = [&](float2 f) {
-        const float mx = fmaxf(top, f.x), ref = mx == -INFINITY ? 0.0f : mx;
-        sum = sum * ex2_ftz((top - ref) * kLog2e) + f.y * ex2_ftz((f.x - ref) * kLog2e);
-        top = mx;
-    };
+    float top = -INFINITY, rest = kNoRest;
     // stats_ld is a multiple of 32: the rows behind the last one are there, whatever they hold
     const float2* p = stats + row0 + lane;
 #pragma unroll 8
-    for (int64_t i = warp; i < parts; i += kJoinWarps) join(p[i * ld]);
-    part[warp][lane] = make_float2(top, sum);
+    for (int64_t i = warp; i < parts; i += kJoinWarps) {
+        const float2 f = p[i * ld];
+        join_rest(top, rest, f.x, f.y);
+    }
+    part[warp][lane] = make_float2(top, rest);
     __syncthreads();
     // a warp for each row: its 32 lanes hold the warps' results
     const int64_t row = row0 + warp;
     if (row >= M) return;
-    float2 f = part[lane][warp];
+    top = part[lane][warp].x;
+    rest = part[lane][warp].y;
     for (int off = 16; off > 0; off >>= 1) {
-        top = f.x;
-        sum = f.y;
-        join(make_float2(__shfl_xor_sync(kFull, f.x, off), __shfl_xor_sync(kFull, f.y, off)));
-        f = make_float2(top, sum);
+        const float top1 = __shfl_xor_sync(kFull, top, off), rest1 = __shfl_xor_sync(kFull, rest, off);
+        join_rest(top, rest, top1, rest1);
     }
     if (lane != 0) return;
-    const float low = logf(sum);
+    const float low = log1pf(rest);
     const int64_t t = index_at(targets, wide, row);
     lse[row] = top + low;
     // (top - z) + log(sum): nothing cancels where the target's logit is the largest
@@ -929,7 +947,7 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     j.rows = a.mn ? a.cols : a.rows;
     j.cols = b.rows;
     j.steps = (int32_t)up(K, kBK);
-    j.segment = mode <= kFewDz ? kSegment : j.steps;
+    j.segment = kind_of(mode) == kLogits ? kSegment : kind_of(mode) == kFewLogits ? kFewSegment : j.steps;
     j.bn = tile_columns(j.rows, j.cols, mode);
     j.parts = 1;
     j.tm = up(j.rows, 2 * kBM);

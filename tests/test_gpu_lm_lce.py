@@ -392,3 +392,36 @@ def test_gradients_that_are_no_numbers_to_divide_by():
         g[0] = 0.0
         ref, _ = backward(x, w, t, lse, g)
         assert not dx[0].isfinite().all() and torch.equal(dx[1:], ref[1:])
+
+
+@pytest.mark.parametrize("M,V,at", [(3, 40001, 7), (129, 40001, 40000), (200, 97, 40), (1, 2, 1)])
+@pytest.mark.parametrize("ahead", [10.0, 15.0, 20.0])
+def test_loss_of_a_certain_token_is_that_of_the_others_terms(M, V, at, ahead):
+    """The target's logit is `ahead` of all others, exactly: loss = log(1 + (V - 1) e^-ahead), of terms as small as 2e-9.  At most
+    31 of them share 32 columns with the target's 1, and may be lost beside it; of 16 additions to the 1, and of 32 columns'
+    sum less 1, each may be off by 2^-23, but by no more than what is added.  The others: joins of V / 32 sums, the exponential's
+    error and its argument's, 2 ahead."""
+    C = 64
+    w = torch.zeros(V, C, dtype=BF, device="cuda")
+    w[at, 3] = ahead / 2
+    x = torch.zeros(M, C, dtype=BF, device="cuda")
+    x[:, 3] = 2
+    loss, lse = forward(x, w, torch.full((M,), at, device="cuda"))
+    term = torch.exp(torch.tensor(-ahead, dtype=torch.float64)).item()
+    ref = torch.log1p(torch.tensor((V - 1) * term, dtype=torch.float64)).expand(M).cuda()
+    err = 31 * min(term, 2.0 ** -23) + ref * (V / 32 + 64 + 2 * ahead) * 4 * E
+    near(loss, ref, err, "loss")
+    near(lse, ref + ahead, err + 4 * E * ahead, "lse")
+
+
+@pytest.mark.parametrize("M", [100, 300])
+def test_logits_that_are_not_numbers_give_nan_in_their_rows_alone(M):
+    x, w, t = inputs(M, 700, 128, 23)
+    t = t.clamp_min(0)
+    good = forward(x, w, t)
+    for bad in (float("nan"), float("inf")):
+        y = x.clone()
+        y[[0, M - 1], 5] = bad
+        loss, lse = forward(y, w, t)
+        assert loss[[0, M - 1]].isnan().all() and lse[[0, M - 1]].isnan().all()
+        assert torch.equal(loss[1:-1], good[0][1:-1]) and torch.equal(lse[1:-1], good[1][1:-1])
