@@ -47,7 +47,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // addition.  Logits are therefore added up by them over 512 of the summed index at a time, and the epilogue adds those sums
 // in its registers, with float32's rounding (lse of C = 4096: 4.6e-6 off in one go, 5.2e-7 so; the plain float32 form 8.6e-7).
 constexpr int kSegment = 8;                    // steps
-// of few tokens, whose time goes to the weight's bytes, 128 (33 x 50304 x 2048 forward, of 64 / 128 / 256 / 512: 50.4 / 43.6 / 42.5 / 42.3 us)
+// of few tokens, whose time goes to the weight's bytes, 128 (33 x 50304 x 2048 forward in tiles of 256 rows, of 64 / 128 / 256 / 512: 50.4 / 43.6 / 42.5 / 42.3 us)
 constexpr int kFewSegment = 2;
 // Registers: the epilogue warps hold their logits, 128 a thread, and take what the other four warps give up.  Every one of
 // 384 threads is launched with kLaunchRegs.
@@ -68,8 +68,8 @@ constexpr int slot_bytes(int bn) { return kABytes + bn / 2 * kBK * 2; }
 constexpr int stages_of(int bn) { return kStageArea / slot_bytes(bn) < kMaxStages ? kStageArea / slot_bytes(bn) : kMaxStages; }
 static_assert(kSmemBytes <= 232448 && stages_of(256) == 6 && stages_of(32) == 10, "shared memory of an SM");
 // Up to so many tokens, the logits are formed with the tokens as the only tile's columns, so that the product has no rows
-// without a token (50304 x 2048 forward, 1 / 33 / 100 tokens: 40 / 41 / 43 us, with the tokens as rows 62 / 46 / 46; 200 / 256
-// tokens 46 / 48, as rows 46 / 47).
+// without a token (50304 x 2048 forward, 1 / 33 / 100 tokens: 37 / 38 / 39 us, with the tokens as rows 62 / 46 / 46; with 200 / 256
+// tokens 46 / 48 in segments of 512, as rows 46 / 47).
 constexpr int64_t kFewTokens = 128;
 constexpr int kFewChunks = (int)kFewTokens / 2 / kChunk;   // of an epilogue warp
 
@@ -90,6 +90,7 @@ struct Job {
     int32_t a_mn;            // A is MN-major
     int32_t steps;           // 64 of the summed index each
     int32_t segment;         // steps that the tensor cores add up by themselves
+    int32_t bm;              // rows of a tile: 2 kBM, or, of few tokens, a multiple of 32 up to it
     int32_t bn;              // columns of a tile: a multiple of 32
     int32_t parts;
     int64_t tm, tn;          // tiles
@@ -115,7 +116,7 @@ struct Work {
     const float* dloss;
     const float* dlse;
     const float* unit;       // backward: what dz is stored times, and its reciprocal (see unit_of)
-    float2* stats;           // {maximum, rest} (see Rest), [half of a tile's columns, or, of few tokens, epilogue warp][token], tokens padded
+    float2* stats;           // {maximum, rest} (see Rest), [half of a tile's columns, or, of few tokens, CTA][token], tokens padded
     int64_t stats_ld;
     float* target_logit;
 };
@@ -329,9 +330,9 @@ __device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t 
 
 // The statistics of few tokens: a warp has 32 rows of the weight and its tokens n0 .. end - 1, 32 of which at a time it turns
 // over in shared memory, so that a lane has one token.
-__device__ __forceinline__ void few_stats(const Work& w, const Job& j, const Logits<kFewChunks>& l, uint32_t buf, int64_t row0, int lane, int64_t n0,
+__device__ __forceinline__ void few_stats(const Work& w, const Logits<kFewChunks>& l, uint32_t buf, int64_t row0, int64_t rows, int lane, int64_t n0,
                                           int64_t end, FewTokens& f) {
-    const bool in = row0 + lane < j.rows;
+    const bool in = row0 + lane < rows;
 #pragma unroll
     for (int c = 0; c < kFewChunks; ++c) {
         if (n0 + kChunk * c >= end) break;   // the same for the whole warp
@@ -349,7 +350,7 @@ __device__ __forceinline__ void few_stats(const Work& w, const Job& j, const Log
         }
         const int64_t token = n0 + kChunk * c + lane;
         const int at = f.r[c].target - (int)row0;
-        if (at >= 0 && at < kChunk && f.r[c].target < j.rows && token < end) {
+        if (at >= 0 && at < kChunk && f.r[c].target < rows && token < end) {
             float z;
             asm volatile("ld.shared.b32 %0, [%1];" : "=f"(z) : "r"(buf + (uint32_t)(4 * (33 * at + lane))));
             w.target_logit[token] = z;
@@ -456,10 +457,10 @@ __device__ __forceinline__ void store_columns(uint16_t* out, int64_t ld, int64_t
 }
 
 // kFewDz.  (A last column without a neighbour takes one of the row's padding with it.)
-__device__ __forceinline__ void few_dz(const Work& w, const Job& j, Logits<kFewChunks>& l, int64_t row0, int lane, int64_t n0, int64_t end,
-                                       const FewTokens& f) {
+__device__ __forceinline__ void few_dz(const Work& w, const Job& j, Logits<kFewChunks>& l, int64_t row0, int64_t rows, int lane, int64_t n0,
+                                       int64_t end, const FewTokens& f) {
     const int64_t row = row0 + lane;
-    const bool ok = row - (lane & 1) < j.rows;
+    const bool ok = row - (lane & 1) < rows;
 #pragma unroll
     for (int c = 0; c < kFewChunks; ++c) {
         const int64_t col = n0 + kChunk * c;
@@ -588,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
     cluster_sync();   // barriers initialised and tensor memory allocated in both CTAs
     tc_fence_after();
     wait_for_primary();
+    dependents_may_start();   // their launch costs nothing then (2048 x 512 x 1024 forward: 8.6 us, at the end or never 9.3)
     const uint32_t tmem = *tmem_slot;
 
     const int64_t pair = blockIdx.x >> 1;
@@ -611,8 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         for (uint32_t i = 0; ok && walk.item(i, w, it); ++i) {
             const Job& j = w.job[it.job];
             const CUtensorMap *ma = &maps.a[it.job], *mb = &maps.b[it.job];
-            const int32_t m0 = (int32_t)(it.m * (2 * kBM) + rank * kBM), n0 = (int32_t)(it.n * j.bn + rank * (j.bn / 2));
-            const uint32_t bytes = 2u * (uint32_t)(kABytes + j.bn / 2 * kBK * 2);   // of both CTAs
+            const int32_t bm = kKind == kFewLogits ? j.bm : 2 * kBM;
+            const int32_t m0 = (int32_t)(it.m * bm + rank * (bm / 2)), n0 = (int32_t)(it.n * j.bn + rank * (j.bn / 2));
+            const uint32_t bytes = 2u * (uint32_t)((bm / 2 + j.bn / 2) * kBK * 2);   // of both CTAs
             const bool a_mn = j.a_mn;
             for (int k = it.from; k < it.to; ++k) {
                 if (!ready) ok = __all_sync(kFull, mbar_wait_fast(empty(s), ph ^ 1u, abort));
@@ -705,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
         for (uint32_t i = 0; walk.item(i, w, it); ++i) {
             if (it.from == it.to) continue;
             const Job& j = w.job[it.job];
-            const int64_t row0 = it.m * (2 * kBM) + rank * kBM + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
+            const int bm = kKind == kFewLogits ? j.bm : 2 * kBM;
+            const int64_t top = it.m * bm + rank * (bm / 2), row0 = top + 32 * q4, row = row0 + lane, col0 = it.n * j.bn;
             if constexpr (kKind != kProducts) {
                 constexpr bool few = kKind == kFewLogits;
                 const RowValues r = row_values(w, j, row, few ? 0 : j.rows, unit);
@@ -725,8 +729,9 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                 }
                 if (!ok) break;
                 if constexpr (few) {
-                    if (j.mode == kFewStats) few_stats(w, j, l, staging, row0, lane, few_n0, few_end, tokens);
-                    else few_dz(w, j, l, row0, lane, few_n0, few_end, tokens);
+                    const int64_t rows = top + bm / 2 < j.rows ? top + bm / 2 : j.rows;   // up to this CTA's last one
+                    if (j.mode == kFewStats) few_stats(w, l, staging, row0, rows, lane, few_n0, few_end, tokens);
+                    else few_dz(w, j, l, row0, rows, lane, few_n0, few_end, tokens);
                 } else {
                     if (j.mode == kStats) stats_of_row(w, j, r, l, row, col0, end, half, 2 * it.n + half);
                     else dz_of_row(w, j, r, l, box, &maps.o[it.job], row0, col0, half, lane);
@@ -745,17 +750,29 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                 release();
             }
         }
-        if (kKind == kFewLogits && w.job[0].mode == kFewStats) {
+        if (kKind == kFewLogits && w.job[0].mode == kFewStats) {   // the four warps of a half, which have the same tokens
+            auto at = [&](int q, int c) { return staging + (uint32_t)((q - q4) * kStagingBytes + 8 * (kChunk * c + lane)); };
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < kFewChunks; ++c)
+                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at(q4, c)), "f"(tokens.top[c]), "f"(tokens.rest[c]) : "memory");
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
 #pragma unroll
             for (int c = 0; c < kFewChunks; ++c) {
                 const int64_t token = few_n0 + kChunk * c + lane;
-                if (token < few_end) w.stats[((2 * pair + rank) * 4 + q4) * w.stats_ld + token] = make_float2(tokens.top[c], tokens.rest[c]);
+                if (q4 != 0 || token >= few_end) continue;
+#pragma unroll
+                for (int q = 1; q < 4; ++q) {
+                    float top1, rest1;
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(top1), "=f"(rest1) : "r"(at(q, c)) : "memory");
+                    join_rest(tokens.top[c], tokens.rest[c], top1, rest1);
+                }
+                w.stats[(2 * pair + rank) * w.stats_ld + token] = make_float2(tokens.top[c], tokens.rest[c]);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the stores by TMA are done
         __syncwarp();
     }
-    dependents_may_start();
     tc_fence_before();
     cluster_sync();   // no arrival or copy is still on its way to either CTA
     tc_fence_after();
@@ -770,8 +787,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
                                                                    int32_t wide, int64_t M, int64_t V, float* loss, float* lse) {
     __shared__ float2 part[kJoinWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row0 = (int64_t)blockIdx.x * 32;
+    const int64_t row0 = (int64_t)blockIdx.x * 32, row = row0 + warp;
     wait_for_primary();
+    dependents_may_start();
+    int64_t t = -1;
+    float z = 0.0f;
+    if (row < M) {   // what the end needs, with the first loads
+        t = index_at(targets, wide, row);
+        z = static_cast<const volatile float*>(loss)[row];
+    }
     float top = -INFINITY, rest = kNoRest;
     // stats_ld is a multiple of 32: the rows behind the last one are there, whatever they hold
     const float2* p = stats + row0 + lane;
@@ -783,7 +807,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
     part[warp][lane] = make_float2(top, rest);
     __syncthreads();
     // a warp for each row: its 32 lanes hold the warps' results
-    const int64_t row = row0 + warp;
     if (row >= M) return;
     top = part[lane][warp].x;
     rest = part[lane][warp].y;
@@ -793,10 +816,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
     }
     if (lane != 0) return;
     const float low = log1pf(rest);
-    const int64_t t = index_at(targets, wide, row);
     lse[row] = top + low;
     // (top - z) + log(sum): nothing cancels where the target's logit is the largest
-    loss[row] = t < 0 ? 0.0f : t >= V ? NAN : (top - loss[row]) + low;
+    loss[row] = t < 0 ? 0.0f : t >= V ? NAN : (top - z) + low;
 }
 
 // The gradient of a target's logit is -g (1 - e^(z - lse)), which is -g for most tokens, and with a mean over the tokens g is
@@ -830,6 +852,7 @@ __global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, i
     __shared__ uint16_t tile[64][66];
     const int64_t across = (M + 63) / 64, m0 = blockIdx.x % across * 64, c0 = blockIdx.x / across * 64;
     wait_for_primary();
+    dependents_may_start();
     if (blockIdx.x == 0 && threadIdx.x < 32) unit_of(targets, wide, dloss, M, (int)threadIdx.x, unit);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -860,6 +883,7 @@ __global__ void __launch_bounds__(32 * kPartWarps) lce_parts_kernel(const float*
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp % teams;
     const int64_t at = ((int64_t)blockIdx.x * (kPartWarps / teams) + warp / teams) * 256 + 8 * lane;
     wait_for_primary();
+    dependents_may_start();
     float x[8] = {};
     auto add = [&](const float* p) {
         const float4 f = *reinterpret_cast<const float4*>(p), g = *reinterpret_cast<const float4*>(p + 4);
@@ -939,6 +963,25 @@ int tile_columns(int64_t rows, int64_t cols, int32_t mode) {
     return bn;
 }
 
+// Rows of a tile of few tokens' logits, which are the weight's, of the multiples of 32: where there are more tiles than pairs,
+// those with which the pairs that have most have fewest rows (50304 rows: 225 tiles of 224 for 76 pairs, three each, instead of
+// 197 of 256: 33 x 50304 x 2048 38.1 us for 39.2, 20 x 24000 x 2048 25.0 for 27.9; otherwise more pairs with fewer rows each
+// only take longer, 20 x 9000 x 2048 15.9 for 15.0 us).  The MMA's other rows hold what was there before: no element of the
+// product but theirs depends on them.
+int tile_rows(int64_t rows, int32_t mode) {
+    int64_t best = 0;
+    int bm = 2 * kBM;
+    if (kind_of(mode) != kFewLogits || up(rows, bm) <= kPairs) return bm;
+    for (int m = 2 * kBM; m >= 128; m -= 32) {
+        const int64_t cost = up(up(rows, m), kPairs) * m;
+        if (best == 0 || cost < best) {
+            best = cost;
+            bm = m;
+        }
+    }
+    return bm;
+}
+
 bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand& b, uint16_t* out, int64_t ld) {
     Job& j = w.job[w.jobs];
     const int64_t K = a.mn ? a.rows : a.cols;
@@ -949,14 +992,15 @@ bool add_job(Work& w, Maps& maps, int32_t mode, const Operand& a, const Operand&
     j.steps = (int32_t)up(K, kBK);
     j.segment = kind_of(mode) == kLogits ? kSegment : kind_of(mode) == kFewLogits ? kFewSegment : j.steps;
     j.bn = tile_columns(j.rows, j.cols, mode);
+    j.bm = tile_rows(j.rows, mode);
     j.parts = 1;
-    j.tm = up(j.rows, 2 * kBM);
+    j.tm = up(j.rows, j.bm);
     j.tn = up(j.cols, j.bn);
     j.out = out;
     j.ld = ld;
     j.sums = nullptr;
     j.first = j.last = 1;
-    if (!encode(&maps.a[w.jobs], a.p, a.rows, a.cols, a.ld, a.mn ? kBK : kBM) ||
+    if (!encode(&maps.a[w.jobs], a.p, a.rows, a.cols, a.ld, a.mn ? kBK : j.bm / 2) ||
         !encode(&maps.b[w.jobs], b.p, b.rows, b.cols, b.ld, j.bn / 2) ||
         ((mode == kDz || mode == kDw) && !encode(&maps.o[w.jobs], out, j.rows, j.cols, ld, 32)))
         return false;
@@ -1085,7 +1129,7 @@ cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s) {
     w.target_logit = a.loss;
     cudaError_t e = launch_work(w, maps, s);
     if (e != cudaSuccess) return e;
-    const int64_t parts = few ? 8 * (int64_t)w.pairs : 2 * w.job[0].tn;   // the epilogue warps, or two of each tile
+    const int64_t parts = few ? 2 * (int64_t)w.pairs : 2 * w.job[0].tn;   // the CTAs, or two of each tile
     return launch_next(lce_join_kernel, (unsigned)up(a.M, 32), 32 * kJoinWarps, 0, s, (const float2*)w.stats, w.stats_ld,
                        parts, a.targets, a.wide, a.M, a.V, a.loss, a.lse);
 }
@@ -1163,7 +1207,7 @@ int64_t lce_sums(int64_t M, int64_t V, int64_t C, int64_t piece) {
     return lce_dx_sums(M, V, C, piece) + (p.dw > 1 ? p.dw * piece * C : 0);
 }
 size_t lce_stats_bytes(int64_t M, int64_t V) {
-    const int64_t parts = M <= kFewTokens ? 8 * kPairs : 2 * up(V, tile_columns(M, V, kStats));
+    const int64_t parts = M <= kFewTokens ? 2 * kPairs : 2 * up(V, tile_columns(M, V, kStats));
     return 8 * (size_t)(up(M, 32) * 32) * (size_t)parts;
 }
 

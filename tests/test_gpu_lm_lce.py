@@ -425,3 +425,20 @@ def test_logits_that_are_not_numbers_give_nan_in_their_rows_alone(M):
         loss, lse = forward(y, w, t)
         assert loss[[0, M - 1]].isnan().all() and lse[[0, M - 1]].isnan().all()
         assert torch.equal(loss[1:-1], good[0][1:-1]) and torch.equal(lse[1:-1], good[1][1:-1])
+
+
+@pytest.mark.parametrize("M,V", [(1, 20001), (33, 25001), (128, 30001), (40, 47003), (100, 38913), (65, 19457)])
+def test_few_tokens_in_tiles_of_fewer_rows_of_the_weight(M, V):
+    """More tiles of the weight's rows than pairs of multiprocessors: every row counts once, wherever a tile ends."""
+    check_forward(*inputs(M, V, 48, V, torch.int32))
+    test_every_operand_in_whole_numbers(M, V, 32)
+    x, w, t = inputs(M, V, 32, V)
+    x[:] = 0
+    x[:, 7] = 1
+    w[:, 7] = torch.arange(V, device="cuda").remainder(5).to(BF)     # the logits, exactly, of which the sum is known
+    loss, lse = forward(x, w, t)
+    count = torch.bincount(torch.arange(V, device="cuda").remainder(5), minlength=5).double()
+    want = (count * torch.exp(torch.arange(5, device="cuda").double())).sum().log().expand(M)
+    near(lse, want, torch.full_like(want, (V / 32 + 64 + 8) * 4 * E + 4 * E * 20), "lse")
+    near(loss, torch.where(t < 0, 0.0, want - w[t.clamp_min(0), 7].double()),
+         torch.where(t < 0, 0.0, (V / 32 + 64 + 8) * 4 * E + 4 * E * 24).double(), "loss")
