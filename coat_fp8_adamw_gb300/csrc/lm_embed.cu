@@ -28,17 +28,20 @@ using lm::index_at;
 using lm::load_index;
 
 constexpr int kBlock = 256;
-constexpr int kWarps = kBlock / 32;
 constexpr int kChunk = 32;            // tokens of a chunk, one of a warp's lanes each
 constexpr int kSlice = 256;           // columns of a warp: 8 per lane
-// Tokens whose loads are on their way at once.  Many chunks: 4, and registers for four blocks per SM, with which all warps of
-// 16411 x 2048 are resident together (41 us; 8 and two blocks 45, 8 and three 47, 4 and three 49; chunks of 16 tokens 46).
-// Up to kFewUnits warps, which find room one block per SM: 16 (300 x 4096, added: 14.6 us, with 4 18.3).
+// Tokens whose loads are on their way at once.  Many chunks: 4, and registers for 32 warps per SM (16411 x 2048, added / 8192 x
+// 4096, all three kernels: 35.7 / 59.4 us; 8 and 20 warps 37.3 / 61.9; 16 and 10 warps 38.4 / 61.3).  Up to kFewUnits warps: 16
+// (300 x 4096, added: 12.2 us; 4 18.3 in blocks of eight warps; 32 13.2: more code to fetch).
 constexpr int kDeep = 4, kDeepest = 16;
+constexpr int kResident = 32, kResidentFew = 8;
 constexpr int64_t kFewUnits = 152 * 8;
 constexpr int kSortBlock = 1024;
 constexpr int kSortWarps = kSortBlock / 32;
-constexpr int kIds = 8;
+// Ids on their way at once; of a warp's last ones, fewer than 32 kIds, which cost more in code to fetch than in waiting, kLastIds
+// (300 / 4099 / 16411 / 40000 tokens, all three kernels, 8 / 4 / 2 / 1: 12.1 / 11.3 / 11.1 / 10.7, 13.7 / 13.9 / 13.7 / 13.6, 35.4 /
+// 34.8 / 34.8 / 35.9, 49.1 / 50.1 / 50.8 / 52.0 us).
+constexpr int kIds = 8, kLastIds = 2;
 constexpr int kMaxRange = 768;        // rows of a sorting block: they take 256 bytes of shared memory each
 constexpr int kJoinBlock = 128;
 constexpr int kTeams = kJoinBlock / 32;
@@ -48,33 +51,50 @@ constexpr int kFill = 8;
 constexpr int kZeroBytes = 8192;
 
 // ---- forward ----
+// A thread has kPer times 16 columns of a row, whose ids and then rows are on their way together.  Two where there are more of them
+// than threads of one each on the device at once (8192 x 4096 / 40000 x 800 / 4099 x 4096: 16.0 / 14.0 / 6.5 us, one each 16.3 /
+// 15.0 / 7.0, four 15.9 / 13.9 / 7.0; 1000 x 4096 / 17 x 2048: 2.6 / 1.3, one each 2.5 / 1.1).
+constexpr int64_t kOneEach = 152 * 2048;
+template <int kPer>
 __global__ void __launch_bounds__(kBlock) embed_fwd_kernel(const EmbedFwdArgs a, const Divider nc, bool wide) {
-    const uint32_t total = (uint32_t)a.M * nc.d, i = blockIdx.x * kBlock + threadIdx.x;
+    const uint32_t total = (uint32_t)a.M * nc.d, i0 = blockIdx.x * (kPer * kBlock) + threadIdx.x;
     wait_for_primary();
-    if (i >= total) return;
-    const uint32_t m = divide(i, nc);
-    const int64_t col = (int64_t)(i - m * nc.d) * 16, id = index_at(a.ids, a.wide, m);
-    uint32_t w[8] = {};
-    if (id >= 0 && id < a.V) {
+    uint32_t w[kPer][8];
+    int64_t id[kPer];
+    uint32_t col[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const uint32_t i = i0 + k * kBlock < total ? i0 + k * kBlock : total - 1, m = divide(i, nc);   // (the last one again: not stored)
+        col[k] = (i - m * nc.d) * 16;
+        id[k] = index_at(a.ids, a.wide, m);
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const bool in = id[k] >= 0 && id[k] < a.V;
+        load_words8(a.table + (in ? id[k] : 0) * a.C + col[k], wide, w[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const uint32_t i = i0 + k * kBlock;
         float x[16];
-        load_words8(a.table + id * a.C + col, wide, w);
-        unpack(w, x);
+        unpack(w[k], x);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[e] *= a.scale;
-        pack(x, w);
-    } else if (id >= a.V) {
+        pack(x, w[k]);
+        if (id[k] < 0 || id[k] >= a.V) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 0x7FFF7FFFu;
+            for (int e = 0; e < 8; ++e) w[k][e] = id[k] < 0 ? 0u : 0x7FFF7FFFu;
+        }
+        if (i < total) store_words8(a.out + (int64_t)i * 16, wide, w[k]);
     }
-    store_words8(a.out + (int64_t)i * 16, wide, w);
 }
 
 // ---- backward: sort ----
 // An id as a row of the table: itself, or -1 where it is none's.
 __device__ __forceinline__ int row_of(int32_t id) { return id; }
 __device__ __forceinline__ int row_of(int64_t id) { return id < 0 || id > 0x7FFFFFFF ? -1 : (int)id; }
-// f(token, id's row) for the tokens m0 + lane, m0 + lane + 32, ... below m1, kIds loads on their way at once; the whole
-// warp calls f together, with a row of -1 behind the last token.
+// f(token, id's row) for the tokens m0 + lane, m0 + lane + 32, ... below m1; the whole warp calls f together, with a row of -1
+// behind the last token.
 template <typename T, typename F>
 __device__ __forceinline__ void for_ids(const void* ids, int64_t m0, int64_t m1, int lane, F f) {
     int64_t m = m0;
@@ -86,16 +106,18 @@ __device__ __forceinline__ void for_ids(const void* ids, int64_t m0, int64_t m1,
 #pragma unroll
         for (int k = 0; k < kIds; ++k) f((int)m + 32 * k + lane, row_of(v[k]));
     }
-    if (m >= m1) return;
-    T v[kIds];
+#pragma unroll 1
+    for (; m < m1; m += 32 * kLastIds) {
+        T v[kLastIds];
 #pragma unroll
-    for (int k = 0; k < kIds; ++k) {   // (a load without a condition: behind a branch every load would wait for the one before it)
-        const int64_t at = m + 32 * k + lane;
-        v[k] = load_index(static_cast<const T*>(ids) + (at < m1 ? at : m1 - 1));
+        for (int k = 0; k < kLastIds; ++k) {   // (a load without a condition: behind a branch every load would wait for the one before it)
+            const int64_t at = m + 32 * k + lane;
+            v[k] = load_index(static_cast<const T*>(ids) + (at < m1 ? at : m1 - 1));
+        }
+#pragma unroll
+        for (int k = 0; k < kLastIds; ++k)
+            if (m + 32 * k < m1) f((int)m + 32 * k + lane, m + 32 * k + lane < m1 ? row_of(v[k]) : -1);
     }
-#pragma unroll
-    for (int k = 0; k < kIds; ++k)
-        if (m + 32 * k < m1) f((int)m + 32 * k + lane, m + 32 * k + lane < m1 ? row_of(v[k]) : -1);
 }
 
 // A block's rows are every B-th row of the table (B a power of two), so that rows that lie together, as frequent tokens' rows
@@ -114,7 +136,7 @@ __global__ void __launch_bounds__(kSortBlock) embed_sort_kernel(const EmbedBwdAr
     extern __shared__ __align__(8) Slot slots[];
     __shared__ int scan[kSortWarps];
     __shared__ int below_all;
-    const int R = by.R, t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int R = by.R, t = threadIdx.x, lane = t & 31, warp = __shfl_sync(kFull, t >> 5, 0);   // (the same for the warp, for the compiler)
     const unsigned b = blockIdx.x, mask = (1u << by.shift) - 1u, V = (unsigned)a.V;
     for (int i = t; i < kSortWarps * R; i += kSortBlock) slots[i] = Slot{0, 0u};
     if (t == 0) below_all = 0;
@@ -224,12 +246,13 @@ __device__ __forceinline__ void store_table(const EmbedBwdArgs& a, int row, int6
     *reinterpret_cast<uint4*>(a.dtable + (int64_t)row * a.C + col) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A block is one warp, so that all that its lanes have in common is so for the compiler too: addresses of entries, counts and
+// branches stay in uniform registers (16411 x 2048, added: 35.6 us; in blocks of two, four and eight warps 39.4, 39.3 and 40.0).
 template <bool kAdd, int kDeep>
-__global__ void __launch_bounds__(kBlock, kDeep == kDeepest ? 1 : 4) embed_chunks_kernel(const EmbedBwdArgs a, int slices) {
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), chunk = unit / slices;
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(32, kDeep == kDeepest ? kResidentFew : kResident) embed_chunks_kernel(const EmbedBwdArgs a, int slices) {
+    const int64_t unit = blockIdx.x, chunk = unit / slices;
+    const int lane = threadIdx.x;
     wait_for_primary();
-    if (chunk * kChunk >= a.M) return;
     const Entry e = entry_at(a, chunk * kChunk + lane);
     const int before = entry_at(a, chunk * kChunk - 1).row, behind = entry_at(a, (chunk + 1) * kChunk).row;
     int next = __shfl_down_sync(kFull, e.row, 1);
@@ -359,7 +382,8 @@ __global__ void __launch_bounds__(kJoinBlock) embed_join_kernel(const EmbedBwdAr
 int64_t embed_chunks(int64_t M) { return (M + kChunk - 1) / kChunk; }
 
 cudaError_t launch_embed_fwd(const EmbedFwdArgs& all, cudaStream_t s) {
-    const int64_t nc = all.C / 16, slab = (((int64_t)1 << 31) - kBlock) / nc;   // a launch's chunks are counted in 31 bits
+    const int64_t nc = all.C / 16, slab = (((int64_t)1 << 31) - 2 * kBlock) / nc;   // a launch's pieces are counted in 31 bits
+    const int per = all.M * nc > kOneEach ? 2 : 1;
     const Divider by = divider((uint32_t)nc);
     const bool wide = aligned32(all.table) && aligned32(all.out);
     for (int64_t m = 0; m < all.M; m += slab) {
@@ -367,7 +391,8 @@ cudaError_t launch_embed_fwd(const EmbedFwdArgs& all, cudaStream_t s) {
         a.M = all.M - m < slab ? all.M - m : slab;
         a.ids = static_cast<const char*>(all.ids) + m * (all.wide ? 8 : 4);
         a.out += m * a.C;
-        const cudaError_t e = launch_next(embed_fwd_kernel, (unsigned)((a.M * nc + kBlock - 1) / kBlock), kBlock, 0, s, a, by, wide);
+        const cudaError_t e = launch_next(per == 2 ? embed_fwd_kernel<2> : embed_fwd_kernel<1>,
+                                          (unsigned)((a.M * nc + per * kBlock - 1) / (per * kBlock)), kBlock, 0, s, a, by, wide);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -400,7 +425,7 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
     auto* const sums = chunks * slices <= kFewUnits
                            ? (a.accumulate ? embed_chunks_kernel<true, kDeepest> : embed_chunks_kernel<false, kDeepest>)
                            : (a.accumulate ? embed_chunks_kernel<true, kDeep> : embed_chunks_kernel<false, kDeep>);
-    e = launch_next(sums, (unsigned)((chunks * slices + kWarps - 1) / kWarps), kBlock, 0, s, a, slices);
+    e = launch_next(sums, (unsigned)(chunks * slices), 32, 0, s, a, slices);
     if (e != cudaSuccess) return e;
     const unsigned fills = a.accumulate ? 0u : (unsigned)((a.V + kFill - 1) / kFill);
     const int64_t joins = chunks > 1 ? chunks * slices : 0;   // one chunk: no row goes on behind it
