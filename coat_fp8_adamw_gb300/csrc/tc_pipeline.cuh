@@ -211,7 +211,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                  CUtensorMapFloatOOBfill);
 
-EncodeTiled encoder() {
+EncodeTiled driver_encoder() {
     static const EncodeTiled fn = []() -> EncodeTiled {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -222,6 +222,22 @@ EncodeTiled encoder() {
         return reinterpret_cast<EncodeTiled>(p);
     }();
     return fn;
+}
+
+// The driver wants a current context, which a thread that has made no call of the runtime but queries does not have.
+EncodeTiled encoder() {
+    if (!driver_encoder()) return nullptr;
+    return [](CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box, const cuuint32_t* elem, CUtensorMapInterleave interleave, CUtensorMapSwizzle swizzle,
+              CUtensorMapL2promotion promotion, CUtensorMapFloatOOBfill fill) -> CUresult {
+        auto encode = [&] {
+            return driver_encoder()(map, type, rank, base, dims, strides, box, elem, interleave, swizzle, promotion, fill);
+        };
+        CUresult r = encode();
+        int dev = 0;
+        if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+        return r;
+    };
 }
 
 // this translation unit's g_wait_timeouts, on the current device

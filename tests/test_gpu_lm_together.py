@@ -107,3 +107,97 @@ def test_the_tied_gradient_is_the_sum_of_both_ends():
     ref = embedding(a.table, a.ids, 4.0)
     assert ((a.x.double() - ref).abs() <= 2.0 ** -8 * ref.abs()).all()
     assert a.loss.dtype == F32
+
+
+def several(tokens):
+    """Both directions of the cross entropy and of the embedding, with a workspace of their own; their results."""
+    m, v, c = tokens, 2500, 192
+    x, w = randn(m, c, seed=tokens).to(BF), (randn(v, c, seed=tokens + 1) * 0.1).to(BF)
+    t = torch.randint(-1, v, (m,), generator=gen(tokens + 2), device="cuda")
+    g = torch.rand(m, generator=gen(tokens + 3), device="cuda")
+    ws = torch.empty(max(coat.coat_linear_cross_entropy_workspace_bytes(m, v),
+                         coat.coat_linear_cross_entropy_backward_workspace_bytes(m, v, c, 1024),
+                         coat.coat_embedding_backward_workspace_bytes(m, v, c)), dtype=U8, device="cuda")
+    out = [torch.zeros(s, dtype=d, device="cuda") for s, d in (((m,), F32), ((m,), F32), ((m, c), BF), ((v, c), BF), ((v, c), BF), ((m, c), BF))]
+
+    def calls(stream=None):
+        loss, lse, dx, dw, dtable, rows = out
+        coat.coat_linear_cross_entropy(x, w, t, loss, lse, ws, stream=stream)
+        coat.coat_linear_cross_entropy_backward(x, w, t, lse, g, dx, dw, ws, piece=1024, stream=stream)
+        coat.coat_embedding_backward(dx, t, 1.5, dtable, ws, stream=stream)
+        coat.coat_embedding(w, t, 2.0, rows, stream=stream)
+    return calls, out
+
+
+@pytest.mark.parametrize("threads", [False, True])
+def test_calls_on_several_streams_at_once(threads):
+    """As one by one, bit for bit, whichever streams they are on and whichever threads make the calls."""
+    import threading
+    work = [several(n) for n in (40, 700, 1500)]
+    want = []
+    for calls, out in work:
+        calls()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in out])
+        for o in out:
+            o.zero_()
+    streams = [torch.cuda.Stream() for _ in work]
+    torch.cuda.synchronize()
+    if threads:
+        def run(k):
+            for _ in range(20):
+                work[k][0](streams[k])
+        every = [threading.Thread(target=run, args=(k,)) for k in range(len(work))]
+        for th in every:
+            th.start()
+        for th in every:
+            th.join()
+    else:
+        for _ in range(20):
+            for (calls, _), s in zip(work, streams):
+                calls(s)
+    torch.cuda.synchronize()
+    for (_, out), ref in zip(work, want):
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))
+    assert coat.coat_kernel_wait_timeouts(reset=True) == 0
+
+
+@pytest.mark.parametrize("which", ["cross entropy", "its gradients", "linear", "weight gradient"])
+def test_the_first_call_of_a_thread(which):
+    """A thread that has done nothing on the device before has no current context of the driver's; the calls that lay out
+    copies by it take the device's."""
+    import threading
+    m, n, k = 256, 256, 256
+    g = gen(3)
+    xq, wq = (torch.randint(0, 100, (s, k), generator=g, device="cuda").to(U8) for s in (m, n))
+    x, w, dy = randn(m, k, seed=1).to(BF), randn(n, k, seed=2).to(BF), randn(m, n, seed=3).to(BF)
+    t, one = torch.arange(m, device="cuda") % n, torch.ones(m, device="cuda")
+    lse = linear_cross_entropy(x, w, t)[1].float()
+    scale = torch.ones(m, k // 128, device="cuda")
+    ws = torch.empty(1 << 24, dtype=U8, device="cuda")
+
+    def call(a, b):
+        if which == "cross entropy":
+            coat.coat_linear_cross_entropy(x, w, t, a[:m], b[:m], ws)
+        elif which == "its gradients":
+            coat.coat_linear_cross_entropy_backward(x, w, t, lse, one, a.view(BF)[:m * k].view(m, k), b.view(BF)[:n * k].view(n, k), ws)
+        elif which == "linear":
+            coat.coat_fp8_linear_group_quantize(xq, 1.0, wq, 1.0, 128, a.view(U8)[:m * n].view(m, n), b[:m * n // 128].view(m, n // 128))
+        else:
+            coat.coat_ckpt_weight_grad(dy, xq, scale, 128, a.view(BF)[:n * k].view(n, k), ws)
+    out = [torch.zeros(m * k, device="cuda") for _ in range(4)]
+    wrong = []
+
+    def run():
+        try:
+            call(*out[:2])
+        except Exception as e:   # a thread's exceptions do not reach the test by themselves
+            wrong.append(e)
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=run)
+    thread.start()
+    thread.join()
+    assert not wrong, wrong
+    call(*out[2:])
+    torch.cuda.synchronize()
+    assert out[0].any() and torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
