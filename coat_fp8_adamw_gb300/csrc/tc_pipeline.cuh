@@ -211,7 +211,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                  CUtensorMapFloatOOBfill);
 
-EncodeTiled driver_encoder() {
+EncodeTiled plain_encoder() {
     static const EncodeTiled fn = []() -> EncodeTiled {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -224,14 +224,14 @@ EncodeTiled driver_encoder() {
     return fn;
 }
 
-// The driver wants a current context, which a thread that has made no call of the runtime but queries does not have.
+// The encoder wants a current CUDA context, which a thread that has made no call of the runtime but queries does not have.
 EncodeTiled encoder() {
-    if (!driver_encoder()) return nullptr;
+    if (!plain_encoder()) return nullptr;
     return [](CUtensorMap* map, CUtensorMapDataType type, cuuint32_t rank, void* base, const cuuint64_t* dims, const cuuint64_t* strides,
               const cuuint32_t* box, const cuuint32_t* elem, CUtensorMapInterleave interleave, CUtensorMapSwizzle swizzle,
               CUtensorMapL2promotion promotion, CUtensorMapFloatOOBfill fill) -> CUresult {
         auto encode = [&] {
-            return driver_encoder()(map, type, rank, base, dims, strides, box, elem, interleave, swizzle, promotion, fill);
+            return plain_encoder()(map, type, rank, base, dims, strides, box, elem, interleave, swizzle, promotion, fill);
         };
         CUresult r = encode();
         int dev = 0;

@@ -164,7 +164,7 @@ def test_calls_on_several_streams_at_once(threads):
 
 @pytest.mark.parametrize("which", ["cross entropy", "its gradients", "linear", "weight gradient"])
 def test_the_first_call_of_a_thread(which):
-    """A thread that has done nothing on the device before has no current context of the driver's; the calls that lay out
+    """A thread that has done nothing on the device before has no current CUDA context; the calls that lay out
     copies by it take the device's."""
     import threading
     m, n, k = 256, 256, 256
