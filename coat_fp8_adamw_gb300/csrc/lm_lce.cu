@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "ckpt_kernels.h"
+#include "divide.h"
 #include "lm_device.cuh"
 #include "lm_kernels.h"
 #include "tc_pipeline.cuh"
@@ -98,6 +99,7 @@ struct Job {
     uint16_t* out;           // kFewDz, kDx (last piece): bf16, rows ld apart (kDz and kDw store by their tensor map)
     int64_t ld;
     float* sums;             // [parts][out's shape] float32: of parts, or of the pieces so far
+    Divider by_tiles, by_band, by_last, by_parts;   // tm tn; kBand tn; the last band's rows; parts
     int32_t first, last;     // sums: the first piece, which writes them; the last one of a product in one part, which ends in out
 };
 // The jobs of a launch, the one with the longer items first.  Of its items every pair has one in turn; `ahead` pairs have one
@@ -108,6 +110,7 @@ struct Work {
     int32_t slot, stages;    // bytes of a stage, and their number
     int32_t pairs, ahead;
     int64_t items[2], extra;
+    Divider by_pairs, by_lot;   // pairs; those that are not ahead
     // rows of the logits
     const void* targets;
     int32_t wide, V;
@@ -148,17 +151,17 @@ struct Item {
     int32_t from, to;        // steps
     int64_t m, n;            // tile
 };
-// A pair's way through the items: the first job's in turn, those that make up for one less of them, and the rest.  In 32 bits
-// and with what does not change taken once: 64-bit divisions took 1500 clocks an item, in every role.
+// A pair's way through the items: the first job's in turn, those that make up for one less of them, and the rest.  Every role
+// reckons its own, so without a division (8192 x 32000 x 4096 with 64-bit divisions: 1500 clocks an item; 1000 x 100000 x 128 with
+// 32-bit ones: 730).
 struct Walk {
-    uint32_t pair, own, behind, lot, mine;
+    uint32_t pair, own, behind, mine;
     __device__ __forceinline__ Walk(const Work& w, uint32_t p) {
         const uint32_t P = (uint32_t)w.pairs, ahead = (uint32_t)w.ahead;
         pair = p;
-        own = ((uint32_t)w.items[0] - p + P - 1u) / P;   // of the first job
+        own = divide((uint32_t)w.items[0] + P - 1u - p, w.by_pairs);   // of the first job
         behind = p - ahead;
-        lot = P - ahead;
-        mine = p >= ahead && behind < (uint32_t)w.extra ? ((uint32_t)w.extra - behind + lot - 1u) / lot : 0u;
+        mine = p >= ahead && behind < (uint32_t)w.extra ? divide((uint32_t)w.extra - behind + P - ahead - 1u, w.by_lot) : 0u;
     }
     // the k-th item; false: there is none
     __device__ __forceinline__ bool item(uint32_t k, const Work& w, Item& it) const {
@@ -169,22 +172,22 @@ struct Walk {
             t = pair + k * P;
         } else {
             k -= own;
-            t = k < mine ? behind + k * lot : (uint32_t)w.extra + (k - mine) * P + pair;
+            t = k < mine ? behind + k * (P - (uint32_t)w.ahead) : (uint32_t)w.extra + (k - mine) * P + pair;
             if (t >= (uint32_t)w.items[1]) return false;
         }
         const Job& j = w.job[it.job];
-        const uint32_t tm = (uint32_t)j.tm, tn = (uint32_t)j.tn, tiles = tm * tn;
         it.part = 0;
         it.from = 0;
         it.to = j.steps;
         if (j.parts > 1) {
-            it.part = (int32_t)(t / tiles);
-            t -= (uint32_t)it.part * tiles;
-            it.from = (int32_t)((int64_t)j.steps * it.part / j.parts);
-            it.to = (int32_t)((int64_t)j.steps * (it.part + 1) / j.parts);
+            it.part = (int32_t)divide(t, j.by_tiles);
+            t -= (uint32_t)it.part * j.by_tiles.d;
+            it.from = (int32_t)divide((uint32_t)(j.steps * it.part), j.by_parts);   // (steps < 2^25, parts <= 32)
+            it.to = (int32_t)divide((uint32_t)(j.steps * (it.part + 1)), j.by_parts);
         }
-        const uint32_t band = t / (kBand * tn), top = band * kBand;
-        const uint32_t rows = tm - top < kBand ? tm - top : kBand, r = t - top * tn, n = r / rows;
+        const uint32_t band = divide(t, j.by_band), top = band * kBand, r = t - band * j.by_band.d;
+        const bool whole = (uint32_t)j.tm - top >= kBand;
+        const uint32_t rows = whole ? kBand : j.by_last.d, n = whole ? r / kBand : divide(r, j.by_last);
         it.m = top + (r - n * rows);
         it.n = n;
         return true;
@@ -1036,15 +1039,22 @@ cudaError_t launch_work(Work& w, const Maps& maps, cudaStream_t s) {
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     int64_t cost[2] = {0, 0};
     for (int i = 0; i < w.jobs; ++i) {
-        w.items[i] = w.job[i].tm * w.job[i].tn * w.job[i].parts;
+        Job& j = w.job[i];
+        w.items[i] = j.tm * j.tn * j.parts;
+        j.by_tiles = divider((uint32_t)(j.tm * j.tn));
+        j.by_band = divider((uint32_t)(kBand * j.tn));
+        j.by_last = divider(j.tm % kBand ? (uint32_t)(j.tm % kBand) : kBand);
+        j.by_parts = divider((uint32_t)j.parts);
         cost[i] = item_cost(w.job[i].steps, w.job[i].parts, w.job[i].bn);
     }
     if (w.jobs < 2) w.items[1] = 0;
-    if (w.items[0] + w.items[1] >= (int64_t)1 << 31) return cudaErrorInvalidValue;   // (2^40 logits are 2^27 tiles)
+    if (w.items[0] + w.items[1] >= ((int64_t)1 << 31) - 2 * kPairs) return cudaErrorInvalidValue;   // (2^40 logits are 2^27 tiles)
     const Split sp = split_of(w.items[0], cost[0], w.items[1], cost[1], pairs);
     w.pairs = (int32_t)sp.pairs;
     w.ahead = (int32_t)sp.ahead;
     w.extra = sp.extra;
+    w.by_pairs = divider((uint32_t)sp.pairs);
+    w.by_lot = divider((uint32_t)(sp.pairs - sp.ahead));
     int bn = 0;
     for (int i = 0; i < w.jobs; ++i) bn = w.job[i].bn > bn ? w.job[i].bn : bn;
     w.slot = slot_bytes(bn);
