@@ -278,11 +278,68 @@ __device__ __forceinline__ void add_to_rest(float& top, float& rest, float mx, f
     top = mx;
 }
 
+// Of a tile with all its columns, the largest of the chunks and the rest of the sum.  Maxima first, then exponentials, the chunks side
+// by side and without a branch: with only two warps of a scheduler their chains of additions are what takes time (1000 x 100000 x
+// 128: 47 us, chunk by chunk 52; other tiles, whose chunks may not be there, go chunk by chunk: 2048 x 512 x 1024 8.6 us, side by
+// side 8.9).
+__device__ __forceinline__ float2 stats_of_all(const Logits<kChunks>& l) {
+    float most[kChunks];
+    uint64_t sums[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        most[c] = -INFINITY;
+        sums[c] = pk(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int e = 0; e < kChunk; e += 2)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) most[c] = max3(most[c], __uint_as_float(l.z[c][e]), __uint_as_float(l.z[c][e + 1]));
+    float top = most[0];
+#pragma unroll
+    for (int c = 1; c < kChunks; ++c) top = fmaxf(top, most[c]);
+    const float ref = top == -INFINITY ? 0.0f : top;   // a row of -inf
+#pragma unroll
+    for (int e = 0; e < kChunk; e += 2)
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            float x, y;
+            exp2_of(l.z[c][e], l.z[c][e + 1], pk(-ref, -ref), x, y);
+            sums[c] = add2(sums[c], pk(x, y));
+        }
+    float rest = 0.0f;
+    bool one = false;   // the largest one's 1 has been left out, of its chunk's sum
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const bool here = !one && most[c] == top;
+        rest += here ? sum2(sums[c]) - 1.0f : sum2(sums[c]);
+        one |= here;
+    }
+    return make_float2(top, rest);
+}
+
 // columns col0 .. end - 1 of the tile are logits
 __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const RowValues& r, Logits<kChunks>& l, int64_t row, int64_t col0, int64_t end,
                                              int half, int64_t part) {
-    float top = -INFINITY, rest = kNoRest;
     const int cols = (int)(end - col0), target = r.target - (int)col0;   // in the tile
+    auto say_target = [&](int c, int off) {
+        const bool has = target >= off && target < off + kChunk;
+        if (!__any_sync(kFull, has)) return;
+        float z = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kChunk; ++e)
+            if (off + e == target) z = __uint_as_float(l.z[c][e]);
+        if (has && target < cols && row < j.rows) w.target_logit[row] = z;
+    };
+    float top = -INFINITY, rest = kNoRest;
+    if (cols == kBN) {
+        if (__any_sync(kFull, target >= 0 && target < kBN && (target >> 6 & 1) == half)) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) say_target(c, chunk_off(half, c));
+        }
+        const float2 f = stats_of_all(l);
+        if (row < j.rows) w.stats[part * w.stats_ld + row] = f;
+        return;
+    }
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
         const int off = chunk_off(half, c);
@@ -293,14 +350,7 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const 
             for (int e = 0; e < kChunk; ++e)
                 if (off + e >= cols) v[e] = 0xFF800000u;   // -inf: not a column
         }
-        const bool has = target >= off && target < off + kChunk;
-        if (__any_sync(kFull, has)) {
-            float z = 0.0f;
-#pragma unroll
-            for (int e = 0; e < kChunk; ++e)
-                if (off + e == target) z = __uint_as_float(v[e]);
-            if (has && target < cols && row < j.rows) w.target_logit[row] = z;
-        }
+        say_target(c, off);
         float mx = top;
 #pragma unroll
         for (int e = 0; e < kChunk; e += 2) mx = max3(mx, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
