@@ -442,3 +442,37 @@ def test_few_tokens_in_tiles_of_fewer_rows_of_the_weight(M, V):
     near(lse, want, torch.full_like(want, (V / 32 + 64 + 8) * 4 * E + 4 * E * 20), "lse")
     near(loss, torch.where(t < 0, 0.0, want - w[t.clamp_min(0), 7].double()),
          torch.where(t < 0, 0.0, (V / 32 + 64 + 8) * 4 * E + 4 * E * 24).double(), "loss")
+
+
+@pytest.mark.parametrize("V", [19456, 19451])
+def test_tiles_with_all_their_columns(V):
+    """Two waves of tiles of 256 x 256, the last one of 251 columns: targets in every place of a tile, and rows whose logits are all
+    or in part -inf, not numbers, or far ahead of each other."""
+    M, C = 512, 64
+    x, w, t = inputs(M, V, C, 31)
+    t = (torch.arange(M, device="cuda") * 38 + 11) % V          # every column of a tile is someone's target
+    t[::2] = torch.arange(M // 2, device="cuda") + V - 256
+    check_forward(x, w, t)
+    good = forward(x, w, t)
+    w[:, 60:] = 0
+    w[:, 60] = -3e38
+    w[1::2, 61] = -3e38
+    w[::3, 62] = 10.0
+    y = x.clone()
+    y[:, 60:] = 0
+    plain = forward(y, w, t)
+    for r, c, v in ((3, 60, 3e38), (4, 61, 3e38), (5, 62, 2.0), (6, 0, float("nan")), (7, 1, float("inf"))):
+        y[r, c] = v
+    loss, lse = forward(y, w, t)
+    assert lse[3] == -float("inf") and not loss[3].isfinite()
+    z = y.double() @ w.double().T
+    size = y.abs().double() @ w.abs().double().T
+    for r, keep in ((4, torch.arange(V, device="cuda") % 2 == 0), (5, torch.ones(V, dtype=torch.bool, device="cuda"))):
+        ref = torch.logsumexp(z[r][keep], 0)
+        err = (C + 8) * 2.0 ** -22 * size[r][keep].amax() + (V / 32 + 64 + 100) * 4 * E + 4 * E * ref.abs()
+        assert (lse[r].double() - ref).abs() <= err
+    assert loss[[6, 7]].isnan().all() and lse[[6, 7]].isnan().all()
+    rest = torch.ones(M, dtype=torch.bool, device="cuda")
+    rest[3:8] = False
+    assert torch.equal(loss[rest], plain[0][rest]) and torch.equal(lse[rest], plain[1][rest])
+    assert good[0].isfinite().all() and good[1].isfinite().all()
