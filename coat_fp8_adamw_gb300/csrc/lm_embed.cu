@@ -43,8 +43,10 @@ constexpr int kSortWarps = kSortBlock / 32;
 // 34.8 / 34.8 / 35.9, 49.1 / 50.1 / 50.8 / 52.0 us).
 constexpr int kIds = 8, kLastIds = 2;
 constexpr int kMaxRange = 768;        // rows of a sorting block: they take 256 bytes of shared memory each
-constexpr int kJoinBlock = 128;
-constexpr int kTeams = kJoinBlock / 32;
+// Warps that add up a row's shares.  Most blocks find that their chunk begins no such row; with zeros to fill there are more blocks,
+// and what they take counts less (16411 x 2048 / 8192 x 4096, added, 1 / 2 / 4: 34.9 / 33.8 / 34.8, 30.1 / 30.1 / 32.1 us; 8192 x
+// 4096 written, 2 / 4 / 8: 62.4 / 59.7 / 62.0).
+constexpr int teams_of(bool add) { return add ? 2 : 4; }
 // Rows of a filling block.  More copies at once per SM are slower: 8192 tokens, 32000 x 4096, all three kernels: 60 us with 4
 // and 8, 62 with 16 and 32, 66 with 64, 67 with 128.
 constexpr int kFill = 8;
@@ -326,7 +328,7 @@ __device__ __noinline__ int64_t chunks_of_row(const EmbedBwdArgs& a, int row, in
 // Zeros over the rows without a token: kFill rows per block, one thread for each, whose copies read
 // the same zeros in shared memory.
 __device__ __forceinline__ void fill_rows(const EmbedBwdArgs& a, const Ranges& by, int64_t block, float* zeros) {
-    for (int i = threadIdx.x; i < kZeroBytes / 4; i += kJoinBlock) zeros[i] = 0.0f;
+    for (int i = threadIdx.x; i < kZeroBytes / 4; i += blockDim.x) zeros[i] = 0.0f;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the copies read them
     __syncthreads();
     const int64_t row = block * kFill + threadIdx.x;
@@ -342,7 +344,8 @@ __device__ __forceinline__ void fill_rows(const EmbedBwdArgs& a, const Ranges& b
 
 // The first `fills` blocks fill.  Of the others each has a chunk and 256 columns, and its warps add up a row's shares.
 template <bool kAdd>
-__global__ void __launch_bounds__(kJoinBlock) embed_join_kernel(const EmbedBwdArgs a, int slices, const Ranges by, unsigned fills) {
+__global__ void __launch_bounds__(32 * teams_of(kAdd)) embed_join_kernel(const EmbedBwdArgs a, int slices, const Ranges by, unsigned fills) {
+    constexpr int kTeams = teams_of(kAdd);
     __shared__ __align__(16) float part[kAdd ? (kTeams - 1) * kSlice : kZeroBytes / 4];
     wait_for_primary();
     if (!kAdd && blockIdx.x < fills) {
@@ -430,8 +433,8 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
     const unsigned fills = a.accumulate ? 0u : (unsigned)((a.V + kFill - 1) / kFill);
     const int64_t joins = chunks > 1 ? chunks * slices : 0;   // one chunk: no row goes on behind it
     if (fills + joins == 0) return cudaSuccess;
-    return launch_next(a.accumulate ? embed_join_kernel<true> : embed_join_kernel<false>, (unsigned)(fills + joins), kJoinBlock, 0, s, a,
-                       slices, by, fills);
+    return launch_next(a.accumulate ? embed_join_kernel<true> : embed_join_kernel<false>, (unsigned)(fills + joins),
+                       32 * teams_of(a.accumulate), 0, s, a, slices, by, fills);
 }
 
 }  // namespace coat
