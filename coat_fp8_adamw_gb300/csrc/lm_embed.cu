@@ -419,7 +419,8 @@ cudaError_t launch_embed_bwd(const EmbedBwdArgs& a, cudaStream_t s) {
     const Ranges by = ranges_of(a.V);
     const size_t smem = (size_t)kSortWarps * (size_t)by.R * sizeof(Slot);
     auto* const sort = a.wide ? embed_sort_kernel<int64_t> : embed_sort_kernel<int32_t>;
-    cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the most of any table, not this one's: another thread, whose table is another one, may set it before this one launches
+    cudaError_t e = cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortWarps * kMaxRange * (int)sizeof(Slot));
     if (e != cudaSuccess) return e;
     e = launch_next(sort, 1u << by.shift, kSortBlock, smem, s, a, by);
     if (e != cudaSuccess) return e;
