@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const ColumnSum first,
 }
 
 constexpr size_t kSmem = 227u << 10;   // shared memory per SM, and at most per block
+constexpr size_t kMostDynamic = kSmem - 2048;
 
 Shape team_shape(int64_t N) {
     const int T = 32 * (int)((N + 32 * kE - 1) / (32 * kE)), teams = T >= 256 ? 1 : 256 / T;
@@ -414,7 +415,7 @@ Shape bwd_shape(int64_t N, bool res) {
     // iterations in the ring: 8192 x 4096 takes 58 us with two, 44 with three or four; one block per SM (T > 320) wants
     // four: 8192 x 8192 69 us with three, 66 with four; fewer where a row is too wide
     sh.depth = sh.T > 320 ? 4 : 3;
-    while (sh.depth > 2 && smem_of(sh) + 2048 > kSmem) --sh.depth;
+    while (sh.depth > 2 && smem_of(sh) > kMostDynamic) --sh.depth;
     return sh;
 }
 // Blocks that run at once, so that the grid is one wave: by registers (`regs` per thread, a multiple of eight; each of the
@@ -433,11 +434,12 @@ int64_t bwd_blocks(int64_t M, int64_t N, bool res, int sms) {
     return blocks_of(M, sh, sh.T <= 320 ? 96 : sh.T <= 512 ? 128 : 64, sms);
 }
 
-// more than the 48 KB that every kernel may have, its static part (under 1 KB) included
+// More than the 48 KB that every kernel may have, its static part (under 1 KB) included.  The most of any width, not this
+// call's: another thread, whose rows are narrower, may set it before this one launches.
 template <typename F>
 cudaError_t allow_smem(F* kernel, size_t bytes) {
     return bytes <= (47u << 10) ? cudaSuccess
-                                : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+                                : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostDynamic);
 }
 
 template <bool kRes>

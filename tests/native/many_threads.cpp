@@ -43,4 +43,21 @@ int64_t embed_at_once(decltype(&coat_embedding_backward) fn, const EmbedCall* ca
     });
 }
 
+struct NormCall {
+    const uint16_t* dy;
+    const uint8_t* q;
+    const float *scale, *rstd, *weight;
+    int64_t M, N;
+    uint16_t *dx, *dweight;
+    void* workspace;
+    size_t workspace_bytes;
+    void* stream;
+};
+int64_t norm_at_once(decltype(&coat_rmsnorm_ckpt_backward) fn, const NormCall* calls, int threads, int64_t times) {
+    return at_once(threads, times, [=](int k) {
+        const NormCall& c = calls[k];
+        return fn(c.dy, c.q, c.scale, c.rstd, c.weight, nullptr, c.M, c.N, 16, c.dx, c.dweight, c.workspace, c.workspace_bytes, c.stream);
+    });
+}
+
 }  // extern "C"

@@ -68,3 +68,29 @@ def test_embedding_gradients_of_several_tables(native):
     torch.cuda.synchronize()
     at_once(native.embed_at_once, "coat_embedding_backward", calls, out, 5000)
     del keep
+
+
+class NormCall(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("dy", "q", "scale", "rstd", "weight")] + [("M", I), ("N", I), ("dx", P), ("dweight", P),
+                                                                            ("workspace", P), ("bytes", N), ("stream", P)]
+
+
+def test_norm_gradients_of_several_widths(native):
+    """The backward kernel's shared memory goes by the width: 52, 96 and 128 KB here, of the same kernel."""
+    M, G = 20, 16
+    calls, out, keep = [], [], []
+    for width in (4096, 6144, 8192):
+        x, w, dy = randn(M, width, seed=width).to(BF), torch.ones(width, device="cuda"), randn(M, width, seed=width + 1).to(BF)
+        y, q = unwritten(M, width), unwritten(M, width, dtype=U8)
+        scale, rstd = torch.empty(M, width // G, device="cuda"), torch.empty(M, device="cuda")
+        coat.coat_rmsnorm_ckpt(x, w, 1e-5, G, y, q, scale, rstd)
+        dx, dw = unwritten(M, width), unwritten(width)
+        ws = workspace(coat.coat_rmsnorm_ckpt_backward_workspace_bytes(M, width))
+        stream = torch.cuda.Stream()
+        keep += [w, dy, q, scale, rstd, ws, stream]
+        calls.append(NormCall(dy.data_ptr(), q.data_ptr(), scale.data_ptr(), rstd.data_ptr(), w.data_ptr(), M, width, dx.data_ptr(),
+                              dw.data_ptr(), ws.data_ptr(), ws.numel(), stream.cuda_stream))
+        out.append([dx, dw])
+    torch.cuda.synchronize()
+    at_once(native.norm_at_once, "coat_rmsnorm_ckpt_backward", calls, out, 5000)
+    del keep
