@@ -33,6 +33,7 @@ namespace {
 
 using namespace ckpt;
 using lm::index_at;
+using lm::load_index;
 
 constexpr int kBM = 128;                       // rows per CTA (the pair's MMA has M = 256)
 constexpr int kBK = 64;                        // of the summed index per stage: 128 bytes
@@ -877,36 +878,63 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
 // The gradient of a target's logit is -g (1 - e^(z - lse)), which is -g for most tokens, and with a mean over the tokens g is
 // the same for all of them: rounded to bf16, they would all be off by the same share of themselves, up to 2^-8, and dx and dW
 // with them (8192 x 32000 x 4096, a mean over the tokens: 2.0e-3 to 2.9e-3 off by the number of tokens, so 2.0e-3).  So dz is
-// stored times a factor within 1 +- 2^-8, with which the g of the first token that has one is a bf16 value, and the products
-// are multiplied by its reciprocal.  (Of the first 1024 tokens; without one, or if
-// it is not a number to divide by, 1.)
-__device__ __forceinline__ void unit_of(const void* targets, int32_t wide, const float* dloss, int64_t M, int lane, float* unit) {
-    float f = 1.0f;
-    for (int64_t m = lane; m - lane < M && m < 1024; m += 32) {
-        float g = 0.0f;
-        if (m < M && index_at(targets, wide, m) >= 0) g = static_cast<const volatile float*>(dloss)[m];
-        const uint32_t some = __ballot_sync(kFull, fabsf(g) > 0x1p-100f && fabsf(g) < 0x1p100f);
-        if (some != 0u) {
-            g = __shfl_sync(kFull, g, __ffs(some) - 1);
-            f = __uint_as_float(bf16x2(g, 0.0f) << 16) / g;
-            break;
+// stored times a factor within 1 +- 2^-8, with which the g of the first token that has a target and a g between 2^-100 and 2^100
+// in size is a bf16 value, and the products are multiplied by its reciprocal.  (Without such a token, 1.)  A block of its own
+// looks for that token, kUnitAhead a thread at once, since a long prompt without targets may come first (2^20 tokens, none with
+// a target: 0.9 us for 2048 of them).
+constexpr int kUnitAhead = 8;
+__device__ __forceinline__ void unit_of(const void* targets, int32_t wide, const float* dloss, int64_t M, float* unit) {
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
+    __shared__ uint32_t first;
+    if (threadIdx.x == 0) first = kNone;
+    __syncthreads();
+    uint32_t mine = kNone;
+    float own = 1.0f;
+    for (int64_t m0 = 0; m0 < M; m0 += kUnitAhead * blockDim.x) {
+        int64_t at[kUnitAhead], t[kUnitAhead];
+        float g[kUnitAhead];
+#pragma unroll
+        for (int k = 0; k < kUnitAhead; ++k) {   // (the last token again: no load behind a branch, see lm_embed.cu)
+            const int64_t m = m0 + k * blockDim.x + threadIdx.x;
+            at[k] = m < M ? m : M - 1;
+            g[k] = static_cast<const volatile float*>(dloss)[at[k]];
         }
+        if (wide) {
+#pragma unroll
+            for (int k = 0; k < kUnitAhead; ++k) t[k] = load_index(static_cast<const int64_t*>(targets) + at[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kUnitAhead; ++k) t[k] = load_index(static_cast<const int32_t*>(targets) + at[k]);
+        }
+#pragma unroll
+        for (int k = kUnitAhead - 1; k >= 0; --k)
+            if (t[k] >= 0 && fabsf(g[k]) > 0x1p-100f && fabsf(g[k]) < 0x1p100f) {
+                mine = (uint32_t)at[k];
+                own = g[k];
+            }
+        const uint32_t lowest = __reduce_min_sync(kFull, mine);
+        if ((threadIdx.x & 31) == 0) atomicMin(&first, lowest);
+        if (__syncthreads_or(mine != kNone)) break;
     }
-    if (lane == 0) {
+    if (first == kNone ? threadIdx.x == 0 : mine == first) {
+        const float f = first == kNone ? 1.0f : __uint_as_float(bf16x2(own, 0.0f) << 16) / own;
         unit[0] = f;
         unit[1] = 1.0f / f;
     }
 }
 
-// xt[c][m] = x[m][c]: tiles of 64 x 64 through shared memory.  (xt's rows are whole 16-byte units; what lies behind their M
-// elements is not read.)
+// xt[c][m] = x[m][c]: tiles of 64 x 64 through shared memory, behind a block that finds the unit.  (xt's rows are whole 16-byte
+// units; what lies behind their M elements is not read.)
 __global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, int64_t x_ld, int64_t M, int64_t C, uint16_t* xt, int64_t ld,
                                                             const void* targets, int32_t wide, const float* dloss, float* unit) {
     __shared__ uint16_t tile[64][66];
-    const int64_t across = (M + 63) / 64, m0 = blockIdx.x % across * 64, c0 = blockIdx.x / across * 64;
+    const int64_t across = (M + 63) / 64, i0 = (int64_t)blockIdx.x - 1, m0 = i0 % across * 64, c0 = i0 / across * 64;
     wait_for_primary();
     dependents_may_start();
-    if (blockIdx.x == 0 && threadIdx.x < 32) unit_of(targets, wide, dloss, M, (int)threadIdx.x, unit);
+    if (blockIdx.x == 0) {
+        unit_of(targets, wide, dloss, M, unit);
+        return;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = threadIdx.x + 256 * h, r = i >> 3, c = (i & 7) * 8;
@@ -1199,7 +1227,7 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
     const Parts parts = parts_of(a.M, a.piece, a.C);
     float* const dw_sums = a.sums + lce_dx_sums(a.M, a.V, a.C, a.piece);
     const bool dx_sums = parts.dx > 1 || a.piece < a.V;
-    cudaError_t e = launch_next(lce_transpose_kernel, (unsigned)(up(a.M, 64) * up(a.C, 64)), 256, 0, s, a.x, a.x_ld, a.M, a.C,
+    cudaError_t e = launch_next(lce_transpose_kernel, (unsigned)(1 + up(a.M, 64) * up(a.C, 64)), 256, 0, s, a.x, a.x_ld, a.M, a.C,
                                 a.xt, lce_xt_ld(a.M), a.targets, a.wide, a.dloss, a.unit);
     if (e != cudaSuccess) return e;
     for (int64_t v0 = 0; v0 < a.V; v0 += a.piece) {

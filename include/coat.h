@@ -505,8 +505,9 @@ size_t coat_linear_cross_entropy_workspace_bytes(int64_t M, int64_t V);
 /*
  * Its gradients, with dloss and dlse the gradients of loss and lse:
  *   dz[m, v] = e^(z[m, v] - lse[m]) (dloss[m] + dlse[m]) - [v = targets[m]] dloss[m],
- *   rounded to bf16 (in units of the first non-zero dloss, so that a dloss that is
- *   the same for all tokens is not rounded);  dx = dz W;  dweight = dz^T x.
+ *   rounded to bf16 (in units of the dloss of the first token with a target whose
+ *   dloss lies between 2^-100 and 2^100 in size, so that one that is the same for
+ *   all tokens is not rounded);  dx = dz W;  dweight = dz^T x.
  *   x, weight, targets as above;  lse [M] as the forward pass left it;  dloss [M]
  *   float32 in (of a token without a target it does not count);  dlse [M] float32
  *   in, or NULL: zeros;  dx [M x C], dweight [V x C] bf16 out.
