@@ -207,11 +207,11 @@ class Decoder:
 
     @torch.no_grad()
     def loss_and_gradients(self, ids, targets):
-        """The mean loss of the tokens with a target (the others' is negative), and all gradients in self.grad."""
+        """The mean loss of the tokens with a target (the others' is negative; without any, 0), and all gradients in self.grad."""
         loss, lse, y, kept, last = self.forward(ids, targets)
         self.kept_bytes = sum(c.bytes() for block in kept for c in block if isinstance(c, Checkpoint)) + last.bytes()
         dloss = (targets >= 0).float()
-        dloss /= dloss.sum()
+        dloss /= dloss.sum().clamp_min(1)
         self.backward(ids, targets, dloss, lse, y, kept, last)
         return (loss * dloss).sum()
 

@@ -89,3 +89,16 @@ def test_masks_change_from_step_to_step_and_not_within_one(example):
     model.step(ids, targets, lr=0.0)
     assert torch.equal(model.rng[:, 1], before[:, 1] + len(before)) and torch.equal(model.rng[:, 0], before[:, 0])
     assert len(set(torch.cat((before, model.rng))[:, 1].tolist())) == 2 * len(before)
+
+
+@pytest.mark.parametrize("tied", [False, True])
+def test_a_batch_without_a_target(example, tied):
+    """Padding alone: loss 0 and zero gradients, and the optimizer's step leaves numbers."""
+    cfg = example.Config(layers=1, width=256, heads=4, kv_heads=2, hidden=688, vocab=64, seq=32, group=16, dropout=0.1, tied=tied)
+    model = example.Decoder(cfg, 128)
+    ids, targets = example.batch(cfg, model.M, 1)
+    targets.fill_(-100)
+    model.grad.fill_(float("nan"))
+    assert model.loss_and_gradients(ids, targets).item() == 0.0 and not model.grad.any()
+    model.step(ids, targets)
+    assert model.flat.isfinite().all()
