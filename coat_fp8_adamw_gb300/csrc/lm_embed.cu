@@ -3,15 +3,17 @@
 //   forward   out[m] = RN(scale table[ids[m]]); a negative id gives zeros, one past the table NaN
 //   backward  dtable[v] = RN(scale sum over m with ids[m] = v of dout[m] (+ dtable[v]))
 //
-// Backward in three kernels, sums in float32 and in a fixed order (that of the tokens, chunk by chunk):
+// Backward in three kernels, sums in float32 and in an order that the ids alone decide (within a chunk that of the tokens; then
+// the chunks' shares, which teams_of warps take in turn; then those warps' sums):
 //   sort    the tokens by their row of the table, stably: block b has rows of its own (every B-th), walks all M ids (they
 //           are few bytes) and counts those of the blocks before it, which is where its part of the sorted order begins, so
 //           that no block waits for another;
 //   chunks  the sorted order in chunks of 32 tokens, a warp for each and 256 columns: rows that begin and end in the chunk
 //           are finished; of one that goes on the chunk's share goes to the workspace, so that the work of a row with
 //           many tokens (text has some that are a tenth of all) goes to many warps;
-//   join    the rows that go on: their shares are added up; and rows without a token become zeros, unless the gradient is
-//           added to what is there.
+//   join    the rows that go on: their shares are added up, by 4 warps, or 2 where the gradient is added to what is there (so
+//           that a long row written, and the same one added to zeros, may differ in float32's last bits); and rows without
+//           a token become zeros, unless the gradient is added.
 #include <cstdint>
 
 #include "ckpt_kernels.h"

@@ -478,7 +478,11 @@ coat_status coat_embedding(const uint16_t *table, const void *ids, int32_t wide_
  * weight too: rows without a token are then not touched; otherwise they become
  * zeros).  Ids outside [0, V) have no gradient.
  *   dout [M x C] bf16, ids [M] in;  dtable [V x C] bf16 out (and in).
- * The sum is taken in float32 in the order of the tokens, in chunks of up to 32.
+ * The sum is taken in float32, in an order that the ids alone decide: the tokens, sorted
+ * by row, are cut every 32; a row's tokens between two cuts are added in their order, to
+ * c0, c1, ...; these to W sums, s0 = c0 + c1 + c(1+W) + ..., st = c(1+t) + c(1+t+W) + ...;
+ * and these to s0 + s1 + ....  W is 4, or 2 where `accumulate` is not 0, so that a row of
+ * many tokens added to zeros may differ in float32's last bits from one that is written.
  */
 coat_status coat_embedding_backward(const uint16_t *dout, const void *ids, int32_t wide_ids, float scale,
                                     int64_t M, int64_t V, int64_t C, int32_t accumulate, uint16_t *dtable,

@@ -237,3 +237,34 @@ def test_refusals():
     with pytest.raises(TypeError, match="workspace"):
         coat.coat_embedding_backward(out, ids, 1.0, table, ws.cpu())
     assert ws.dtype == U8
+
+
+def in_order(terms):
+    s = torch.zeros_like(terms[0])
+    for t in terms:
+        s = s + t
+    return s
+
+
+@pytest.mark.parametrize("before,n", [(0, 20), (0, 33), (10, 22), (10, 23), (0, 400), (17, 1000), (31, 5000)])
+@pytest.mark.parametrize("add", [False, True])
+def test_the_order_of_a_rows_sum(before, n, add):
+    """The header's: a row's tokens in their order between cuts at every 32nd of the sorted tokens; then those sums, the first one
+    and then every W-th in turn for each of W warps, 4 where the table is written and 2 where it is added to; then the warps'.
+    Terms of sizes that differ by 2^12 and cancel, so that what is left is each addition's rounding, float32 for float32 as
+    here."""
+    C, W = 512, 2 if add else 4
+    ids = torch.cat((torch.zeros(before), torch.ones(n))).long().cuda()
+    ids = ids[torch.randperm(before + n, generator=gen(n), device="cuda")]
+    half = (randn(n - n // 2, C, seed=n) * torch.exp2(12 * torch.rand(n - n // 2, C, generator=gen(n + 1), device="cuda"))).to(BF)
+    own = torch.cat((half, -half[:n // 2]))[torch.randperm(n, generator=gen(n + 2), device="cuda")]
+    dout = randn(before + n, C, seed=3).to(BF)
+    dout[ids == 1] = own
+    got = backward(dout, ids, 1.0, 2, torch.zeros(2, C, dtype=BF, device="cuda") if add else None)
+    cuts = [0, *range(32 - before % 32, n, 32), n]
+    parts = [in_order(own[a:b].float()) for a, b in zip(cuts, cuts[1:])]
+    assert len(cuts) == 2 or cuts[1] > 0
+    warps = [in_order(parts[:1] * (t == 0) + parts[1 + t::W]) if (t == 0 or parts[1 + t:]) else torch.zeros(C, device="cuda")
+             for t in range(W)]
+    want = in_order(warps)
+    assert torch.equal(got[1], want.to(BF))
