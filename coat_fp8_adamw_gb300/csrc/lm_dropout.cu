@@ -1,7 +1,7 @@
 // lm_dropout.cu -- dropout whose mask is drawn where it is needed and stored nowhere (forward and backward), with an
 // optional residual addition.
 //
-//   y[i] = keep[i] x[i] 65536 / (65536 - T) (+ residual[i]),  keep[i] = draw[i] >= T,  T = round(65536 p)
+//   y[i] = keep[i] x[i] 65536 / (65536 - T) (+ residual[i]),  keep[i] = draw[i] >= T,  T = round(65536 p), halves up
 //
 // draw[i] is 16 bits of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3",
 // SC 2011): counter (i / 8, rng[1]), key rng[0]; the four words hold eight draws, the low half of each word first.  The

@@ -103,12 +103,12 @@ def _rng(t, device):
 
 
 def coat_dropout(x, p: float, rng, y, residual=None, stream=None) -> None:
-    """y = keep x 65536 / (65536 - T) (+ residual), T = round(65536 p): dropout of x
-    (bf16, contiguous, any shape) whose mask is drawn from rng, an int64 tensor
-    (key, upper half of the counter) on the device, by Philox4x32-10 and stored
-    nowhere.  Calls that may not share their masks need one that differs in either;
-    it is read when the kernel runs, so a captured graph draws new bits once it has
-    changed."""
+    """y = keep x 65536 / (65536 - T) (+ residual), T = round(65536 p), halves up:
+    dropout of x (bf16, contiguous, any shape) whose mask is drawn from rng, an
+    int64 tensor (key, upper half of the counter) on the device, by Philox4x32-10
+    and stored nowhere.  Calls that may not share their masks need one that differs
+    in either; it is read when the kernel runs, so a captured graph draws new bits
+    once it has changed."""
     n, dev = x.numel(), x.device
     _call("coat_dropout", dev, stream, _ptr(x, _BF16, n, "x", dev),
           None if residual is None else _ptr(residual, _BF16, n, "residual", dev), float(p),

@@ -478,11 +478,12 @@ coat_status coat_embedding(const uint16_t *table, const void *ids, int32_t wide_
  * weight too: rows without a token are then not touched; otherwise they become
  * zeros).  Ids outside [0, V) have no gradient.
  *   dout [M x C] bf16, ids [M] in;  dtable [V x C] bf16 out (and in).
- * The sum is taken in float32, in an order that the ids alone decide: the tokens, sorted
- * by row, are cut every 32; a row's tokens between two cuts are added in their order, to
- * c0, c1, ...; these to W sums, s0 = c0 + c1 + c(1+W) + ..., st = c(1+t) + c(1+t+W) + ...;
- * and these to s0 + s1 + ....  W is 4, or 2 where `accumulate` is not 0, so that a row of
- * many tokens added to zeros may differ in float32's last bits from one that is written.
+ * The sum is taken in float32, in an order that the ids alone decide: the tokens are
+ * sorted by row modulo a power of two, then by row, and cut every 32; a row's tokens
+ * between two cuts are added in their order, to c0, c1, ...; these to W sums, s0 = c0 +
+ * c1 + c(1+W) + ..., st = c(1+t) + c(1+t+W) + ...; and these to s0 + s1 + ....  W is 4, or
+ * 2 where `accumulate` is not 0, so that a row of many tokens added to zeros may differ
+ * in float32's last bits from one that is written.
  */
 coat_status coat_embedding_backward(const uint16_t *dout, const void *ids, int32_t wide_ids, float scale,
                                     int64_t M, int64_t V, int64_t C, int32_t accumulate, uint16_t *dtable,
@@ -532,8 +533,8 @@ coat_status coat_linear_cross_entropy_backward(const uint16_t *x, int64_t x_ld, 
 size_t coat_linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t V, int64_t C, int64_t piece);
 
 /*
- * Dropout: y = keep x 65536 / (65536 - T) (+ residual), T = round(65536 p), p in
- * [0, 1) with T < 65536.  An element is kept where its 16 random bits are T or
+ * Dropout: y = keep x 65536 / (65536 - T) (+ residual), T = round(65536 p), halves up,
+ * p in [0, 1) with T < 65536.  An element is kept where its 16 random bits are T or
  * more: of counter (i / 8, rng[1]) and key rng[0], Philox4x32-10 (Salmon et al.,
  * SC 2011) gives four 32-bit words, whose halves, the low one first, belong to
  * elements i = 8 (i / 8) .. + 7.  A dropped element does not count, whatever it holds.

@@ -159,3 +159,15 @@ def test_refusals():
         coat.coat_dropout(x, 0.1, rng, y, residual=y[:32])
     with pytest.raises(ValueError, match="contiguous"):
         coat.coat_dropout_backward(torch.zeros(64, 2, dtype=BF, device="cuda")[:, 0], 0.1, rng, y)
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 65535])
+def test_the_threshold_is_rounded_up_from_the_middle(T):
+    """p = (T - 1/2) / 65536, which float32 holds: draws of T - 1 are dropped, draws of T kept.  Of 2^22 draws 64 are one value, in the
+    mean."""
+    n, rng = 1 << 22, key(21, T)
+    x, y = torch.ones(n, dtype=BF, device="cuda"), unwritten(n)
+    coat.coat_dropout(x, (T - 0.5) / 65536, rng, y)
+    d = draws(rng.tolist(), 0, n).cuda()
+    assert (d == T - 1).any() and (d == T).any()
+    assert torch.equal(y != 0, d >= T)
