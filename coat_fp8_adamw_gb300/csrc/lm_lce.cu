@@ -881,8 +881,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
 // stored times a factor within 1 +- 2^-8, with which the g of the first token that has a target and a g between 2^-100 and 2^100
 // in size is a bf16 value, and the products are multiplied by its reciprocal.  (Without such a token, 1.)  A block of its own
 // looks for that token, kUnitAhead a thread at once, since a long prompt without targets may come first (2^20 tokens, none with
-// a target: 0.9 us for 2048 of them).
-constexpr int kUnitAhead = 8;
+// a target: 0.8 us for 1024 of them).
+constexpr int kUnitAhead = 4;   // 8: 40 registers and six blocks per SM instead of eight, 8192 x 4096 22.7 us for 21.2
 __device__ __forceinline__ void unit_of(const void* targets, int32_t wide, const float* dloss, int64_t M, float* unit) {
     constexpr uint32_t kNone = 0xFFFFFFFFu;
     __shared__ uint32_t first;
