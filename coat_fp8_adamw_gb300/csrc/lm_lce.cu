@@ -263,8 +263,9 @@ __device__ __forceinline__ void add_segment(uint32_t acc0, int half, int bn, int
 }
 
 // Of a sum of e^(z - top), with top the largest z, a float32 keeps the terms but the largest only in units of 2^-23 of it, and the
-// loss of a certain token is the sum of those.  So what is kept is the rest: the sum without the largest one's 1 (of no logits,
-// or of -inf alone, -1).
+// loss of a certain token is the sum of those.  So what is kept of a sum is the rest: what it is beside the largest one's 1 (of
+// no logits, or of -inf alone, -1).  The 1 is summed with the up to 31 terms of its own chunk of columns, or of rows of the
+// weight, and then taken off, so that those terms alone are still in units of 2^-23.
 constexpr float kNoRest = -1.0f;
 // joined with the rest of others
 __device__ __forceinline__ void join_rest(float& top, float& rest, float top1, float rest1) {
