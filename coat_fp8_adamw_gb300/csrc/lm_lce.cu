@@ -264,8 +264,8 @@ __device__ __forceinline__ void add_segment(uint32_t acc0, int half, int bn, int
 
 // Of a sum of e^(z - top), with top the largest z, a float32 keeps the terms but the largest only in units of 2^-23 of it, and the
 // loss of a certain token is the sum of those.  So what is kept of a sum is the rest: what it is beside the largest one's 1 (of
-// no logits, or of -inf alone, -1).  The 1 is summed with the up to 31 terms of its own chunk of columns, or of rows of the
-// weight, and then taken off, so that those terms alone are still in units of 2^-23.
+// no logits, or of -inf alone, -1).  Of many tokens, the 1 is summed with the up to 31 terms of its own chunk of columns and then
+// taken off, so that those terms alone are still in units of 2^-23; of few, it is left out.
 constexpr float kNoRest = -1.0f;
 // joined with the rest of others
 __device__ __forceinline__ void join_rest(float& top, float& rest, float top1, float rest1) {
@@ -410,15 +410,24 @@ __device__ __forceinline__ void few_stats(const Work& w, const Logits<kFewChunks
             asm volatile("ld.shared.b32 %0, [%1];" : "=f"(z) : "r"(buf + (uint32_t)(4 * (33 * at + lane))));
             w.target_logit[token] = z;
         }
+        const bool more = mx > f.top[c];   // seldom behind the first tiles
+        int32_t at_k = -1;
+        if (__any_sync(kFull, more)) {
+#pragma unroll
+            for (int k = 0; k < kChunk; ++k)
+                if (more && __uint_as_float(v[k]) == mx) at_k = k;
+        }
         const float ref = mx == -INFINITY ? 0.0f : mx;
         uint64_t sums = pk(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < kChunk; k += 2) {
             float x, y;
-            exp2_of(v[k], v[k + 1], pk(-ref, -ref), x, y);
+            exp2_of(k == at_k ? 0xFF800000u : v[k], k + 1 == at_k ? 0xFF800000u : v[k + 1], pk(-ref, -ref), x, y);
             sums = add2(sums, pk(x, y));
         }
-        add_to_rest(f.top[c], f.rest[c], mx, ex2_ftz((f.top[c] - ref) * kLog2e), sum2(sums));
+        // the largest one's 1 is not in the sum, or, where an earlier chunk has it, its whole sum is beside that
+        f.rest[c] = sum2(sums) + (more ? (1.0f + f.rest[c]) * ex2_ftz((f.top[c] - ref) * kLog2e) : f.rest[c]);
+        f.top[c] = mx;
     }
 }
 
