@@ -6,7 +6,8 @@
 //
 // Four matrix products of 2 M V C operations, one forward and three backward (z is formed again), on the tensor cores:
 //   forward   a tile's logits stay in tensor memory; each of its rows leaves its maximum and sum of exponentials per
-//             half a tile (and the target's logit), which a second kernel joins: loss and lse;
+//             half a tile (and the target's logit), which a second kernel joins: loss and lse (of few tokens with the
+//             largest and the target's logit formed by itself);
 //   backward  in pieces of the vocabulary: a piece's logits again, whose epilogue leaves dz (bf16, in the workspace); then
 //             dx (added up over the pieces in float32) and the piece's rows of dW in one launch.
 // dz is rounded to bf16, since it is an operand of the tensor cores, like a layer's gradient that a step keeps as bf16.
@@ -120,8 +121,11 @@ struct Work {
     const float* dloss;
     const float* dlse;
     const float* unit;       // backward: what dz is stored times, and its reciprocal (see unit_of)
-    float2* stats;           // {maximum, rest} (see Rest), [half of a tile's columns, or, of few tokens, CTA][token], tokens padded
+    const float* share;      // backward, of few tokens: e^(z - lse) - 1 of the target's logit (see exact_parts), share_ld apart
+    int64_t share_ld;
+    float2* stats;           // {maximum, rest} (see kNoRest), [half of a tile's columns, or, of few tokens, CTA][token], tokens padded
     int64_t stats_ld;
+    int32_t* tops;           // of few tokens: the maximum's row of the weight, likewise (-1: of no logits, or of -inf alone)
     float* target_logit;
 };
 
@@ -200,7 +204,7 @@ struct Walk {
 // What is needed of a token (a lane's row of the logits, or its column of 32), loaded while the tile's MMAs still run.
 struct RowValues {
     int32_t target;          // -1: none; V: past the vocabulary
-    float lse, g, p;         // dz = p e^(z - lse) - [v = target] g
+    float lse, g, p;         // dz = p e^(z - lse) - [v = target] g; of few tokens, g is the target's dz itself
 };
 __device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int64_t token, int64_t tokens, float unit) {
     RowValues r{-1, 0.0f, 0.0f, 0.0f};
@@ -213,6 +217,11 @@ __device__ __forceinline__ RowValues row_values(const Work& w, const Job& j, int
     r.g = r.target < 0 ? 0.0f : r.target < w.V ? g : NAN;
     r.p = (r.g + h) * unit;
     r.g *= unit;
+    if (j.mode == kFewDz) {   // (g + h) e^(z - lse) - g, without a difference of e^(z - lse) and 1
+        r.g = h * unit;
+        if (r.target >= 0 && r.target < w.V && r.p != 0.0f)
+            r.g = fmaf(r.p, static_cast<const volatile float*>(w.share)[token * w.share_ld], r.g);
+    }
     return r;
 }
 
@@ -373,6 +382,7 @@ __device__ __forceinline__ void stats_of_row(const Work& w, const Job& j, const 
 struct FewTokens {
     RowValues r[kFewChunks];
     float top[kFewChunks], rest[kFewChunks];
+    int32_t at[kFewChunks];          // top's row of the weight
 };
 __device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t n0, int64_t end, int lane, float unit, FewTokens& f) {
 #pragma unroll
@@ -380,6 +390,7 @@ __device__ __forceinline__ void few_tokens(const Work& w, const Job& j, int64_t 
         f.r[c] = row_values(w, j, n0 + kChunk * c + lane, end, unit);
         f.top[c] = -INFINITY;
         f.rest[c] = kNoRest;
+        f.at[c] = -1;
     }
 }
 
@@ -416,6 +427,7 @@ __device__ __forceinline__ void few_stats(const Work& w, const Logits<kFewChunks
 #pragma unroll
             for (int k = 0; k < kChunk; ++k)
                 if (more && __uint_as_float(v[k]) == mx) at_k = k;
+            if (more) f.at[c] = (int32_t)row0 + at_k;
         }
         const float ref = mx == -INFINITY ? 0.0f : mx;
         uint64_t sums = pk(0.0f, 0.0f);
@@ -549,7 +561,7 @@ __device__ __forceinline__ void few_dz(const Work& w, const Job& j, Logits<kFewC
             for (int e = 0; e < kChunk; ++e) {
                 const int t = __shfl_sync(kFull, mine, e);
                 const float g = __shfl_sync(kFull, r.g, e);
-                if (t == lane) v[e] = __float_as_uint(__uint_as_float(v[e]) - g);
+                if (t == lane) v[e] = __float_as_uint(g);
             }
         }
         store_columns(j.out, j.ld, row, col, ok ? end - col : 0, lane, v);
@@ -815,11 +827,13 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
             }
         }
         if (kKind == kFewLogits && w.job[0].mode == kFewStats) {   // the four warps of a half, which have the same tokens
-            auto at = [&](int q, int c) { return staging + (uint32_t)((q - q4) * kStagingBytes + 8 * (kChunk * c + lane)); };
+            auto at = [&](int q, int c) { return staging + (uint32_t)((q - q4) * kStagingBytes + 16 * (kChunk * c + lane)); };
             __syncwarp();
 #pragma unroll
             for (int c = 0; c < kFewChunks; ++c)
-                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at(q4, c)), "f"(tokens.top[c]), "f"(tokens.rest[c]) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %3};" ::"r"(at(q4, c)), "r"(__float_as_uint(tokens.top[c])),
+                             "r"(__float_as_uint(tokens.rest[c])), "r"(tokens.at[c])
+                             : "memory");
             asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory");
 #pragma unroll
             for (int c = 0; c < kFewChunks; ++c) {
@@ -827,11 +841,14 @@ __global__ void __launch_bounds__(kThreads, 1) lce_kernel(const __grid_constant_
                 if (q4 != 0 || token >= few_end) continue;
 #pragma unroll
                 for (int q = 1; q < 4; ++q) {
-                    float top1, rest1;
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(top1), "=f"(rest1) : "r"(at(q, c)) : "memory");
-                    join_rest(tokens.top[c], tokens.rest[c], top1, rest1);
+                    uint32_t top1, rest1, at1, same;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(top1), "=r"(rest1), "=r"(at1), "=r"(same) : "r"(at(q, c)) : "memory");
+                    if (__uint_as_float(top1) > tokens.top[c]) tokens.at[c] = (int32_t)at1;
+                    join_rest(tokens.top[c], tokens.rest[c], __uint_as_float(top1), __uint_as_float(rest1));
                 }
-                w.stats[(2 * pair + rank) * w.stats_ld + token] = make_float2(tokens.top[c], tokens.rest[c]);
+                const int64_t i = (2 * pair + rank) * w.stats_ld + token;
+                w.stats[i] = make_float2(tokens.top[c], tokens.rest[c]);
+                w.tops[i] = tokens.at[c];
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the stores by TMA are done
@@ -885,6 +902,115 @@ __global__ void __launch_bounds__(32 * kJoinWarps) lce_join_kernel(const float2*
     loss[row] = t < 0 ? 0.0f : t >= V ? NAN : (top - z) + low;
 }
 
+// Of few tokens, logits by themselves: four warps have one token and kN rows of the weight, every fourth 256 columns each, products
+// added in float32 with its rounding, C / 512 of them in a chain.  What the tensor cores make of a logit falls short by about
+// 2e-7 of its size (lse of logits of 64: 1.2e-5, in all tokens alike), and the gradient of a token that is all but certain is a
+// difference with its logit: 6 % off with a probability of 1 - 2e-4, and with fewer than ten tokens all results may be one
+// such token's.  So few tokens' loss and gradient are formed with these, for the largest and the target's logit (33 x 50304 x
+// 2048 forward 39.3 us for 38.4, 33 x 512 x 2048 14.5 for 12.5; backward of 33 x 512 x 256 12.3 for 12.0).
+constexpr int kSplit = 4;
+template <int kN>
+__device__ __forceinline__ void exact_parts(const uint16_t* x, const uint16_t* const (&w)[kN], int64_t C, int lane, int quarter, float (&z)[kN]) {
+    constexpr int kDot = 2, kStep = 256 * kSplit;   // chunks of 256 columns on their way at once
+    float sum[kN][4] = {};
+#pragma unroll 1
+    for (int64_t c0 = 256 * quarter + 8 * lane; c0 < C; c0 += kStep * kDot) {
+        uint32_t xv[kDot][4], wv[kN][kDot][4];
+#pragma unroll
+        for (int k = 0; k < kDot; ++k) {   // (no load behind a branch: behind the end the ones before again, which do not count)
+            const int64_t c = c0 + kStep * k < C ? c0 + kStep * k : c0;
+            load_words<4>(x + c, xv[k]);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) load_words<4>(w[n] + c, wv[n][k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kDot; ++k) {
+            if (c0 + kStep * k >= C) continue;
+            float a[8], b[8];
+            unpack(xv[k], a);
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                unpack(wv[n][k], b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[n][e & 3] = fmaf(a[e], b[e], sum[n][e & 3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+        z[n] = (sum[n][0] + sum[n][1]) + (sum[n][2] + sum[n][3]);
+        for (int off = 16; off > 0; off >>= 1) z[n] += __shfl_xor_sync(kFull, z[n], off);
+    }
+}
+__device__ __forceinline__ float exact_logit(const float (&parts)[kSplit]) { return (parts[0] + parts[1]) + (parts[2] + parts[3]); }
+
+// loss and lse of few tokens from the CTAs' maxima and rests: kFewRows rows per block, with kSplit warps each in the end.  lse is
+// the same whatever the targets are.
+constexpr int kFewRows = 8;
+static_assert(kFewRows * kSplit == 32, "a block's warps");
+__global__ void __launch_bounds__(1024) lce_join_few_kernel(const LceFwdArgs a, const float2* stats, const int32_t* tops, int64_t ld, int64_t parts) {
+    __shared__ float2 part[32][kFewRows];
+    __shared__ int32_t part_at[32][kFewRows];
+    __shared__ float exact[2][kFewRows][kSplit];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / kSplit, quarter = warp % kSplit;
+    const int64_t row0 = (int64_t)blockIdx.x * kFewRows, row = row0 + mine;
+    wait_for_primary();
+    dependents_may_start();
+    int64_t t = -1;
+    float z = 0.0f;
+    if (row < a.M) {   // what the end needs, with the first loads
+        t = index_at(a.targets, a.wide, row);
+        z = static_cast<const volatile float*>(a.loss)[row];
+    }
+    float top = -INFINITY, rest = kNoRest;
+    int32_t at = -1;
+    auto join = [&](float top1, float rest1, int32_t at1) {   // (of two that are the largest alike, the lower row: all lanes hold the same)
+        if (top1 > top || (top1 == top && (uint32_t)at1 < (uint32_t)at)) at = at1;
+        join_rest(top, rest, top1, rest1);
+    };
+    auto join_lanes = [&](int least) {
+        for (int off = 16; off >= least; off >>= 1)
+            join(__shfl_xor_sync(kFull, top, off), __shfl_xor_sync(kFull, rest, off), __shfl_xor_sync(kFull, at, off));
+    };
+    // stats_ld is a multiple of 32: the rows behind the last one are there, whatever they hold
+    const int64_t from = row0 + lane % kFewRows;
+#pragma unroll 2
+    for (int64_t i = kSplit * warp + lane / kFewRows; i < parts; i += 32 * kSplit) {
+        const float2 f = stats[i * ld + from];
+        join(f.x, f.y, tops[i * ld + from]);
+    }
+    join_lanes(kFewRows);
+    if (lane < kFewRows) {
+        part[warp][lane] = make_float2(top, rest);
+        part_at[warp][lane] = at;
+    }
+    __syncthreads();
+    top = part[lane][mine].x;
+    rest = part[lane][mine].y;
+    at = part_at[lane][mine];
+    join_lanes(1);
+    if (row < a.M && at >= 0) {
+        const uint16_t* const w[2] = {a.weight + at * a.C, a.weight + (t >= 0 && t < a.V ? t : at) * a.C};
+        float e[2];
+        exact_parts(a.x + row * a.x_ld, w, a.C, lane, quarter, e);
+        if (lane < 2) exact[lane][mine][quarter] = lane == 0 ? e[0] : e[1];
+    }
+    __syncthreads();
+    if (row >= a.M || quarter != 0 || lane != 0) return;
+    if (at >= 0) {
+        const float e = exact_logit(exact[0][mine]);
+        if (fabsf(e) < INFINITY) {   // the rest is of the others, against the largest one
+            rest *= expf(top - e);
+            top = e;
+            z = exact_logit(exact[1][mine]);
+        }
+    }
+    const float low = log1pf(rest);
+    a.lse[row] = top + low;
+    // (top - z) + log(sum): nothing cancels where the target's logit is the largest
+    a.loss[row] = t < 0 ? 0.0f : t >= a.V ? NAN : (top - z) + low;
+}
+
 // The gradient of a target's logit is -g (1 - e^(z - lse)), which is -g for most tokens, and with a mean over the tokens g is
 // the same for all of them: rounded to bf16, they would all be off by the same share of themselves, up to 2^-8, and dx and dW
 // with them (8192 x 32000 x 4096, a mean over the tokens: 2.0e-3 to 2.9e-3 off by the number of tokens, so 2.0e-3).  So dz is
@@ -933,23 +1059,43 @@ __device__ __forceinline__ void unit_of(const void* targets, int32_t wide, const
     }
 }
 
-// xt[c][m] = x[m][c]: tiles of 64 x 64 through shared memory, behind a block that finds the unit.  (xt's rows are whole 16-byte
-// units; what lies behind their M elements is not read.)
-__global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, int64_t x_ld, int64_t M, int64_t C, uint16_t* xt, int64_t ld,
-                                                            const void* targets, int32_t wide, const float* dloss, float* unit) {
+// Where few tokens' shares are kept until dx is written: in dx itself, at the beginning of the token's row.
+__host__ __device__ __forceinline__ float* share_of(const LceBwdArgs& a) { return reinterpret_cast<float*>(a.dx); }
+
+// xt[c][m] = x[m][c]: tiles of 64 x 64 through shared memory, behind a block that finds the unit and, of few tokens, in front of
+// those that find their shares.  (xt's rows are whole 16-byte units; what lies behind their M elements is not read.)
+template <bool kFew>
+__global__ void __launch_bounds__(256) lce_transpose_kernel(const LceBwdArgs a) {
     __shared__ uint16_t tile[64][66];
-    const int64_t across = (M + 63) / 64, i0 = (int64_t)blockIdx.x - 1, m0 = i0 % across * 64, c0 = i0 / across * 64;
+    const int64_t M = a.M, C = a.C, ld = (M + 7) / 8 * 8, across = (M + 63) / 64;
+    const int64_t i0 = (int64_t)blockIdx.x - 1, m0 = i0 % across * 64, c0 = i0 / across * 64;
     wait_for_primary();
     dependents_may_start();
-    if (blockIdx.x == 0) {
-        unit_of(targets, wide, dloss, M, unit);
+    if (i0 < 0) {
+        unit_of(a.targets, a.wide, a.dloss, M, a.unit);
+        return;
+    }
+    if (kFew && c0 >= C) {
+        __shared__ float exact[8 / kSplit][kSplit];
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = warp / kSplit, quarter = warp % kSplit;
+        const int64_t m = (i0 - across * ((C + 63) / 64)) * (8 / kSplit) + mine, t = m < M ? index_at(a.targets, a.wide, m) : -1;
+        const bool has = t >= 0 && t < a.V;
+        if (has) {
+            const uint16_t* const w[1] = {a.weight + t * C};
+            float z[1];
+            exact_parts(a.x + m * a.x_ld, w, C, lane, quarter, z);
+            if (lane == 0) exact[mine][quarter] = z[0];
+        }
+        __syncthreads();
+        if (has && quarter == 0 && lane == 0)
+            share_of(a)[m * (C / 2)] = expm1f(exact_logit(exact[mine]) - static_cast<const volatile float*>(a.lse)[m]);
         return;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int i = threadIdx.x + 256 * h, r = i >> 3, c = (i & 7) * 8;
         uint32_t w[4] = {};
-        if (m0 + r < M && c0 + c < C) load_words<4>(x + (m0 + r) * x_ld + c0 + c, w);
+        if (m0 + r < M && c0 + c < C) load_words<4>(a.x + (m0 + r) * a.x_ld + c0 + c, w);
 #pragma unroll
         for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t*>(&tile[r][c + 2 * k]) = w[k];
     }
@@ -961,7 +1107,7 @@ __global__ void __launch_bounds__(256) lce_transpose_kernel(const uint16_t* x, i
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = (uint32_t)tile[r + 2 * k][c] | (uint32_t)tile[r + 2 * k + 1][c] << 16;
-        *reinterpret_cast<uint4*>(xt + (c0 + c) * ld + m0 + r) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(a.xt + (c0 + c) * ld + m0 + r) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -1224,10 +1370,14 @@ cudaError_t launch_lce_fwd(const LceFwdArgs& a, cudaStream_t s) {
     w.V = (int32_t)a.V;
     w.stats = reinterpret_cast<float2*>(a.stats);
     w.stats_ld = up(a.M, 32) * 32;
+    w.tops = reinterpret_cast<int32_t*>(w.stats + w.stats_ld * 2 * kPairs);
     w.target_logit = a.loss;
     cudaError_t e = launch_work(w, maps, s);
     if (e != cudaSuccess) return e;
     const int64_t parts = few ? 2 * (int64_t)w.pairs : 2 * w.job[0].tn;   // the CTAs, or two of each tile
+    if (few)
+        return launch_next(lce_join_few_kernel, (unsigned)up(a.M, kFewRows), 1024, 0, s, a, (const float2*)w.stats, (const int32_t*)w.tops,
+                           w.stats_ld, parts);
     return launch_next(lce_join_kernel, (unsigned)up(a.M, 32), 32 * kJoinWarps, 0, s, (const float2*)w.stats, w.stats_ld,
                        parts, a.targets, a.wide, a.M, a.V, a.loss, a.lse);
 }
@@ -1237,8 +1387,9 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
     const Parts parts = parts_of(a.M, a.piece, a.C);
     float* const dw_sums = a.sums + lce_dx_sums(a.M, a.V, a.C, a.piece);
     const bool dx_sums = parts.dx > 1 || a.piece < a.V;
-    cudaError_t e = launch_next(lce_transpose_kernel, (unsigned)(1 + up(a.M, 64) * up(a.C, 64)), 256, 0, s, a.x, a.x_ld, a.M, a.C,
-                                a.xt, lce_xt_ld(a.M), a.targets, a.wide, a.dloss, a.unit);
+    const bool few = a.M <= kFewTokens;
+    cudaError_t e = launch_next(few ? lce_transpose_kernel<true> : lce_transpose_kernel<false>,
+                                (unsigned)(1 + up(a.M, 64) * up(a.C, 64) + (few ? up(a.M * kSplit, 8) : 0)), 256, 0, s, a);
     if (e != cudaSuccess) return e;
     for (int64_t v0 = 0; v0 < a.V; v0 += a.piece) {
         const int64_t n = a.V - v0 < a.piece ? a.V - v0 : a.piece;
@@ -1246,7 +1397,7 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
         Work w = {};
         alignas(64) Maps maps;
         const Operand x{a.x, a.M, a.C, a.x_ld, false}, Wz{W, n, a.C, a.C, false};
-        if (!(a.M <= kFewTokens ? add_job(w, maps, kFewDz, Wz, x, a.dz, ld) : add_job(w, maps, kDz, x, Wz, a.dz, ld)))
+        if (!(few ? add_job(w, maps, kFewDz, Wz, x, a.dz, ld) : add_job(w, maps, kDz, x, Wz, a.dz, ld)))
             return cudaErrorInvalidValue;
         w.targets = a.targets;
         w.wide = a.wide;
@@ -1256,6 +1407,8 @@ cudaError_t launch_lce_bwd(const LceBwdArgs& a, cudaStream_t s) {
         w.dloss = a.dloss;
         w.dlse = a.dlse;
         w.unit = a.unit;
+        w.share = share_of(a);
+        w.share_ld = a.C / 2;
         e = launch_work(w, maps, s);
         if (e != cudaSuccess) return e;
         w.jobs = 0;
@@ -1305,8 +1458,8 @@ int64_t lce_sums(int64_t M, int64_t V, int64_t C, int64_t piece) {
     return lce_dx_sums(M, V, C, piece) + (p.dw > 1 ? p.dw * piece * C : 0);
 }
 size_t lce_stats_bytes(int64_t M, int64_t V) {
-    const int64_t parts = M <= kFewTokens ? 2 * kPairs : 2 * up(V, tile_columns(M, V, kStats));
-    return 8 * (size_t)(up(M, 32) * 32) * (size_t)parts;
+    const size_t tokens = (size_t)(up(M, 32) * 32);
+    return M <= kFewTokens ? 12 * tokens * (size_t)(2 * kPairs) : 8 * tokens * (size_t)(2 * up(V, tile_columns(M, V, kStats)));
 }
 
 cudaError_t read_lce_wait_timeouts(unsigned long long* out, bool reset) { return read_own_wait_timeouts(out, reset); }

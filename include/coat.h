@@ -498,8 +498,11 @@ size_t coat_embedding_backward_workspace_bytes(int64_t M, int64_t V, int64_t C);
  *   of V or more NaN;  loss, lse [M] float32 out.
  * Products are added in float32, by the tensor cores, which truncate, over 512 of C
  * at a time: a logit is within (C + 8) 2^-22 sum |x W| of the sum at worst, and lse
- * and loss of theirs, with float32's roundings of what they are formed of.  The logits have to be
- * finite or -inf (a token whose logits all are -inf has lse -inf and loss NaN).  M V at most COAT_MAX_N, here and below.
+ * and loss of theirs, with float32's roundings of what they are formed of.  Of up to
+ * 128 tokens, a token's largest logit and its target's are added up with float32's
+ * rounding, here and in the backward pass.  The logits have to be finite or -inf (a
+ * token whose logits all are -inf has lse -inf and loss NaN).  M V at most COAT_MAX_N,
+ * here and below.
  */
 coat_status coat_linear_cross_entropy(const uint16_t *x, int64_t x_ld, const uint16_t *weight,
                                       const void *targets, int32_t wide_targets, int64_t M, int64_t V, int64_t C,
