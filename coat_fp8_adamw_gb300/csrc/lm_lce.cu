@@ -989,6 +989,7 @@ __global__ void __launch_bounds__(1024) lce_join_few_kernel(const LceFwdArgs a, 
     rest = part[lane][mine].y;
     at = part_at[lane][mine];
     join_lanes(1);
+    if (at >= a.V) at = -1;   // a row of the weight, whatever another call has done to the workspace
     if (row < a.M && at >= 0) {
         const uint16_t* const w[2] = {a.weight + at * a.C, a.weight + (t >= 0 && t < a.V ? t : at) * a.C};
         float e[2];
